@@ -315,6 +315,39 @@ w4a16_status w4a16_linear_dense(const void* x, const void* w, const void* bias, 
 size_t w4a16_dense_workspace_size(int64_t M, int64_t N, int64_t K, int32_t dtype,
                                   int32_t has_bias);
 
+/* ------------------------------------------------- low-rank adapters ---
+ * The projection with low-rank adapters of many requests beside it: token m
+ * names adapter a = ids[m], and
+ *   u[m, :] = x[m, :] . A_a^T                       (fp32, [M, R])
+ *   y[m, :] = x[m, :] . dequant(Wq)^T + bias + alpha_a * (u[m, :] . B_a^T)
+ * accumulated in fp32 and rounded once to the activation dtype.
+ *   la    act   [S, R, K]  the adapters' first factors A
+ *   lb    act   [S, N, R]  their second factors B
+ *   ids   int32 [M]        device; an id outside [0, S) means no adapter: u is
+ *                          zero and y is w4a16_linear's value.  Any order;
+ *                          tokens of one adapter need not be neighbours.
+ *   alpha fp32  [S] or NULL (1)
+ *   u     fp32  [M, R] or NULL; kept for w4a16_lora_backward when given
+ * R, one rank for the whole stack, is a multiple of 8 up to 128 (an adapter of
+ * a lower rank is padded with zero rows of A and zero columns of B).  The
+ * other arguments, their layout and their alignment as for w4a16_linear; la
+ * and lb 16-byte, u 16-byte, ids and alpha 4-byte aligned.  y and u must not
+ * overlap any input or each other.  Above the decode threshold alpha * u is
+ * carried as two values of the activation dtype, so with fp16 it has to stay
+ * below 65504 there.
+ * Workspace: always needed (w4a16_lora_workspace_size), 256-byte aligned,
+ * under w4a16_linear's rules: zero-filled before its first use, then
+ * reusable by calls of any entry point on the same stream.
+ * Errors: those of w4a16_linear; W4A16_ERR_INVALID_ARG for S < 1 or a rank
+ * that is no positive multiple of 8, W4A16_ERR_UNSUPPORTED for one above 128. */
+size_t w4a16_lora_workspace_size(int64_t M, int64_t N, int64_t K, int32_t group_size, int32_t dtype,
+                                 int32_t has_zp, int64_t R, int32_t save_u);
+w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* scales, const int32_t* zp,
+                               const void* bias, const void* la, const void* lb, const int32_t* ids,
+                               const float* alpha, void* y, float* u, int64_t M, int64_t N, int64_t K,
+                               int32_t group_size, int64_t S, int64_t R, int32_t dtype, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 /* The 4-bit codes q[N, K] (uint8, 0..15) unpacked on the device from wq. */
 w4a16_status w4a16_unpack_device(const int32_t* wq, uint8_t* q, int64_t N, int64_t K,
                                  void* stream);

@@ -54,6 +54,9 @@ SIGNATURES = {
     "w4a16_linear_dense": (_c_int, [_vp, _vp, _vp, _vp, _c_i64, _c_i64, _c_i64, _c_i32, _vp, _c_sz,
                                     _vp]),
     "w4a16_dense_workspace_size": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i32, _c_i32]),
+    "w4a16_lora_workspace_size": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_i64, _c_i32]),
+    "w4a16_lora_linear": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_i64,
+                                   _c_i64, _c_i32, _c_i64, _c_i64, _c_i32, _vp, _c_sz, _vp]),
     "w4a16_moe_linear": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_i64, _c_i64,
                                   _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _vp]),
 }
@@ -435,3 +438,50 @@ def w4a16_moe_linear(x, wq, scales, topk_ids, zp=None, bias=None, topk_weights=N
                                     topk_ids.data_ptr(), _ptr(topk_weights), out.data_ptr(), M, topk, E,
                                     N, K, group_size, dt, int(bool(x_per_slot)), stream))
     return out
+
+
+# ------------------------------------------------------ low-rank adapters ---
+
+def w4a16_lora_workspace_size(M, N, K, group_size, dtype, has_zp, R, save_u=False) -> int:
+    return int(lib.w4a16_lora_workspace_size(M, N, K, group_size, dtype, int(bool(has_zp)), R, int(bool(save_u))))
+
+
+def _adapter_args(x, la, lb, ids, alpha, M, N, K):
+    torch = _torch()
+    if la.dim() != 3 or la.shape[2] != K:
+        raise ValueError(f"la is {tuple(la.shape)}, expected [S, R, {K}]")
+    S, R = la.shape[0], la.shape[1]
+    if tuple(lb.shape) != (S, N, R):
+        raise ValueError(f"lb is {tuple(lb.shape)}, expected {(S, N, R)}")
+    if la.dtype != x.dtype or lb.dtype != x.dtype:
+        raise TypeError(f"la and lb must be {x.dtype}, got {la.dtype} and {lb.dtype}")
+    if ids.dtype != torch.int32 or tuple(ids.shape) != (M,):
+        raise TypeError(f"ids must be int32 [{M}], got {ids.dtype} {tuple(ids.shape)}")
+    if alpha is not None and (alpha.dtype != torch.float32 or tuple(alpha.shape) != (S,)):
+        raise TypeError(f"alpha must be float32 [{S}]")
+    for t, name in ((la, "la"), (lb, "lb"), (ids, "ids"), (alpha, "alpha")):
+        _require_device(t, name, x.device)
+    return S, R
+
+
+def w4a16_lora_linear(x, wq, scales, la, lb, ids, zp=None, bias=None, alpha=None, *, group_size: int,
+                      save_u: bool = False, out=None, workspace=None):
+    """y = x . dequant(wq, scales, zp)^T (+ bias) + alpha_a * (x . A_a^T) . B_a^T with token
+    m's adapter a = ids[m] out of the stacks la [S, R, K] and lb [S, N, R] (an id outside
+    [0, S): no adapter).  With save_u returns (y, u), u = x . A_a^T in float32 [M, R] for
+    w4a16_lora_backward."""
+    torch = _torch()
+    dt, M, N, K, out = _linear_args(x, wq, scales, zp, bias, group_size, out)
+    S, R = _adapter_args(x, la, lb, ids, alpha, M, N, K)
+    u = torch.empty((M, R), dtype=torch.float32, device=x.device) if save_u else None
+    stream = torch.cuda.current_stream(x.device).cuda_stream
+    with torch.cuda.device(x.device):
+        if workspace is None:
+            workspace = _workspace(x.device, stream, w4a16_lora_workspace_size(M, N, K, group_size, dt, zp is not None,
+                                                                               R, save_u))
+        ws_ptr = None if workspace is None else workspace.data_ptr()
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(lib.w4a16_lora_linear(x.data_ptr(), wq.data_ptr(), scales.data_ptr(), _ptr(zp), _ptr(bias),
+                                     la.data_ptr(), lb.data_ptr(), ids.data_ptr(), _ptr(alpha), out.data_ptr(),
+                                     _ptr(u), M, N, K, group_size, S, R, dt, ws_ptr, ws_bytes, stream))
+    return (out, u) if save_u else out

@@ -32,7 +32,8 @@ COMMON = [
     "-Wall", "-Wno-unused-function",
     f"-I{INCLUDE}", f"-I{CSRC}",
 ]
-SOURCES = ["w4a16_host.cpp", "w4a16_gemv.hip", "w4a16_gemm.hip", "w4a16_elementwise.hip"]
+SOURCES = ["w4a16_host.cpp", "w4a16_gemv.hip", "w4a16_gemm.hip", "w4a16_gemm_lora.hip", "w4a16_lora.hip",
+           "w4a16_elementwise.hip"]
 # measurement kernels for the benchmark's ceilings, a library of their own
 CEILING_SOURCES = ["w4a16_ceilings.hip"]
 CEILINGS_LIB = os.path.join(PKG, "libw4a16_ceilings.so")
@@ -97,7 +98,7 @@ def _llvm_tool(name: str) -> str:
     raise RuntimeError(f"{name} not found")
 
 
-_THIN = re.compile(r"<(_Z\S*gemm_kernelILi\d+ELi\d+ELb(\d)ELi1ELi(\d)ELb(\d)E\S*)>:")
+_THIN = re.compile(r"<(_Z\S*gemm_(?:lora_)?kernelILi\d+ELi\d+ELb(\d)ELi1ELi(\d)E(?:Lb(\d)E)?\S*)>:")
 _META = ("global_load_ushort", "global_load_short_d16", "global_load_dword", "global_load_sshort")
 
 
@@ -173,8 +174,9 @@ def build(verbose: bool = False) -> str:
     with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES) + len(CEILING_SOURCES))) as ex:
         objs = list(ex.map(_compile, SOURCES + CEILING_SOURCES))
     # the thin GEMM tiles' partial wait relies on the compiled load order
-    if check_thin_tile_waits(objs[SOURCES.index("w4a16_gemm.hip")]) == 0:
-        raise RuntimeError("no partial-wait step barrier found in the 32-token GEMM tiles")
+    for src in ("w4a16_gemm.hip", "w4a16_gemm_lora.hip"):
+        if check_thin_tile_waits(objs[SOURCES.index(src)]) == 0:
+            raise RuntimeError(f"no partial-wait step barrier found in the 32-token GEMM tiles of {src}")
     _link(objs[:len(SOURCES)], LIB)
     _link(objs[len(SOURCES):], CEILINGS_LIB)
     if verbose:

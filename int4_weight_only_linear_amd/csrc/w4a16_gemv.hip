@@ -50,6 +50,7 @@
 
 #include "w4a16_device.hpp"
 #include "w4a16_internal.h"
+#include "w4a16_lora.hpp"
 
 
 namespace w4a16 {
@@ -87,6 +88,7 @@ struct GemvParams {
   int topk, experts, x_per_slot;
   size_t w_estride, s_estride, z_estride;  // words / halves / words per expert
   int slots;  // workgroups along z: 1, or the expert slots
+  LoraTerm lora;  // low-rank adapters beside the projection (ids NULL: none)
 };
 
 // One 16-byte global->LDS load per active lane: lane l reads base + off and
@@ -180,6 +182,7 @@ __device__ __forceinline__ void finish_tile(const GemvParams& p, const float* re
       for (int w = 0; w < nwaves; ++w) v += red[w * nel + e];
       if (p.splits == 1) {
         if (p.bias) v += act_to_f32<DT>(p.bias[nn]);
+        if (p.lora.ids) v += lora_dot<DT>(p.lora, p.M, p.N, m, nn);
         p.y[(size_t)m * p.N + nn] = f32_to_act<DT>(v * p.yscale);
       } else {
         store_coherent(p.partial + ((size_t)split * p.M + m) * p.N + nn, v);
@@ -203,6 +206,7 @@ __device__ __forceinline__ void finish_tile(const GemvParams& p, const float* re
       float v = 0.f;
       for (int s = 0; s < p.splits; ++s) v += load_coherent(p.partial + ((size_t)s * p.M + m) * p.N + nn);
       if (p.bias) v += act_to_f32<DT>(p.bias[nn]);
+      if (p.lora.ids) v += lora_dot<DT>(p.lora, p.M, p.N, m, nn);
       p.y[(size_t)m * p.N + nn] = f32_to_act<DT>(v * p.yscale);
     }
   }
@@ -627,6 +631,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(small_wave
         float v = 0.f;
         for (int w = 0; w < nwaves; ++w) v += red[w * 256 + tid];
         if (p.bias) v += act_to_f32<DT>(p.bias[nn]);
+        if (p.lora.ids) v += lora_dot<DT>(p.lora, p.M, p.N, 0, nn);
         p.y[nn] = f32_to_act<DT>(v * p.yscale);
       }
       return;
@@ -643,6 +648,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(small_wave
       float v = 0.f;
       for (int w = 0; w < nwaves; ++w) v += red[w * 256 + m * 64 + (tid & 15)];
       if (p.bias) v += act_to_f32<DT>(p.bias[nn]);
+      if (p.lora.ids) v += lora_dot<DT>(p.lora, p.M, p.N, m, nn);
       p.y[(size_t)m * p.N + nn] = f32_to_act<DT>(v * p.yscale);
     }
     return;
@@ -766,6 +772,7 @@ struct OneArgs {
   float* partial;
   uint32_t* counters;
   int splits, runs_per_split;
+  LoraTerm lora;  // low-rank adapters beside the projection (ids NULL: none)
 };
 
 // PART: the last wave's run may be shorter (otherwise every run is whole and
@@ -1014,6 +1021,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(one_waves_
       for (int w = 0; w < nwaves; ++w) v += red_of(w)[m * 16 + (e & 15)];
       if constexpr (!SPLIT) {
         if (bias) v += act_to_f32<DT>(bias[nn]);
+        if (!MOE && moe.lora.ids) v += lora_dot<DT>(moe.lora, M, N, m, nn);
         y[(size_t)m * N + nn] = f32_to_act<DT>(MOE ? v * yscale : v);
       } else {
         store_coherent(moe.partial + ((size_t)blockIdx.y * M + m) * N + nn, v);
@@ -1038,6 +1046,7 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(one_waves_
       float v = 0.f;
       for (int sp = 0; sp < splits; ++sp) v += load_coherent(moe.partial + ((size_t)sp * M + m) * N + nn);
       if (bias) v += act_to_f32<DT>(bias[nn]);
+      if (moe.lora.ids) v += lora_dot<DT>(moe.lora, M, N, m, nn);
       y[(size_t)m * N + nn] = f32_to_act<DT>(v);
     }
   }
@@ -1249,7 +1258,7 @@ static hipError_t launch_g(const GemvParams& prm, int group, const GemvPlan& pla
 
 template <int DT, int GS, bool ASYM, int KPW, int MT>
 static hipError_t launch_one_k(const LinearArgs& a, const GemvPlan& plan, hipStream_t s, const MoeArgs* moe,
-                               void* workspace) {
+                               void* workspace, const LoraTerm* lora) {
   // instances: at most 16 groups a run, at most 4 finished by a 16-lane row,
   // at most 32 group sums per result register
   constexpr int NGW = kGemvKStep * KPW / GS;
@@ -1261,6 +1270,7 @@ static hipError_t launch_one_k(const LinearArgs& a, const GemvPlan& plan, hipStr
     const int runs = (int)((a.K / kGemvKStep + KPW - 1) / KPW);
     const bool part = (int64_t)runs * KPW * kGemvKStep != a.K || plan.one_splits * plan.one_waves != runs;
     OneArgs om{};
+    if (lora) om.lora = *lora;
     om.splits = plan.one_splits;
     om.runs_per_split = plan.one_waves;
     if (plan.one_splits > 1) {
@@ -1300,30 +1310,30 @@ static hipError_t launch_one_k(const LinearArgs& a, const GemvPlan& plan, hipStr
 
 template <int DT, int GS, bool ASYM>
 static hipError_t launch_one(const LinearArgs& a, const GemvPlan& plan, hipStream_t s, const MoeArgs* moe,
-                             void* ws) {
+                             void* ws, const LoraTerm* lora) {
   const int key = plan.one_kpw * 10 + plan.one_mt;
   switch (key) {
-    case 81: return launch_one_k<DT, GS, ASYM, 8, 1>(a, plan, s, moe, ws);
-    case 82: return launch_one_k<DT, GS, ASYM, 8, 2>(a, plan, s, moe, ws);
-    case 84: return launch_one_k<DT, GS, ASYM, 8, 4>(a, plan, s, moe, ws);
-    case 41: return launch_one_k<DT, GS, ASYM, 4, 1>(a, plan, s, moe, ws);
-    case 42: return launch_one_k<DT, GS, ASYM, 4, 2>(a, plan, s, moe, ws);
-    case 44: return launch_one_k<DT, GS, ASYM, 4, 4>(a, plan, s, moe, ws);
-    case 88: return launch_one_k<DT, GS, ASYM, 8, 8>(a, plan, s, moe, ws);
-    case 48: return launch_one_k<DT, GS, ASYM, 4, 8>(a, plan, s, moe, ws);
+    case 81: return launch_one_k<DT, GS, ASYM, 8, 1>(a, plan, s, moe, ws, lora);
+    case 82: return launch_one_k<DT, GS, ASYM, 8, 2>(a, plan, s, moe, ws, lora);
+    case 84: return launch_one_k<DT, GS, ASYM, 8, 4>(a, plan, s, moe, ws, lora);
+    case 41: return launch_one_k<DT, GS, ASYM, 4, 1>(a, plan, s, moe, ws, lora);
+    case 42: return launch_one_k<DT, GS, ASYM, 4, 2>(a, plan, s, moe, ws, lora);
+    case 44: return launch_one_k<DT, GS, ASYM, 4, 4>(a, plan, s, moe, ws, lora);
+    case 88: return launch_one_k<DT, GS, ASYM, 8, 8>(a, plan, s, moe, ws, lora);
+    case 48: return launch_one_k<DT, GS, ASYM, 4, 8>(a, plan, s, moe, ws, lora);
     default: return hipErrorInvalidConfiguration;
   }
 }
 
 template <int DT>
 static hipError_t launch_one_g(const LinearArgs& a, const GemvPlan& plan, hipStream_t s, const MoeArgs* moe,
-                               void* ws) {
+                               void* ws, const LoraTerm* lora) {
   const bool asym = a.zp != nullptr;
   switch (a.group) {
-    case 32: return asym ? launch_one<DT, 32, true>(a, plan, s, moe, ws) : launch_one<DT, 32, false>(a, plan, s, moe, ws);
-    case 64: return asym ? launch_one<DT, 64, true>(a, plan, s, moe, ws) : launch_one<DT, 64, false>(a, plan, s, moe, ws);
+    case 32: return asym ? launch_one<DT, 32, true>(a, plan, s, moe, ws, lora) : launch_one<DT, 32, false>(a, plan, s, moe, ws, lora);
+    case 64: return asym ? launch_one<DT, 64, true>(a, plan, s, moe, ws, lora) : launch_one<DT, 64, false>(a, plan, s, moe, ws, lora);
     case 128:
-      return asym ? launch_one<DT, 128, true>(a, plan, s, moe, ws) : launch_one<DT, 128, false>(a, plan, s, moe, ws);
+      return asym ? launch_one<DT, 128, true>(a, plan, s, moe, ws, lora) : launch_one<DT, 128, false>(a, plan, s, moe, ws, lora);
     default: return hipErrorInvalidValue;
   }
 }
@@ -1346,11 +1356,11 @@ bool gemv_one_runs(const LinearArgs& a, const GemvPlan& plan, const MoeArgs* moe
 }
 
 hipError_t launch_gemv(const LinearArgs& a, const GemvPlan& plan, void* workspace,
-                       hipStream_t stream, const MoeArgs* moe) {
+                       hipStream_t stream, const MoeArgs* moe, const LoraTerm* lora) {
   if (gemv_one_runs(a, plan, moe)) {
     if (plan.one_splits > 1 && !workspace) return hipErrorInvalidValue;
-    return a.dtype == DT_F16 ? launch_one_g<DT_F16>(a, plan, stream, moe, workspace)
-                             : launch_one_g<DT_BF16>(a, plan, stream, moe, workspace);
+    return a.dtype == DT_F16 ? launch_one_g<DT_F16>(a, plan, stream, moe, workspace, lora)
+                             : launch_one_g<DT_BF16>(a, plan, stream, moe, workspace, lora);
   }
   if (plan.waves < 1 || plan.waves > kGemvMaxWaves || plan.lds_bytes > kGemvLdsBudget ||
       plan.kpw < 1 || plan.kpw > kGemvStepsPerWave)
@@ -1361,6 +1371,7 @@ hipError_t launch_gemv(const LinearArgs& a, const GemvPlan& plan, void* workspac
               moe->slots > kMaxGridZ))
     return hipErrorInvalidConfiguration;
   GemvParams prm;
+  if (lora) prm.lora = *lora;
   prm.yscale = 1.0f;
   prm.moe_ids = nullptr;
   prm.moe_weights = nullptr;

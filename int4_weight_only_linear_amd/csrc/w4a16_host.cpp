@@ -258,7 +258,8 @@ bool log_enabled() { return w4a16::tuning().log; }
 w4a16_status linear_impl(const void* x, const int32_t* wq, const void* scales, const int32_t* zp,
                          const void* bias, void* y, int64_t M, int64_t N, int64_t K,
                          int32_t group_size, int32_t dtype, void* workspace,
-                         size_t workspace_bytes, void* stream, int32_t path) {
+                         size_t workspace_bytes, void* stream, int32_t path,
+                         const w4a16::LoraTerm* lora = nullptr) {
   w4a16_status st = w4a16_check_args(x, wq, scales, zp, bias, y, M, N, K, group_size, dtype);
   if (st != W4A16_OK) return st;
   const GroupMap gm = group_map(group_size, K);
@@ -301,7 +302,7 @@ w4a16_status linear_impl(const void* x, const int32_t* wq, const void* scales, c
                    (long long)M, (long long)N, (long long)K, group_size,
                    dtype == W4A16_F16 ? "f16" : "bf16", zp ? "asym" : "sym", plan.tiles,
                    plan.splits, plan.waves);
-    e = w4a16::launch_gemv(a, plan, workspace, s);
+    e = w4a16::launch_gemv(a, plan, workspace, s, nullptr, lora);
   } else {
     if (log_enabled()) {
       const w4a16::GemmPlan plan = w4a16::plan_gemm(M, N, K, group_size, dtype, zp != nullptr, dev->cu_count);
@@ -311,10 +312,54 @@ w4a16_status linear_impl(const void* x, const int32_t* wq, const void* scales, c
                    dtype == W4A16_F16 ? "f16" : "bf16", zp ? "asym" : "sym", 32 * plan.mb,
                    128 * plan.cb, plan.splits, plan.units);
     }
-    e = w4a16::launch_gemm(a, workspace, dev->cu_count, s);
+    e = w4a16::launch_gemm(a, workspace, dev->cu_count, s, lora);
   }
   if (e != hipSuccess) return fail(W4A16_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
   return ok();
+}
+
+// the CU count that plans are made for: the current device's, or MI355X's
+// where none is visible
+int planning_cus() {
+  int cus = kPlanningCUs, dev = -1;
+  if (hipGetDevice(&dev) == hipSuccess && dev >= 0 && dev < kMaxDevices) {
+    const DeviceInfo* d = nullptr;
+    if (device_info(&d) == W4A16_OK) cus = d->cu_count;
+    g_last_error.clear();
+  }
+  return cus;
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// ---- low-rank adapters ------------------------------------------------------
+w4a16_status check_adapters(const char* what, const void* la, const void* lb, const int32_t* ids,
+                            const float* alpha, int64_t M, int64_t N, int64_t K, int64_t S, int64_t R) {
+  if (S < 1 || S > INT32_MAX) return fail(W4A16_ERR_INVALID_ARG, "%s: need at least one adapter, got S=%lld", what, (long long)S);
+  if (R < 8 || R % 8) return fail(W4A16_ERR_INVALID_ARG, "%s: the rank must be a positive multiple of 8, got %lld", what, (long long)R);
+  if (R > w4a16::kMaxRank)
+    return fail(W4A16_ERR_UNSUPPORTED, "%s: ranks above %d are not supported, got %lld", what, w4a16::kMaxRank, (long long)R);
+  if (S > INT64_MAX / 4 / (R * std::max(N, K)))
+    return fail(W4A16_ERR_INVALID_ARG, "%s: adapter stacks too large", what);
+  if (M == 0) return ok();
+  if (!la || !lb || !ids) return fail(W4A16_ERR_INVALID_ARG, "%s: la, lb and ids must not be NULL", what);
+  if (!aligned(la, 16) || !aligned(lb, 16)) return fail(W4A16_ERR_ALIGNMENT, "%s: la and lb must be 16-byte aligned", what);
+  if (!aligned(ids, 4) || (alpha && !aligned(alpha, 4)))
+    return fail(W4A16_ERR_ALIGNMENT, "%s: ids and alpha must be 4-byte aligned", what);
+  return ok();
+}
+
+// [out, out + bytes) against the adapters' inputs
+bool overlaps_adapters(const void* out, size_t bytes, const void* la, const void* lb, const int32_t* ids,
+                       const float* alpha, int64_t M, int64_t N, int64_t K, int64_t S, int64_t R) {
+  return overlap(out, bytes, la, act_bytes(S * R * K)) || overlap(out, bytes, lb, act_bytes(S * N * R)) ||
+         overlap(out, bytes, ids, (size_t)M * 4) || (alpha && overlap(out, bytes, alpha, (size_t)S * 4));
+}
+
+// the workspace of w4a16_lora_linear: the projection's own (its counter region
+// always kept, so that one workspace serves every entry point), then u
+size_t lora_u_offset(int64_t M, int64_t N, int64_t K, int32_t kgroup, int32_t dtype, bool asym, w4a16_path p, int cus) {
+  return round256(std::max(w4a16::kCounterBytes, workspace_for(M, N, K, kgroup, dtype, asym, p, cus)));
 }
 
 }  // namespace
@@ -721,6 +766,69 @@ w4a16_status w4a16_linear_dense(const void* x, const void* w, const void* bias, 
   const hipError_t e = w4a16::launch_gemm(a, workspace, dev->cu_count, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(W4A16_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
   return ok();
+}
+
+size_t w4a16_lora_workspace_size(int64_t M, int64_t N, int64_t K, int32_t group_size, int32_t dtype,
+                                 int32_t has_zp, int64_t R, int32_t save_u) {
+  if (M <= 0 || N <= 0 || K <= 0 || !group_ok(group_size, K) || K % group_size || R < 8 || R % 8 || R > w4a16::kMaxRank)
+    return 0;
+  const int cus = planning_cus();
+  const int kgroup = group_map(group_size, K).kgroup;
+  const w4a16_path p = resolve_path(M, N, K, kgroup, dtype, has_zp, W4A16_PATH_AUTO);
+  const w4a16::ShrinkPlan sp = w4a16::plan_shrink(M, K, (int)R, cus);
+  // the K ranges' sums, and u itself where the caller does not keep it
+  return lora_u_offset(M, N, K, kgroup, dtype, has_zp != 0, p, cus) +
+         round256((size_t)(sp.splits + (save_u ? 0 : 1)) * (size_t)M * (size_t)R * sizeof(float));
+}
+
+w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* scales, const int32_t* zp,
+                               const void* bias, const void* la, const void* lb, const int32_t* ids,
+                               const float* alpha, void* y, float* u, int64_t M, int64_t N, int64_t K,
+                               int32_t group_size, int64_t S, int64_t R, int32_t dtype, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  w4a16_status st = w4a16_check_args(x, wq, scales, zp, bias, y, M, N, K, group_size, dtype);
+  if (st != W4A16_OK) return st;
+  st = check_adapters("lora_linear", la, lb, ids, alpha, M, N, K, S, R);
+  if (st != W4A16_OK) return st;
+  if (M == 0) return ok();
+  if (u && !aligned(u, 16)) return fail(W4A16_ERR_ALIGNMENT, "lora_linear: u must be 16-byte aligned");
+  const size_t ubytes = (size_t)M * (size_t)R * sizeof(float), ybytes = act_bytes(M * N);
+  if (overlaps_adapters(y, ybytes, la, lb, ids, alpha, M, N, K, S, R) ||
+      (u && (overlaps_adapters(u, ubytes, la, lb, ids, alpha, M, N, K, S, R) || overlap(u, ubytes, y, ybytes) ||
+             overlap(u, ubytes, x, act_bytes(M * K)) || overlap(u, ubytes, wq, (size_t)N * (K / 8) * 4) ||
+             overlap(u, ubytes, scales, act_bytes(N * (K / group_size))) ||
+             (zp && overlap(u, ubytes, zp, (size_t)(N / 8) * (K / group_size) * 4)) ||
+             (bias && overlap(u, ubytes, bias, act_bytes(N))))))
+    return fail(W4A16_ERR_INVALID_ARG, "lora_linear: y and u must not overlap any input or each other");
+  const DeviceInfo* dev = nullptr;
+  st = device_info(&dev);
+  if (st != W4A16_OK) return st;
+  const size_t need = w4a16_lora_workspace_size(M, N, K, group_size, dtype, zp != nullptr, R, u != nullptr);
+  if (workspace == nullptr || workspace_bytes < need)
+    return fail(W4A16_ERR_WORKSPACE, "lora_linear: workspace of %zu bytes needed, got %zu%s", need, workspace_bytes,
+                workspace ? "" : " (NULL)");
+  if (!aligned(workspace, 256)) return fail(W4A16_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  const int kgroup = group_map(group_size, K).kgroup;
+  const w4a16_path p = resolve_path(M, N, K, kgroup, dtype, zp != nullptr, W4A16_PATH_AUTO);
+  const size_t at = lora_u_offset(M, N, K, kgroup, dtype, zp != nullptr, p, dev->cu_count);
+  const w4a16::ShrinkPlan sp = w4a16::plan_shrink(M, K, (int)R, dev->cu_count);
+  // Decode: the epilogue adds the K ranges' sums itself, which saves a launch
+  // (a few floats per output).  Above it every tile of the GEMM reads all of
+  // its tokens' u, so the ranges are added once, before it.
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(workspace) + at);
+  float* const sums = u ? u : (p == W4A16_PATH_GEMV ? nullptr : part + (size_t)sp.splits * M * R);
+  const w4a16::ShrinkArgs sa{x, la, ids, part, sums, M, K, (int)S, (int)R, dtype};
+  const hipError_t e = w4a16::launch_shrink(sa, sp, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(W4A16_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
+  w4a16::LoraTerm t;
+  t.ids = ids;
+  t.up = lb;
+  t.u = sums ? sums : part;
+  t.alpha = alpha;
+  t.S = (int)S;
+  t.R = (int)R;
+  t.usplits = sums ? 1 : sp.splits;
+  return linear_impl(x, wq, scales, zp, bias, y, M, N, K, group_size, dtype, workspace, at, stream, p, &t);
 }
 
 w4a16_status w4a16_unpack_device(const int32_t* wq, uint8_t* q, int64_t N, int64_t K, void* stream) {

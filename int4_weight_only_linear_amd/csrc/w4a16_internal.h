@@ -25,6 +25,38 @@ struct LinearArgs {
   bool dense = false;  // prefill GEMM only: wq points at act-dtype weights w[N, K]
 };
 
+// ---- low-rank adapters -----------------------------------------------------
+// The adapters' second product, added by the projection's kernels (see
+// w4a16_lora.hpp): token m's adapter ids[m] (outside [0, S): none), the stack
+// up[S][N][R], u[usplits][M][R] in fp32 from shrink_kernel, alpha[S] or NULL.
+struct LoraTerm {
+  const int32_t* ids = nullptr;  // NULL: no adapters
+  const void* up = nullptr;
+  const float* u = nullptr;
+  const float* alpha = nullptr;
+  int S = 0, R = 0, usplits = 1;
+};
+// u[m][r] = sum over k of x[m, k] * down[ids[m]][r, k]
+struct ShrinkArgs {
+  const void* x;       // [M, K]
+  const void* down;    // [S][R][K]
+  const int32_t* ids;  // [M]
+  float* part;         // [splits][M][R]: the K ranges' sums
+  float* u;            // [M][R], or NULL: the sums of the K ranges are left in part
+  int64_t M, K;
+  int S, R, dtype;
+};
+struct ShrinkPlan {
+  int tt;                // 16-token blocks of a workgroup: 1 or 4
+  int rc;                // 16-rank blocks of a workgroup
+  int splits;            // K ranges
+  int chunks_per_split;  // 32-k chunks of a range
+};
+constexpr int kMaxShrinkSplits = 16;
+constexpr int kMaxRank = 128;
+ShrinkPlan plan_shrink(int64_t M, int64_t K, int R, int cu_count);
+hipError_t launch_shrink(const ShrinkArgs& a, const ShrinkPlan& p, hipStream_t s);
+
 // ---- tuning overrides ------------------------------------------------------
 // Read from the environment once, at the first call that needs them (so a
 // launch costs no getenv), and again on w4a16_reload_tuning().  None is
@@ -140,7 +172,7 @@ struct MoeArgs {
 constexpr int64_t kMaxGridZ = 65535;
 
 hipError_t launch_gemv(const LinearArgs& a, const GemvPlan& p, void* workspace,
-                       hipStream_t stream, const MoeArgs* moe = nullptr);
+                       hipStream_t stream, const MoeArgs* moe = nullptr, const LoraTerm* lora = nullptr);
 // whether launch_gemv runs the single-token instance for these arguments
 bool gemv_one_runs(const LinearArgs& a, const GemvPlan& p, const MoeArgs* moe = nullptr);
 
@@ -168,7 +200,8 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t K, int group, int dtype, bool a
                    bool dense = false);
 size_t gemm_workspace_bytes(int64_t M, int64_t N, int64_t K, int group, int dtype, bool asym,
                             int cu_count, bool dense = false);
-hipError_t launch_gemm(const LinearArgs& a, void* workspace, int cu_count, hipStream_t stream);
+hipError_t launch_gemm(const LinearArgs& a, void* workspace, int cu_count, hipStream_t stream,
+                       const LoraTerm* lora = nullptr);
 
 // ---- elementwise -----------------------------------------------------------
 hipError_t launch_dequant(const int32_t* wq, const void* scales, const int32_t* zp, int sG, int gmul, void* w,

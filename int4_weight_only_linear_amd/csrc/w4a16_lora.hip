@@ -1,0 +1,155 @@
+// The low-rank adapters' first product: u[m, r] = sum_k x[m, k] * A_a[r, k],
+// a = ids[m], in fp32 (the second product is added by the projection's own
+// kernels, w4a16_lora.hpp).
+#include <algorithm>
+
+#include "w4a16_lora.hpp"
+
+namespace w4a16 {
+
+namespace {
+
+// waves of a workgroup, and 32-k chunks a wave loads before it multiplies
+// (about 100 registers of loads in flight)
+constexpr int shrink_waves(int tt, int rc) { return tt + rc > 4 ? 8 : 16; }
+constexpr int shrink_depth(int tt, int rc) { return tt + rc > 8 ? 1 : (tt + rc > 4 ? 2 : 4); }
+
+// A workgroup owns a tile of 16 TT tokens, 16 RC ranks, one K range and one
+// adapter: that of token `slot` of its tile, unless an earlier token of the
+// tile names the same one (then it leaves).  So the adapters of a tile are
+// read side by side, each once per tile.  Its waves take the range's chunks
+// in turn.  The tokens are the MFMA's A rows, the adapter's ranks its B
+// columns, both loaded straight from their rows (16 bytes a lane); the waves
+// are added through LDS in wave order, and the rows of the adapter's own
+// tokens stored: u[split][M][R].  A token without an adapter gets zeros, from
+// the workgroup of its own slot.
+template <int DT, int TT, int RC>
+__global__ __launch_bounds__(64 * shrink_waves(TT, RC)) void shrink_kernel(
+    const uint16_t* __restrict__ x, const uint16_t* __restrict__ down, const int32_t* __restrict__ ids,
+    float* __restrict__ u, int M, int K, int S, int R, int chunks_per_split) {
+  constexpr int WAVES = shrink_waves(TT, RC), DEPTH = shrink_depth(TT, RC), BM = 16 * TT, BR = 16 * RC;
+  __shared__ __attribute__((aligned(16))) float red[WAVES * 256 * RC];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int col = lane & 15, row4 = lane >> 4;
+  const int tile = blockIdx.x / BM, slot = blockIdx.x - tile * BM;
+  const int m0 = tile * BM, r0 = blockIdx.z * BR;
+  if (m0 + slot >= M) return;
+  const int a = ids[m0 + slot];
+  float* const out = u + (size_t)blockIdx.y * M * R;
+  if (a < 0 || a >= S) {
+    for (int r = r0 + tid; r < min(R, r0 + BR); r += blockDim.x) out[(size_t)(m0 + slot) * R + r] = 0.f;
+    return;
+  }
+  // an earlier token of the tile with the same adapter: its workgroup's work
+  if (__ballot(lane < min(slot, BM) && ids[min(m0 + lane, M - 1)] == a) != 0) return;
+
+  const int c_begin = blockIdx.y * chunks_per_split;
+  const int c_end = min(K >> 5, c_begin + chunks_per_split);
+  const uint16_t* xrow[TT];
+  const uint16_t* arow[RC];
+#pragma unroll
+  for (int t = 0; t < TT; ++t) xrow[t] = x + (size_t)min(m0 + 16 * t + col, M - 1) * K + 8 * row4;
+#pragma unroll
+  for (int rc = 0; rc < RC; ++rc) arow[rc] = down + ((size_t)a * R + min(r0 + 16 * rc + col, R - 1)) * K + 8 * row4;
+  f32x4 acc[TT][RC];
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int rc = 0; rc < RC; ++rc) acc[t][rc] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int c0 = c_begin + wave * DEPTH; c0 < c_end; c0 += WAVES * DEPTH) {
+    u32x4 xv[DEPTH][TT], av[DEPTH][RC];
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) {
+      const int c = min(c0 + i, c_end - 1);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) xv[i][t] = *reinterpret_cast<const u32x4*>(xrow[t] + 32 * c);
+#pragma unroll
+      for (int rc = 0; rc < RC; ++rc) av[i][rc] = *reinterpret_cast<const u32x4*>(arow[rc] + 32 * c);
+    }
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i)
+      if (c0 + i < c_end) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+#pragma unroll
+          for (int rc = 0; rc < RC; ++rc) acc[t][rc] = mfma16x16x32<DT>(xv[i][t], av[i][rc], acc[t][rc]);
+      }
+  }
+#pragma unroll
+  for (int t = 0; t < TT; ++t) {
+    if (t) __syncthreads();  // the previous block's sums are read
+#pragma unroll
+    for (int rc = 0; rc < RC; ++rc)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) red[wave * (16 * BR) + (4 * row4 + e) * BR + 16 * rc + col] = acc[t][rc][e];
+    __syncthreads();
+    for (int i = tid; i < 16 * BR; i += blockDim.x) {
+      const int m = m0 + 16 * t + i / BR, r = r0 + i % BR;
+      if (m < M && r < R && ids[m] == a) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) v += red[w * (16 * BR) + i];
+        out[(size_t)m * R + r] = v;
+      }
+    }
+  }
+}
+
+// u = the K ranges' sums in range order; n a multiple of 4
+__global__ __launch_bounds__(256) void shrink_reduce_kernel(const float* __restrict__ part, float* __restrict__ u,
+                                                            int64_t n, int splits) {
+  const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
+  if (i >= n) return;
+  f32x4 v = *reinterpret_cast<const f32x4*>(part + i);
+  for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(part + s * n + i);
+  *reinterpret_cast<f32x4*>(u + i) = v;
+}
+
+template <int DT, int TT, int RC>
+hipError_t launch_t(const ShrinkArgs& a, const ShrinkPlan& p, float* out, hipStream_t s) {
+  const int64_t tiles = (a.M + 16 * TT - 1) / (16 * TT);
+  const dim3 grid((unsigned)(tiles * 16 * TT), p.splits, (a.R + 16 * RC - 1) / (16 * RC));
+  hipLaunchKernelGGL((shrink_kernel<DT, TT, RC>), grid, dim3(64 * shrink_waves(TT, RC)), 0, s,
+                     static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.down), a.ids, out, (int)a.M,
+                     (int)a.K, a.S, a.R, p.chunks_per_split);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_dt(const ShrinkArgs& a, const ShrinkPlan& p, float* out, hipStream_t s) {
+  switch (10 * p.tt + p.rc) {
+    case 11: return launch_t<DT, 1, 1>(a, p, out, s);
+    case 41: return launch_t<DT, 4, 1>(a, p, out, s);
+    case 42: return launch_t<DT, 4, 2>(a, p, out, s);
+    case 44: return launch_t<DT, 4, 4>(a, p, out, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+ShrinkPlan plan_shrink(int64_t M, int64_t K, int R, int cu_count) {
+  ShrinkPlan p;
+  const int chunks = (int)(K / 32);
+  p.tt = M <= 256 ? 1 : 4;
+  const int blocks_r = (R + 15) / 16;
+  p.rc = p.tt == 1 ? 1 : (blocks_r > 2 ? 4 : blocks_r);
+  const int64_t groups = (M + 16 * p.tt - 1) / (16 * p.tt) * ((blocks_r + p.rc - 1) / p.rc);
+  int splits = (int)std::min<int64_t>((K + 2047) / 2048, std::max<int64_t>(1, 2 * cu_count / groups));
+  splits = std::min(splits, kMaxShrinkSplits);
+  p.chunks_per_split = (chunks + splits - 1) / splits;
+  p.splits = (chunks + p.chunks_per_split - 1) / p.chunks_per_split;
+  return p;
+}
+
+hipError_t launch_shrink(const ShrinkArgs& a, const ShrinkPlan& p, hipStream_t s) {
+  float* const out = p.splits > 1 && a.u ? a.part : (a.u ? a.u : a.part);
+  const hipError_t e = a.dtype == DT_F16 ? launch_dt<DT_F16>(a, p, out, s) : launch_dt<DT_BF16>(a, p, out, s);
+  if (e != hipSuccess || p.splits == 1 || !a.u) return e;
+  const int64_t n = a.M * a.R;
+  hipLaunchKernelGGL(shrink_reduce_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, s, a.part, a.u, n, p.splits);
+  return hipGetLastError();
+}
+
+}  // namespace w4a16

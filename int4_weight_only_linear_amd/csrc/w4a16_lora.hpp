@@ -1,0 +1,133 @@
+// Low-rank adapters beside the shared projection (device side, gfx950 only).
+//
+// Token m names an adapter a = ids[m]; its output row gains
+//   alpha_a * sum_r u[m, r] * up_a[n, r],   u[m, r] = sum_k x[m, k] * A_a[r, k]
+// u is formed first, in fp32, by shrink_kernel (w4a16_lora.hip); the
+// projection's kernels then add the sum to their fp32 accumulators before
+// their one rounding.  up is the stack [S][N][R], R a multiple of 8, so 16
+// bytes are eight ranks of one row.
+#pragma once
+
+#include "w4a16_device.hpp"
+#include "w4a16_internal.h"
+
+namespace w4a16 {
+
+// the adapter of token m, or -1 (no adapter, or no such token)
+__device__ __forceinline__ int lora_id(const LoraTerm& t, int M, int m) {
+  const int a = m < M ? t.ids[m] : -1;
+  return a >= 0 && a < t.S ? a : -1;
+}
+
+// eight ranks r0.. of alpha * u[m], summed over the K ranges u was formed in
+__device__ __forceinline__ void lora_u8(const LoraTerm& t, int M, int m, int r0, float alpha, float (&v)[8]) {
+  const float* src = t.u + (size_t)m * t.R + r0;
+  f32x4 a = *reinterpret_cast<const f32x4*>(src), b = *reinterpret_cast<const f32x4*>(src + 4);
+  for (int sp = 1; sp < t.usplits; ++sp) {
+    src += (size_t)M * t.R;
+    a += *reinterpret_cast<const f32x4*>(src);
+    b += *reinterpret_cast<const f32x4*>(src + 4);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = a[e] * alpha;
+    v[4 + e] = b[e] * alpha;
+  }
+}
+
+__device__ __forceinline__ float lora_alpha(const LoraTerm& t, int a) { return t.alpha ? t.alpha[a] : 1.f; }
+
+// The term of output (m, n), in fp32 throughout (the decode kernels' epilogue).
+template <int DT>
+__device__ __forceinline__ float lora_dot(const LoraTerm& t, int M, int N, int m, int n) {
+  const int a = lora_id(t, M, m);
+  if (a < 0) return 0.f;
+  const float alpha = lora_alpha(t, a);
+  const uint16_t* up = static_cast<const uint16_t*>(t.up) + ((size_t)a * N + n) * t.R;
+  float s = 0.f;
+  for (int r = 0; r < t.R; r += 8) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(up + r);
+    float u[8];
+    lora_u8(t, M, m, r, alpha, u);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      s = __builtin_fmaf(u[e], act_to_f32<DT>((uint16_t)(w[e >> 1] >> (16 * (e & 1)))), s);
+  }
+  return s;
+}
+
+// Eight fp32 values as two MFMA operands whose sum is the value to about 16
+// (bf16) or 22 (fp16) significant bits: v rounded, and what that left.  One
+// operand alone would add a rounding of u as large as the output's own.
+template <int DT>
+__device__ __forceinline__ void split_hi_lo(const float (&v)[8], u32x4& hi, u32x4& lo) {
+  uint32_t h[4], l[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    h[i] = f32x2_to_act_pair<DT>(v[2 * i], v[2 * i + 1]);
+    l[i] = f32x2_to_act_pair<DT>(v[2 * i] - act_to_f32<DT>((uint16_t)h[i]),
+                                 v[2 * i + 1] - act_to_f32<DT>((uint16_t)(h[i] >> 16)));
+  }
+  hi = u32x4{h[0], h[1], h[2], h[3]};
+  lo = u32x4{l[0], l[1], l[2], l[3]};
+}
+
+// the smallest value over the wave's 64 lanes
+__device__ __forceinline__ int wave_min(int v) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v = min(v, __shfl_xor(v, d));
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
+// The GEMM tile's adapter term, as more k of its product: for every adapter
+// that a token of the tile names (in ascending order), ceil(R / 16) k-subs
+// whose A operand is the wave's rows of up_a and whose B operand is alpha * u
+// of the adapter's own tokens, zero for the others.
+//   acc[rb][cb]: tokens m0 + 32 rb + (lane & 31), features nw0 + 32 cb + ...
+template <int DT, int MB, int CB>
+__device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int m0, int nw0, int lane,
+                                           f32x16 (&acc)[MB][CB]) {
+  const int j = lane & 31, h = lane >> 5;
+  int id[MB];
+#pragma unroll
+  for (int rb = 0; rb < MB; ++rb) {
+    const int a = lora_id(t, M, m0 + 32 * rb + j);
+    id[rb] = a < 0 ? t.S : a;
+  }
+  for (int prev = -1;;) {
+    int next = t.S;
+#pragma unroll
+    for (int rb = 0; rb < MB; ++rb)
+      if (id[rb] > prev) next = min(next, id[rb]);
+    next = wave_min(next);
+    if (next >= t.S) return;
+    const float alpha = lora_alpha(t, next);
+    for (int r0 = 8 * h; r0 - 8 * h < t.R; r0 += 16) {
+      const bool in = r0 < t.R;  // R a multiple of 8: the upper half of a last k-sub may lie past it
+      u32x4 a[CB];
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) {
+        const int n = min(nw0 + 32 * cb + j, N - 1);
+        a[cb] = in ? *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(t.up) + ((size_t)next * N + n) * t.R + r0)
+                   : u32x4{0u, 0u, 0u, 0u};
+      }
+#pragma unroll
+      for (int rb = 0; rb < MB; ++rb) {
+        u32x4 hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
+        if (in && id[rb] == next) {
+          float v[8];
+          lora_u8(t, M, m0 + 32 * rb + j, r0, alpha, v);
+          split_hi_lo<DT>(v, hi, lo);
+        }
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+          acc[rb][cb] = mfma32x32x16<DT>(a[cb], hi, acc[rb][cb]);
+          acc[rb][cb] = mfma32x32x16<DT>(a[cb], lo, acc[rb][cb]);
+        }
+      }
+    }
+    prev = next;
+  }
+}
+
+}  // namespace w4a16
