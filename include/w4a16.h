@@ -81,7 +81,8 @@ typedef enum w4a16_status {
   W4A16_ERR_WORKSPACE = 6     /* workspace missing or smaller than w4a16_workspace_size */
 } w4a16_status;
 
-typedef enum w4a16_dtype { W4A16_F16 = 0, W4A16_BF16 = 1 } w4a16_dtype;
+/* W4A16_F32: the optimiser's tensors only, never activations */
+typedef enum w4a16_dtype { W4A16_F16 = 0, W4A16_BF16 = 1, W4A16_F32 = 2 } w4a16_dtype;
 
 typedef enum w4a16_path {
   W4A16_PATH_AUTO = 0,  /* pick by M, N, K, group and dtype */
@@ -347,6 +348,71 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
                                const float* alpha, void* y, float* u, int64_t M, int64_t N, int64_t K,
                                int32_t group_size, int64_t S, int64_t R, int32_t dtype, void* workspace,
                                size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------- AdamW ---
+ * One AdamW step over a list of tensors (the adapters of a model) in one
+ * launch, in fp32 whatever the tensors' types:
+ *   g = grad * grad_scale
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * p is rounded once, to nearest-even, to its type; copy, where given, is p
+ * rounded once to fp16 or bf16 (the operand of w4a16_lora_linear beside an
+ * fp32 master).
+ * Moments in 32 bits: m, v fp32 [n].  In 8 bits: m int8 [n], v uint8 [n], and
+ * one fp32 scale each per 256 consecutive elements ([ceil(n / 256)], from the
+ * tensor's first element on):
+ *   m = sign(c) (c / 127)^2 m_scale        m_scale = the block's max |m|
+ *   v = ((c / 255)^2 v_scale)^2            v_scale = the block's max sqrt(v)
+ * Codes are rounded up or down with the probability of the nearer share
+ * (floor of the exact code plus a dither in [0, 1)); the dither is a hash of
+ * seed and of the element's place (block number in the table * 256 + place in
+ * the block, modulo 2^32), so a step is a function of its arguments.  Give
+ * every step another seed.  All-zero moments are all-zero codes and scales.  A
+ * gradient that is not finite makes its element, and in 8 bits the moments of
+ * its block, NaN or infinite: check gradients before the step.
+ *
+ * w4a16_adamw_table (host) checks the tensors and lays out the table that the
+ * steps read, w4a16_adamw_table_size bytes in host memory; the caller copies
+ * it to device memory (8-byte aligned) and keeps it, and the tensors where
+ * they are, for as long as it calls w4a16_adamw_step.  All tensors of a table
+ * share their types (param, grad: W4A16_F16, W4A16_BF16 or W4A16_F32; copy:
+ * W4A16_F16 or W4A16_BF16).  n may be 0.  Pointers are aligned to their
+ * elements; four-element alignment of all of a tensor's pointers is faster.
+ * A tensor's buffers must not overlap one another.
+ * Errors: W4A16_ERR_INVALID_ARG, W4A16_ERR_ALIGNMENT, W4A16_ERR_WORKSPACE (a
+ * table too small); nothing is written then. */
+typedef struct w4a16_adamw_tensor {
+  void* param;
+  const void* grad;
+  void* m;
+  void* v;
+  float* m_scale;  /* 8 bits only */
+  float* v_scale;
+  void* copy;      /* or NULL */
+  int64_t n;       /* elements */
+} w4a16_adamw_tensor;
+
+typedef struct w4a16_adamw_plan {  /* filled by w4a16_adamw_table */
+  int64_t tensors, chunks, blocks; /* blocks: of 256 elements, over all tensors */
+  int32_t state_bits, param_dtype, grad_dtype, reserved;
+} w4a16_adamw_plan;
+
+size_t w4a16_adamw_table_size(const w4a16_adamw_tensor* tensors, int64_t count);
+w4a16_status w4a16_adamw_table(const w4a16_adamw_tensor* tensors, int64_t count, int32_t state_bits,
+                               int32_t param_dtype, int32_t grad_dtype, int32_t copy_dtype, void* table,
+                               size_t table_bytes, w4a16_adamw_plan* plan);
+
+/* The step (device): asynchronous on `stream`; the numbers are taken when it
+ * is called.  Needs betas in [0, 1), eps >= 0, step >= 1 and finite rates. */
+w4a16_status w4a16_adamw_step(const void* table, const w4a16_adamw_plan* plan, double lr, double beta1, double beta2,
+                              double eps, double weight_decay, int64_t step, double grad_scale, uint32_t seed,
+                              void* stream);
+
+/* The moments that 8-bit codes stand for, in fp32 (a checkpoint, a look at the
+ * state): m, v fp32 [plan->blocks * 256], 16-byte aligned, the tensors' blocks
+ * in the table's order, zeros past a tensor's last element. */
+w4a16_status w4a16_adamw_moments(const void* table, const w4a16_adamw_plan* plan, float* m, float* v, void* stream);
 
 /* The 4-bit codes q[N, K] (uint8, 0..15) unpacked on the device from wq. */
 w4a16_status w4a16_unpack_device(const int32_t* wq, uint8_t* q, int64_t N, int64_t K,

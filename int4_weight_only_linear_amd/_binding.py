@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libw4a16.so")
 W4A16_OK = 0
 W4A16_F16 = 0
 W4A16_BF16 = 1
+W4A16_F32 = 2
 PATH_AUTO, PATH_GEMV, PATH_GEMM = 0, 1, 2
 GEMV_MAX_M = 16
 ABI_VERSION = 4
@@ -78,6 +79,27 @@ class PlanInfo(ctypes.Structure):
 
 SIGNATURES["w4a16_plan"] = (_c_int, [_c_i64, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_i32,
                                      ctypes.POINTER(PlanInfo)])
+
+
+class AdamwTensor(ctypes.Structure):
+    """w4a16_adamw_tensor (include/w4a16.h)."""
+    _fields_ = [("param", _vp), ("grad", _vp), ("m", _vp), ("v", _vp), ("m_scale", _vp), ("v_scale", _vp),
+                ("copy", _vp), ("n", _c_i64)]
+
+
+class AdamwPlanInfo(ctypes.Structure):
+    """w4a16_adamw_plan (include/w4a16.h)."""
+    _fields_ = [("tensors", _c_i64), ("chunks", _c_i64), ("blocks", _c_i64), ("state_bits", _c_i32),
+                ("param_dtype", _c_i32), ("grad_dtype", _c_i32), ("reserved", _c_i32)]
+
+
+_c_dbl = ctypes.c_double
+SIGNATURES["w4a16_adamw_table_size"] = (_c_sz, [ctypes.POINTER(AdamwTensor), _c_i64])
+SIGNATURES["w4a16_adamw_table"] = (_c_int, [ctypes.POINTER(AdamwTensor), _c_i64, _c_i32, _c_i32, _c_i32, _c_i32, _vp,
+                                            _c_sz, ctypes.POINTER(AdamwPlanInfo)])
+SIGNATURES["w4a16_adamw_step"] = (_c_int, [_vp, ctypes.POINTER(AdamwPlanInfo), _c_dbl, _c_dbl, _c_dbl, _c_dbl, _c_dbl,
+                                           _c_i64, _c_dbl, ctypes.c_uint32, _vp])
+SIGNATURES["w4a16_adamw_moments"] = (_c_int, [_vp, ctypes.POINTER(AdamwPlanInfo), _vp, _vp, _vp])
 
 
 class W4A16Error(RuntimeError):
@@ -485,3 +507,108 @@ def w4a16_lora_linear(x, wq, scales, la, lb, ids, zp=None, bias=None, alpha=None
                                      la.data_ptr(), lb.data_ptr(), ids.data_ptr(), _ptr(alpha), out.data_ptr(),
                                      _ptr(u), M, N, K, group_size, S, R, dt, ws_ptr, ws_bytes, stream))
     return (out, u) if save_u else out
+
+
+# ---------------------------------------------------------------- AdamW ---
+
+class AdamwPlan:
+    """The table of a list of tensors on their device, with the tensors it names."""
+
+    def __init__(self, info, table, tensors, device):
+        self.info, self.table, self.tensors, self.device = info, table, tensors, device
+
+    @property
+    def state_bits(self) -> int:
+        return self.info.state_bits
+
+    @property
+    def blocks(self) -> int:
+        """256-element blocks over all tensors."""
+        return self.info.blocks
+
+
+def _float_code(t, name) -> int:
+    torch = _torch()
+    if t.dtype == torch.float32:
+        return W4A16_F32
+    if t.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"{name} must be float16, bfloat16 or float32, got {t.dtype}")
+    return _act_code(t)
+
+
+def w4a16_adamw_plan(params, grads, exp_avgs, exp_avg_sqs, *, m_scales=None, v_scales=None, copies=None) -> AdamwPlan:
+    """Lays out the table for w4a16_adamw_step over lists of tensors of equal length.
+
+    exp_avgs / exp_avg_sqs are float32 (moments in 32 bits), or int8 / uint8 with
+    m_scales / v_scales float32 [ceil(n / 256)] (moments in 8 bits; zeros to begin
+    with).  copies: float16 or bfloat16 copies of the parameters, written by every
+    step.  The plan keeps the tensors; they must stay where they are."""
+    torch = _torch()
+    params, grads, ms, vs = list(params), list(grads), list(exp_avgs), list(exp_avg_sqs)
+    count = len(params)
+    if count == 0:
+        raise ValueError("need at least one tensor")
+    eight = m_scales is not None or v_scales is not None
+    if eight and (m_scales is None or v_scales is None):
+        raise ValueError("moments in 8 bits need both m_scales and v_scales")
+    msc, vsc = (list(m_scales), list(v_scales)) if eight else ([None] * count, [None] * count)
+    cps = [None] * count if copies is None else list(copies)
+    for name, got in (("grads", grads), ("exp_avgs", ms), ("exp_avg_sqs", vs), ("m_scales", msc), ("v_scales", vsc),
+                      ("copies", cps)):
+        if len(got) != count:
+            raise ValueError(f"{len(got)} {name} for {count} params")
+    device = params[0].device
+    want_m, want_v = (torch.int8, torch.uint8) if eight else (torch.float32, torch.float32)
+    rows = (AdamwTensor * count)()
+    for i, (p, g, m, v, a, b, c) in enumerate(zip(params, grads, ms, vs, msc, vsc, cps)):
+        n = p.numel()
+        if p.dtype != params[0].dtype or g.dtype != grads[0].dtype or (c is not None and c.dtype != cps[0].dtype):
+            raise TypeError(f"tensor {i}: all tensors of a plan share their types")
+        if m.dtype != want_m or v.dtype != want_v:
+            raise TypeError(f"tensor {i}: moments must be {want_m} and {want_v}, got {m.dtype} and {v.dtype}")
+        if g.numel() != n or m.numel() != n or v.numel() != n or (c is not None and c.numel() != n):
+            raise ValueError(f"tensor {i}: sizes differ")
+        if eight and (a.dtype != torch.float32 or b.dtype != torch.float32 or a.numel() != (n + 255) // 256
+                      or b.numel() != (n + 255) // 256):
+            raise ValueError(f"tensor {i}: scales must be float32 [{(n + 255) // 256}]")
+        for t, name in ((p, "param"), (g, "grad"), (m, "exp_avg"), (v, "exp_avg_sq"), (a, "m_scale"), (b, "v_scale"),
+                        (c, "copy")):
+            _require_device(t, f"tensor {i}: {name}", device)
+        rows[i] = AdamwTensor(p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), _ptr(a), _ptr(b), _ptr(c), n)
+    copy_dtype = W4A16_BF16 if copies is None else _act_code(cps[0])
+    size = int(lib.w4a16_adamw_table_size(rows, count))
+    host = np.zeros((size + 7) // 8, dtype=np.int64)
+    info = AdamwPlanInfo()
+    _check(lib.w4a16_adamw_table(rows, count, 8 if eight else 32, _float_code(params[0], "params"),
+                                 _float_code(grads[0], "grads"), copy_dtype, host.ctypes.data, size, ctypes.byref(info)))
+    table = torch.from_numpy(host).to(device)
+    return AdamwPlan(info, table, (params, grads, ms, vs, msc, vsc, cps), device)
+
+
+def w4a16_adamw_step(plan: AdamwPlan, *, lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
+                     step: int, grad_scale: float = 1.0, seed: int = 0) -> None:
+    """One AdamW step (number `step`, from 1) over the plan's tensors, on the current stream.
+    Moments in 8 bits are rounded with a dither that seed chooses: give every step another."""
+    torch = _torch()
+    stream = torch.cuda.current_stream(plan.device).cuda_stream
+    with torch.cuda.device(plan.device):
+        _check(lib.w4a16_adamw_step(plan.table.data_ptr(), ctypes.byref(plan.info), lr, betas[0], betas[1], eps,
+                                    weight_decay, step, grad_scale, seed & 0xFFFFFFFF, stream))
+
+
+def w4a16_adamw_moments(plan: AdamwPlan, m=None, v=None):
+    """The moments that a plan's 8-bit codes stand for: two float32 tensors [blocks * 256], the
+    tensors' blocks one after another, zeros past each tensor's last element."""
+    torch = _torch()
+    if m is None:
+        m = torch.empty(plan.blocks * 256, dtype=torch.float32, device=plan.device)
+    if v is None:
+        v = torch.empty(plan.blocks * 256, dtype=torch.float32, device=plan.device)
+    for t, name in ((m, "m"), (v, "v")):
+        if t.dtype != torch.float32 or tuple(t.shape) != (plan.blocks * 256,):
+            raise ValueError(f"{name} must be float32 [{plan.blocks * 256}]")
+        _require_device(t, name, plan.device)
+    stream = torch.cuda.current_stream(plan.device).cuda_stream
+    with torch.cuda.device(plan.device):
+        _check(lib.w4a16_adamw_moments(plan.table.data_ptr(), ctypes.byref(plan.info), m.data_ptr(), v.data_ptr(), stream))
+    return m, v

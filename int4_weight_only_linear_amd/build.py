@@ -33,12 +33,14 @@ COMMON = [
     f"-I{INCLUDE}", f"-I{CSRC}",
 ]
 SOURCES = ["w4a16_host.cpp", "w4a16_gemv.hip", "w4a16_gemm.hip", "w4a16_gemm_lora.hip", "w4a16_lora.hip",
-           "w4a16_elementwise.hip"]
+           "w4a16_adamw.hip", "w4a16_elementwise.hip"]
 # measurement kernels for the benchmark's ceilings, a library of their own
 CEILING_SOURCES = ["w4a16_ceilings.hip"]
 CEILINGS_LIB = os.path.join(PKG, "libw4a16_ceilings.so")
 # the decode kernel takes its first ten arguments preloaded into SGPRs
-EXTRA = {"w4a16_gemv.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=10"]}
+EXTRA = {"w4a16_gemv.hip": ["-mllvm", "-amdgpu-kernarg-preload-count=10"],
+         # every fp32 operation of the step rounds once
+         "w4a16_adamw.hip": ["-ffp-contract=off"]}
 
 
 def _hipcc() -> str:

@@ -12,6 +12,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -20,6 +21,7 @@
 #include <mutex>
 #include <string>
 
+#include "w4a16_adamw.h"
 #include "w4a16_internal.h"
 
 namespace w4a16 {
@@ -829,6 +831,136 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
   t.R = (int)R;
   t.usplits = sums ? 1 : sp.splits;
   return linear_impl(x, wq, scales, zp, bias, y, M, N, K, group_size, dtype, workspace, at, stream, p, &t);
+}
+
+static int elem_bytes(int32_t dtype) { return dtype == W4A16_F32 ? 4 : 2; }
+
+// chunks of a list of tensors, or -1 where a size is out of range
+static int64_t adamw_chunks(const w4a16_adamw_tensor* t, int64_t count) {
+  int64_t chunks = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    if (t[i].n < 0 || t[i].n > (int64_t(1) << 38)) return -1;
+    const int64_t blocks = (t[i].n + 255) / 256;
+    chunks += (blocks + w4a16::kAdamwChunkBlocks - 1) / w4a16::kAdamwChunkBlocks;
+  }
+  return chunks > INT32_MAX ? -1 : chunks;
+}
+
+size_t w4a16_adamw_table_size(const w4a16_adamw_tensor* tensors, int64_t count) {
+  if (!tensors || count < 1 || count > INT32_MAX) return 0;
+  const int64_t chunks = adamw_chunks(tensors, count);
+  return chunks < 0 ? 0 : (size_t)count * sizeof(w4a16::AdamwTensor) + (size_t)chunks * sizeof(w4a16::AdamwChunk);
+}
+
+w4a16_status w4a16_adamw_table(const w4a16_adamw_tensor* tensors, int64_t count, int32_t state_bits,
+                               int32_t param_dtype, int32_t grad_dtype, int32_t copy_dtype, void* table,
+                               size_t table_bytes, w4a16_adamw_plan* plan) {
+  if (!tensors || !table || !plan || count < 1 || count > INT32_MAX)
+    return fail(W4A16_ERR_INVALID_ARG, "adamw_table: need at least one tensor, a table and a plan");
+  if (state_bits != 8 && state_bits != 32)
+    return fail(W4A16_ERR_INVALID_ARG, "adamw_table: moments are held in 8 or 32 bits, got %d", (int)state_bits);
+  if (param_dtype < W4A16_F16 || param_dtype > W4A16_F32 || grad_dtype < W4A16_F16 || grad_dtype > W4A16_F32)
+    return fail(W4A16_ERR_INVALID_ARG, "adamw_table: parameters and gradients must be fp16, bf16 or fp32");
+  const int64_t chunks = adamw_chunks(tensors, count);
+  if (chunks < 0) return fail(W4A16_ERR_INVALID_ARG, "adamw_table: a tensor's size is out of range");
+  const size_t need = w4a16_adamw_table_size(tensors, count);
+  if (table_bytes < need)
+    return fail(W4A16_ERR_WORKSPACE, "adamw_table: %zu bytes needed, got %zu", need, table_bytes);
+  if (!aligned(table, 8)) return fail(W4A16_ERR_ALIGNMENT, "adamw_table: the table must be 8-byte aligned");
+  const int pb = elem_bytes(param_dtype), gb = elem_bytes(grad_dtype), sb = state_bits == 8 ? 1 : 4;
+  // first every tensor is checked, then the table is written
+  for (int64_t i = 0; i < count; ++i) {
+    const w4a16_adamw_tensor& t = tensors[i];
+    if (t.n == 0) continue;
+    if (!t.param || !t.grad || !t.m || !t.v || (state_bits == 8 && (!t.m_scale || !t.v_scale)))
+      return fail(W4A16_ERR_INVALID_ARG, "adamw_table: tensor %lld has a NULL pointer", (long long)i);
+    if (t.copy && copy_dtype != W4A16_F16 && copy_dtype != W4A16_BF16)
+      return fail(W4A16_ERR_INVALID_ARG, "adamw_table: copies must be fp16 or bf16");
+    if (!aligned(t.param, pb) || !aligned(t.grad, gb) || !aligned(t.m, sb) || !aligned(t.v, sb) ||
+        (t.copy && !aligned(t.copy, 2)) || (state_bits == 8 && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))))
+      return fail(W4A16_ERR_ALIGNMENT, "adamw_table: a pointer of tensor %lld is not aligned to its elements", (long long)i);
+    const struct { const void* p; size_t n; } own[7] = {
+        {t.param, (size_t)t.n * pb}, {t.m, (size_t)t.n * sb}, {t.v, (size_t)t.n * sb},
+        {state_bits == 8 ? t.m_scale : nullptr, (size_t)((t.n + 255) / 256) * 4},
+        {state_bits == 8 ? t.v_scale : nullptr, (size_t)((t.n + 255) / 256) * 4},
+        {t.copy, (size_t)t.n * 2}, {t.grad, (size_t)t.n * gb}};
+    for (int a = 0; a < 7; ++a)
+      for (int b = 0; b < a; ++b)
+        if (overlap(own[a].p, own[a].n, own[b].p, own[b].n))
+          return fail(W4A16_ERR_INVALID_ARG, "adamw_table: buffers of tensor %lld overlap", (long long)i);
+  }
+  w4a16::AdamwTensor* out = static_cast<w4a16::AdamwTensor*>(table);
+  w4a16::AdamwChunk* ch = reinterpret_cast<w4a16::AdamwChunk*>(out + count);
+  int64_t first = 0;
+  for (int64_t i = 0; i < count; ++i) {
+    const w4a16_adamw_tensor& t = tensors[i];
+    const bool vec = aligned(t.param, 4 * pb) && aligned(t.grad, 4 * gb) && aligned(t.m, 4 * sb) &&
+                     aligned(t.v, 4 * sb) && (!t.copy || aligned(t.copy, 8));
+    out[i] = w4a16::AdamwTensor{t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.copy, t.n, first, copy_dtype, vec};
+    const int64_t blocks = (t.n + 255) / 256;
+    for (int64_t b = 0; b < blocks; b += w4a16::kAdamwChunkBlocks) *ch++ = {(int32_t)i, (int32_t)b};
+    first += blocks;
+  }
+  *plan = w4a16_adamw_plan{count, chunks, first, state_bits, param_dtype, grad_dtype, 0};
+  return ok();
+}
+
+static w4a16_status check_adamw_plan(const char* what, const void* table, const w4a16_adamw_plan* plan) {
+  if (!plan || plan->tensors < 1 || plan->tensors > INT32_MAX || plan->chunks < 0 || plan->chunks > INT32_MAX ||
+      (plan->state_bits != 8 && plan->state_bits != 32) || plan->param_dtype < W4A16_F16 || plan->param_dtype > W4A16_F32 ||
+      plan->grad_dtype < W4A16_F16 || plan->grad_dtype > W4A16_F32)
+    return fail(W4A16_ERR_INVALID_ARG, "%s: not a plan of w4a16_adamw_table", what);
+  if (!table) return fail(W4A16_ERR_INVALID_ARG, "%s: the table must not be NULL", what);
+  if (!aligned(table, 8)) return fail(W4A16_ERR_ALIGNMENT, "%s: the table must be 8-byte aligned", what);
+  return ok();
+}
+
+w4a16_status w4a16_adamw_step(const void* table, const w4a16_adamw_plan* plan, double lr, double beta1, double beta2,
+                              double eps, double weight_decay, int64_t step, double grad_scale, uint32_t seed,
+                              void* stream) {
+  w4a16_status st = check_adamw_plan("adamw_step", table, plan);
+  if (st != W4A16_OK) return st;
+  if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps >= 0) || step < 1 || !std::isfinite(lr) ||
+      !std::isfinite(weight_decay) || !std::isfinite(eps))
+    return fail(W4A16_ERR_INVALID_ARG, "adamw_step: need betas in [0, 1), eps >= 0, finite rates and step >= 1");
+  if (plan->chunks == 0) return ok();
+  const DeviceInfo* dev = nullptr;
+  st = device_info(&dev);
+  if (st != W4A16_OK) return st;
+  w4a16::AdamwScalars h;
+  h.beta1 = (float)beta1;
+  h.one_beta1 = (float)(1.0 - beta1);
+  h.beta2 = (float)beta2;
+  h.one_beta2 = (float)(1.0 - beta2);
+  h.eps = (float)eps;
+  h.decay = (float)(1.0 - lr * weight_decay);
+  h.rate = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
+  h.root = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
+  h.grad_scale = (float)grad_scale;
+  h.seed = seed * 0x9E3779B9u;
+  const hipError_t e = w4a16::launch_adamw(table, (int)plan->tensors, (int)plan->chunks, plan->param_dtype,
+                                           plan->grad_dtype, plan->state_bits, h, static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(W4A16_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
+  return ok();
+}
+
+w4a16_status w4a16_adamw_moments(const void* table, const w4a16_adamw_plan* plan, float* m, float* v, void* stream) {
+  w4a16_status st = check_adamw_plan("adamw_moments", table, plan);
+  if (st != W4A16_OK) return st;
+  if (plan->state_bits != 8)
+    return fail(W4A16_ERR_UNSUPPORTED, "adamw_moments: moments in 32 bits are read where they lie");
+  if (plan->chunks == 0) return ok();
+  if (!m || !v) return fail(W4A16_ERR_INVALID_ARG, "adamw_moments: m and v must not be NULL");
+  if (!aligned(m, 16) || !aligned(v, 16)) return fail(W4A16_ERR_ALIGNMENT, "adamw_moments: m and v must be 16-byte aligned");
+  if (overlap(m, (size_t)plan->blocks * 1024, v, (size_t)plan->blocks * 1024))
+    return fail(W4A16_ERR_INVALID_ARG, "adamw_moments: m and v must not overlap");
+  const DeviceInfo* dev = nullptr;
+  st = device_info(&dev);
+  if (st != W4A16_OK) return st;
+  const hipError_t e = w4a16::launch_adamw_moments(table, (int)plan->tensors, (int)plan->chunks, m, v,
+                                                   static_cast<hipStream_t>(stream));
+  if (e != hipSuccess) return fail(W4A16_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
+  return ok();
 }
 
 w4a16_status w4a16_unpack_device(const int32_t* wq, uint8_t* q, int64_t N, int64_t K, void* stream) {

@@ -41,3 +41,31 @@ def lora_backward_ref(dy_bits, x_bits, u, wq, scale_bits, zpk, la_bits, lb_bits,
             dla[a] += np.outer(g, x[m])
             dlb[a] += np.outer(dy[m], k * np.asarray(u[m], dtype=np.float64))
     return dx, dla, dlb
+
+
+def adamw_ref(p, g, m, v, *, lr, beta1, beta2, eps, weight_decay, step, grad_scale):
+    """(p, m, v) after one step on float64 arrays."""
+    g = g * grad_scale
+    m = beta1 * m + (1 - beta1) * g
+    v = beta2 * v + (1 - beta2) * g * g
+    mh, vh = m / (1 - beta1 ** step), v / (1 - beta2 ** step)
+    return p - lr * weight_decay * p - lr * mh / (np.sqrt(vh) + eps), m, v
+
+
+def adamw_dither(count, seed: int):
+    """The (m, v) dithers of the elements at places `count` (block * 256 + place in the block)."""
+    x = (np.asarray(count, dtype=np.uint64) + np.uint64(seed * 0x9E3779B9 % (1 << 32))) % np.uint64(1 << 32)
+    x ^= x >> np.uint64(16)
+    x = x * np.uint64(0x7FEB352D) % np.uint64(1 << 32)
+    x ^= x >> np.uint64(15)
+    x = x * np.uint64(0x846CA68B) % np.uint64(1 << 32)
+    x ^= x >> np.uint64(16)
+    return (x & np.uint64(0xFFFF)).astype(np.float64) / 65536, (x >> np.uint64(16)).astype(np.float64) / 65536
+
+
+def adamw_decode(cm, cv, ms, rs):
+    """The float64 moments that codes [n] and block scales stand for."""
+    n = len(cm)
+    ms, rs = (np.repeat(np.asarray(t, dtype=np.float64), 256)[:n] for t in (ms, rs))
+    c = np.asarray(cm, dtype=np.float64) / 127
+    return np.sign(c) * c * c * ms, ((np.asarray(cv, dtype=np.float64) / 255) ** 2 * rs) ** 2
