@@ -349,6 +349,33 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
                                int32_t group_size, int64_t S, int64_t R, int32_t dtype, void* workspace,
                                size_t workspace_bytes, void* stream);
 
+/* The gradients of w4a16_lora_linear for dy = d loss / d y [M, N] (the packed
+ * weights are frozen and have none):
+ *   g[m, :]  = alpha_a * (dy[m, :] . B_a)            a = ids[m]
+ *   dx[m, :] = dy[m, :] . dequant(Wq) + g[m, :] . A_a
+ *   dla_s    = sum over the tokens m of adapter s of g[m, :]^T x[m, :]
+ *   dlb_s    = alpha_s * sum over the tokens m of s of dy[m, :]^T u[m, :]
+ * dx [M, K], dla [S, R, K] and dlb [S, N, R] in the activation dtype,
+ * accumulated in fp32 and rounded once; W enters as its values rounded to the
+ * activation dtype, as in the prefill GEMM (with bf16, |s| < 2^119).  Every
+ * element of dla and dlb is written; an adapter that no token names gets
+ * zeros, and tokens without an adapter add to dx only.  u is w4a16_lora_linear's
+ * (its rows of tokens without an adapter are not read).  dx may be NULL (not
+ * wanted).  The sums over tokens run in a fixed order: equal inputs give equal
+ * bits.  With fp16, alpha * u and g have to stay below 65504.
+ * x, wq, la, lb, dy, u, dx, dla, dlb 16-byte aligned, the others as for
+ * w4a16_lora_linear; outputs must not overlap any input or each other; S at
+ * most 65535, N*K/2 below 4 GiB.
+ * Workspace: w4a16_lora_backward_workspace_size bytes, always needed, under
+ * the rules above.  It holds the transposed factors (S*R*(K+N) values) and the
+ * partial sums. */
+size_t w4a16_lora_backward_workspace_size(int64_t M, int64_t N, int64_t K, int64_t S, int64_t R);
+w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, const int32_t* wq, const void* scales,
+                                 const int32_t* zp, const void* la, const void* lb, const int32_t* ids,
+                                 const float* alpha, void* dx, void* dla, void* dlb, int64_t M, int64_t N, int64_t K,
+                                 int32_t group_size, int64_t S, int64_t R, int32_t dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+
 /* ------------------------------------------------------------- AdamW ---
  * One AdamW step over a list of tensors (the adapters of a model) in one
  * launch, in fp32 whatever the tensors' types:

@@ -10,7 +10,7 @@ from ._binding import (  # noqa: F401
     w4a16_linear_path, w4a16_pack_weights, w4a16_pack_zeros, w4a16_select_path,
     w4a16_unpack_device, w4a16_unpack_weights, w4a16_unpack_zeros, w4a16_workspace_size,
     w4a16_linear_dense, w4a16_dense_workspace_size, w4a16_moe_linear, w4a16_reload_tuning, w4a16_plan,
-    w4a16_lora_linear, w4a16_lora_workspace_size,
+    w4a16_lora_backward, w4a16_lora_backward_workspace_size, w4a16_lora_linear, w4a16_lora_workspace_size,
     AdamwPlan, W4A16_F32, w4a16_adamw_moments, w4a16_adamw_plan, w4a16_adamw_step,
     w4a16_linear_noalloc, NOALLOC_SCRATCH_BYTES,
 )

@@ -58,6 +58,8 @@ SIGNATURES = {
     "w4a16_lora_workspace_size": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_i64, _c_i32]),
     "w4a16_lora_linear": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_i64,
                                    _c_i64, _c_i32, _c_i64, _c_i64, _c_i32, _vp, _c_sz, _vp]),
+    "w4a16_lora_backward_workspace_size": (_c_sz, [_c_i64] * 5),
+    "w4a16_lora_backward": (_c_int, [_vp] * 13 + [_c_i64, _c_i64, _c_i64, _c_i32, _c_i64, _c_i64, _c_i32, _vp, _c_sz, _vp]),
     "w4a16_moe_linear": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_i64, _c_i64,
                                   _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _vp]),
 }
@@ -507,6 +509,48 @@ def w4a16_lora_linear(x, wq, scales, la, lb, ids, zp=None, bias=None, alpha=None
                                      la.data_ptr(), lb.data_ptr(), ids.data_ptr(), _ptr(alpha), out.data_ptr(),
                                      _ptr(u), M, N, K, group_size, S, R, dt, ws_ptr, ws_bytes, stream))
     return (out, u) if save_u else out
+
+
+def w4a16_lora_backward_workspace_size(M, N, K, S, R) -> int:
+    return int(lib.w4a16_lora_backward_workspace_size(M, N, K, S, R))
+
+
+def w4a16_lora_backward(dy, x, u, wq, scales, la, lb, ids, zp=None, alpha=None, *, group_size: int,
+                        need_dx: bool = True, out=None, workspace=None):
+    """Gradients of w4a16_lora_linear: (dx, dla, dlb) for dy [M, N], with x and the u that the
+    forward call kept (save_u).  dx is None where need_dx is false.  out: (dx or None, dla, dlb)
+    to write into."""
+    torch = _torch()
+    if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0] or dy.shape[1] != wq.shape[0]:
+        raise ValueError(f"dy is {tuple(dy.shape)}, expected {(x.shape[0], wq.shape[0])}")
+    if dy.dtype != x.dtype:
+        raise TypeError(f"dy must be {x.dtype}, got {dy.dtype}")
+    # the projection's own checks (dy stands where its output would)
+    dt, M, N, K, _ = _linear_args(x, wq, scales, zp, None, group_size, dy)
+    S, R = _adapter_args(x, la, lb, ids, alpha, M, N, K)
+    if u.dtype != torch.float32 or tuple(u.shape) != (M, R):
+        raise TypeError(f"u must be float32 {(M, R)}, got {u.dtype} {tuple(u.shape)}")
+    _require_device(u, "u", x.device)
+    if out is None:
+        out = (torch.empty_like(x) if need_dx else None, torch.empty_like(la), torch.empty_like(lb))
+    dx, dla, dlb = out
+    for t, like, name in ((dx, x, "dx"), (dla, la, "dla"), (dlb, lb, "dlb")):
+        if t is not None and (t.dtype != x.dtype or t.shape != like.shape):
+            raise ValueError(f"{name} must be {x.dtype} {tuple(like.shape)}")
+        _require_device(t, name, x.device)
+    if dla is None or dlb is None:
+        raise ValueError("dla and dlb must be given")
+    stream = torch.cuda.current_stream(x.device).cuda_stream
+    with torch.cuda.device(x.device):
+        if workspace is None:
+            workspace = _workspace(x.device, stream, w4a16_lora_backward_workspace_size(M, N, K, S, R))
+        ws_ptr = None if workspace is None else workspace.data_ptr()
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(lib.w4a16_lora_backward(dy.data_ptr(), x.data_ptr(), u.data_ptr(), wq.data_ptr(), scales.data_ptr(),
+                                       _ptr(zp), la.data_ptr(), lb.data_ptr(), ids.data_ptr(), _ptr(alpha), _ptr(dx),
+                                       dla.data_ptr(), dlb.data_ptr(), M, N, K, group_size, S, R, dt, ws_ptr, ws_bytes,
+                                       stream))
+    return dx, dla, dlb
 
 
 # ---------------------------------------------------------------- AdamW ---

@@ -33,7 +33,7 @@ COMMON = [
     f"-I{INCLUDE}", f"-I{CSRC}",
 ]
 SOURCES = ["w4a16_host.cpp", "w4a16_gemv.hip", "w4a16_gemm.hip", "w4a16_gemm_lora.hip", "w4a16_lora.hip",
-           "w4a16_adamw.hip", "w4a16_elementwise.hip"]
+           "w4a16_lora_bwd.hip", "w4a16_dx.hip", "w4a16_adamw.hip", "w4a16_elementwise.hip"]
 # measurement kernels for the benchmark's ceilings, a library of their own
 CEILING_SOURCES = ["w4a16_ceilings.hip"]
 CEILINGS_LIB = os.path.join(PKG, "libw4a16_ceilings.so")

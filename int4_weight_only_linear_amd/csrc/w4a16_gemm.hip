@@ -34,6 +34,7 @@
 #include <algorithm>
 
 #include "w4a16_gemm_tile.hpp"
+#include "w4a16_lora_bwd.hpp"
 
 
 namespace w4a16 {
@@ -374,14 +375,17 @@ hipError_t launch_gemm(const LinearArgs& a, void* workspace, int cu_count, hipSt
     e = tiles(t, plan.tail_mb);
   }
   if (e != hipSuccess || !prm.two_pass) return e;
-  const int64_t quads = (int64_t)prm.M * (prm.np / 4);
+  return launch_splitk_reduce(a.dtype, prm.partial, prm.bias, prm.y, prm.M, prm.N, prm.np, prm.splits, stream);
+}
+
+hipError_t launch_splitk_reduce(int dtype, const float* partial, const uint16_t* bias, uint16_t* y, int M, int N, int np,
+                                int splits, hipStream_t s) {
+  const int64_t quads = (int64_t)M * (np / 4);
   const int blocks = (int)((quads + 255) / 256);
-  if (a.dtype == DT_F16)
-    hipLaunchKernelGGL(splitk_reduce_kernel<DT_F16>, dim3(blocks), dim3(256), 0, stream, prm.partial,
-                       prm.bias, prm.y, prm.M, prm.N, prm.np, prm.splits);
+  if (dtype == DT_F16)
+    hipLaunchKernelGGL(splitk_reduce_kernel<DT_F16>, dim3(blocks), dim3(256), 0, s, partial, bias, y, M, N, np, splits);
   else
-    hipLaunchKernelGGL(splitk_reduce_kernel<DT_BF16>, dim3(blocks), dim3(256), 0, stream, prm.partial,
-                       prm.bias, prm.y, prm.M, prm.N, prm.np, prm.splits);
+    hipLaunchKernelGGL(splitk_reduce_kernel<DT_BF16>, dim3(blocks), dim3(256), 0, s, partial, bias, y, M, N, np, splits);
   return hipGetLastError();
 }
 

@@ -23,6 +23,7 @@
 
 #include "w4a16_adamw.h"
 #include "w4a16_internal.h"
+#include "w4a16_lora_bwd.hpp"
 
 namespace w4a16 {
 
@@ -364,6 +365,44 @@ size_t lora_u_offset(int64_t M, int64_t N, int64_t K, int32_t kgroup, int32_t dt
   return round256(std::max(w4a16::kCounterBytes, workspace_for(M, N, K, kgroup, dtype, asym, p, cus)));
 }
 
+// the workspace of w4a16_lora_backward, by byte offsets behind the counter
+// region that every entry point leaves zero
+struct BackwardPlan {
+  int64_t np;  // N rounded up to 8: the rows of dy and of the transposed lb
+  w4a16::ShrinkPlan shrink;
+  w4a16::OuterPlan outer;
+  w4a16::DxPlan dx;
+  size_t zeros, perm, seg, la_t, lb_t, dy_pad, part, g, outer_part, dx_part, bytes;
+  size_t zero_bytes;  // from `zeros` on: 16 zero bytes, then the outer products' counters
+};
+BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K, int64_t S, int64_t R, int cus) {
+  BackwardPlan p;
+  p.np = (N + 7) / 8 * 8;
+  p.shrink = w4a16::plan_shrink(M, p.np, (int)R, cus);
+  p.outer = w4a16::plan_outer(M, K, N, (int)S, (int)R, cus);
+  p.dx = w4a16::plan_dx(M, N, K, cus);
+  size_t at = w4a16::kCounterBytes;
+  auto take = [&](size_t n) {
+    const size_t was = at;
+    at += round256(n);
+    return was;
+  };
+  p.zero_bytes = 16 + w4a16::outer_counter_bytes(p.outer, (int)S);
+  p.zeros = take(p.zero_bytes);
+  p.perm = take((size_t)M * 4);
+  p.seg = take((size_t)(S + 1) * 4);
+  p.la_t = take(act_bytes(S * K * R));
+  p.lb_t = take(act_bytes(S * p.np * R));
+  p.dy_pad = take(p.np != N ? act_bytes(M * p.np) : 0);
+  p.part = take((size_t)p.shrink.splits * (size_t)M * (size_t)R * 4);
+  p.g = take((size_t)M * (size_t)R * 4);
+  // the two are not in use at the same time, but both stay clear of the rest
+  p.outer_part = take(w4a16::outer_partial_bytes(p.outer, M));
+  p.dx_part = take(w4a16::dx_partial_bytes(p.dx, M, K));
+  p.bytes = at;
+  return p;
+}
+
 }  // namespace
 
 extern "C" {
@@ -457,9 +496,10 @@ w4a16_status w4a16_unpack_zeros(const int32_t* zpk, int64_t N, int64_t G, uint8_
   return ok();
 }
 
-w4a16_status w4a16_check_args(const void* x, const int32_t* wq, const void* scales,
-                              const int32_t* zp, const void* bias, const void* y, int64_t M,
-                              int64_t N, int64_t K, int32_t group_size, int32_t dtype) {
+// everything of w4a16_check_args but the overlap of y
+static w4a16_status check_problem(const void* x, const int32_t* wq, const void* scales,
+                                  const int32_t* zp, const void* bias, const void* y, int64_t M,
+                                  int64_t N, int64_t K, int32_t group_size, int32_t dtype) {
   if (dtype != W4A16_F16 && dtype != W4A16_BF16)
     return fail(W4A16_ERR_INVALID_ARG, "activation dtype must be fp16 (0) or bf16 (1), got %d", (int)dtype);
   if (!group_ok(group_size, K))
@@ -485,6 +525,14 @@ w4a16_status w4a16_check_args(const void* x, const int32_t* wq, const void* scal
   if (!aligned(scales, 2) || !aligned(y, 2) || (bias && !aligned(bias, 2)))
     return fail(W4A16_ERR_ALIGNMENT, "scales, bias and y must be 2-byte aligned");
   if (zp && !aligned(zp, 4)) return fail(W4A16_ERR_ALIGNMENT, "zp must be 4-byte aligned");
+  return ok();
+}
+
+w4a16_status w4a16_check_args(const void* x, const int32_t* wq, const void* scales,
+                              const int32_t* zp, const void* bias, const void* y, int64_t M,
+                              int64_t N, int64_t K, int32_t group_size, int32_t dtype) {
+  const w4a16_status st = check_problem(x, wq, scales, zp, bias, y, M, N, K, group_size, dtype);
+  if (st != W4A16_OK || M == 0) return st;
   const int64_t G = K / group_size;
   const size_t ybytes = act_bytes(M * N);
   if (overlap(y, ybytes, x, act_bytes(M * K)) || overlap(y, ybytes, wq, (size_t)N * (K / 8) * 4) ||
@@ -831,6 +879,115 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
   t.R = (int)R;
   t.usplits = sums ? 1 : sp.splits;
   return linear_impl(x, wq, scales, zp, bias, y, M, N, K, group_size, dtype, workspace, at, stream, p, &t);
+}
+
+size_t w4a16_lora_backward_workspace_size(int64_t M, int64_t N, int64_t K, int64_t S, int64_t R) {
+  if (M <= 0 || N <= 0 || K <= 0 || K % 32 || S < 1 || S > 65535 || R < 8 || R % 8 || R > w4a16::kMaxRank) return 0;
+  return plan_backward(M, N, K, S, R, planning_cus()).bytes;
+}
+
+w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, const int32_t* wq, const void* scales,
+                                 const int32_t* zp, const void* la, const void* lb, const int32_t* ids,
+                                 const float* alpha, void* dx, void* dla, void* dlb, int64_t M, int64_t N, int64_t K,
+                                 int32_t group_size, int64_t S, int64_t R, int32_t dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  // the projection's rules (dy stands where its output would)
+  w4a16_status st = check_problem(x, wq, scales, zp, nullptr, dy, M, N, K, group_size, dtype);
+  if (st != W4A16_OK) return st;
+  st = check_adapters("lora_backward", la, lb, ids, alpha, M, N, K, S, R);
+  if (st != W4A16_OK) return st;
+  if (S > 65535) return fail(W4A16_ERR_UNSUPPORTED, "lora_backward: at most 65535 adapters, got %lld", (long long)S);
+  if ((uint64_t)N * (uint64_t)K / 2 > 0xFFFFFFFFull)
+    return fail(W4A16_ERR_UNSUPPORTED, "lora_backward: N*K/2 must be below 4 GiB (N=%lld K=%lld)", (long long)N, (long long)K);
+  if (M > 0 && !u) return fail(W4A16_ERR_INVALID_ARG, "lora_backward: u must not be NULL");
+  if (!dla || !dlb) return fail(W4A16_ERR_INVALID_ARG, "lora_backward: dla and dlb must not be NULL");
+  if ((dy && !aligned(dy, 16)) || (u && !aligned(u, 16)) || (dx && !aligned(dx, 16)) || !aligned(dla, 16) || !aligned(dlb, 16))
+    return fail(W4A16_ERR_ALIGNMENT, "lora_backward: dy, u, dx, dla and dlb must be 16-byte aligned");
+  const int64_t G = K / group_size;
+  const struct { const void* p; size_t n; } out[3] = {{dx, act_bytes(M * K)}, {dla, act_bytes(S * R * K)}, {dlb, act_bytes(S * N * R)}},
+      in[6] = {{dy, act_bytes(M * N)}, {x, act_bytes(M * K)}, {u, (size_t)M * R * 4}, {wq, (size_t)N * (K / 8) * 4},
+               {scales, act_bytes(N * G)}, {zp, zp ? (size_t)(N / 8) * G * 4 : 0}};
+  for (int i = 0; i < 3; ++i) {
+    bool bad = overlaps_adapters(out[i].p, out[i].n, la, lb, ids, alpha, M, N, K, S, R);
+    for (int j = 0; j < 6; ++j) bad |= overlap(out[i].p, out[i].n, in[j].p, in[j].n);
+    for (int j = 0; j < i; ++j) bad |= overlap(out[i].p, out[i].n, out[j].p, out[j].n);
+    if (bad) return fail(W4A16_ERR_INVALID_ARG, "lora_backward: dx, dla and dlb must not overlap any input or each other");
+  }
+  const DeviceInfo* dev = nullptr;
+  st = device_info(&dev);
+  if (st != W4A16_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e;
+  if (M == 0) {
+    // no tokens: the gradients are zero (S R K and S N R are multiples of 8)
+    e = w4a16::launch_zero_words(dla, act_bytes(S * R * K), s);
+    if (e == hipSuccess) e = w4a16::launch_zero_words(dlb, act_bytes(S * N * R), s);
+    return e == hipSuccess ? ok() : fail(W4A16_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
+  }
+  const BackwardPlan p = plan_backward(M, N, K, S, R, dev->cu_count);
+  if (workspace == nullptr || workspace_bytes < p.bytes)
+    return fail(W4A16_ERR_WORKSPACE, "lora_backward: workspace of %zu bytes needed, got %zu%s", p.bytes, workspace_bytes,
+                workspace ? "" : " (NULL)");
+  if (!aligned(workspace, 256)) return fail(W4A16_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  char* const ws = static_cast<char*>(workspace);
+  auto at = [&](size_t o) { return static_cast<void*>(ws + o); };
+  const bool pad = p.np != N;
+  w4a16::PrepArgs prep;
+  prep.ids = ids;
+  prep.perm = static_cast<int32_t*>(at(p.perm));
+  prep.seg = static_cast<int32_t*>(at(p.seg));
+  prep.la = static_cast<const uint16_t*>(la);
+  prep.lb = static_cast<const uint16_t*>(lb);
+  prep.la_t = static_cast<uint16_t*>(at(p.la_t));
+  prep.lb_t = static_cast<uint16_t*>(at(p.lb_t));
+  prep.dy = static_cast<const uint16_t*>(dy);
+  prep.dy_pad = pad ? static_cast<uint16_t*>(at(p.dy_pad)) : nullptr;
+  prep.zero = static_cast<uint32_t*>(at(p.zeros));
+  prep.zero_words = (int)(p.zero_bytes / 4);
+  prep.M = (int)M;
+  prep.N = (int)N;
+  prep.K = (int)K;
+  prep.S = (int)S;
+  prep.R = (int)R;
+  prep.np = (int)p.np;
+  const uint16_t* const dyr = pad ? prep.dy_pad : prep.dy;
+  float* const g = static_cast<float*>(at(p.g));
+  e = w4a16::launch_prep(prep, s);
+  if (e == hipSuccess) {
+    // g / alpha = dy . B: the transposed lb in the first factor's place
+    const w4a16::ShrinkArgs sa{dyr, prep.lb_t, ids, static_cast<float*>(at(p.part)), g, M, p.np, (int)S, (int)R, dtype};
+    e = w4a16::launch_shrink(sa, p.shrink, s);
+  }
+  if (e == hipSuccess && dx) {
+    const GroupMap gm = group_map(group_size, K);
+    const w4a16::DxArgs da{dyr, wq, scales, zp, dx, at(p.zeros), static_cast<float*>(at(p.dx_part)), M, N, K, (int)p.np,
+                           gm.kgroup, dtype, gm.sG, gm.gmul};
+    w4a16::LoraTerm t;
+    t.ids = ids;
+    t.up = prep.la_t;
+    t.u = g;
+    t.alpha = alpha;
+    t.S = (int)S;
+    t.R = (int)R;
+    e = w4a16::launch_dx(da, p.dx, t, s);
+  }
+  if (e == hipSuccess) {
+    w4a16::OuterArgs oa;
+    oa.p[0] = {static_cast<const uint16_t*>(x), g, static_cast<uint16_t*>(dla), (int)K, (int)K, 1};
+    oa.p[1] = {dyr, u, static_cast<uint16_t*>(dlb), (int)p.np, (int)N, 0};
+    oa.perm = prep.perm;
+    oa.seg = prep.seg;
+    oa.alpha = alpha;
+    oa.partial = static_cast<float*>(at(p.outer_part));
+    oa.counters = prep.zero + 4;
+    oa.M = (int)M;
+    oa.S = (int)S;
+    oa.R = (int)R;
+    oa.dtype = dtype;
+    e = w4a16::launch_outer(oa, p.outer, s);
+  }
+  if (e != hipSuccess) return fail(W4A16_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
+  return ok();
 }
 
 static int elem_bytes(int32_t dtype) { return dtype == W4A16_F32 ? 4 : 2; }

@@ -45,13 +45,13 @@ __global__ __launch_bounds__(64 * shrink_waves(TT, RC)) void shrink_kernel(
   if (__ballot(lane < min(slot, BM) && ids[min(m0 + lane, M - 1)] == a) != 0) return;
 
   const int c_begin = blockIdx.y * chunks_per_split;
-  const int c_end = min(K >> 5, c_begin + chunks_per_split);
+  const int c_end = min((K + 31) >> 5, c_begin + chunks_per_split);
   const uint16_t* xrow[TT];
   const uint16_t* arow[RC];
 #pragma unroll
-  for (int t = 0; t < TT; ++t) xrow[t] = x + (size_t)min(m0 + 16 * t + col, M - 1) * K + 8 * row4;
+  for (int t = 0; t < TT; ++t) xrow[t] = x + (size_t)min(m0 + 16 * t + col, M - 1) * K;
 #pragma unroll
-  for (int rc = 0; rc < RC; ++rc) arow[rc] = down + ((size_t)a * R + min(r0 + 16 * rc + col, R - 1)) * K + 8 * row4;
+  for (int rc = 0; rc < RC; ++rc) arow[rc] = down + ((size_t)a * R + min(r0 + 16 * rc + col, R - 1)) * K;
   f32x4 acc[TT][RC];
 #pragma unroll
   for (int t = 0; t < TT; ++t)
@@ -61,11 +61,21 @@ __global__ __launch_bounds__(64 * shrink_waves(TT, RC)) void shrink_kernel(
     u32x4 xv[DEPTH][TT], av[DEPTH][RC];
 #pragma unroll
     for (int i = 0; i < DEPTH; ++i) {
-      const int c = min(c0 + i, c_end - 1);
+      // K is a multiple of 8: past it (a last chunk's upper lanes, a depth past
+      // the range) both operands are zero
+      const int k = 32 * (c0 + i) + 8 * row4;
+      const bool in = k < K;
+      const int kc = in ? k : K - 8;
 #pragma unroll
-      for (int t = 0; t < TT; ++t) xv[i][t] = *reinterpret_cast<const u32x4*>(xrow[t] + 32 * c);
+      for (int t = 0; t < TT; ++t) {
+        xv[i][t] = *reinterpret_cast<const u32x4*>(xrow[t] + kc);
+        if (!in) xv[i][t] = u32x4{0u, 0u, 0u, 0u};
+      }
 #pragma unroll
-      for (int rc = 0; rc < RC; ++rc) av[i][rc] = *reinterpret_cast<const u32x4*>(arow[rc] + 32 * c);
+      for (int rc = 0; rc < RC; ++rc) {
+        av[i][rc] = *reinterpret_cast<const u32x4*>(arow[rc] + kc);
+        if (!in) av[i][rc] = u32x4{0u, 0u, 0u, 0u};
+      }
     }
 #pragma unroll
     for (int i = 0; i < DEPTH; ++i)
@@ -131,7 +141,7 @@ hipError_t launch_dt(const ShrinkArgs& a, const ShrinkPlan& p, float* out, hipSt
 
 ShrinkPlan plan_shrink(int64_t M, int64_t K, int R, int cu_count) {
   ShrinkPlan p;
-  const int chunks = (int)(K / 32);
+  const int chunks = (int)((K + 31) / 32);
   p.tt = M <= 256 ? 1 : 4;
   const int blocks_r = (R + 15) / 16;
   p.rc = p.tt == 1 ? 1 : (blocks_r > 2 ? 4 : blocks_r);
