@@ -14,93 +14,106 @@ namespace {
 constexpr int shrink_waves(int tt, int rc) { return tt + rc > 4 ? 8 : 16; }
 constexpr int shrink_depth(int tt, int rc) { return tt + rc > 8 ? 1 : (tt + rc > 4 ? 2 : 4); }
 
-// A workgroup owns a tile of 16 TT tokens, 16 RC ranks, one K range and one
-// adapter: that of token `slot` of its tile, unless an earlier token of the
-// tile names the same one (then it leaves).  So the adapters of a tile are
-// read side by side, each once per tile.  Its waves take the range's chunks
-// in turn.  The tokens are the MFMA's A rows, the adapter's ranks its B
-// columns, both loaded straight from their rows (16 bytes a lane); the waves
-// are added through LDS in wave order, and the rows of the adapter's own
-// tokens stored: u[split][M][R].  A token without an adapter gets zeros, from
-// the workgroup of its own slot.
+// A workgroup owns a tile of 16 TT tokens, 16 RC ranks and one K range, and of
+// the adapters that the tile's tokens name, in the order of their first token,
+// every `turns`-th (blockIdx.z): an adapter's rows are read once per tile,
+// several adapters of a tile side by side.  (The tile is the fastest index:
+// with one adapter only the first turn has work, and its workgroups spread
+// over all XCDs; as multiples of the turns they all fell on one, 6-9x slower.)
+// The waves take the range's chunks in turn.  The tokens are the MFMA's A
+// rows, the adapter's ranks its B columns, both loaded straight from their
+// rows (16 bytes a lane); the waves are added through LDS in wave order, and
+// the rows of the adapter's own tokens stored: u[split][M][R].  Tokens without
+// an adapter get zeros.
 template <int DT, int TT, int RC>
 __global__ __launch_bounds__(64 * shrink_waves(TT, RC)) void shrink_kernel(
     const uint16_t* __restrict__ x, const uint16_t* __restrict__ down, const int32_t* __restrict__ ids,
-    float* __restrict__ u, int M, int K, int S, int R, int chunks_per_split) {
+    float* __restrict__ u, int M, int K, int S, int R, int chunks_per_split, int turns) {
   constexpr int WAVES = shrink_waves(TT, RC), DEPTH = shrink_depth(TT, RC), BM = 16 * TT, BR = 16 * RC;
   __shared__ __attribute__((aligned(16))) float red[WAVES * 256 * RC];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, row4 = lane >> 4;
-  const int tile = blockIdx.x / BM, slot = blockIdx.x - tile * BM;
-  const int m0 = tile * BM, r0 = blockIdx.z * BR;
-  if (m0 + slot >= M) return;
-  const int a = ids[m0 + slot];
+  const int m0 = blockIdx.x * BM;
+  const int rg = blockIdx.z / turns, turn = blockIdx.z - rg * turns;
+  const int r0 = rg * BR;
   float* const out = u + (size_t)blockIdx.y * M * R;
-  if (a < 0 || a >= S) {
-    for (int r = r0 + tid; r < min(R, r0 + BR); r += blockDim.x) out[(size_t)(m0 + slot) * R + r] = 0.f;
-    return;
-  }
-  // an earlier token of the tile with the same adapter: its workgroup's work
-  if (__ballot(lane < min(slot, BM) && ids[min(m0 + lane, M - 1)] == a) != 0) return;
 
-  const int c_begin = blockIdx.y * chunks_per_split;
-  const int c_end = min((K + 31) >> 5, c_begin + chunks_per_split);
+  const bool token = lane < BM && m0 + lane < M;
+  const int mine = token ? ids[m0 + lane] : -1;
+  const bool named = mine >= 0 && mine < S;
+  if (turn == 0) {
+    uint64_t none = __ballot(token && !named);
+    for (; none; none &= none - 1) {
+      const int m = m0 + __builtin_ctzll(none);
+      for (int r = r0 + tid; r < min(R, r0 + BR); r += blockDim.x) out[(size_t)m * R + r] = 0.f;
+    }
+  }
   const uint16_t* xrow[TT];
-  const uint16_t* arow[RC];
 #pragma unroll
   for (int t = 0; t < TT; ++t) xrow[t] = x + (size_t)min(m0 + 16 * t + col, M - 1) * K;
+  const int c_begin = blockIdx.y * chunks_per_split;
+  const int c_end = min((K + 31) >> 5, c_begin + chunks_per_split);
+
+  uint64_t todo = __ballot(named);
+  for (int n = 0; todo; ++n) {
+    const int a = __builtin_amdgcn_readlane(mine, __builtin_ctzll(todo));
+    const uint64_t own = __ballot(named && mine == a);
+    todo &= ~own;
+    if (n % turns != turn) continue;
+    const uint16_t* arow[RC];
+    f32x4 acc[TT][RC];
 #pragma unroll
-  for (int rc = 0; rc < RC; ++rc) arow[rc] = down + ((size_t)a * R + min(r0 + 16 * rc + col, R - 1)) * K;
-  f32x4 acc[TT][RC];
+    for (int rc = 0; rc < RC; ++rc) {
+      arow[rc] = down + ((size_t)a * R + min(r0 + 16 * rc + col, R - 1)) * K;
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
+      for (int t = 0; t < TT; ++t) acc[t][rc] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    for (int c0 = c_begin + wave * DEPTH; c0 < c_end; c0 += WAVES * DEPTH) {
+      u32x4 xv[DEPTH][TT], av[DEPTH][RC];
 #pragma unroll
-    for (int rc = 0; rc < RC; ++rc) acc[t][rc] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int c0 = c_begin + wave * DEPTH; c0 < c_end; c0 += WAVES * DEPTH) {
-    u32x4 xv[DEPTH][TT], av[DEPTH][RC];
+      for (int i = 0; i < DEPTH; ++i) {
+        // K is a multiple of 8: past it (a last chunk's upper lanes, a depth
+        // past the range) both operands are zero
+        const int k = 32 * (c0 + i) + 8 * row4;
+        const bool in = k < K;
+        const int kc = in ? k : K - 8;
 #pragma unroll
-    for (int i = 0; i < DEPTH; ++i) {
-      // K is a multiple of 8: past it (a last chunk's upper lanes, a depth past
-      // the range) both operands are zero
-      const int k = 32 * (c0 + i) + 8 * row4;
-      const bool in = k < K;
-      const int kc = in ? k : K - 8;
+        for (int t = 0; t < TT; ++t) {
+          xv[i][t] = *reinterpret_cast<const u32x4*>(xrow[t] + kc);
+          if (!in) xv[i][t] = u32x4{0u, 0u, 0u, 0u};
+        }
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        xv[i][t] = *reinterpret_cast<const u32x4*>(xrow[t] + kc);
-        if (!in) xv[i][t] = u32x4{0u, 0u, 0u, 0u};
+        for (int rc = 0; rc < RC; ++rc) {
+          av[i][rc] = *reinterpret_cast<const u32x4*>(arow[rc] + kc);
+          if (!in) av[i][rc] = u32x4{0u, 0u, 0u, 0u};
+        }
       }
 #pragma unroll
-      for (int rc = 0; rc < RC; ++rc) {
-        av[i][rc] = *reinterpret_cast<const u32x4*>(arow[rc] + kc);
-        if (!in) av[i][rc] = u32x4{0u, 0u, 0u, 0u};
-      }
+      for (int i = 0; i < DEPTH; ++i)
+        if (c0 + i < c_end) {
+#pragma unroll
+          for (int t = 0; t < TT; ++t)
+#pragma unroll
+            for (int rc = 0; rc < RC; ++rc) acc[t][rc] = mfma16x16x32<DT>(xv[i][t], av[i][rc], acc[t][rc]);
+        }
     }
 #pragma unroll
-    for (int i = 0; i < DEPTH; ++i)
-      if (c0 + i < c_end) {
+    for (int t = 0; t < TT; ++t) {
+      if (t || n) __syncthreads();  // the previous block's sums are read
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
+      for (int rc = 0; rc < RC; ++rc)
 #pragma unroll
-          for (int rc = 0; rc < RC; ++rc) acc[t][rc] = mfma16x16x32<DT>(xv[i][t], av[i][rc], acc[t][rc]);
-      }
-  }
+        for (int e = 0; e < 4; ++e) red[wave * (16 * BR) + (4 * row4 + e) * BR + 16 * rc + col] = acc[t][rc][e];
+      __syncthreads();
+      for (int i = tid; i < 16 * BR; i += blockDim.x) {
+        const int m = 16 * t + i / BR, r = r0 + i % BR;
+        if (r < R && (own >> m) & 1) {
+          float v = 0.f;
 #pragma unroll
-  for (int t = 0; t < TT; ++t) {
-    if (t) __syncthreads();  // the previous block's sums are read
-#pragma unroll
-    for (int rc = 0; rc < RC; ++rc)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) red[wave * (16 * BR) + (4 * row4 + e) * BR + 16 * rc + col] = acc[t][rc][e];
-    __syncthreads();
-    for (int i = tid; i < 16 * BR; i += blockDim.x) {
-      const int m = m0 + 16 * t + i / BR, r = r0 + i % BR;
-      if (m < M && r < R && ids[m] == a) {
-        float v = 0.f;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) v += red[w * (16 * BR) + i];
-        out[(size_t)m * R + r] = v;
+          for (int w = 0; w < WAVES; ++w) v += red[w * (16 * BR) + i];
+          out[(size_t)(m0 + m) * R + r] = v;
+        }
       }
     }
   }
@@ -119,10 +132,11 @@ __global__ __launch_bounds__(256) void shrink_reduce_kernel(const float* __restr
 template <int DT, int TT, int RC>
 hipError_t launch_t(const ShrinkArgs& a, const ShrinkPlan& p, float* out, hipStream_t s) {
   const int64_t tiles = (a.M + 16 * TT - 1) / (16 * TT);
-  const dim3 grid((unsigned)(tiles * 16 * TT), p.splits, (a.R + 16 * RC - 1) / (16 * RC));
+  const int turns = std::min(a.S, TT == 1 ? 16 : 8);  // (adapters of a tile: at most its tokens)
+  const dim3 grid((unsigned)tiles, p.splits, (a.R + 16 * RC - 1) / (16 * RC) * turns);
   hipLaunchKernelGGL((shrink_kernel<DT, TT, RC>), grid, dim3(64 * shrink_waves(TT, RC)), 0, s,
                      static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.down), a.ids, out, (int)a.M,
-                     (int)a.K, a.S, a.R, p.chunks_per_split);
+                     (int)a.K, a.S, a.R, p.chunks_per_split, turns);
   return hipGetLastError();
 }
 
