@@ -182,7 +182,6 @@ __device__ __forceinline__ void finish_tile(const GemvParams& p, const float* re
       for (int w = 0; w < nwaves; ++w) v += red[w * nel + e];
       if (p.splits == 1) {
         if (p.bias) v += act_to_f32<DT>(p.bias[nn]);
-        if (p.lora.ids) v += lora_dot<DT>(p.lora, p.M, p.N, m, nn);
         p.y[(size_t)m * p.N + nn] = f32_to_act<DT>(v * p.yscale);
       } else {
         store_coherent(p.partial + ((size_t)split * p.M + m) * p.N + nn, v);
@@ -206,7 +205,6 @@ __device__ __forceinline__ void finish_tile(const GemvParams& p, const float* re
       float v = 0.f;
       for (int s = 0; s < p.splits; ++s) v += load_coherent(p.partial + ((size_t)s * p.M + m) * p.N + nn);
       if (p.bias) v += act_to_f32<DT>(p.bias[nn]);
-      if (p.lora.ids) v += lora_dot<DT>(p.lora, p.M, p.N, m, nn);
       p.y[(size_t)m * p.N + nn] = f32_to_act<DT>(v * p.yscale);
     }
   }
@@ -621,17 +619,23 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(small_wave
   }
 
   // ---- 4. reduce the waves in order, then the K ranges ----
+  // (low-rank adapters: each wave adds its tokens' term to its own sums)
+  auto add_lora = [&]() {
+    lora_wave_add<DT>(p.lora, p.M, p.N, n0, wave, nwaves, lane, [&](int m, int row, float v) {
+      red[wave * 256 + (m & 3) * 64 + 16 * (m >> 2) + row] += v;
+    });
+  };
   if constexpr (ONE) {
     if (p.splits == 1) {
       // one token, one K range: the sums are register 0 of lanes 0..15
       red[wave * 256 + lane] = acc[0];
+      if (p.lora.ids) add_lora();
       __syncthreads();
       const int nn = n0 + tid;
       if (tid < kGemvRowsPerTile && nn < p.N) {
         float v = 0.f;
         for (int w = 0; w < nwaves; ++w) v += red[w * 256 + tid];
         if (p.bias) v += act_to_f32<DT>(p.bias[nn]);
-        if (p.lora.ids) v += lora_dot<DT>(p.lora, p.M, p.N, 0, nn);
         p.y[nn] = f32_to_act<DT>(v * p.yscale);
       }
       return;
@@ -642,19 +646,20 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(small_wave
     // 0..15 (the general path's order: waves in order, then bias, rounding)
 #pragma unroll
     for (int r = 0; r < 4; ++r) red[wave * 256 + r * 64 + lane] = acc[r];
+    if (p.lora.ids) add_lora();
     __syncthreads();
     const int m = tid >> 4, nn = n0 + (tid & 15);
     if (tid < 16 * p.M && nn < p.N) {
       float v = 0.f;
       for (int w = 0; w < nwaves; ++w) v += red[w * 256 + m * 64 + (tid & 15)];
       if (p.bias) v += act_to_f32<DT>(p.bias[nn]);
-      if (p.lora.ids) v += lora_dot<DT>(p.lora, p.M, p.N, m, nn);
       p.y[(size_t)m * p.N + nn] = f32_to_act<DT>(v * p.yscale);
     }
     return;
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) red[wave * 256 + r * 64 + lane] = acc[r];
+  if (p.lora.ids && split == 0) add_lora();
   __syncthreads();
   finish_tile<DT>(p, red, nwaves, 256, tile, split, &last_flag);
 }
@@ -1011,6 +1016,13 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(one_waves_
       if (lane < 16) red_of(wave)[r * 16 + lane] = v;
     }
   }
+  // low-rank adapters: each wave adds its tokens' term to its own sums (of the
+  // first K range)
+  if constexpr (!MOE) {
+    if (moe.lora.ids && blockIdx.y == 0)
+      lora_wave_add<DT>(moe.lora, M, N, n0, wave, nwaves, lane,
+                        [&](int m, int row, float v) { red_of(wave)[m * 16 + row] += v; });
+  }
   __syncthreads();
   // 16 M outputs (a workgroup of one wave covers eight tokens in two passes)
   for (int e = tid; e < 16 * M; e += blockDim.x) {
@@ -1021,7 +1033,6 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(one_waves_
       for (int w = 0; w < nwaves; ++w) v += red_of(w)[m * 16 + (e & 15)];
       if constexpr (!SPLIT) {
         if (bias) v += act_to_f32<DT>(bias[nn]);
-        if (!MOE && moe.lora.ids) v += lora_dot<DT>(moe.lora, M, N, m, nn);
         y[(size_t)m * N + nn] = f32_to_act<DT>(MOE ? v * yscale : v);
       } else {
         store_coherent(moe.partial + ((size_t)blockIdx.y * M + m) * N + nn, v);
@@ -1046,7 +1057,6 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(one_waves_
       float v = 0.f;
       for (int sp = 0; sp < splits; ++sp) v += load_coherent(moe.partial + ((size_t)sp * M + m) * N + nn);
       if (bias) v += act_to_f32<DT>(bias[nn]);
-      if (moe.lora.ids) v += lora_dot<DT>(moe.lora, M, N, m, nn);
       y[(size_t)m * N + nn] = f32_to_act<DT>(v);
     }
   }

@@ -359,6 +359,14 @@ bool overlaps_adapters(const void* out, size_t bytes, const void* la, const void
          overlap(out, bytes, ids, (size_t)M * 4) || (alpha && overlap(out, bytes, alpha, (size_t)S * 4));
 }
 
+// The kernel beside adapters: the decode kernel for every M it takes, also
+// where the thin GEMM tiles alone would be faster (they need the K ranges of u
+// added by a launch of their own, and mostly a second pass for their K split).
+w4a16_path lora_path(int64_t M, int64_t N, int64_t K, int32_t group, int32_t dtype, int32_t has_zp) {
+  const w4a16_path p = resolve_path(M, N, K, group, dtype, has_zp, W4A16_PATH_AUTO);
+  return M <= W4A16_GEMV_MAX_M && w4a16::tuning().force_path == 0 && w4a16::tuning().m_threshold < 0 ? W4A16_PATH_GEMV : p;
+}
+
 // the workspace of w4a16_lora_linear: the projection's own (its counter region
 // always kept, so that one workspace serves every entry point), then u
 size_t lora_u_offset(int64_t M, int64_t N, int64_t K, int32_t kgroup, int32_t dtype, bool asym, w4a16_path p, int cus) {
@@ -378,7 +386,7 @@ struct BackwardPlan {
 BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K, int64_t S, int64_t R, int cus) {
   BackwardPlan p;
   p.np = (N + 7) / 8 * 8;
-  p.shrink = w4a16::plan_shrink(M, p.np, (int)R, cus);
+  p.shrink = w4a16::plan_shrink(M, p.np, (int)R, cus, false);
   p.outer = w4a16::plan_outer(M, K, N, (int)S, (int)R, cus);
   p.dx = w4a16::plan_dx(M, N, K, cus);
   size_t at = w4a16::kCounterBytes;
@@ -824,8 +832,8 @@ size_t w4a16_lora_workspace_size(int64_t M, int64_t N, int64_t K, int32_t group_
     return 0;
   const int cus = planning_cus();
   const int kgroup = group_map(group_size, K).kgroup;
-  const w4a16_path p = resolve_path(M, N, K, kgroup, dtype, has_zp, W4A16_PATH_AUTO);
-  const w4a16::ShrinkPlan sp = w4a16::plan_shrink(M, K, (int)R, cus);
+  const w4a16_path p = lora_path(M, N, K, kgroup, dtype, has_zp);
+  const w4a16::ShrinkPlan sp = w4a16::plan_shrink(M, K, (int)R, cus, p == W4A16_PATH_GEMV);
   // the K ranges' sums, and u itself where the caller does not keep it
   return lora_u_offset(M, N, K, kgroup, dtype, has_zp != 0, p, cus) +
          round256((size_t)(sp.splits + (save_u ? 0 : 1)) * (size_t)M * (size_t)R * sizeof(float));
@@ -859,9 +867,9 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
                 workspace ? "" : " (NULL)");
   if (!aligned(workspace, 256)) return fail(W4A16_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
   const int kgroup = group_map(group_size, K).kgroup;
-  const w4a16_path p = resolve_path(M, N, K, kgroup, dtype, zp != nullptr, W4A16_PATH_AUTO);
+  const w4a16_path p = lora_path(M, N, K, kgroup, dtype, zp != nullptr);
   const size_t at = lora_u_offset(M, N, K, kgroup, dtype, zp != nullptr, p, dev->cu_count);
-  const w4a16::ShrinkPlan sp = w4a16::plan_shrink(M, K, (int)R, dev->cu_count);
+  const w4a16::ShrinkPlan sp = w4a16::plan_shrink(M, K, (int)R, dev->cu_count, p == W4A16_PATH_GEMV);
   // Decode: the epilogue adds the K ranges' sums itself, which saves a launch
   // (a few floats per output).  Above it every tile of the GEMM reads all of
   // its tokens' u, so the ranges are added once, before it.

@@ -54,7 +54,7 @@ struct ShrinkPlan {
 };
 constexpr int kMaxShrinkSplits = 16;
 constexpr int kMaxRank = 128;
-ShrinkPlan plan_shrink(int64_t M, int64_t K, int R, int cu_count);
+ShrinkPlan plan_shrink(int64_t M, int64_t K, int R, int cu_count, bool few);
 hipError_t launch_shrink(const ShrinkArgs& a, const ShrinkPlan& p, hipStream_t s);
 
 // ---- tuning overrides ------------------------------------------------------

@@ -19,15 +19,10 @@ __device__ __forceinline__ int lora_id(const LoraTerm& t, int M, int m) {
   return a >= 0 && a < t.S ? a : -1;
 }
 
-// eight ranks r0.. of alpha * u[m], summed over the K ranges u was formed in
-__device__ __forceinline__ void lora_u8(const LoraTerm& t, int M, int m, int r0, float alpha, float (&v)[8]) {
+// eight ranks r0.. of alpha * u[m] (one K range)
+__device__ __forceinline__ void lora_u8(const LoraTerm& t, int m, int r0, float alpha, float (&v)[8]) {
   const float* src = t.u + (size_t)m * t.R + r0;
-  f32x4 a = *reinterpret_cast<const f32x4*>(src), b = *reinterpret_cast<const f32x4*>(src + 4);
-  for (int sp = 1; sp < t.usplits; ++sp) {
-    src += (size_t)M * t.R;
-    a += *reinterpret_cast<const f32x4*>(src);
-    b += *reinterpret_cast<const f32x4*>(src + 4);
-  }
+  const f32x4 a = *reinterpret_cast<const f32x4*>(src), b = *reinterpret_cast<const f32x4*>(src + 4);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     v[e] = a[e] * alpha;
@@ -37,23 +32,49 @@ __device__ __forceinline__ void lora_u8(const LoraTerm& t, int M, int m, int r0,
 
 __device__ __forceinline__ float lora_alpha(const LoraTerm& t, int a) { return t.alpha ? t.alpha[a] : 1.f; }
 
-// The term of output (m, n), in fp32 throughout (the decode kernels' epilogue).
-template <int DT>
-__device__ __forceinline__ float lora_dot(const LoraTerm& t, int M, int N, int m, int n) {
-  const int a = lora_id(t, M, m);
-  if (a < 0) return 0.f;
-  const float alpha = lora_alpha(t, a);
-  const uint16_t* up = static_cast<const uint16_t*>(t.up) + ((size_t)a * N + n) * t.R;
-  float s = 0.f;
-  for (int r = 0; r < t.R; r += 8) {
-    const u32x4 w = *reinterpret_cast<const u32x4*>(up + r);
-    float u[8];
-    lora_u8(t, M, m, r, alpha, u);
+// The decode kernels' term, in fp32 throughout.  Token m belongs to the wave
+// m % waves, which adds the term of the tile's 16 rows n0.. to its own sums
+// before the waves are added (add(m, row, value), lanes 0..15): no further
+// barrier, and every wave's loads are under way at once.  A lane takes every
+// fourth run of eight ranks of one row; the K ranges of u are read four at a
+// time, so that their loads overlap.
+template <int DT, typename Add>
+__device__ __forceinline__ void lora_wave_add(const LoraTerm& t, int M, int N, int n0, int wave, int waves, int lane,
+                                              Add&& add) {
+  const int n = min(n0 + (lane & 15), N - 1);
+  const size_t plane = (size_t)M * t.R;
+  for (int m = wave; m < M; m += waves) {
+    const int a = __builtin_amdgcn_readfirstlane(lora_id(t, M, m));
+    if (a < 0) continue;
+    const uint16_t* up = static_cast<const uint16_t*>(t.up) + ((size_t)a * N + n) * t.R;
+    const float alpha = lora_alpha(t, a);
+    float s = 0.f;
+    for (int r = 8 * (lane >> 4); r < t.R; r += 32) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(up + r);
+      float u[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      for (int s0 = 0; s0 < t.usplits; s0 += 4) {
+        f32x4 v[4][2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      s = __builtin_fmaf(u[e], act_to_f32<DT>((uint16_t)(w[e >> 1] >> (16 * (e & 1)))), s);
+        for (int i = 0; i < 4; ++i) {
+          const float* src = t.u + (size_t)min(s0 + i, t.usplits - 1) * plane + (size_t)m * t.R + r;
+          v[i][0] = *reinterpret_cast<const f32x4*>(src);
+          v[i][1] = *reinterpret_cast<const f32x4*>(src + 4);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (s0 + i < t.usplits) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) u[e] += v[i][e >> 2][e & 3];
+          }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        s = __builtin_fmaf(u[e], act_to_f32<DT>((uint16_t)(w[e >> 1] >> (16 * (e & 1)))), s);
+    }
+    s += __shfl_xor(s, 16);
+    s += __shfl_xor(s, 32);
+    if (lane < 16) add(m, lane, s * alpha);
   }
-  return s;
 }
 
 // Eight fp32 values as two MFMA operands whose sum is the value to about 16
@@ -116,7 +137,7 @@ __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int 
         u32x4 hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
         if (in && id[rb] == next) {
           float v[8];
-          lora_u8(t, M, m0 + 32 * rb + j, r0, alpha, v);
+          lora_u8(t, m0 + 32 * rb + j, r0, alpha, v);
           split_hi_lo<DT>(v, hi, lo);
         }
 #pragma unroll
