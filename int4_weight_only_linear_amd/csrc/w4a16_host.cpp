@@ -380,7 +380,8 @@ struct BackwardPlan {
   w4a16::ShrinkPlan shrink;
   w4a16::OuterPlan outer;
   w4a16::DxPlan dx;
-  size_t zeros, perm, seg, la_t, lb_t, dy_pad, part, g, outer_part, dx_part, bytes;
+  int64_t places;  // of the tokens' order
+  size_t zeros, order, start, count, la_t, lb_t, dy_pad, part, g, op[2], outer_part, dx_part, bytes;
   size_t zero_bytes;  // from `zeros` on: 16 zero bytes, then the outer products' counters
 };
 BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K, int64_t S, int64_t R, int cus) {
@@ -397,15 +398,18 @@ BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K, int64_t S, int64_t R
   };
   p.zero_bytes = 16 + w4a16::outer_counter_bytes(p.outer, (int)S);
   p.zeros = take(p.zero_bytes);
-  p.perm = take((size_t)M * 4);
-  p.seg = take((size_t)(S + 1) * 4);
+  p.places = w4a16::order_places(M, S);
+  p.order = take((size_t)p.places * 4);
+  p.start = take((size_t)S * 4);
+  p.count = take((size_t)S * 4);
   p.la_t = take(act_bytes(S * K * R));
   p.lb_t = take(act_bytes(S * p.np * R));
   p.dy_pad = take(p.np != N ? act_bytes(M * p.np) : 0);
   p.part = take((size_t)p.shrink.splits * (size_t)M * (size_t)R * 4);
   p.g = take((size_t)M * (size_t)R * 4);
+  for (size_t& o : p.op) o = take(act_bytes(2 * R * p.places));
   // the two are not in use at the same time, but both stay clear of the rest
-  p.outer_part = take(w4a16::outer_partial_bytes(p.outer, M));
+  p.outer_part = take(w4a16::outer_partial_bytes(p.outer, p.places));
   p.dx_part = take(w4a16::dx_partial_bytes(p.dx, M, K));
   p.bytes = at;
   return p;
@@ -904,6 +908,8 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
   if (st != W4A16_OK) return st;
   st = check_adapters("lora_backward", la, lb, ids, alpha, M, N, K, S, R);
   if (st != W4A16_OK) return st;
+  if (w4a16::order_places(M, S) * 4 > INT32_MAX)
+    return fail(W4A16_ERR_UNSUPPORTED, "lora_backward: too many tokens, got M=%lld", (long long)M);
   if (S > 65535) return fail(W4A16_ERR_UNSUPPORTED, "lora_backward: at most 65535 adapters, got %lld", (long long)S);
   if ((uint64_t)N * (uint64_t)K / 2 > 0xFFFFFFFFull)
     return fail(W4A16_ERR_UNSUPPORTED, "lora_backward: N*K/2 must be below 4 GiB (N=%lld K=%lld)", (long long)N, (long long)K);
@@ -942,8 +948,10 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
   const bool pad = p.np != N;
   w4a16::PrepArgs prep;
   prep.ids = ids;
-  prep.perm = static_cast<int32_t*>(at(p.perm));
-  prep.seg = static_cast<int32_t*>(at(p.seg));
+  prep.order = static_cast<int32_t*>(at(p.order));
+  prep.start = static_cast<int32_t*>(at(p.start));
+  prep.count = static_cast<int32_t*>(at(p.count));
+  prep.places = (int)p.places;
   prep.la = static_cast<const uint16_t*>(la);
   prep.lb = static_cast<const uint16_t*>(lb);
   prep.la_t = static_cast<uint16_t*>(at(p.la_t));
@@ -963,8 +971,14 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
   e = w4a16::launch_prep(prep, s);
   if (e == hipSuccess) {
     // g / alpha = dy . B: the transposed lb in the first factor's place
-    const w4a16::ShrinkArgs sa{dyr, prep.lb_t, ids, static_cast<float*>(at(p.part)), g, M, p.np, (int)S, (int)R, dtype};
+    const w4a16::ShrinkArgs sa{dyr, prep.lb_t, ids, static_cast<float*>(at(p.part)), nullptr, M, p.np, (int)S, (int)R, dtype};
     e = w4a16::launch_shrink(sa, p.shrink, s);
+  }
+  uint16_t* const op[2] = {static_cast<uint16_t*>(at(p.op[0])), static_cast<uint16_t*>(at(p.op[1]))};
+  if (e == hipSuccess) {
+    const w4a16::OperandArgs pa{static_cast<const float*>(at(p.part)), u, ids, prep.order, alpha, g, {op[0], op[1]},
+                                (int)M, (int)R, p.shrink.splits, (int)p.places, dtype};
+    e = w4a16::launch_operands(pa, s);
   }
   if (e == hipSuccess && dx) {
     const GroupMap gm = group_map(group_size, K);
@@ -981,11 +995,12 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
   }
   if (e == hipSuccess) {
     w4a16::OuterArgs oa;
-    oa.p[0] = {static_cast<const uint16_t*>(x), g, static_cast<uint16_t*>(dla), (int)K, (int)K, 1};
-    oa.p[1] = {dyr, u, static_cast<uint16_t*>(dlb), (int)p.np, (int)N, 0};
-    oa.perm = prep.perm;
-    oa.seg = prep.seg;
-    oa.alpha = alpha;
+    oa.p[0] = {static_cast<const uint16_t*>(x), op[0], static_cast<uint16_t*>(dla), (int)K, (int)K, 1};
+    oa.p[1] = {dyr, op[1], static_cast<uint16_t*>(dlb), (int)p.np, (int)N, 0};
+    oa.order = prep.order;
+    oa.start = prep.start;
+    oa.count = prep.count;
+    oa.places = (int)p.places;
     oa.partial = static_cast<float*>(at(p.outer_part));
     oa.counters = prep.zero + 4;
     oa.M = (int)M;

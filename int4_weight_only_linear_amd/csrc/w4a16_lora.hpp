@@ -19,17 +19,6 @@ __device__ __forceinline__ int lora_id(const LoraTerm& t, int M, int m) {
   return a >= 0 && a < t.S ? a : -1;
 }
 
-// eight ranks r0.. of alpha * u[m] (one K range)
-__device__ __forceinline__ void lora_u8(const LoraTerm& t, int m, int r0, float alpha, float (&v)[8]) {
-  const float* src = t.u + (size_t)m * t.R + r0;
-  const f32x4 a = *reinterpret_cast<const f32x4*>(src), b = *reinterpret_cast<const f32x4*>(src + 4);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[e] = a[e] * alpha;
-    v[4 + e] = b[e] * alpha;
-  }
-}
-
 __device__ __forceinline__ float lora_alpha(const LoraTerm& t, int a) { return t.alpha ? t.alpha[a] : 1.f; }
 
 // The decode kernels' term, in fp32 throughout.  Token m belongs to the wave
@@ -93,61 +82,100 @@ __device__ __forceinline__ void split_hi_lo(const float (&v)[8], u32x4& hi, u32x
   lo = u32x4{l[0], l[1], l[2], l[3]};
 }
 
-// the smallest value over the wave's 64 lanes
-__device__ __forceinline__ int wave_min(int v) {
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v = min(v, __shfl_xor(v, d));
-  return __builtin_amdgcn_readfirstlane(v);
-}
-
 // The GEMM tile's adapter term, as more k of its product: for every adapter
-// that a token of the tile names (in ascending order), ceil(R / 16) k-subs
-// whose A operand is the wave's rows of up_a and whose B operand is alpha * u
-// of the adapter's own tokens, zero for the others.
+// that a token of the tile names (in the order of their first tokens),
+// ceil(R / 16) k-subs whose A operand is the wave's rows of up_a and whose B
+// operand is alpha * u of the adapter's own tokens, zero for the others; token
+// blocks without such a token are left out.  The operands of the next k-sub
+// are loaded while one is multiplied (a tile of many adapters is a chain of
+// them, each a memory round trip otherwise: 16 adapters of rank 32 among 67
+// tokens 48 -> 26 us).
 //   acc[rb][cb]: tokens m0 + 32 rb + (lane & 31), features nw0 + 32 cb + ...
 template <int DT, int MB, int CB>
 __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int m0, int nw0, int lane,
                                            f32x16 (&acc)[MB][CB]) {
   const int j = lane & 31, h = lane >> 5;
   int id[MB];
+  uint64_t todo[MB];
 #pragma unroll
   for (int rb = 0; rb < MB; ++rb) {
-    const int a = lora_id(t, M, m0 + 32 * rb + j);
-    id[rb] = a < 0 ? t.S : a;
+    id[rb] = lora_id(t, M, m0 + 32 * rb + j);
+    todo[rb] = __ballot(id[rb] >= 0);
   }
-  for (int prev = -1;;) {
-    int next = t.S;
+  const uint16_t* up = static_cast<const uint16_t*>(t.up) + 8 * h;
+  uint32_t row[CB];
 #pragma unroll
-    for (int rb = 0; rb < MB; ++rb)
-      if (id[rb] > prev) next = min(next, id[rb]);
-    next = wave_min(next);
-    if (next >= t.S) return;
-    const float alpha = lora_alpha(t, next);
-    for (int r0 = 8 * h; r0 - 8 * h < t.R; r0 += 16) {
-      const bool in = r0 < t.R;  // R a multiple of 8: the upper half of a last k-sub may lie past it
-      u32x4 a[CB];
+  for (int cb = 0; cb < CB; ++cb) row[cb] = (uint32_t)min(nw0 + 32 * cb + j, N - 1);
+
+  struct Item {
+    int a, r0;           // adapter (-1: no more), first rank (of both halves)
+    uint64_t own[MB];    // lanes whose token is the adapter's
+    float alpha;
+    u32x4 w[CB];
+    f32x4 u[MB][2];
+  };
+  // the item after `it`: the next ranks of its adapter, or the next adapter
+  auto next = [&](const Item& it) {
+    Item n;
+    n.a = it.a;
+    n.r0 = it.r0 + 16;
+    n.alpha = it.alpha;
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb) {
-        const int n = min(nw0 + 32 * cb + j, N - 1);
-        a[cb] = in ? *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(t.up) + ((size_t)next * N + n) * t.R + r0)
-                   : u32x4{0u, 0u, 0u, 0u};
-      }
+    for (int rb = 0; rb < MB; ++rb) n.own[rb] = it.own[rb];
+    if (n.r0 >= t.R) {
+      n.a = -1;
+      n.r0 = 0;
+#pragma unroll
+      for (int rb = MB - 1; rb >= 0; --rb)
+        if (todo[rb]) n.a = __builtin_amdgcn_readlane(id[rb], __builtin_ctzll(todo[rb]));
+      if (n.a < 0) return n;
 #pragma unroll
       for (int rb = 0; rb < MB; ++rb) {
-        u32x4 hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
-        if (in && id[rb] == next) {
-          float v[8];
-          lora_u8(t, m0 + 32 * rb + j, r0, alpha, v);
-          split_hi_lo<DT>(v, hi, lo);
-        }
+        n.own[rb] = __ballot(id[rb] == n.a);
+        todo[rb] &= ~n.own[rb];
+      }
+      n.alpha = lora_alpha(t, n.a);
+    }
+    // (R is a multiple of 8: the upper half of a last k-sub may lie past it)
+    const bool in = n.r0 + 8 * h < t.R;
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb)
+      n.w[cb] = in ? *reinterpret_cast<const u32x4*>(up + ((size_t)n.a * N + row[cb]) * t.R + n.r0) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int rb = 0; rb < MB; ++rb)
+      if (n.own[rb]) {
+        const bool own = in && ((n.own[rb] >> lane) & 1);
+        const float* src = t.u + (size_t)(m0 + 32 * rb + j) * t.R + n.r0 + 8 * h;
+        n.u[rb][0] = own ? *reinterpret_cast<const f32x4*>(src) : f32x4{0.f, 0.f, 0.f, 0.f};
+        n.u[rb][1] = own ? *reinterpret_cast<const f32x4*>(src + 4) : f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+    return n;
+  };
+  auto multiply = [&](const Item& it) {
+#pragma unroll
+    for (int rb = 0; rb < MB; ++rb)
+      if (it.own[rb]) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = it.u[rb][e >> 2][e & 3] * it.alpha;
+        u32x4 hi, lo;
+        split_hi_lo<DT>(v, hi, lo);
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb) {
-          acc[rb][cb] = mfma32x32x16<DT>(a[cb], hi, acc[rb][cb]);
-          acc[rb][cb] = mfma32x32x16<DT>(a[cb], lo, acc[rb][cb]);
+          acc[rb][cb] = mfma32x32x16<DT>(it.w[cb], hi, acc[rb][cb]);
+          acc[rb][cb] = mfma32x32x16<DT>(it.w[cb], lo, acc[rb][cb]);
         }
       }
-    }
-    prev = next;
+  };
+  Item none{};
+  none.r0 = t.R;
+  Item p = next(none);
+  while (p.a >= 0) {
+    const Item q = next(p);
+    multiply(p);
+    if (q.a < 0) break;
+    p = next(q);
+    multiply(q);
   }
 }
 

@@ -34,8 +34,9 @@ __global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n
     }
     if (lane == 0) counts[wave] = below;
     __syncthreads();
-    int at = counts[0] + counts[1] + counts[2] + counts[3];
-    if (tid == 0) a.seg[s] = at;
+    const int before_all = counts[0] + counts[1] + counts[2] + counts[3];
+    const int first = (before_all + 31) / 32 * 32 + 32 * s;
+    int at = first;
     for (int m0 = 0; m0 < a.M; m0 += 256) {
       const int m = m0 + tid;
       const bool own = m < a.M && a.ids[m] == s;
@@ -48,10 +49,17 @@ __global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n
         before += w < wave ? counts[4 + w] : 0;
         all += counts[4 + w];
       }
-      if (own) a.perm[at + before + __popcll(mask & ((1ull << lane) - 1))] = m;
+      if (own) a.order[at + before + __popcll(mask & ((1ull << lane) - 1))] = m;
       at += all;
     }
-    if (s == a.S - 1 && tid == 0) a.seg[a.S] = at;
+    // nothing up to where the next adapter begins (the last: to the end; the
+    // first: from the beginning, which is its own)
+    const int next = s == a.S - 1 ? a.places : (before_all + (at - first) + 31) / 32 * 32 + 32 * (s + 1);
+    for (int i = at + tid; i < next; i += 256) a.order[i] = -1;
+    if (tid == 0) {
+      a.start[s] = first;
+      a.count[s] = at - first;
+    }
     return;
   }
   job -= a.S;
@@ -103,19 +111,77 @@ __global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n
   for (int i = tid; i < a.zero_words; i += 256) a.zero[i] = 0u;
 }
 
-// A workgroup owns 128 columns of one problem, 16 RC ranks, one adapter and a
-// range of its tokens; its four waves take steps of 32 tokens in turn.  The
-// tokens are the MFMA's reduction (16x16x32): a lane loads 8 columns of 8
-// tokens (16 bytes each) and pairs the tokens' halves with v_perm into the A
-// operands of its 8 columns; the B operand is its rank's 8 tokens of w as
-// value + remainder (split_hi_lo), so nothing is rounded but the result.
-// The waves are added through LDS in wave order; where an adapter has more
-// tokens than one workgroup takes, the ranges' fp32 sums go through the
-// workspace and the last to arrive adds them in range order.
+// Workgroups below row_blocks sum g's K ranges row by row; the others take 64
+// places of one problem each and transpose its rows through LDS into operands.
+template <int DT>
+__global__ __launch_bounds__(256) void operand_kernel(const OperandArgs a, int row_blocks, int place_blocks) {
+  __shared__ float lds[kMaxRank * (kTile + 1)];
+  const int tid = threadIdx.x;
+  const int64_t n = (int64_t)a.M * a.R;
+  if ((int)blockIdx.x < row_blocks) {
+    const int64_t i = ((int64_t)blockIdx.x * 256 + tid) * 4;
+    if (i >= n) return;
+    f32x4 v = *reinterpret_cast<const f32x4*>(a.part + i);
+    for (int s = 1; s < a.splits; ++s) v += *reinterpret_cast<const f32x4*>(a.part + s * n + i);
+    *reinterpret_cast<f32x4*>(a.g + i) = v;
+    return;
+  }
+  const int job = blockIdx.x - row_blocks;
+  const bool second = job >= place_blocks;
+  const int p0 = (job - (second ? place_blocks : 0)) * kTile;
+  for (int i = tid; i < kTile * (a.R / 4); i += 256) {
+    const int pl = i / (a.R / 4), r = 4 * (i - pl * (a.R / 4));
+    const int m = p0 + pl < a.places ? a.order[p0 + pl] : -1;
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
+    if (m >= 0) {
+      const float alpha = a.alpha ? a.alpha[a.ids[m]] : 1.f;
+      if (second) {
+        v = *reinterpret_cast<const f32x4*>(a.u + (size_t)m * a.R + r);
+      } else {
+        const float* src = a.part + (size_t)m * a.R + r;
+        v = *reinterpret_cast<const f32x4*>(src);
+        for (int s = 1; s < a.splits; ++s) v += *reinterpret_cast<const f32x4*>(src + s * n);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= alpha;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) lds[(r + e) * (kTile + 1) + pl] = v[e];
+  }
+  __syncthreads();
+  uint16_t* const out = second ? a.op[1] : a.op[0];
+  for (int i = tid; i < a.R * (kTile / 8); i += 256) {
+    const int r = i / (kTile / 8), pl = 8 * (i - r * (kTile / 8));
+    if (p0 + pl >= a.places) continue;  // places is a multiple of 32
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = lds[r * (kTile + 1) + pl + e];
+    u32x4 hi, lo;
+    split_hi_lo<DT>(v, hi, lo);
+    uint16_t* const d = out + (size_t)r * a.places + p0 + pl;
+    *reinterpret_cast<u32x4*>(d) = hi;
+    *reinterpret_cast<u32x4*>(d + (size_t)a.R * a.places) = lo;
+  }
+}
+
+// columns per lane: with 64 ranks, four (eight would spill the accumulators)
+constexpr int outer_cpl(int rc) { return rc == 4 ? 4 : 8; }
+
+// A workgroup owns 16 CPL columns of one problem, 16 RC ranks, one adapter and
+// a range of its tokens; its eight waves take steps of 32 places in turn.  The
+// tokens are the MFMA's reduction (16x16x32): a lane loads CPL columns of 8
+// tokens (a step later in flight) and pairs the tokens' halves with v_perm
+// into the A operands of its columns; the B operands, value and
+// remainder of w, come ready by rank and place.  Nothing is rounded but the
+// result.  The waves are added through four LDS buffers in two passes, always
+// in the same order; where an adapter has more tokens than one workgroup
+// takes, the ranges' fp32 sums go through the workspace and the last to arrive
+// adds them in range order.
 template <int DT, int RC>
-__global__ __launch_bounds__(256) void outer_kernel(const OuterArgs a, const OuterPlan pl) {
-  constexpr int BR = 16 * RC, LD = 128 + 4;
-  __shared__ __attribute__((aligned(16))) float sum[BR * LD];
+__global__ __launch_bounds__(512) void outer_kernel(const OuterArgs a, const OuterPlan pl) {
+  constexpr int CPL = outer_cpl(RC), BC = 16 * CPL, BR = 16 * RC, LD = BC + 4, WAVES = 8, STRIDE = 32 * WAVES;
+  typedef uint32_t cols_t __attribute__((ext_vector_type(CPL / 2)));
+  __shared__ __attribute__((aligned(16))) float sum[4 * BR * LD];
   __shared__ uint32_t last_flag;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -125,99 +191,144 @@ __global__ __launch_bounds__(256) void outer_kernel(const OuterArgs a, const Out
   const int tile = blockIdx.x - (second ? pl.tiles[0] : 0);
   const int s = blockIdx.y;
   const int split = blockIdx.z / pl.rgroups, rg = blockIdx.z - split * pl.rgroups;
-  const int start = a.seg[s], count = a.seg[s + 1] - start;
+  const int start = a.start[s], count = a.count[s];
   const int ranges = max(1, (count + pl.tokens - 1) / pl.tokens);
   if (split >= ranges) return;
   const int t_begin = start + split * pl.tokens, t_end = start + min(count, (split + 1) * pl.tokens);
-  const int c0 = tile * 128, r0 = rg * BR;
-  const float alpha = a.alpha ? a.alpha[s] : 1.f;
+  const int c0 = tile * BC, r0 = rg * BR;
 
-  f32x4 acc[8][RC];
+  f32x4 acc[CPL][RC];
 #pragma unroll
-  for (int t = 0; t < 8; ++t)
+  for (int t = 0; t < CPL; ++t)
 #pragma unroll
     for (int rc = 0; rc < RC; ++rc) acc[t][rc] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const uint16_t* vcol = p.v + min(c0 + 8 * col, p.ld - 8);
-  for (int t0 = t_begin + 32 * wave; t0 < t_end; t0 += 128) {
-    u32x4 v[8];
-    float w[RC][8];
+  const uint16_t* vcol = p.v + min(c0 + CPL * col, p.ld - CPL);
+  const uint16_t* wrow[RC];
+#pragma unroll
+  for (int rc = 0; rc < RC; ++rc) wrow[rc] = p.op + (size_t)min(r0 + 16 * rc + col, a.R - 1) * a.places;
+  const size_t lo_at = (size_t)a.R * a.places;
+
+  // places of an adapter's last step past its tokens are -1: their v is zero
+  struct Step {
+    int m[8];
+    cols_t v[8];
+    u32x4 hi[RC], lo[RC];
+  };
+  auto load = [&](int t0, Step& st) {
+    const int4 m0 = *reinterpret_cast<const int4*>(a.order + t0 + 8 * q);
+    const int4 m1 = *reinterpret_cast<const int4*>(a.order + t0 + 8 * q + 4);
+    const int m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int i = t0 + 8 * q + e;
-      const bool in = i < t_end;
-      const int m = a.perm[in ? i : t_end - 1];
-      v[e] = *reinterpret_cast<const u32x4*>(vcol + (size_t)m * p.ld);
-      if (!in) v[e] = u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int rc = 0; rc < RC; ++rc) {
-        const int r = r0 + 16 * rc + col;
-        w[rc][e] = in && r < a.R ? p.w[(size_t)m * a.R + r] * alpha : 0.f;
-      }
+      st.m[e] = m[e];
+      st.v[e] = *reinterpret_cast<const cols_t*>(vcol + (size_t)max(m[e], 0) * p.ld);
     }
-    u32x4 hi[RC], lo[RC];
 #pragma unroll
-    for (int rc = 0; rc < RC; ++rc) split_hi_lo<DT>(w[rc], hi[rc], lo[rc]);
+    for (int rc = 0; rc < RC; ++rc) {
+      st.hi[rc] = *reinterpret_cast<const u32x4*>(wrow[rc] + t0 + 8 * q);
+      st.lo[rc] = *reinterpret_cast<const u32x4*>(wrow[rc] + lo_at + t0 + 8 * q);
+    }
+  };
+  auto multiply = [&](Step& st, bool last) {
+    if (last) {  // wave-uniform: only an adapter's last step holds empty places
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
+      for (int e = 0; e < 8; ++e)
+        if (st.m[e] < 0) st.v[e] = cols_t{};
+    }
+#pragma unroll
+    for (int t = 0; t < CPL; ++t) {
       const uint32_t sel = (t & 1) ? 0x07060302u : 0x05040100u;
-      const u32x4 f = {__builtin_amdgcn_perm(v[1][t >> 1], v[0][t >> 1], sel),
-                       __builtin_amdgcn_perm(v[3][t >> 1], v[2][t >> 1], sel),
-                       __builtin_amdgcn_perm(v[5][t >> 1], v[4][t >> 1], sel),
-                       __builtin_amdgcn_perm(v[7][t >> 1], v[6][t >> 1], sel)};
+      const u32x4 f = {__builtin_amdgcn_perm(st.v[1][t >> 1], st.v[0][t >> 1], sel),
+                       __builtin_amdgcn_perm(st.v[3][t >> 1], st.v[2][t >> 1], sel),
+                       __builtin_amdgcn_perm(st.v[5][t >> 1], st.v[4][t >> 1], sel),
+                       __builtin_amdgcn_perm(st.v[7][t >> 1], st.v[6][t >> 1], sel)};
 #pragma unroll
       for (int rc = 0; rc < RC; ++rc) {
-        acc[t][rc] = mfma16x16x32<DT>(f, hi[rc], acc[t][rc]);
-        acc[t][rc] = mfma16x16x32<DT>(f, lo[rc], acc[t][rc]);
+        acc[t][rc] = mfma16x16x32<DT>(f, st.hi[rc], acc[t][rc]);
+        acc[t][rc] = mfma16x16x32<DT>(f, st.lo[rc], acc[t][rc]);
       }
     }
-  }
-  // acc[t][rc][e]: column 8 (4 q + e) + t, rank 16 rc + col
-  for (int w = 0; w < 4; ++w) {
-    if (wave == w) {
-#pragma unroll
-      for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int rc = 0; rc < RC; ++rc)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float* d = sum + (16 * rc + col) * LD + 8 * (4 * q + e) + t;
-            *d = w == 0 ? acc[t][rc][e] : *d + acc[t][rc][e];
-          }
+  };
+  int t0 = t_begin + 32 * wave;
+  if (t0 < t_end) {
+    Step x, y;
+    load(t0, x);
+    for (;;) {
+      if (t0 + STRIDE < t_end) load(t0 + STRIDE, y);
+      multiply(x, t0 + 32 > t_end);
+      t0 += STRIDE;
+      if (t0 >= t_end) break;
+      if (t0 + STRIDE < t_end) load(t0 + STRIDE, x);
+      multiply(y, t0 + 32 > t_end);
+      t0 += STRIDE;
+      if (t0 >= t_end) break;
     }
-    __syncthreads();
   }
+  // acc[t][rc][e]: column CPL (4 q + e) + t, rank 16 rc + col
+  auto put = [&](bool add) {
+    float* const buf = sum + (wave & 3) * (BR * LD);
+#pragma unroll
+    for (int rc = 0; rc < RC; ++rc)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int half = 0; half < CPL / 4; ++half) {
+          f32x4* d = reinterpret_cast<f32x4*>(buf + (16 * rc + col) * LD + CPL * (4 * q + e) + 4 * half);
+          f32x4 v = {acc[4 * half][rc][e], acc[4 * half + 1][rc][e], acc[4 * half + 2][rc][e], acc[4 * half + 3][rc][e]};
+          if (add) v = *d + v;
+          *d = v;
+        }
+  };
+  if (wave < 4) put(false);
+  __syncthreads();
+  if (wave >= 4) put(true);
+  __syncthreads();
+  auto total = [&](int r, int c) {
+    const float* d = sum + r * LD + c;
+    return (d[0] + d[BR * LD]) + (d[2 * BR * LD] + d[3 * BR * LD]);
+  };
   if (ranges > 1) {
     // slots of an adapter with several ranges: from 2 floor(start / tokens),
-    // which no other such adapter reaches (ceil(c / t) <= 2 floor(c / t), c > t)
+    // which no other such adapter reaches (ceil(c / t) <= 2 floor(c / t) where
+    // c > t, and starts are at least their adapters' tokens apart)
     const size_t tiles = (size_t)(pl.tiles[0] + pl.tiles[1]) * pl.rgroups;
     const size_t place = (size_t)blockIdx.x * pl.rgroups + rg;
     const size_t slot = 2 * (size_t)(start / pl.tokens);
-    float* const mine = a.partial + ((slot + split) * tiles + place) * (BR * 128);
-    for (int i = tid; i < BR * 128; i += 256) store_coherent(mine + i, sum[(i >> 7) * LD + (i & 127)]);
+    float* const mine = a.partial + ((slot + split) * tiles + place) * (BR * BC);
+    for (int i = tid; i < BR * BC; i += 512) store_coherent(mine + i, total(i / BC, i % BC));
     wait_vm_all();  // every store of this thread has completed before the arrival
     __syncthreads();
     uint32_t* const counter = a.counters + (size_t)s * tiles + place;
     if (tid == 0) last_flag = arrive(counter) == (uint32_t)(ranges - 1);
     __syncthreads();
     if (!last_flag) return;
-    for (int i = tid; i < BR * 128; i += 256) {
+    for (int i = tid; i < BR * BC; i += 512) {
       float v = 0.f;
-      for (int sp = 0; sp < ranges; ++sp) v += load_coherent(a.partial + ((slot + sp) * tiles + place) * (BR * 128) + i);
-      sum[(i >> 7) * LD + (i & 127)] = v;
+      for (int sp = 0; sp < ranges; ++sp) v += load_coherent(a.partial + ((slot + sp) * tiles + place) * (BR * BC) + i);
+      float* d = sum + (i / BC) * LD + i % BC;
+      d[0] = v;
+      d[BR * LD] = d[2 * BR * LD] = d[3 * BR * LD] = 0.f;
     }
     __syncthreads();
   }
   if (p.by_rank) {
-    for (int i = tid; i < BR * 128; i += 256) {
-      const int r = i >> 7, c = i & 127;
-      if (r0 + r < a.R && c0 + c < p.C)
-        p.out[((size_t)s * a.R + r0 + r) * p.C + c0 + c] = f32_to_act<DT>(sum[r * LD + c]);
+    for (int i = tid; i < BR * (BC / 8); i += 512) {
+      const int r = i / (BC / 8), c = 8 * (i % (BC / 8));
+      if (r0 + r >= a.R || c0 + c >= p.C) continue;
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = f32x2_to_act_pair<DT>(total(r, c + 2 * e), total(r, c + 2 * e + 1));
+      // C is K here, a multiple of 32
+      *reinterpret_cast<u32x4*>(p.out + ((size_t)s * a.R + r0 + r) * p.C + c0 + c) = u32x4{w[0], w[1], w[2], w[3]};
     }
   } else {
-    for (int i = tid; i < BR * 128; i += 256) {
-      const int c = i / BR, r = i - c * BR;
-      if (r0 + r < a.R && c0 + c < p.C)
-        p.out[((size_t)s * p.C + c0 + c) * a.R + r0 + r] = f32_to_act<DT>(sum[r * LD + c]);
+    for (int i = tid; i < BC * (BR / 8); i += 512) {
+      const int r = 8 * (i / BC), c = i % BC;
+      if (r0 + r >= a.R || c0 + c >= p.C) continue;
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = f32x2_to_act_pair<DT>(total(r + 2 * e, c), total(r + 2 * e + 1, c));
+      *reinterpret_cast<u32x4*>(p.out + ((size_t)s * p.C + c0 + c) * a.R + r0 + r) = u32x4{w[0], w[1], w[2], w[3]};
     }
   }
 }
@@ -233,22 +344,33 @@ hipError_t launch_prep(const PrepArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+hipError_t launch_operands(const OperandArgs& a, hipStream_t s) {
+  const int row_blocks = (int)(((int64_t)a.M * a.R / 4 + 255) / 256), place_blocks = (a.places + kTile - 1) / kTile;
+  auto kern = a.dtype == DT_F16 ? operand_kernel<DT_F16> : operand_kernel<DT_BF16>;
+  hipLaunchKernelGGL(kern, dim3(row_blocks + 2 * place_blocks), dim3(256), 0, s, a, row_blocks, place_blocks);
+  return hipGetLastError();
+}
+
 OuterPlan plan_outer(int64_t M, int64_t C0, int64_t C1, int S, int R, int cu_count) {
   OuterPlan p;
   const int blocks = (R + 15) / 16;
   p.rc = blocks > 2 ? 4 : blocks;
   p.rgroups = (blocks + p.rc - 1) / p.rc;
-  p.tiles[0] = (int)((C0 + 127) / 128);
-  p.tiles[1] = (int)((C1 + 127) / 128);
-  // about two workgroups per CU when one adapter has all tokens
-  const int64_t want = std::max<int64_t>(1, 2 * cu_count / ((int64_t)(p.tiles[0] + p.tiles[1]) * p.rgroups));
-  p.tokens = (int)std::max<int64_t>(128, (M / want + 127) / 128 * 128);
+  const int cols = 16 * outer_cpl(p.rc);
+  p.tiles[0] = (int)((C0 + cols - 1) / cols);
+  p.tiles[1] = (int)((C1 + cols - 1) / cols);
+  // about one workgroup per CU when one adapter has all tokens (a range costs
+  // its sums' round trip through memory)
+  const int64_t want = std::max<int64_t>(1, cu_count / ((int64_t)(p.tiles[0] + p.tiles[1]) * p.rgroups));
+  p.tokens = (int)std::max<int64_t>(256, (M / want + 255) / 256 * 256);
   p.splits = (int)((M + p.tokens - 1) / p.tokens);
   return p;
 }
-size_t outer_partial_bytes(const OuterPlan& p, int64_t M) {
+size_t outer_partial_bytes(const OuterPlan& p, int64_t places) {
   if (p.splits <= 1) return 0;
-  return (size_t)(2 * (M / p.tokens) + 2 + p.splits) * (size_t)(p.tiles[0] + p.tiles[1]) * p.rgroups * (16 * p.rc * 128) * sizeof(float);
+  // starts lie below order_places(M, S): 32 per adapter past the tokens, and an
+  // adapter of several ranges has more than `tokens` >= 256 of them
+  return (size_t)(2 * (places / p.tokens) + 2 + p.splits) * (size_t)(p.tiles[0] + p.tiles[1]) * p.rgroups * (16 * p.rc * 16 * outer_cpl(p.rc)) * sizeof(float);
 }
 size_t outer_counter_bytes(const OuterPlan& p, int S) {
   return (size_t)S * (size_t)(p.tiles[0] + p.tiles[1]) * p.rgroups * sizeof(uint32_t);
@@ -258,7 +380,7 @@ hipError_t launch_outer(const OuterArgs& a, const OuterPlan& p, hipStream_t s) {
   if (a.S > 65535 || (int64_t)p.splits * p.rgroups > 65535) return hipErrorInvalidValue;
   const dim3 grid(p.tiles[0] + p.tiles[1], a.S, p.splits * p.rgroups);
   auto go = [&](auto kern) {
-    hipLaunchKernelGGL(kern, grid, dim3(256), 0, s, a, p);
+    hipLaunchKernelGGL(kern, grid, dim3(512), 0, s, a, p);
     return hipGetLastError();
   };
   if (a.dtype == DT_F16)

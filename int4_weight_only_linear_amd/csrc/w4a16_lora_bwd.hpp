@@ -6,12 +6,16 @@
 
 namespace w4a16 {
 
-// Tokens in the order of their adapters: seg[s] .. seg[s + 1] are the places
-// in perm of the tokens of adapter s, in token order.
+// Tokens in the order of their adapters: the places start[s] ..
+// start[s] + count[s] of `order` hold the tokens of adapter s, in token order.
+// start[s] = round32(tokens of smaller adapters) + 32 s, a multiple of 32 that
+// every adapter's workgroup can form by itself; places between are -1.
+inline int64_t order_places(int64_t M, int64_t S) { return (M + 31) / 32 * 32 + 32 * S; }
 struct PrepArgs {
   const int32_t* ids;
-  int32_t* perm;        // [M]
-  int32_t* seg;         // [S + 1]
+  int32_t* order;       // [order_places(M, S)]
+  int32_t* start;       // [S]
+  int32_t* count;       // [S]
   const uint16_t* la;   // [S][R][K]
   const uint16_t* lb;   // [S][N][R]
   uint16_t* la_t;       // [S][K][R]
@@ -20,34 +24,48 @@ struct PrepArgs {
   uint16_t* dy_pad;     // [M][np], zero past N; NULL: dy's rows are used as they are
   uint32_t* zero;       // zero_words words set to zero
   int zero_words;
-  int M, N, K, S, R, np;
+  int M, N, K, S, R, np, places;
 };
 hipError_t launch_prep(const PrepArgs& a, hipStream_t s);
 
-// out_s[c, r] = sum over the tokens m of adapter s of v[m, c] * alpha_s * w[m, r]
+// g[m][r] = sum of its K ranges, and alpha * g and alpha * u as MFMA operands:
+// value and remainder in the activation dtype (split_hi_lo), by rank and place
+struct OperandArgs {
+  const float* part;    // [splits][M][R]
+  const float* u;       // [M][R]
+  const int32_t* ids;
+  const int32_t* order;
+  const float* alpha;   // [S] or NULL
+  float* g;             // [M][R]
+  uint16_t* op[2];      // of g and of u: [2][R][places]
+  int M, R, splits, places, dtype;
+};
+hipError_t launch_operands(const OperandArgs& a, hipStream_t s);
+
+// out_s[c, r] = sum over the tokens m of adapter s of v[m, c] * w[m, r]
 struct OuterProblem {
-  const uint16_t* v;  // [M][ld]
-  const float* w;     // [M][R]
-  uint16_t* out;      // [S][R][C] (by_rank) or [S][C][R]
+  const uint16_t* v;   // [M][ld]
+  const uint16_t* op;  // [2][R][places]
+  uint16_t* out;       // [S][R][C] (by_rank) or [S][C][R]
   int ld, C, by_rank;
 };
 struct OuterArgs {
   OuterProblem p[2];
-  const int32_t* perm;
-  const int32_t* seg;
-  const float* alpha;  // [S] or NULL
+  const int32_t* order;
+  const int32_t* start;
+  const int32_t* count;
   float* partial;
-  uint32_t* counters;  // outer_counters(...) zeros
-  int M, S, R, dtype;
+  uint32_t* counters;  // outer_counter_bytes(...) of zeros
+  int M, S, R, places, dtype;
 };
 struct OuterPlan {
-  int tokens;        // of one workgroup, a multiple of 128
+  int tokens;        // of one workgroup, a multiple of 256
   int splits;        // token ranges at most
   int rc, rgroups;   // 16-rank blocks of a workgroup, groups of them
-  int tiles[2];      // 128-column tiles of the two problems
+  int tiles[2];      // column tiles of the two problems
 };
 OuterPlan plan_outer(int64_t M, int64_t C0, int64_t C1, int S, int R, int cu_count);
-size_t outer_partial_bytes(const OuterPlan& p, int64_t M);
+size_t outer_partial_bytes(const OuterPlan& p, int64_t places);
 size_t outer_counter_bytes(const OuterPlan& p, int S);
 hipError_t launch_outer(const OuterArgs& a, const OuterPlan& p, hipStream_t s);
 
