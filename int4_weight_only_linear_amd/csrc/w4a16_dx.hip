@@ -228,7 +228,7 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
     }
     if (s < s_end) multiply(w0, d0);
   }
-  if (split == 0 && lora.ids) lora_steps<DT, MW, 4>(lora, p.M, p.K, m0 + 32 * MW * wm, k0 + 128 * wk, lane, acc);
+  lora_steps<DT, MW, 4>(lora, p.M, p.K, m0 + 32 * MW * wm, k0 + 128 * wk, lane, split, p.splits, acc);
 
   // acc[mb][kb][4a + e]: token m0 + 32 (MW wm + mb) + j, k = k0 + 128 wk + 32 kb + 8a + 4h + e
 #pragma unroll

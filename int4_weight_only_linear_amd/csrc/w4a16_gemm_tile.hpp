@@ -470,10 +470,9 @@ __device__ __forceinline__ void gemm_tile(const GemmParams& p, const LoraTerm& l
     compute_tail(buf0, ra, (p.K - s * kBK) / 16);
   }
 
-  // ---- adapters beside the projection: more k of the same product, in the
-  // first K range's accumulators
-  if constexpr (LORA)
-    if (split == 0) lora_steps<DT, MB, CB>(lora, p.M, p.N, m0, nw0, lane, acc);
+  // ---- adapters beside the projection: more k of the same product, spread
+  // over the K ranges' accumulators
+  if constexpr (LORA) lora_steps<DT, MB, CB>(lora, p.M, p.N, m0, nw0, lane, split, p.splits, acc);
 
   // ---- split-K: store the partial tile; the last unit of the tile sums them
   // in split order (cross-workgroup hand-off as described at store_coherent).

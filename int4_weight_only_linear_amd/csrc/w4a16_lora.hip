@@ -124,8 +124,15 @@ __global__ __launch_bounds__(256) void shrink_reduce_kernel(const float* __restr
                                                             int64_t n, int splits) {
   const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
   if (i >= n) return;
-  f32x4 v = *reinterpret_cast<const f32x4*>(part + i);
-  for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(part + s * n + i);
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < splits; s0 += 4) {  // four at a time, so that their loads overlap
+    f32x4 p[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) p[k] = *reinterpret_cast<const f32x4*>(part + min(s0 + k, splits - 1) * n + i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (s0 + k < splits) v += p[k];
+  }
   *reinterpret_cast<f32x4*>(u + i) = v;
 }
 

@@ -86,14 +86,18 @@ __device__ __forceinline__ void split_hi_lo(const float (&v)[8], u32x4& hi, u32x
 // that a token of the tile names (in the order of their first tokens),
 // ceil(R / 16) k-subs whose A operand is the wave's rows of up_a and whose B
 // operand is alpha * u of the adapter's own tokens, zero for the others; token
-// blocks without such a token are left out.  The operands of the next k-sub
-// are loaded while one is multiplied (a tile of many adapters is a chain of
-// them, each a memory round trip otherwise: 16 adapters of rank 32 among 67
-// tokens 48 -> 26 us).
+// blocks without such a token are left out.  The K ranges of a split tile take
+// the adapters in turns, and the operands of the next two k-subs are loaded
+// while two are multiplied: a tile of many adapters is otherwise a chain of
+// memory round trips (16 adapters of rank 32 among 67 tokens, 19456 x 2560:
+// 28 us of 48, now 11 of 31).  The tall tiles (MB > 4), whose accumulators
+// leave few registers and whose tokens are mostly of one request, take one
+// k-sub at a time.
 //   acc[rb][cb]: tokens m0 + 32 rb + (lane & 31), features nw0 + 32 cb + ...
 template <int DT, int MB, int CB>
-__device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int m0, int nw0, int lane,
+__device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int m0, int nw0, int lane, int turn, int turns,
                                            f32x16 (&acc)[MB][CB]) {
+  constexpr int KS = MB <= 4 ? 2 : 1;  // k-subs of an item
   const int j = lane & 31, h = lane >> 5;
   int id[MB];
   uint64_t todo[MB];
@@ -106,70 +110,85 @@ __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int 
   uint32_t row[CB];
 #pragma unroll
   for (int cb = 0; cb < CB; ++cb) row[cb] = (uint32_t)min(nw0 + 32 * cb + j, N - 1);
+  int count = 0;  // adapters of the tile seen so far
 
   struct Item {
     int a, r0;           // adapter (-1: no more), first rank (of both halves)
     uint64_t own[MB];    // lanes whose token is the adapter's
     float alpha;
-    u32x4 w[CB];
-    f32x4 u[MB][2];
+    u32x4 w[KS][CB];
+    f32x4 u[KS][MB][2];
   };
   // the item after `it`: the next ranks of its adapter, or the next adapter
   auto next = [&](const Item& it) {
     Item n;
     n.a = it.a;
-    n.r0 = it.r0 + 16;
+    n.r0 = it.r0 + 16 * KS;
     n.alpha = it.alpha;
 #pragma unroll
     for (int rb = 0; rb < MB; ++rb) n.own[rb] = it.own[rb];
     if (n.r0 >= t.R) {
-      n.a = -1;
       n.r0 = 0;
+      do {
+        n.a = -1;
 #pragma unroll
-      for (int rb = MB - 1; rb >= 0; --rb)
-        if (todo[rb]) n.a = __builtin_amdgcn_readlane(id[rb], __builtin_ctzll(todo[rb]));
-      if (n.a < 0) return n;
+        for (int rb = MB - 1; rb >= 0; --rb)
+          if (todo[rb]) n.a = __builtin_amdgcn_readlane(id[rb], __builtin_ctzll(todo[rb]));
+        if (n.a < 0) return n;
 #pragma unroll
-      for (int rb = 0; rb < MB; ++rb) {
-        n.own[rb] = __ballot(id[rb] == n.a);
-        todo[rb] &= ~n.own[rb];
-      }
+        for (int rb = 0; rb < MB; ++rb) {
+          n.own[rb] = __ballot(id[rb] == n.a);
+          todo[rb] &= ~n.own[rb];
+        }
+      } while (count++ % turns != turn);
       n.alpha = lora_alpha(t, n.a);
     }
-    // (R is a multiple of 8: the upper half of a last k-sub may lie past it)
-    const bool in = n.r0 + 8 * h < t.R;
+    // (R is a multiple of 8: a last k-sub may lie past it, wholly or its upper half)
 #pragma unroll
-    for (int cb = 0; cb < CB; ++cb)
-      n.w[cb] = in ? *reinterpret_cast<const u32x4*>(up + ((size_t)n.a * N + row[cb]) * t.R + n.r0) : u32x4{0u, 0u, 0u, 0u};
+    for (int ks = 0; ks < KS; ++ks) {
+      const int r = n.r0 + 16 * ks;
+      const bool in = r + 8 * h < t.R;
 #pragma unroll
-    for (int rb = 0; rb < MB; ++rb)
-      if (n.own[rb]) {
-        const bool own = in && ((n.own[rb] >> lane) & 1);
-        const float* src = t.u + (size_t)(m0 + 32 * rb + j) * t.R + n.r0 + 8 * h;
-        n.u[rb][0] = own ? *reinterpret_cast<const f32x4*>(src) : f32x4{0.f, 0.f, 0.f, 0.f};
-        n.u[rb][1] = own ? *reinterpret_cast<const f32x4*>(src + 4) : f32x4{0.f, 0.f, 0.f, 0.f};
-      }
+      for (int cb = 0; cb < CB; ++cb)
+        n.w[ks][cb] = in ? *reinterpret_cast<const u32x4*>(up + ((size_t)n.a * N + row[cb]) * t.R + r) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int rb = 0; rb < MB; ++rb)
+        if (n.own[rb]) {
+          const bool own = in && ((n.own[rb] >> lane) & 1);
+          const float* src = t.u + (size_t)(m0 + 32 * rb + j) * t.R + r + 8 * h;
+          n.u[ks][rb][0] = own ? *reinterpret_cast<const f32x4*>(src) : f32x4{0.f, 0.f, 0.f, 0.f};
+          n.u[ks][rb][1] = own ? *reinterpret_cast<const f32x4*>(src + 4) : f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+    }
     return n;
   };
   auto multiply = [&](const Item& it) {
 #pragma unroll
-    for (int rb = 0; rb < MB; ++rb)
-      if (it.own[rb]) {
-        float v[8];
+    for (int ks = 0; ks < KS; ++ks) {
+      if (it.r0 + 16 * ks >= t.R) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = it.u[rb][e >> 2][e & 3] * it.alpha;
-        u32x4 hi, lo;
-        split_hi_lo<DT>(v, hi, lo);
+      for (int rb = 0; rb < MB; ++rb)
+        if (it.own[rb]) {
+          float v[8];
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb) {
-          acc[rb][cb] = mfma32x32x16<DT>(it.w[cb], hi, acc[rb][cb]);
-          acc[rb][cb] = mfma32x32x16<DT>(it.w[cb], lo, acc[rb][cb]);
+          for (int e = 0; e < 8; ++e) v[e] = it.u[ks][rb][e >> 2][e & 3] * it.alpha;
+          u32x4 hi, lo;
+          split_hi_lo<DT>(v, hi, lo);
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb) {
+            acc[rb][cb] = mfma32x32x16<DT>(it.w[ks][cb], hi, acc[rb][cb]);
+            acc[rb][cb] = mfma32x32x16<DT>(it.w[ks][cb], lo, acc[rb][cb]);
+          }
         }
-      }
+    }
   };
   Item none{};
   none.r0 = t.R;
   Item p = next(none);
+  if constexpr (MB > 4) {
+    for (; p.a >= 0; p = next(p)) multiply(p);
+    return;
+  }
   while (p.a >= 0) {
     const Item q = next(p);
     multiply(p);

@@ -113,6 +113,20 @@ __global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n
 
 // Workgroups below row_blocks sum g's K ranges row by row; the others take 64
 // places of one problem each and transpose its rows through LDS into operands.
+// (the sum over K ranges, four at a time so that their loads overlap)
+__device__ __forceinline__ f32x4 sum_ranges(const float* src, int64_t plane, int splits) {
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < splits; s0 += 4) {
+    f32x4 p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const f32x4*>(src + min(s0 + i, splits - 1) * plane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (s0 + i < splits) v += p[i];
+  }
+  return v;
+}
+
 template <int DT>
 __global__ __launch_bounds__(256) void operand_kernel(const OperandArgs a, int row_blocks, int place_blocks) {
   __shared__ float lds[kMaxRank * (kTile + 1)];
@@ -121,9 +135,7 @@ __global__ __launch_bounds__(256) void operand_kernel(const OperandArgs a, int r
   if ((int)blockIdx.x < row_blocks) {
     const int64_t i = ((int64_t)blockIdx.x * 256 + tid) * 4;
     if (i >= n) return;
-    f32x4 v = *reinterpret_cast<const f32x4*>(a.part + i);
-    for (int s = 1; s < a.splits; ++s) v += *reinterpret_cast<const f32x4*>(a.part + s * n + i);
-    *reinterpret_cast<f32x4*>(a.g + i) = v;
+    *reinterpret_cast<f32x4*>(a.g + i) = sum_ranges(a.part + i, n, a.splits);
     return;
   }
   const int job = blockIdx.x - row_blocks;
@@ -135,13 +147,8 @@ __global__ __launch_bounds__(256) void operand_kernel(const OperandArgs a, int r
     f32x4 v = {0.f, 0.f, 0.f, 0.f};
     if (m >= 0) {
       const float alpha = a.alpha ? a.alpha[a.ids[m]] : 1.f;
-      if (second) {
-        v = *reinterpret_cast<const f32x4*>(a.u + (size_t)m * a.R + r);
-      } else {
-        const float* src = a.part + (size_t)m * a.R + r;
-        v = *reinterpret_cast<const f32x4*>(src);
-        for (int s = 1; s < a.splits; ++s) v += *reinterpret_cast<const f32x4*>(src + s * n);
-      }
+      v = second ? *reinterpret_cast<const f32x4*>(a.u + (size_t)m * a.R + r)
+                 : sum_ranges(a.part + (size_t)m * a.R + r, n, a.splits);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] *= alpha;
     }
