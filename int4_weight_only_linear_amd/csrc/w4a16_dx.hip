@@ -14,7 +14,7 @@
 // time: every thread dequantises one block into LDS, where the waves (each 32
 // MW tokens x 128 k) read them as A operands; dy is staged as B operands by
 // direct global->LDS loads.  Both are double buffered, the words of the step
-// after next in registers, and one barrier ends a step.  Each weight is
+// after next in registers, and a step has one barrier.  Each weight is
 // dequantised once per workgroup.
 #include <algorithm>
 
@@ -38,8 +38,11 @@ struct DxParams {
   const uint32_t* wq;
   const uint16_t* scales;
   const uint32_t* zp;
+  const uint32_t* wq_tail;  // the tail copy (DxArgs), of step tail_step (-1: none)
+  const uint16_t* scales_tail;
+  const uint32_t* zp_tail;
+  int tail_step;
   uint16_t* dx;
-  const void* zeros;
   float* partial;
   int M, N, K, ldy;
   int sG, gmul;
@@ -80,58 +83,62 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
   const int s_begin = split * p.steps_per_split;
   const int s_end = min(p.nsteps, s_begin + p.steps_per_split);
 
-  // ---- dy: load d of this wave fills LDS rows (wave NDMA + d) 8 + lane / 8;
-  // position lane & 7 of a row holds its piece pos ^ (row & 7)
-  const uint16_t* dyrow[NDMA];
-  const int piece = (lane & 7) ^ ((lane >> 3) & 7);
+  // ---- dy (rows of a multiple of 64 values, zero past N): load d of this wave
+  // fills LDS rows (wave NDMA + d) 8 + lane / 8; position lane & 7 of a row
+  // holds its piece pos ^ (row / 2 & 7)
+  const char* const dytile = reinterpret_cast<const char*>(p.dy + (size_t)m0 * p.ldy);
+  uint32_t dyoff[NDMA];  // (NDMA is even)
 #pragma unroll
-  for (int d = 0; d < NDMA; ++d)
-    dyrow[d] = p.dy + (size_t)min(m0 + (wave * NDMA + d) * 8 + (lane >> 3), p.M - 1) * p.ldy + 8 * piece;
+  for (int d = 0; d < NDMA; ++d) {
+    const int row = min((wave * NDMA + d) * 8 + (lane >> 3), p.M - 1 - m0);
+    dyoff[d] = (uint32_t)row * (uint32_t)p.ldy * 2u + 16u * (uint32_t)((lane & 7) ^ (4 * (d & 1) + (lane >> 4)));
+  }
   auto stage_dy = [&](int s, lds_u8* buf) {
-    const bool in = s * kBN + 8 * piece < p.ldy;  // (dy is zero from N up to ldy)
+    const char* base = dytile + (size_t)s * (kBN * 2);
 #pragma unroll
-    for (int d = 0; d < NDMA; ++d) {
-      const void* src = in ? static_cast<const void*>(dyrow[d] + s * kBN) : p.zeros;
-      __builtin_amdgcn_global_load_lds(src, buf + (wave * NDMA + d) * 1024, 16, 0, 0);
-    }
+    for (int d = 0; d < NDMA; ++d)
+      __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(base + dyoff[d]), buf + (wave * NDMA + d) * 1024, 16, 0, 0);
   };
 
-  // ---- weights: this thread's block is rows 8 o.. of the step, slice c of the tile
+  // ---- weights: this thread's block is rows 8 o.. of the step, slice c of the
+  // tile; row i's word is woff + i wstride from the step's first (a complete
+  // run keeps a tile's rows 16 bytes apart, an incomplete last one back to
+  // back).  A last step that N ends inside comes from the tail copy, where it
+  // is whole.
   const int c = tid & 31, o = tid >> 5;
   const int slice = min((k0 >> 3) + c, p.wpr - 1);
-  const int g = (8 * slice) / GS * p.gmul;
   const int runs = p.wpr >> 4, tail = p.wpr & 15;
   const bool full_run = (slice >> 4) < runs;
-  const int sl = slice & 15;
-  // place of the slice in a complete tile of 16 rows, and in a row kept alone
-  const uint32_t in_tile = full_run ? 256u * (uint32_t)(slice >> 4) + 64u * (uint32_t)(sl & 3) + (uint32_t)(sl >> 2)
-                                    : 256u * (uint32_t)runs + (uint32_t)(slice - 16 * runs);
-  const uint32_t tile_stride = full_run ? 4u : (uint32_t)tail;
-  const uint32_t in_row = full_run ? (uint32_t)(slice - sl) + 4u * (uint32_t)(sl & 3) + (uint32_t)(sl >> 2) : (uint32_t)slice;
+  const uint32_t wstride = full_run ? 16u : 4u * (uint32_t)tail;
+  const uint32_t woff = 64u * (uint32_t)p.wpr * (uint32_t)(o >> 1) + 8u * (uint32_t)(o & 1) * wstride +
+                        4u * (full_run ? 256u * (uint32_t)(slice >> 4) + 64u * (uint32_t)(slice & 3) + (uint32_t)((slice & 15) >> 2)
+                                       : 256u * (uint32_t)runs + (uint32_t)(slice - 16 * runs));
+  const uint32_t goff = (uint32_t)((8 * slice) / GS * p.gmul);
+  const uint32_t soff = 2u * ((uint32_t)(8 * o * p.sG) + goff), zoff = 4u * ((uint32_t)(o * p.sG) + goff);
   auto load_block = [&](int s, Block& b) {
-    const int n = s * kBN + 8 * o;
-    const bool whole = (n | 15) < p.N;  // the block's 16-row tile is complete
-    const uint32_t row16 = (uint32_t)(n & ~15);
+    const bool at_tail = s == p.tail_step;  // wave-uniform
+    const char* wb = reinterpret_cast<const char*>(at_tail ? p.wq_tail : p.wq + (size_t)s * kBN * (size_t)p.wpr);
+    const char* sb = reinterpret_cast<const char*>(at_tail ? p.scales_tail : p.scales + (size_t)s * kBN * (size_t)p.sG);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t at = whole ? row16 * (uint32_t)p.wpr + in_tile + (uint32_t)((n & 8) + i) * tile_stride
-                                : (uint32_t)min(n + i, p.N - 1) * (uint32_t)p.wpr + in_row;
-      b.w[i] = p.wq[at];
-    }
+    for (int i = 0; i < 8; ++i) b.w[i] = *reinterpret_cast<const uint32_t*>(wb + (woff + i * wstride));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = min(n + i, p.N - 1);
-      b.s[i] = p.scales[(size_t)r * p.sG + g];
-      if (n + i >= p.N) b.s[i] = 0;  // rows past N weigh nothing
-    }
-    if constexpr (ASYM) b.z = p.zp[(size_t)(min(n, p.N - 1) >> 3) * p.sG + g];
+    for (int i = 0; i < 8; ++i) b.s[i] = *reinterpret_cast<const uint16_t*>(sb + (size_t)(2 * i) * (size_t)p.sG + soff);
+    if constexpr (ASYM)
+      b.z = *reinterpret_cast<const uint32_t*>(
+          reinterpret_cast<const char*>(at_tail ? p.zp_tail : p.zp + (size_t)s * (kBN / 8) * (size_t)p.sG) + zoff);
   };
-  // the block's eight operands (k = 0..7 of the slice) at [octet o][slice c][k ^ (c & 7)]
-  auto put_block = [&](const Block& b, lds_u8* buf) {
-    uint32_t out[8][4];
+  // Half of the block's operands: k = 0, 1, 4, 5 (part 0) or 2, 3, 6, 7 of the
+  // slice -- the even or odd nibbles of the paired words -- each 16 bytes at
+  // [octet o][slice c][k ^ (c / 2 & 7)]: sixteen lanes in a row,
+  // writing (slices c) or reading (k of two slices), touch sixteen banks of 16
+  // bytes.
+  typedef __attribute__((address_space(3))) u32x4 lds_out;
+  auto put_half = [&](const Block& b, lds_u8* buf, int part) {
+    uint32_t out[4][4];  // [k of the part][row pair]
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const uint32_t z0 = ASYM ? (b.z >> (8 * q)) & 15u : 8u, z1 = ASYM ? (b.z >> (8 * q + 4)) & 15u : 8u;
+      // rows 2q, 2q + 1 at the word's lower nibbles (even k) and upper ones (odd k)
       const uint32_t half[2] = {__builtin_amdgcn_perm(b.w[2 * q + 1], b.w[2 * q], 0x05040100u),
                                 __builtin_amdgcn_perm(b.w[2 * q + 1], b.w[2 * q], 0x07060302u)};
       if constexpr (DT == DT_F16) {
@@ -140,33 +147,31 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
 #pragma unroll
         for (int H = 0; H < 2; ++H)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            half2_t v = __builtin_bit_cast(half2_t, magic_pair<DT_F16>(half[H], i));
+          for (int e = 0; e < 2; ++e) {
+            half2_t v = __builtin_bit_cast(half2_t, magic_pair<DT_F16>(half[H], part + 2 * e));
             v = v + __builtin_bit_cast(half2_t, nmz);
             v = v * sp;
-            out[2 * i + H][q] = __builtin_bit_cast(uint32_t, v);
+            out[2 * e + H][q] = __builtin_bit_cast(uint32_t, v);
           }
       } else {
         const GroupConst<DT> g0 = group_const<DT, true>(b.s[2 * q], z0), g1 = group_const<DT, true>(b.s[2 * q + 1], z1);
 #pragma unroll
         for (int H = 0; H < 2; ++H) {
-          const uint32_t ev = mask_nibbles(half[H]), od = mask_nibbles(half[H] >> 4);
-          const f32x2 e0 = __builtin_amdgcn_cvt_pk_f32_fp8(ev, false), e1 = __builtin_amdgcn_cvt_pk_f32_fp8(ev, true);
-          const f32x2 o0 = __builtin_amdgcn_cvt_pk_f32_fp8(od, false), o1 = __builtin_amdgcn_cvt_pk_f32_fp8(od, true);
-          auto pair = [&](float a, float b2) {
-            return f32x2_to_act_pair<DT_BF16>(__builtin_fmaf(a, g0.s_f32, g0.c_f32), __builtin_fmaf(b2, g1.s_f32, g1.c_f32));
-          };
-          out[0 + H][q] = pair(e0[0], e1[0]);
-          out[2 + H][q] = pair(o0[0], o1[0]);
-          out[4 + H][q] = pair(e0[1], e1[1]);
-          out[6 + H][q] = pair(o0[1], o1[1]);
+          // bytes: nibbles part and part + 2 of the first row, then of the second
+          const uint32_t n = mask_nibbles(half[H] >> (4 * part));
+          const f32x2 r0 = __builtin_amdgcn_cvt_pk_f32_fp8(n, false), r1 = __builtin_amdgcn_cvt_pk_f32_fp8(n, true);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            out[2 * e + H][q] = f32x2_to_act_pair<DT_BF16>(__builtin_fmaf(r0[e], g0.s_f32, g0.c_f32),
+                                                           __builtin_fmaf(r1[e], g1.s_f32, g1.c_f32));
         }
       }
     }
-    typedef __attribute__((address_space(3))) u32x4 lds_out;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      *(lds_out*)(buf + (uint32_t)(((o * 32 + c) * 8 + (k ^ (c & 7))) * 16)) = u32x4{out[k][0], out[k][1], out[k][2], out[k][3]};
+    for (int i = 0; i < 4; ++i) {
+      const int k = 4 * (i >> 1) + 2 * part + (i & 1);
+      *(lds_out*)(buf + (uint32_t)(((o * 32 + c) * 8 + (k ^ ((c >> 1) & 7))) * 16)) = u32x4{out[i][0], out[i][1], out[i][2], out[i][3]};
+    }
   };
 
   const int wk = wave & 1, wm = wave >> 1;
@@ -179,23 +184,16 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
       for (int e = 0; e < 16; ++e) acc[mb][kb][e] = 0.f;
   // operand addresses: k = 128 wk + 32 kb + j is slice 16 wk + 4 kb + j / 8, value j & 7
   const int cl = 16 * wk + (j >> 3);
-  auto multiply = [&](const lds_u8* wbuf, const lds_u8* dbuf) {
+  u32x4 fa[2][4], fb[2][MW];  // operands of a k-sub (16 rows of W), by parity
+  auto read = [&](const lds_u8* wbuf, const lds_u8* dbuf, int ks, u32x4 (&a)[4], u32x4 (&b)[MW]) {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      u32x4 a[4], b[MW];
-#pragma unroll
-      for (int kb = 0; kb < 4; ++kb) {
-        const int cc = cl + 4 * kb;
-        a[kb] = *(lds_u32x4*)(wbuf + (uint32_t)((((2 * ks + h) * 32 + cc) * 8 + ((j & 7) ^ (cc & 7))) * 16));
-      }
-#pragma unroll
-      for (int mb = 0; mb < MW; ++mb)
-        b[mb] = *(lds_u32x4*)(dbuf + (uint32_t)((wm * MW + mb) * 32 + j) * 128u + (uint32_t)(((2 * ks + h) ^ (j & 7)) * 16));
-#pragma unroll
-      for (int mb = 0; mb < MW; ++mb)
-#pragma unroll
-        for (int kb = 0; kb < 4; ++kb) acc[mb][kb] = mfma32x32x16<DT>(a[kb], b[mb], acc[mb][kb]);
+    for (int kb = 0; kb < 4; ++kb) {
+      const int cc = cl + 4 * kb;
+      a[kb] = *(lds_u32x4*)(wbuf + (uint32_t)((((2 * ks + h) * 32 + cc) * 8 + ((j & 7) ^ ((cc >> 1) & 7))) * 16));
     }
+#pragma unroll
+    for (int mb = 0; mb < MW; ++mb)
+      b[mb] = *(lds_u32x4*)(dbuf + (uint32_t)((wm * MW + mb) * 32 + j) * 128u + (uint32_t)(((2 * ks + h) ^ ((j >> 1) & 7)) * 16));
   };
 
   lds_u8* const w0 = (lds_u8*)ws0;
@@ -208,25 +206,56 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
     load_block(s_begin, b0);
     stage_dy(s_begin, d0);
     load_block(min(s_begin + 1, last), b1);
-    put_block(b0, w0);
+    stage_dy(min(s_begin + 1, last), d1);
+    put_half(b0, w0, 0);
+    put_half(b0, w0, 1);
     wait_vm_all();
     __syncthreads();
-    // step s multiplies from (w0, d0) while step s + 1 is staged and
-    // dequantised into (w1, d1); its words (b1) were loaded one step before
+    read(w0, d0, 0, fa[0], fb[0]);
+    // Step s multiplies from (wc, dc).  Meanwhile the block of step s + 1
+    // (next: its words came during the step before) is dequantised into wn, the
+    // words of step s + 2 are loaded, and each k-sub's operands are read one
+    // k-sub ahead.  The barrier stands before the last k-sub: by then every
+    // wave has written its part of wn, has its dy of step s + 1 in dn and has
+    // read its last operands of (wc, dc), so dc takes the dy of step s + 2.
     auto step = [&](int s, lds_u8* wc, lds_u8* dc, lds_u8* wn, lds_u8* dn, Block& next, Block& after) {
-      stage_dy(min(s + 1, last), dn);
-      load_block(min(s + 2, last), after);
-      multiply(wc, dc);
-      put_block(next, wn);
-      wait_vm_all();
-      __syncthreads();
+static_for<0, 4>([&](auto kc) {
+        constexpr int ks = decltype(kc)::value, cur = ks & 1, nx = cur ^ 1;
+        constexpr int NM = 4 * MW;  // MFMAs
+        if constexpr (ks < 3) {
+          read(wc, dc, ks + 1, fa[nx], fb[nx]);
+          if constexpr (ks == 0) load_block(min(s + 2, last), after);
+          if constexpr (ks < 2) put_half(next, wn, ks);
+        } else {
+          __builtin_amdgcn_sched_barrier(0);
+          __builtin_amdgcn_s_waitcnt(0);
+          asm volatile("s_barrier" ::: "memory");
+          __builtin_amdgcn_sched_barrier(0);
+          read(wn, dn, 0, fa[nx], fb[nx]);
+          stage_dy(min(s + 2, last), dc);
+        }
+#pragma unroll
+        for (int mb = 0; mb < MW; ++mb)
+#pragma unroll
+          for (int kb = 0; kb < 4; ++kb) acc[mb][kb] = mfma32x32x16<DT>(fa[cur][kb], fb[cur][mb], acc[mb][kb]);
+#pragma unroll
+        for (int i = 0; i < NM; ++i) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  // one MFMA
+          if (i < 4 + MW) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // one LDS read
+          __builtin_amdgcn_sched_group_barrier(0x002, ((ks < 2 ? 112 : 32) + NM - 1) / NM, 0);  // VALU
+          if constexpr (ks == 0 || ks == 3) __builtin_amdgcn_sched_group_barrier(0x020, (18 + NM - 1) / NM, 0);  // global loads
+          if constexpr (ks == 1 || ks == 2) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);  // LDS writes
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
     };
     int s = s_begin;
     for (; s + 1 < s_end; s += 2) {
       step(s, w0, d0, w1, d1, b1, b0);
       step(s + 1, w1, d1, w0, d0, b0, b1);
     }
-    if (s < s_end) multiply(w0, d0);
+    if (s < s_end) step(s, w0, d0, w1, d1, b1, b0);
+    wait_vm_all();  // no load into LDS in flight past the loop
   }
   lora_steps<DT, MW, 4>(lora, p.M, p.K, m0 + 32 * MW * wm, k0 + 128 * wk, lane, split, p.splits, acc);
 
@@ -329,8 +358,11 @@ hipError_t launch_dx(const DxArgs& a, const DxPlan& p, const LoraTerm& lora, hip
   prm.scales = static_cast<const uint16_t*>(a.scales);
   prm.zp = reinterpret_cast<const uint32_t*>(a.zp);
   prm.dx = static_cast<uint16_t*>(a.dx);
-  prm.zeros = a.zeros;
   prm.partial = a.partial;
+  prm.wq_tail = a.wq_tail;
+  prm.scales_tail = a.scales_tail;
+  prm.zp_tail = a.zp_tail;
+  prm.tail_step = a.N % kBN ? (int)(a.N / kBN) : -1;
   prm.M = (int)a.M;
   prm.N = (int)a.N;
   prm.K = (int)a.K;

@@ -376,17 +376,17 @@ size_t lora_u_offset(int64_t M, int64_t N, int64_t K, int32_t kgroup, int32_t dt
 // the workspace of w4a16_lora_backward, by byte offsets behind the counter
 // region that every entry point leaves zero
 struct BackwardPlan {
-  int64_t np;  // N rounded up to 8: the rows of dy and of the transposed lb
+  int64_t np;  // N rounded up to 64: the rows of dy and of the transposed lb
   w4a16::ShrinkPlan shrink;
   w4a16::OuterPlan outer;
   w4a16::DxPlan dx;
   int64_t places;  // of the tokens' order
-  size_t zeros, order, start, count, la_t, lb_t, dy_pad, part, g, op[2], outer_part, dx_part, bytes;
-  size_t zero_bytes;  // from `zeros` on: 16 zero bytes, then the outer products' counters
+  size_t zeros, order, start, count, la_t, lb_t, dy_pad, part, g, op[2], outer_part, dx_part, tail_w, tail_s, tail_z, bytes;
+  size_t zero_bytes;  // the outer products' counters, zero when they start
 };
 BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K, int64_t S, int64_t R, int cus) {
   BackwardPlan p;
-  p.np = (N + 7) / 8 * 8;
+  p.np = (N + 63) / 64 * 64;
   p.shrink = w4a16::plan_shrink(M, p.np, (int)R, cus, false);
   p.outer = w4a16::plan_outer(M, K, N, (int)S, (int)R, cus);
   p.dx = w4a16::plan_dx(M, N, K, cus);
@@ -396,7 +396,7 @@ BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K, int64_t S, int64_t R
     at += round256(n);
     return was;
   };
-  p.zero_bytes = 16 + w4a16::outer_counter_bytes(p.outer, (int)S);
+  p.zero_bytes = w4a16::outer_counter_bytes(p.outer, (int)S);
   p.zeros = take(p.zero_bytes);
   p.places = w4a16::order_places(M, S);
   p.order = take((size_t)p.places * 4);
@@ -411,6 +411,10 @@ BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K, int64_t S, int64_t R
   // the two are not in use at the same time, but both stay clear of the rest
   p.outer_part = take(w4a16::outer_partial_bytes(p.outer, p.places));
   p.dx_part = take(w4a16::dx_partial_bytes(p.dx, M, K));
+  // (scales of the smallest group, 32, whatever the call's group)
+  p.tail_w = take(p.np != N ? (size_t)K * 32 : 0);
+  p.tail_s = take(p.np != N ? act_bytes(64 * (K / 32)) : 0);
+  p.tail_z = take(p.np != N ? (size_t)(K / 32) * 32 : 0);
   p.bytes = at;
   return p;
 }
@@ -966,6 +970,16 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
   prep.S = (int)S;
   prep.R = (int)R;
   prep.np = (int)p.np;
+  const GroupMap gm = group_map(group_size, K);
+  if (pad && dx) {
+    prep.tail.wq = reinterpret_cast<const uint32_t*>(wq);
+    prep.tail.scales = static_cast<const uint16_t*>(scales);
+    prep.tail.zp = reinterpret_cast<const uint32_t*>(zp);
+    prep.tail.wq_out = static_cast<uint32_t*>(at(p.tail_w));
+    prep.tail.scales_out = static_cast<uint16_t*>(at(p.tail_s));
+    prep.tail.zp_out = static_cast<uint32_t*>(at(p.tail_z));
+    prep.tail.sG = gm.sG;
+  }
   const uint16_t* const dyr = pad ? prep.dy_pad : prep.dy;
   float* const g = static_cast<float*>(at(p.g));
   e = w4a16::launch_prep(prep, s);
@@ -981,8 +995,7 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
     e = w4a16::launch_operands(pa, s);
   }
   if (e == hipSuccess && dx) {
-    const GroupMap gm = group_map(group_size, K);
-    const w4a16::DxArgs da{dyr, wq, scales, zp, dx, at(p.zeros), static_cast<float*>(at(p.dx_part)), M, N, K, (int)p.np,
+    const w4a16::DxArgs da{dyr, wq, scales, zp, prep.tail.wq_out, prep.tail.scales_out, prep.tail.zp_out, dx, static_cast<float*>(at(p.dx_part)), M, N, K, (int)p.np,
                            gm.kgroup, dtype, gm.sG, gm.gmul};
     w4a16::LoraTerm t;
     t.ids = ids;
@@ -1002,7 +1015,7 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
     oa.count = prep.count;
     oa.places = (int)p.places;
     oa.partial = static_cast<float*>(at(p.outer_part));
-    oa.counters = prep.zero + 4;
+    oa.counters = prep.zero;
     oa.M = (int)M;
     oa.S = (int)S;
     oa.R = (int)R;

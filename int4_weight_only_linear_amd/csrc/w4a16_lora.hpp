@@ -90,14 +90,15 @@ __device__ __forceinline__ void split_hi_lo(const float (&v)[8], u32x4& hi, u32x
 // the adapters in turns, and the operands of the next two k-subs are loaded
 // while two are multiplied: a tile of many adapters is otherwise a chain of
 // memory round trips (16 adapters of rank 32 among 67 tokens, 19456 x 2560:
-// 28 us of 48, now 11 of 31).  The tall tiles (MB > 4), whose accumulators
-// leave few registers and whose tokens are mostly of one request, take one
-// k-sub at a time.
+// 28 us of 48, now 11 of 31).  The large tiles, whose accumulators leave
+// few registers and whose tokens are mostly of one request, take one k-sub at
+// a time.
 //   acc[rb][cb]: tokens m0 + 32 rb + (lane & 31), features nw0 + 32 cb + ...
 template <int DT, int MB, int CB>
 __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int m0, int nw0, int lane, int turn, int turns,
                                            f32x16 (&acc)[MB][CB]) {
-  constexpr int KS = MB <= 4 ? 2 : 1;  // k-subs of an item
+  constexpr bool DEEP = MB * CB <= 8;  // registers for operands in flight beside the accumulators
+  constexpr int KS = DEEP ? 2 : 1;      // k-subs of an item
   const int j = lane & 31, h = lane >> 5;
   int id[MB];
   uint64_t todo[MB];
@@ -185,7 +186,7 @@ __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int 
   Item none{};
   none.r0 = t.R;
   Item p = next(none);
-  if constexpr (MB > 4) {
+  if constexpr (!DEEP) {
     for (; p.a >= 0; p = next(p)) multiply(p);
     return;
   }

@@ -18,9 +18,10 @@ constexpr int kTile = 64;  // rows / columns of a transposed tile (the rank side
 //   S        the tokens of one adapter, in order: each scans all ids, counting
 //            those of smaller adapters (its segment's start) and ranking its own
 //   S tiles  lb[s][n..][:] and la[s][:][k..] transposed through LDS
-//   rows     dy with its rows padded to np, where N is no multiple of 8
+//   rows     dy with its rows padded to np, where N is no multiple of 64
+//   tail     the weights' last rows as a whole step, where N is no multiple of 64
 //   1        the words that later kernels find zero
-__global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n, int tiles_k, int pad_blocks) {
+__global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n, int tiles_k, int pad_blocks, int tail_blocks) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[kMaxRank * (kTile + 2)];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int job = blockIdx.x;
@@ -106,6 +107,31 @@ __global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n
       const int n = (int)(i - m * a.np);
       a.dy_pad[i] = n < a.N ? a.dy[m * a.N + n] : (uint16_t)0;
     }
+    return;
+  }
+  job -= pad_blocks;
+  if (job < tail_blocks) {
+    const int J = a.K >> 3, n0 = a.N / 64 * 64, runs = J >> 4, tail = J & 15, G = a.tail.sG;
+    for (int i = job * 256 + tid; i < 64 * J; i += tail_blocks * 256) {
+      const int t = i / (16 * J), off = i - t * 16 * J, first = n0 + 16 * t;
+      uint32_t w = 0u;
+      if (first + 16 <= a.N) {
+        w = a.tail.wq[(size_t)first * J + off];
+      } else {
+        // row and word of the row at this place of a complete tile
+        const bool run = off < 256 * runs;
+        const int piece = (off & 255) >> 2, rest = off - 256 * runs;
+        const int row = run ? piece & 15 : rest / max(tail, 1);
+        const int word = run ? (off >> 8) * 16 + 4 * (piece >> 4) + (off & 3) : 16 * runs + rest - row * tail;
+        if (first + row < a.N) w = a.tail.wq[(size_t)(first + row) * J + word];
+      }
+      a.tail.wq_out[i] = w;
+    }
+    for (int i = job * 256 + tid; i < 64 * G; i += tail_blocks * 256)
+      a.tail.scales_out[i] = n0 + i / G < a.N ? a.tail.scales[(size_t)n0 * G + i] : (uint16_t)0;
+    if (a.tail.zp)
+      for (int i = job * 256 + tid; i < 8 * G; i += tail_blocks * 256)
+        a.tail.zp_out[i] = n0 / 8 + i / G < a.N / 8 ? a.tail.zp[(size_t)(n0 / 8) * G + i] : 0u;
     return;
   }
   for (int i = tid; i < a.zero_words; i += 256) a.zero[i] = 0u;
@@ -345,9 +371,10 @@ __global__ __launch_bounds__(512) void outer_kernel(const OuterArgs a, const Out
 hipError_t launch_prep(const PrepArgs& a, hipStream_t s) {
   const int tiles_n = (a.np + kTile - 1) / kTile, tiles_k = (a.K + kTile - 1) / kTile;
   const int pad_blocks = a.dy_pad ? (int)std::min<int64_t>(2048, ((int64_t)a.M * a.np + 255) / 256) : 0;
-  const int64_t jobs = (int64_t)a.S * (1 + tiles_n + tiles_k) + pad_blocks + 1;
+  const int tail_blocks = a.tail.wq_out ? (8 * a.K + 1023) / 1024 : 0;  // four words a thread
+  const int64_t jobs = (int64_t)a.S * (1 + tiles_n + tiles_k) + pad_blocks + tail_blocks + 1;
   if (jobs > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(prep_kernel, dim3((unsigned)jobs), dim3(256), 0, s, a, tiles_n, tiles_k, pad_blocks);
+  hipLaunchKernelGGL(prep_kernel, dim3((unsigned)jobs), dim3(256), 0, s, a, tiles_n, tiles_k, pad_blocks, tail_blocks);
   return hipGetLastError();
 }
 

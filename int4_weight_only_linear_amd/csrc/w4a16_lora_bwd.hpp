@@ -11,6 +11,17 @@ namespace w4a16 {
 // start[s] = round32(tokens of smaller adapters) + 32 s, a multiple of 32 that
 // every adapter's workgroup can form by itself; places between are -1.
 inline int64_t order_places(int64_t M, int64_t S) { return (M + 31) / 32 * 32 + 32 * S; }
+// Where N is no multiple of 64: the weights' last N % 64 rows as 64, zero past
+// N, laid out as complete tiles; their scales and zero points likewise.
+struct TailCopy {
+  const uint32_t* wq = nullptr;
+  const uint16_t* scales = nullptr;
+  const uint32_t* zp = nullptr;  // NULL: symmetric
+  uint32_t* wq_out = nullptr;    // [4][16 * K / 8]; NULL: no tail
+  uint16_t* scales_out = nullptr;
+  uint32_t* zp_out = nullptr;
+  int sG = 0;                    // scales per row
+};
 struct PrepArgs {
   const int32_t* ids;
   int32_t* order;       // [order_places(M, S)]
@@ -25,6 +36,7 @@ struct PrepArgs {
   uint32_t* zero;       // zero_words words set to zero
   int zero_words;
   int M, N, K, S, R, np, places;
+  TailCopy tail;
 };
 hipError_t launch_prep(const PrepArgs& a, hipStream_t s);
 
@@ -71,12 +83,14 @@ hipError_t launch_outer(const OuterArgs& a, const OuterPlan& p, hipStream_t s);
 
 // dx[m, k] = sum over n of dy[m, n] * W[n, k] (+ the adapters' term)
 struct DxArgs {
-  const uint16_t* dy;  // [M][ldy], ldy a multiple of 8
+  const uint16_t* dy;  // [M][ldy], ldy a multiple of 64, zero past N
   const int32_t* wq;
   const void* scales;
   const int32_t* zp;
+  const uint32_t* wq_tail;  // TailCopy's, where N is no multiple of 64
+  const uint16_t* scales_tail;
+  const uint32_t* zp_tail;
   void* dx;            // [M][K]
-  const void* zeros;   // 16 zero bytes on the device
   float* partial;
   int64_t M, N, K;
   int ldy, group, dtype, sG, gmul;
