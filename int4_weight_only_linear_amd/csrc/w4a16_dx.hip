@@ -13,8 +13,8 @@
 // A workgroup (4 waves) owns 64 MW tokens x 256 k and steps over 64 rows at a
 // time: every thread dequantises one block into LDS, where the waves (each 32
 // MW tokens x 128 k) read them as A operands; dy is staged as B operands by
-// direct global->LDS loads.  Both are double buffered, the words of the step
-// after next in registers, and a step has one barrier.  Each weight is
+// direct global->LDS loads.  Both are double buffered, the words of the two
+// steps after next in registers, and a step has one barrier.  Each weight is
 // dequantised once per workgroup.
 #include <algorithm>
 
@@ -38,10 +38,8 @@ struct DxParams {
   const uint32_t* wq;
   const uint16_t* scales;
   const uint32_t* zp;
-  const uint32_t* wq_tail;  // the tail copy (DxArgs), of step tail_step (-1: none)
-  const uint16_t* scales_tail;
-  const uint32_t* zp_tail;
-  int tail_step;
+  int tail_step;            // whose rows come from the tail copy (-1: none), so many
+  int64_t wq_to_tail, scales_to_tail, zp_to_tail;  // bytes from their place in wq, scales, zp
   uint16_t* dx;
   float* partial;
   int M, N, K, ldy;
@@ -54,6 +52,17 @@ struct DxParams {
 __device__ __forceinline__ int xcd_unit(int b, int units) {
   const int q = units / 8, r = units % 8, xcd = b % 8, local = b / 8;
   return xcd < r ? xcd * (q + 1) + local : r * (q + 1) + (xcd - r) * q + local;
+}
+
+// A wave-uniform global address in scalar registers: loads then take it with a
+// 32-bit lane offset, without 64-bit vector address arithmetic.
+typedef __attribute__((address_space(1))) const char g_char;
+typedef __attribute__((address_space(1))) const uint32_t g_u32;
+typedef __attribute__((address_space(1))) const uint16_t g_u16;
+__device__ __forceinline__ g_char* uniform(uint64_t a) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
+  return (g_char*)((uint64_t)lo | ((uint64_t)hi << 32));
 }
 
 // the words, scales and zero points of one 8 x 8 block
@@ -86,7 +95,7 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
   // ---- dy (rows of a multiple of 64 values, zero past N): load d of this wave
   // fills LDS rows (wave NDMA + d) 8 + lane / 8; position lane & 7 of a row
   // holds its piece pos ^ (row / 2 & 7)
-  const char* const dytile = reinterpret_cast<const char*>(p.dy + (size_t)m0 * p.ldy);
+  const uint64_t dytile = reinterpret_cast<uint64_t>(p.dy + (size_t)m0 * p.ldy);
   uint32_t dyoff[NDMA];  // (NDMA is even)
 #pragma unroll
   for (int d = 0; d < NDMA; ++d) {
@@ -94,10 +103,10 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
     dyoff[d] = (uint32_t)row * (uint32_t)p.ldy * 2u + 16u * (uint32_t)((lane & 7) ^ (4 * (d & 1) + (lane >> 4)));
   }
   auto stage_dy = [&](int s, lds_u8* buf) {
-    const char* base = dytile + (size_t)s * (kBN * 2);
+    g_char* base = uniform(dytile + (uint64_t)s * (kBN * 2));
 #pragma unroll
     for (int d = 0; d < NDMA; ++d)
-      __builtin_amdgcn_global_load_lds(reinterpret_cast<const void*>(base + dyoff[d]), buf + (wave * NDMA + d) * 1024, 16, 0, 0);
+      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) const void*)(base + dyoff[d]), buf + (wave * NDMA + d) * 1024, 16, 0, 0);
   };
 
   // ---- weights: this thread's block is rows 8 o.. of the step, slice c of the
@@ -116,16 +125,17 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
   const uint32_t goff = (uint32_t)((8 * slice) / GS * p.gmul);
   const uint32_t soff = 2u * ((uint32_t)(8 * o * p.sG) + goff), zoff = 4u * ((uint32_t)(o * p.sG) + goff);
   auto load_block = [&](int s, Block& b) {
-    const bool at_tail = s == p.tail_step;  // wave-uniform
-    const char* wb = reinterpret_cast<const char*>(at_tail ? p.wq_tail : p.wq + (size_t)s * kBN * (size_t)p.wpr);
-    const char* sb = reinterpret_cast<const char*>(at_tail ? p.scales_tail : p.scales + (size_t)s * kBN * (size_t)p.sG);
+    // (a mask rather than a choice of pointers, which became branches, and at a
+    // branch the compiler waits for every load)
+    const int64_t at_tail = -(int64_t)(s == p.tail_step);
+    const uint64_t sb = reinterpret_cast<uint64_t>(p.scales) + (uint64_t)s * (kBN * 2) * (uint64_t)p.sG + (uint64_t)(at_tail & p.scales_to_tail);
+    g_char* wb = uniform(reinterpret_cast<uint64_t>(p.wq) + (uint64_t)s * (kBN * 4) * (uint64_t)p.wpr + (uint64_t)(at_tail & p.wq_to_tail));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b.w[i] = *reinterpret_cast<const uint32_t*>(wb + (woff + i * wstride));
+    for (int i = 0; i < 8; ++i) b.w[i] = *(g_u32*)(wb + (woff + i * wstride));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b.s[i] = *reinterpret_cast<const uint16_t*>(sb + (size_t)(2 * i) * (size_t)p.sG + soff);
+    for (int i = 0; i < 8; ++i) b.s[i] = *(g_u16*)(uniform(sb + (uint64_t)(2 * i) * (uint64_t)p.sG) + soff);
     if constexpr (ASYM)
-      b.z = *reinterpret_cast<const uint32_t*>(
-          reinterpret_cast<const char*>(at_tail ? p.zp_tail : p.zp + (size_t)s * (kBN / 8) * (size_t)p.sG) + zoff);
+      b.z = *(g_u32*)(uniform(reinterpret_cast<uint64_t>(p.zp) + (uint64_t)s * (kBN / 2) * (uint64_t)p.sG + (uint64_t)(at_tail & p.zp_to_tail)) + zoff);
   };
   // Half of the block's operands: k = 0, 1, 4, 5 (part 0) or 2, 3, 6, 7 of the
   // slice -- the even or odd nibbles of the paired words -- each 16 bytes at
@@ -209,26 +219,33 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
     stage_dy(min(s_begin + 1, last), d1);
     put_half(b0, w0, 0);
     put_half(b0, w0, 1);
+    load_block(min(s_begin + 2, last), b0);
     wait_vm_all();
     __syncthreads();
     read(w0, d0, 0, fa[0], fb[0]);
-    // Step s multiplies from (wc, dc).  Meanwhile the block of step s + 1
-    // (next: its words came during the step before) is dequantised into wn, the
-    // words of step s + 2 are loaded, and each k-sub's operands are read one
-    // k-sub ahead.  The barrier stands before the last k-sub: by then every
-    // wave has written its part of wn, has its dy of step s + 1 in dn and has
-    // read its last operands of (wc, dc), so dc takes the dy of step s + 2.
-    auto step = [&](int s, lds_u8* wc, lds_u8* dc, lds_u8* wn, lds_u8* dn, Block& next, Block& after) {
+    // Step s multiplies from (wc, dc), each k-sub's operands read one k-sub
+    // ahead.  Meanwhile the block of step s + 1 is dequantised into wn, then the
+    // words of step s + 3 are loaded in its place.  The barrier stands before
+    // the last k-sub: by then every wave has written its part of wn, has its dy
+    // of step s + 1 in dn and has read its last operands of (wc, dc), so dc takes
+    // the dy of step s + 2.  It waits for everything but the kKeep words, scales
+    // and zero points just loaded (the vector memory instructions since the last
+    // dy load; the build checks that), which have the whole of step s + 1.
+    constexpr int kKeep = 16 + (ASYM ? 1 : 0);
+    auto step = [&](int s, lds_u8* wc, lds_u8* dc, lds_u8* wn, lds_u8* dn, Block& next, auto keep) {
 static_for<0, 4>([&](auto kc) {
         constexpr int ks = decltype(kc)::value, cur = ks & 1, nx = cur ^ 1;
         constexpr int NM = 4 * MW;  // MFMAs
         if constexpr (ks < 3) {
           read(wc, dc, ks + 1, fa[nx], fb[nx]);
-          if constexpr (ks == 0) load_block(min(s + 2, last), after);
           if constexpr (ks < 2) put_half(next, wn, ks);
+          if constexpr (ks == 2) load_block(min(s + 3, last), next);
         } else {
           __builtin_amdgcn_sched_barrier(0);
-          __builtin_amdgcn_s_waitcnt(0);
+          if constexpr (decltype(keep)::value)
+            __builtin_amdgcn_s_waitcnt((kKeep & 15) | ((kKeep >> 4) << 14) | (7 << 4));  // vmcnt(kKeep), lgkmcnt(0)
+          else
+            __builtin_amdgcn_s_waitcnt(0);
           asm volatile("s_barrier" ::: "memory");
           __builtin_amdgcn_sched_barrier(0);
           read(wn, dn, 0, fa[nx], fb[nx]);
@@ -243,7 +260,7 @@ static_for<0, 4>([&](auto kc) {
           __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                  // one MFMA
           if (i < 4 + MW) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // one LDS read
           __builtin_amdgcn_sched_group_barrier(0x002, ((ks < 2 ? 112 : 32) + NM - 1) / NM, 0);  // VALU
-          if constexpr (ks == 0 || ks == 3) __builtin_amdgcn_sched_group_barrier(0x020, (18 + NM - 1) / NM, 0);  // global loads
+          if constexpr (ks >= 2) __builtin_amdgcn_sched_group_barrier(0x020, (18 + NM - 1) / NM, 0);  // global loads
           if constexpr (ks == 1 || ks == 2) __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);  // LDS writes
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -251,10 +268,11 @@ static_for<0, 4>([&](auto kc) {
     };
     int s = s_begin;
     for (; s + 1 < s_end; s += 2) {
-      step(s, w0, d0, w1, d1, b1, b0);
-      step(s + 1, w1, d1, w0, d0, b0, b1);
+      step(s, w0, d0, w1, d1, b1, std::true_type{});
+      step(s + 1, w1, d1, w0, d0, b0, std::true_type{});
     }
-    if (s < s_end) step(s, w0, d0, w1, d1, b1, b0);
+    // (what a peeled step loads is never used and may be dropped: no count)
+    if (s < s_end) step(s, w0, d0, w1, d1, b1, std::false_type{});
     wait_vm_all();  // no load into LDS in flight past the loop
   }
   lora_steps<DT, MW, 4>(lora, p.M, p.K, m0 + 32 * MW * wm, k0 + 128 * wk, lane, split, p.splits, acc);
@@ -359,10 +377,6 @@ hipError_t launch_dx(const DxArgs& a, const DxPlan& p, const LoraTerm& lora, hip
   prm.zp = reinterpret_cast<const uint32_t*>(a.zp);
   prm.dx = static_cast<uint16_t*>(a.dx);
   prm.partial = a.partial;
-  prm.wq_tail = a.wq_tail;
-  prm.scales_tail = a.scales_tail;
-  prm.zp_tail = a.zp_tail;
-  prm.tail_step = a.N % kBN ? (int)(a.N / kBN) : -1;
   prm.M = (int)a.M;
   prm.N = (int)a.N;
   prm.K = (int)a.K;
@@ -370,6 +384,18 @@ hipError_t launch_dx(const DxArgs& a, const DxPlan& p, const LoraTerm& lora, hip
   prm.sG = a.sG;
   prm.gmul = a.gmul;
   prm.wpr = (int)(a.K / 8);
+  prm.tail_step = -1;
+  prm.wq_to_tail = prm.scales_to_tail = prm.zp_to_tail = 0;
+  if (a.N % kBN) {
+    const int64_t s = a.N / kBN;
+    const auto from = [](const void* tail, const void* base, int64_t at) {
+      return (int64_t)(reinterpret_cast<uintptr_t>(tail) - reinterpret_cast<uintptr_t>(base)) - at;
+    };
+    prm.tail_step = (int)s;
+    prm.wq_to_tail = from(a.wq_tail, a.wq, s * kBN * 4 * (a.K / 8));
+    prm.scales_to_tail = from(a.scales_tail, a.scales, s * kBN * 2 * a.sG);
+    prm.zp_to_tail = from(a.zp_tail, a.zp, s * (kBN / 2) * a.sG);
+  }
   prm.nsteps = (int)((a.N + kBN - 1) / kBN);
   prm.tiles_k = p.tiles_k;
   prm.splits = p.splits;
