@@ -367,9 +367,10 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
  * w4a16_lora_linear; outputs must not overlap any input or each other; S at
  * most 65535, N*K/2 below 4 GiB.
  * Workspace: w4a16_lora_backward_workspace_size bytes, always needed, under
- * the rules above.  It holds the transposed factors (S*R*(K+N) values) and the
- * partial sums. */
-size_t w4a16_lora_backward_workspace_size(int64_t M, int64_t N, int64_t K, int64_t S, int64_t R);
+ * the rules above.  It holds the transposed factors (S*R*(K+N) values), the
+ * scales and zero points in the kernel's order and the partial sums. */
+size_t w4a16_lora_backward_workspace_size(int64_t M, int64_t N, int64_t K, int32_t group_size, int64_t S, int64_t R,
+                                          int32_t dtype);
 w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, const int32_t* wq, const void* scales,
                                  const int32_t* zp, const void* la, const void* lb, const int32_t* ids,
                                  const float* alpha, void* dx, void* dla, void* dlb, int64_t M, int64_t N, int64_t K,

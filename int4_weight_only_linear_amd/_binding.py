@@ -58,7 +58,7 @@ SIGNATURES = {
     "w4a16_lora_workspace_size": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _c_i64, _c_i32]),
     "w4a16_lora_linear": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_i64,
                                    _c_i64, _c_i32, _c_i64, _c_i64, _c_i32, _vp, _c_sz, _vp]),
-    "w4a16_lora_backward_workspace_size": (_c_sz, [_c_i64] * 5),
+    "w4a16_lora_backward_workspace_size": (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i32, _c_i64, _c_i64, _c_i32]),
     "w4a16_lora_backward": (_c_int, [_vp] * 13 + [_c_i64, _c_i64, _c_i64, _c_i32, _c_i64, _c_i64, _c_i32, _vp, _c_sz, _vp]),
     "w4a16_moe_linear": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_i64, _c_i64, _c_i64,
                                   _c_i64, _c_i64, _c_i32, _c_i32, _c_i32, _vp]),
@@ -511,8 +511,8 @@ def w4a16_lora_linear(x, wq, scales, la, lb, ids, zp=None, bias=None, alpha=None
     return (out, u) if save_u else out
 
 
-def w4a16_lora_backward_workspace_size(M, N, K, S, R) -> int:
-    return int(lib.w4a16_lora_backward_workspace_size(M, N, K, S, R))
+def w4a16_lora_backward_workspace_size(M, N, K, group_size, S, R, dtype) -> int:
+    return int(lib.w4a16_lora_backward_workspace_size(M, N, K, group_size, S, R, dtype))
 
 
 def w4a16_lora_backward(dy, x, u, wq, scales, la, lb, ids, zp=None, alpha=None, *, group_size: int,
@@ -543,7 +543,7 @@ def w4a16_lora_backward(dy, x, u, wq, scales, la, lb, ids, zp=None, alpha=None, 
     stream = torch.cuda.current_stream(x.device).cuda_stream
     with torch.cuda.device(x.device):
         if workspace is None:
-            workspace = _workspace(x.device, stream, w4a16_lora_backward_workspace_size(M, N, K, S, R))
+            workspace = _workspace(x.device, stream, w4a16_lora_backward_workspace_size(M, N, K, group_size, S, R, dt))
         ws_ptr = None if workspace is None else workspace.data_ptr()
         ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
         _check(lib.w4a16_lora_backward(dy.data_ptr(), x.data_ptr(), u.data_ptr(), wq.data_ptr(), scales.data_ptr(),

@@ -36,14 +36,12 @@ typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
 struct DxParams {
   const uint16_t* dy;
   const uint32_t* wq;
-  const uint16_t* scales;
-  const uint32_t* zp;
-  int tail_step;            // whose rows come from the tail copy (-1: none), so many
-  int64_t wq_to_tail, scales_to_tail, zp_to_tail;  // bytes from their place in wq, scales, zp
+  int tail_step;       // whose words come from the tail copy (-1: none),
+  int64_t wq_to_tail;  // so many bytes from their place in wq
+  const void* constants;
   uint16_t* dx;
   float* partial;
-  int M, N, K, ldy;
-  int sG, gmul;
+  int M, N, K, ldy, group;
   int wpr;      // words per weight row
   int nsteps, tiles_k, units, splits, steps_per_split;
 };
@@ -58,21 +56,22 @@ __device__ __forceinline__ int xcd_unit(int b, int units) {
 // 32-bit lane offset, without 64-bit vector address arithmetic.
 typedef __attribute__((address_space(1))) const char g_char;
 typedef __attribute__((address_space(1))) const uint32_t g_u32;
-typedef __attribute__((address_space(1))) const uint16_t g_u16;
+typedef __attribute__((address_space(1))) const u32x4 g_u32x4;
 __device__ __forceinline__ g_char* uniform(uint64_t a) {
   const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a);
   const uint32_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(a >> 32));
   return (g_char*)((uint64_t)lo | ((uint64_t)hi << 32));
 }
 
-// the words, scales and zero points of one 8 x 8 block
+// the words of one 8 x 8 block and its rows' constants: per pair of rows, what
+// prep_kernel formed of their scales and zero points (dx_constants)
+template <int DT>
 struct Block {
   uint32_t w[8];
-  uint16_t s[8];
-  uint32_t z;
+  u32x4 g[DT == DT_F16 ? 2 : 4];
 };
 
-template <int DT, int GS, bool ASYM, int MW>
+template <int DT, int MW>
 __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const LoraTerm lora) {
   constexpr int BM = 64 * MW;
   constexpr int DYB = BM * kBN * 2;       // one dy buffer
@@ -105,8 +104,11 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
   auto stage_dy = [&](int s, lds_u8* buf) {
     g_char* base = uniform(dytile + (uint64_t)s * (kBN * 2));
 #pragma unroll
-    for (int d = 0; d < NDMA; ++d)
-      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) const void*)(base + dyoff[d]), buf + (wave * NDMA + d) * 1024, 16, 0, 0);
+    for (int d = 0; d < NDMA; ++d) {
+      uint32_t at = dyoff[d];
+      asm("" : "+v"(at));  // (as in load_block)
+      __builtin_amdgcn_global_load_lds((__attribute__((address_space(1))) const void*)(base + at), buf + (wave * NDMA + d) * 1024, 16, 0, 0);
+    }
   };
 
   // ---- weights: this thread's block is rows 8 o.. of the step, slice c of the
@@ -122,20 +124,23 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
   const uint32_t woff = 64u * (uint32_t)p.wpr * (uint32_t)(o >> 1) + 8u * (uint32_t)(o & 1) * wstride +
                         4u * (full_run ? 256u * (uint32_t)(slice >> 4) + 64u * (uint32_t)(slice & 3) + (uint32_t)((slice & 15) >> 2)
                                        : 256u * (uint32_t)runs + (uint32_t)(slice - 16 * runs));
-  const uint32_t goff = (uint32_t)((8 * slice) / GS * p.gmul);
-  const uint32_t soff = 2u * ((uint32_t)(8 * o * p.sG) + goff), zoff = 4u * ((uint32_t)(o * p.sG) + goff);
-  auto load_block = [&](int s, Block& b) {
+  // constants: [group][rows of the padded N], 4 (fp16) or 8 bytes a row
+  constexpr uint32_t kRowBytes = DT == DT_F16 ? 4 : 8;
+  const uint32_t goff = kRowBytes * ((uint32_t)(8 * slice / p.group) * (uint32_t)p.ldy + 8u * (uint32_t)o);
+  auto load_block = [&](int s, Block<DT>& b) {
     // (a mask rather than a choice of pointers, which became branches, and at a
-    // branch the compiler waits for every load)
+    // branch the compiler waits for every load; N * K / 2 is below 4 GiB)
     const int64_t at_tail = -(int64_t)(s == p.tail_step);
-    const uint64_t sb = reinterpret_cast<uint64_t>(p.scales) + (uint64_t)s * (kBN * 2) * (uint64_t)p.sG + (uint64_t)(at_tail & p.scales_to_tail);
-    g_char* wb = uniform(reinterpret_cast<uint64_t>(p.wq) + (uint64_t)s * (kBN * 4) * (uint64_t)p.wpr + (uint64_t)(at_tail & p.wq_to_tail));
+    g_char* wb = uniform(reinterpret_cast<uint64_t>(p.wq) + (uint32_t)s * (uint32_t)(kBN * 4 * p.wpr) + (uint64_t)(at_tail & p.wq_to_tail));
+    g_char* gb = uniform(reinterpret_cast<uint64_t>(p.constants) + (uint32_t)s * (kBN * kRowBytes));
+    // the offsets are formed here, as 32-bit values that the compiler cannot
+    // move out of the loop as 64-bit ones
+    uint32_t at = woff, gat = goff;
+    asm("" : "+v"(at), "+v"(gat));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b.w[i] = *(g_u32*)(wb + (woff + i * wstride));
+    for (int i = 0; i < 8; ++i) b.w[i] = *(g_u32*)(wb + (at + i * wstride));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) b.s[i] = *(g_u16*)(uniform(sb + (uint64_t)(2 * i) * (uint64_t)p.sG) + soff);
-    if constexpr (ASYM)
-      b.z = *(g_u32*)(uniform(reinterpret_cast<uint64_t>(p.zp) + (uint64_t)s * (kBN / 2) * (uint64_t)p.sG + (uint64_t)(at_tail & p.zp_to_tail)) + zoff);
+    for (int i = 0; i < (int)(kRowBytes / 2); ++i) b.g[i] = *(g_u32x4*)(gb + gat + 16 * i);
   };
   // Half of the block's operands: k = 0, 1, 4, 5 (part 0) or 2, 3, 6, 7 of the
   // slice -- the even or odd nibbles of the paired words -- each 16 bytes at
@@ -143,28 +148,29 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
   // writing (slices c) or reading (k of two slices), touch sixteen banks of 16
   // bytes.
   typedef __attribute__((address_space(3))) u32x4 lds_out;
-  auto put_half = [&](const Block& b, lds_u8* buf, int part) {
+  auto put_half = [&](const Block<DT>& b, lds_u8* buf, int part) {
     uint32_t out[4][4];  // [k of the part][row pair]
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const uint32_t z0 = ASYM ? (b.z >> (8 * q)) & 15u : 8u, z1 = ASYM ? (b.z >> (8 * q + 4)) & 15u : 8u;
       // rows 2q, 2q + 1 at the word's lower nibbles (even k) and upper ones (odd k)
       const uint32_t half[2] = {__builtin_amdgcn_perm(b.w[2 * q + 1], b.w[2 * q], 0x05040100u),
                                 __builtin_amdgcn_perm(b.w[2 * q + 1], b.w[2 * q], 0x07060302u)};
       if constexpr (DT == DT_F16) {
-        const uint32_t nmz = (Magic<DT_F16>::neg | z0) | ((Magic<DT_F16>::neg | z1) << 16);
-        const half2_t sp = __builtin_bit_cast(half2_t, (uint32_t)b.s[2 * q] | ((uint32_t)b.s[2 * q + 1] << 16));
+        // both scales, then both -(1024 + z)
+        const uint32_t sp = b.g[q >> 1][2 * (q & 1)], nmz = b.g[q >> 1][2 * (q & 1) + 1];
 #pragma unroll
         for (int H = 0; H < 2; ++H)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            half2_t v = __builtin_bit_cast(half2_t, magic_pair<DT_F16>(half[H], part + 2 * e));
-            v = v + __builtin_bit_cast(half2_t, nmz);
-            v = v * sp;
-            out[2 * e + H][q] = __builtin_bit_cast(uint32_t, v);
+            const uint32_t qz = add_f16x2(magic_pair<DT_F16>(half[H], part + 2 * e), nmz);
+            out[2 * e + H][q] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, qz) * __builtin_bit_cast(half2_t, sp));
           }
       } else {
-        const GroupConst<DT> g0 = group_const<DT, true>(b.s[2 * q], z0), g1 = group_const<DT, true>(b.s[2 * q + 1], z1);
+        // s 2^9 and -z s of either row
+        const uint32_t kb[4] = {b.g[q][0], b.g[q][1], b.g[q][2], b.g[q][3]};
+        float k[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) k[e] = __builtin_bit_cast(float, kb[e]);
 #pragma unroll
         for (int H = 0; H < 2; ++H) {
           // bytes: nibbles part and part + 2 of the first row, then of the second
@@ -172,8 +178,7 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
           const f32x2 r0 = __builtin_amdgcn_cvt_pk_f32_fp8(n, false), r1 = __builtin_amdgcn_cvt_pk_f32_fp8(n, true);
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            out[2 * e + H][q] = f32x2_to_act_pair<DT_BF16>(__builtin_fmaf(r0[e], g0.s_f32, g0.c_f32),
-                                                           __builtin_fmaf(r1[e], g1.s_f32, g1.c_f32));
+            out[2 * e + H][q] = f32x2_to_act_pair<DT_BF16>(__builtin_fmaf(r0[e], k[0], k[1]), __builtin_fmaf(r1[e], k[2], k[3]));
         }
       }
     }
@@ -211,7 +216,7 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
   lds_u8* const d0 = (lds_u8*)ds0;
   lds_u8* const d1 = (lds_u8*)ds1;
   if (s_begin < s_end) {
-    Block b0 = {}, b1 = {};
+    Block<DT> b0 = {}, b1 = {};
     const int last = s_end - 1;
     load_block(s_begin, b0);
     stage_dy(s_begin, d0);
@@ -228,11 +233,11 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
     // words of step s + 3 are loaded in its place.  The barrier stands before
     // the last k-sub: by then every wave has written its part of wn, has its dy
     // of step s + 1 in dn and has read its last operands of (wc, dc), so dc takes
-    // the dy of step s + 2.  It waits for everything but the kKeep words, scales
-    // and zero points just loaded (the vector memory instructions since the last
+    // the dy of step s + 2.  It waits for everything but the kKeep words and
+    // constants just loaded (the vector memory instructions since the last
     // dy load; the build checks that), which have the whole of step s + 1.
-    constexpr int kKeep = 16 + (ASYM ? 1 : 0);
-    auto step = [&](int s, lds_u8* wc, lds_u8* dc, lds_u8* wn, lds_u8* dn, Block& next, auto keep) {
+    constexpr int kKeep = 8 + (int)(kRowBytes / 2);
+    auto step = [&](int s, lds_u8* wc, lds_u8* dc, lds_u8* wn, lds_u8* dn, Block<DT>& next, auto keep) {
 static_for<0, 4>([&](auto kc) {
         constexpr int ks = decltype(kc)::value, cur = ks & 1, nx = cur ^ 1;
         constexpr int NM = 4 * MW;  // MFMAs
@@ -315,27 +320,16 @@ static_for<0, 4>([&](auto kc) {
   }
 }
 
-template <int DT, int GS, bool ASYM>
+template <int DT>
 hipError_t launch_mw(const DxParams& prm, const LoraTerm& lora, int mw, hipStream_t s) {
   auto go = [&](auto kern) {
     hipLaunchKernelGGL(kern, dim3(prm.units), dim3(kThreads), 0, s, prm, lora);
     return hipGetLastError();
   };
   switch (mw) {
-    case 1: return go(dx_kernel<DT, GS, ASYM, 1>);
-    case 2: return go(dx_kernel<DT, GS, ASYM, 2>);
-    case 4: return go(dx_kernel<DT, GS, ASYM, 4>);
-    default: return hipErrorInvalidValue;
-  }
-}
-
-template <int DT>
-hipError_t launch_g(const DxParams& prm, const LoraTerm& lora, int group, int mw, hipStream_t s) {
-  const bool z = prm.zp != nullptr;
-  switch (group) {
-    case 32: return z ? launch_mw<DT, 32, true>(prm, lora, mw, s) : launch_mw<DT, 32, false>(prm, lora, mw, s);
-    case 64: return z ? launch_mw<DT, 64, true>(prm, lora, mw, s) : launch_mw<DT, 64, false>(prm, lora, mw, s);
-    case 128: return z ? launch_mw<DT, 128, true>(prm, lora, mw, s) : launch_mw<DT, 128, false>(prm, lora, mw, s);
+    case 1: return go(dx_kernel<DT, 1>);
+    case 2: return go(dx_kernel<DT, 2>);
+    case 4: return go(dx_kernel<DT, 4>);
     default: return hipErrorInvalidValue;
   }
 }
@@ -373,35 +367,28 @@ hipError_t launch_dx(const DxArgs& a, const DxPlan& p, const LoraTerm& lora, hip
   DxParams prm;
   prm.dy = a.dy;
   prm.wq = reinterpret_cast<const uint32_t*>(a.wq);
-  prm.scales = static_cast<const uint16_t*>(a.scales);
-  prm.zp = reinterpret_cast<const uint32_t*>(a.zp);
+  prm.constants = a.constants;
   prm.dx = static_cast<uint16_t*>(a.dx);
   prm.partial = a.partial;
   prm.M = (int)a.M;
   prm.N = (int)a.N;
   prm.K = (int)a.K;
   prm.ldy = a.ldy;
-  prm.sG = a.sG;
-  prm.gmul = a.gmul;
+  prm.group = a.group;
   prm.wpr = (int)(a.K / 8);
   prm.tail_step = -1;
-  prm.wq_to_tail = prm.scales_to_tail = prm.zp_to_tail = 0;
+  prm.wq_to_tail = 0;
   if (a.N % kBN) {
-    const int64_t s = a.N / kBN;
-    const auto from = [](const void* tail, const void* base, int64_t at) {
-      return (int64_t)(reinterpret_cast<uintptr_t>(tail) - reinterpret_cast<uintptr_t>(base)) - at;
-    };
-    prm.tail_step = (int)s;
-    prm.wq_to_tail = from(a.wq_tail, a.wq, s * kBN * 4 * (a.K / 8));
-    prm.scales_to_tail = from(a.scales_tail, a.scales, s * kBN * 2 * a.sG);
-    prm.zp_to_tail = from(a.zp_tail, a.zp, s * (kBN / 2) * a.sG);
+    const int64_t t = a.N / kBN;
+    prm.tail_step = (int)t;
+    prm.wq_to_tail = (int64_t)(reinterpret_cast<uintptr_t>(a.wq_tail) - reinterpret_cast<uintptr_t>(a.wq)) - t * kBN * 4 * (a.K / 8);
   }
   prm.nsteps = (int)((a.N + kBN - 1) / kBN);
   prm.tiles_k = p.tiles_k;
   prm.splits = p.splits;
   prm.steps_per_split = p.steps_per_split;
   prm.units = p.tiles * p.splits;
-  const hipError_t e = a.dtype == DT_F16 ? launch_g<DT_F16>(prm, lora, a.group, p.mw, s) : launch_g<DT_BF16>(prm, lora, a.group, p.mw, s);
+  const hipError_t e = a.dtype == DT_F16 ? launch_mw<DT_F16>(prm, lora, p.mw, s) : launch_mw<DT_BF16>(prm, lora, p.mw, s);
   if (e != hipSuccess || p.splits == 1) return e;
   return launch_splitk_reduce(a.dtype, a.partial, nullptr, prm.dx, prm.M, prm.K, prm.K, p.splits, s);
 }

@@ -381,10 +381,10 @@ struct BackwardPlan {
   w4a16::OuterPlan outer;
   w4a16::DxPlan dx;
   int64_t places;  // of the tokens' order
-  size_t zeros, order, start, count, la_t, lb_t, dy_pad, part, g, op[2], outer_part, dx_part, tail_w, tail_s, tail_z, bytes;
+  size_t zeros, order, start, count, la_t, lb_t, dy_pad, part, g, op[2], outer_part, dx_part, tail_w, constants, bytes;
   size_t zero_bytes;  // the outer products' counters, zero when they start
 };
-BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K, int64_t S, int64_t R, int cus) {
+BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K, int32_t group_size, int64_t S, int64_t R, int32_t dtype, int cus) {
   BackwardPlan p;
   p.np = (N + 63) / 64 * 64;
   p.shrink = w4a16::plan_shrink(M, p.np, (int)R, cus, false);
@@ -411,10 +411,8 @@ BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K, int64_t S, int64_t R
   // the two are not in use at the same time, but both stay clear of the rest
   p.outer_part = take(w4a16::outer_partial_bytes(p.outer, p.places));
   p.dx_part = take(w4a16::dx_partial_bytes(p.dx, M, K));
-  // (scales of the smallest group, 32, whatever the call's group)
   p.tail_w = take(p.np != N ? (size_t)K * 32 : 0);
-  p.tail_s = take(p.np != N ? act_bytes(64 * (K / 32)) : 0);
-  p.tail_z = take(p.np != N ? (size_t)(K / 32) * 32 : 0);
+  p.constants = take(w4a16::dx_constant_bytes(p.np, K / group_size, dtype));
   p.bytes = at;
   return p;
 }
@@ -897,9 +895,12 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
   return linear_impl(x, wq, scales, zp, bias, y, M, N, K, group_size, dtype, workspace, at, stream, p, &t);
 }
 
-size_t w4a16_lora_backward_workspace_size(int64_t M, int64_t N, int64_t K, int64_t S, int64_t R) {
-  if (M <= 0 || N <= 0 || K <= 0 || K % 32 || S < 1 || S > 65535 || R < 8 || R % 8 || R > w4a16::kMaxRank) return 0;
-  return plan_backward(M, N, K, S, R, planning_cus()).bytes;
+size_t w4a16_lora_backward_workspace_size(int64_t M, int64_t N, int64_t K, int32_t group_size, int64_t S, int64_t R,
+                                          int32_t dtype) {
+  if (M <= 0 || N <= 0 || K <= 0 || !group_ok(group_size, K) || K % group_size || S < 1 || S > 65535 || R < 8 || R % 8 ||
+      R > w4a16::kMaxRank || (dtype != W4A16_F16 && dtype != W4A16_BF16))
+    return 0;
+  return plan_backward(M, N, K, group_size, S, R, dtype, planning_cus()).bytes;
 }
 
 w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, const int32_t* wq, const void* scales,
@@ -942,7 +943,7 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
     if (e == hipSuccess) e = w4a16::launch_zero_words(dlb, act_bytes(S * N * R), s);
     return e == hipSuccess ? ok() : fail(W4A16_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
   }
-  const BackwardPlan p = plan_backward(M, N, K, S, R, dev->cu_count);
+  const BackwardPlan p = plan_backward(M, N, K, group_size, S, R, dtype, dev->cu_count);
   if (workspace == nullptr || workspace_bytes < p.bytes)
     return fail(W4A16_ERR_WORKSPACE, "lora_backward: workspace of %zu bytes needed, got %zu%s", p.bytes, workspace_bytes,
                 workspace ? "" : " (NULL)");
@@ -970,15 +971,14 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
   prep.S = (int)S;
   prep.R = (int)R;
   prep.np = (int)p.np;
-  const GroupMap gm = group_map(group_size, K);
-  if (pad && dx) {
-    prep.tail.wq = reinterpret_cast<const uint32_t*>(wq);
-    prep.tail.scales = static_cast<const uint16_t*>(scales);
-    prep.tail.zp = reinterpret_cast<const uint32_t*>(zp);
-    prep.tail.wq_out = static_cast<uint32_t*>(at(p.tail_w));
-    prep.tail.scales_out = static_cast<uint16_t*>(at(p.tail_s));
-    prep.tail.zp_out = static_cast<uint32_t*>(at(p.tail_z));
-    prep.tail.sG = gm.sG;
+  if (dx) {
+    prep.dx.wq = reinterpret_cast<const uint32_t*>(wq);
+    prep.dx.scales = static_cast<const uint16_t*>(scales);
+    prep.dx.zp = reinterpret_cast<const uint32_t*>(zp);
+    prep.dx.constants = at(p.constants);
+    prep.dx.wq_tail = pad ? static_cast<uint32_t*>(at(p.tail_w)) : nullptr;
+    prep.dx.G = (int)G;
+    prep.dx.dtype = dtype;
   }
   const uint16_t* const dyr = pad ? prep.dy_pad : prep.dy;
   float* const g = static_cast<float*>(at(p.g));
@@ -995,8 +995,8 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
     e = w4a16::launch_operands(pa, s);
   }
   if (e == hipSuccess && dx) {
-    const w4a16::DxArgs da{dyr, wq, scales, zp, prep.tail.wq_out, prep.tail.scales_out, prep.tail.zp_out, dx, static_cast<float*>(at(p.dx_part)), M, N, K, (int)p.np,
-                           gm.kgroup, dtype, gm.sG, gm.gmul};
+    const w4a16::DxArgs da{dyr, wq, prep.dx.wq_tail, prep.dx.constants, dx, static_cast<float*>(at(p.dx_part)), M, N, K,
+                           (int)p.np, group_size, dtype};
     w4a16::LoraTerm t;
     t.ids = ids;
     t.up = prep.la_t;

@@ -20,8 +20,10 @@ constexpr int kTile = 64;  // rows / columns of a transposed tile (the rank side
 //   S tiles  lb[s][n..][:] and la[s][:][k..] transposed through LDS
 //   rows     dy with its rows padded to np, where N is no multiple of 64
 //   tail     the weights' last rows as a whole step, where N is no multiple of 64
+//   consts   the rows' constants by group, as dx_kernel takes them (DxPrep)
 //   1        the words that later kernels find zero
-__global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n, int tiles_k, int pad_blocks, int tail_blocks) {
+__global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n, int tiles_k, int pad_blocks, int tail_blocks,
+                                                   int const_blocks) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[kMaxRank * (kTile + 2)];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int job = blockIdx.x;
@@ -111,27 +113,55 @@ __global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n
   }
   job -= pad_blocks;
   if (job < tail_blocks) {
-    const int J = a.K >> 3, n0 = a.N / 64 * 64, runs = J >> 4, tail = J & 15, G = a.tail.sG;
+    const int J = a.K >> 3, n0 = a.N / 64 * 64, runs = J >> 4, tail = J & 15;
     for (int i = job * 256 + tid; i < 64 * J; i += tail_blocks * 256) {
       const int t = i / (16 * J), off = i - t * 16 * J, first = n0 + 16 * t;
       uint32_t w = 0u;
       if (first + 16 <= a.N) {
-        w = a.tail.wq[(size_t)first * J + off];
+        w = a.dx.wq[(size_t)first * J + off];
       } else {
         // row and word of the row at this place of a complete tile
         const bool run = off < 256 * runs;
         const int piece = (off & 255) >> 2, rest = off - 256 * runs;
         const int row = run ? piece & 15 : rest / max(tail, 1);
         const int word = run ? (off >> 8) * 16 + 4 * (piece >> 4) + (off & 3) : 16 * runs + rest - row * tail;
-        if (first + row < a.N) w = a.tail.wq[(size_t)(first + row) * J + word];
+        if (first + row < a.N) w = a.dx.wq[(size_t)(first + row) * J + word];
       }
-      a.tail.wq_out[i] = w;
+      a.dx.wq_tail[i] = w;
     }
-    for (int i = job * 256 + tid; i < 64 * G; i += tail_blocks * 256)
-      a.tail.scales_out[i] = n0 + i / G < a.N ? a.tail.scales[(size_t)n0 * G + i] : (uint16_t)0;
-    if (a.tail.zp)
-      for (int i = job * 256 + tid; i < 8 * G; i += tail_blocks * 256)
-        a.tail.zp_out[i] = n0 / 8 + i / G < a.N / 8 ? a.tail.zp[(size_t)(n0 / 8) * G + i] : 0u;
+    return;
+  }
+  job -= tail_blocks;
+  if (job < const_blocks) {
+    // 64 rows x 32 groups through LDS: scale bits and zero point of each
+    uint32_t* const sz = reinterpret_cast<uint32_t*>(lds);  // [64][33]
+    const int gb = (a.dx.G + 31) / 32, n0 = job / gb * 64, g0 = (job - job / gb * gb) * 32;
+    const int groups = min(32, a.dx.G - g0);
+    for (int i = tid; i < 64 * 32; i += 256) {
+      const int n = n0 + (i >> 5), g = i & 31;
+      if (g < groups) {
+        uint32_t v = 0u;
+        if (n < a.N) {
+          const uint32_t z = a.dx.zp ? (a.dx.zp[(size_t)(n >> 3) * a.dx.G + g0 + g] >> (4 * (n & 7))) & 15u : 8u;
+          v = a.dx.scales[(size_t)n * a.dx.G + g0 + g] | (z << 16);
+        }
+        sz[(i >> 5) * 33 + g] = v;
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < 32 * groups; i += 256) {
+      const int g = i >> 5, q = i & 31;  // group, pair of rows
+      const uint32_t a0 = sz[2 * q * 33 + g], a1 = sz[(2 * q + 1) * 33 + g];
+      const size_t at = (size_t)(g0 + g) * a.np / 2 + n0 / 2 + q;
+      if (a.dx.dtype == DT_F16) {
+        constexpr uint32_t NEG = Magic<DT_F16>::neg;
+        static_cast<u32x2*>(a.dx.constants)[at] = u32x2{(a0 & 0xFFFFu) | (a1 << 16), (NEG | (a0 >> 16)) | ((NEG | (a1 >> 16)) << 16)};
+      } else {
+        const GroupConst<DT_BF16> c0 = group_const<DT_BF16, true>((uint16_t)a0, a0 >> 16);
+        const GroupConst<DT_BF16> c1 = group_const<DT_BF16, true>((uint16_t)a1, a1 >> 16);
+        static_cast<f32x4*>(a.dx.constants)[at] = f32x4{c0.s_f32, c0.c_f32, c1.s_f32, c1.c_f32};
+      }
+    }
     return;
   }
   for (int i = tid; i < a.zero_words; i += 256) a.zero[i] = 0u;
@@ -371,10 +401,11 @@ __global__ __launch_bounds__(512) void outer_kernel(const OuterArgs a, const Out
 hipError_t launch_prep(const PrepArgs& a, hipStream_t s) {
   const int tiles_n = (a.np + kTile - 1) / kTile, tiles_k = (a.K + kTile - 1) / kTile;
   const int pad_blocks = a.dy_pad ? (int)std::min<int64_t>(2048, ((int64_t)a.M * a.np + 255) / 256) : 0;
-  const int tail_blocks = a.tail.wq_out ? (8 * a.K + 1023) / 1024 : 0;  // four words a thread
-  const int64_t jobs = (int64_t)a.S * (1 + tiles_n + tiles_k) + pad_blocks + tail_blocks + 1;
+  const int tail_blocks = a.dx.wq_tail ? (8 * a.K + 1023) / 1024 : 0;  // four words a thread
+  const int const_blocks = a.dx.constants ? a.np / 64 * ((a.dx.G + 31) / 32) : 0;
+  const int64_t jobs = (int64_t)a.S * (1 + tiles_n + tiles_k) + pad_blocks + tail_blocks + const_blocks + 1;
   if (jobs > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(prep_kernel, dim3((unsigned)jobs), dim3(256), 0, s, a, tiles_n, tiles_k, pad_blocks, tail_blocks);
+  hipLaunchKernelGGL(prep_kernel, dim3((unsigned)jobs), dim3(256), 0, s, a, tiles_n, tiles_k, pad_blocks, tail_blocks, const_blocks);
   return hipGetLastError();
 }
 

@@ -11,17 +11,20 @@ namespace w4a16 {
 // start[s] = round32(tokens of smaller adapters) + 32 s, a multiple of 32 that
 // every adapter's workgroup can form by itself; places between are -1.
 inline int64_t order_places(int64_t M, int64_t S) { return (M + 31) / 32 * 32 + 32 * S; }
-// Where N is no multiple of 64: the weights' last N % 64 rows as 64, zero past
-// N, laid out as complete tiles; their scales and zero points likewise.
-struct TailCopy {
+// What dx_kernel reads beside the packed words.  Constants of every row and
+// group, by group and row, in the form its conversions take (zero past N):
+// fp16, per pair of rows, both scales and both -(1024 + z) as fp16 (8 bytes);
+// bf16, per row, s 2^9 and -z s as fp32 (8 bytes).  And where N is no multiple
+// of 64, the weights' last N % 64 rows as 64 (zero past N) in complete tiles.
+struct DxPrep {
   const uint32_t* wq = nullptr;
   const uint16_t* scales = nullptr;
-  const uint32_t* zp = nullptr;  // NULL: symmetric
-  uint32_t* wq_out = nullptr;    // [4][16 * K / 8]; NULL: no tail
-  uint16_t* scales_out = nullptr;
-  uint32_t* zp_out = nullptr;
-  int sG = 0;                    // scales per row
+  const uint32_t* zp = nullptr;   // NULL: symmetric
+  void* constants = nullptr;      // [G][np]; NULL: no dx wanted
+  uint32_t* wq_tail = nullptr;    // [4][16 * K / 8]; NULL: no tail
+  int G = 0, dtype = 0;           // scales per row
 };
+inline size_t dx_constant_bytes(int64_t np, int64_t G, int dtype) { return (size_t)np * (size_t)G * (dtype == 0 ? 4 : 8); }
 struct PrepArgs {
   const int32_t* ids;
   int32_t* order;       // [order_places(M, S)]
@@ -36,7 +39,7 @@ struct PrepArgs {
   uint32_t* zero;       // zero_words words set to zero
   int zero_words;
   int M, N, K, S, R, np, places;
-  TailCopy tail;
+  DxPrep dx;
 };
 hipError_t launch_prep(const PrepArgs& a, hipStream_t s);
 
@@ -85,15 +88,12 @@ hipError_t launch_outer(const OuterArgs& a, const OuterPlan& p, hipStream_t s);
 struct DxArgs {
   const uint16_t* dy;  // [M][ldy], ldy a multiple of 64, zero past N
   const int32_t* wq;
-  const void* scales;
-  const int32_t* zp;
-  const uint32_t* wq_tail;  // TailCopy's, where N is no multiple of 64
-  const uint16_t* scales_tail;
-  const uint32_t* zp_tail;
+  const uint32_t* wq_tail;  // DxPrep's
+  const void* constants;
   void* dx;            // [M][K]
   float* partial;
   int64_t M, N, K;
-  int ldy, group, dtype, sG, gmul;
+  int ldy, group, dtype;  // group: k of one scale (K for per-channel scales)
 };
 struct DxPlan {
   int mw;              // 32-token blocks of a wave: a tile is 64 mw tokens x 256 k

@@ -196,7 +196,7 @@ def test_infinite_dy_beside_ragged_rows():
 @pytest.mark.parametrize("M", [70, 600])
 def test_graph_replays(M):
     case = Grad(M, 264, 512, 64, O.BF16, False, 3, 16, "mixed")
-    ws = torch.zeros(L.w4a16_lora_backward_workspace_size(M, 264, 512, 3, 16), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(L.w4a16_lora_backward_workspace_size(M, 264, 512, 64, 3, 16, L.W4A16_BF16), dtype=torch.uint8, device="cuda")
     out = tuple(torch.empty_like(t) for t in (case.d.x, case.t_la, case.t_lb))
     s = torch.cuda.Stream()
     g = torch.cuda.CUDAGraph()
