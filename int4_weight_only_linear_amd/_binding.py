@@ -152,6 +152,7 @@ def w4a16_last_error() -> str:
 def w4a16_reload_tuning() -> None:
     """Re-read the tuning environment variables (the library reads them once)."""
     lib.w4a16_reload_tuning()
+    _sizes.clear()
 
 
 # ------------------------------------------------------------------ host ---
@@ -232,9 +233,15 @@ def w4a16_check_args(x_ptr, wq_ptr, s_ptr, zp_ptr, bias_ptr, y_ptr, M, N, K, gro
 _ZP_MSG = "Zero points must be int32 or uint32 (packed 8x uint4 along dim 0), got {}"
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _act_code(t) -> int:
@@ -257,6 +264,48 @@ def _require_device(t, name, device):
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _require_all(device, *named):
+    """_require_device for (tensor, name) pairs: one pass over those that pass."""
+    index = device.index
+    for t, name in named:
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            _require_device(t, name, device)
+
+
+def _invoke(device, fn, *args):
+    """Call a device entry point with `device` current (it mostly is already:
+    the check costs a tenth of a device guard) and raise on its error."""
+    torch = _torch()
+    if torch._C._cuda_getDevice() == device.index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status != W4A16_OK:
+        _check(status)
+
+
+def _raw_stream(device) -> int:
+    """The current stream's handle, without building a Stream object."""
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
+
+
+# workspace sizes by (entry point, device, sizes): the plan behind one is the
+# same for every call of these sizes until the tuning variables are read again
+_sizes: dict = {}
+
+
+def _size_of(device, fn, *args) -> int:
+    key = (fn.__name__, device.index, args)
+    n = _sizes.get(key)
+    if n is None:
+        torch = _torch()
+        with torch.cuda.device(device):
+            n = int(fn(*args))
+        _sizes[key] = n
+    return n
 
 
 _ws_lock = threading.Lock()
@@ -297,23 +346,23 @@ def _linear_args(x, wq, scales, zp, bias, group_size, out):
     if group_size <= 0 or K % group_size:
         raise ValueError(f"K={K} is not a multiple of group_size={group_size}")
     G = K // group_size
-    if tuple(scales.shape) != (N, G):
+    if scales.shape != (N, G):
         raise ValueError(f"scales are {tuple(scales.shape)}, expected {(N, G)}")
     if zp is not None:
         if zp.dtype not in (torch.int32, getattr(torch, "uint32", torch.int32)):
             raise RuntimeError(_ZP_MSG.format(zp.dtype))
-        if tuple(zp.shape) != (N // 8, G) or N % 8:
+        if zp.shape != (N // 8, G) or N % 8:
             raise ValueError(f"zp is {tuple(zp.shape)}, expected {(N // 8, G)} (N % 8 == 0)")
     if bias is not None:
         if bias.dtype != x.dtype or tuple(bias.shape) != (N,):
             raise ValueError(f"bias must be {x.dtype} [{N}]")
     device = x.device
-    for t, name in ((x, "x"), (wq, "wq"), (scales, "scales"), (zp, "zp"), (bias, "bias")):
-        _require_device(t, name, device)
+    _require_device(x, "x", device)
+    _require_all(device, (wq, "wq"), (scales, "scales"), (zp, "zp"), (bias, "bias"))
     if out is None:
         out = torch.empty((M, N), dtype=x.dtype, device=device)
     else:
-        if out.dtype != x.dtype or tuple(out.shape) != (M, N):
+        if out.dtype != x.dtype or out.shape != (M, N):
             raise ValueError(f"out must be {x.dtype} [{M}, {N}]")
         _require_device(out, "out", device)
     return dt, M, N, K, out
@@ -474,17 +523,16 @@ def _adapter_args(x, la, lb, ids, alpha, M, N, K):
     torch = _torch()
     if la.dim() != 3 or la.shape[2] != K:
         raise ValueError(f"la is {tuple(la.shape)}, expected [S, R, {K}]")
-    S, R = la.shape[0], la.shape[1]
-    if tuple(lb.shape) != (S, N, R):
+    S, R, _ = la.shape
+    if lb.shape != (S, N, R):
         raise ValueError(f"lb is {tuple(lb.shape)}, expected {(S, N, R)}")
     if la.dtype != x.dtype or lb.dtype != x.dtype:
         raise TypeError(f"la and lb must be {x.dtype}, got {la.dtype} and {lb.dtype}")
-    if ids.dtype != torch.int32 or tuple(ids.shape) != (M,):
+    if ids.dtype != torch.int32 or ids.shape != (M,):
         raise TypeError(f"ids must be int32 [{M}], got {ids.dtype} {tuple(ids.shape)}")
-    if alpha is not None and (alpha.dtype != torch.float32 or tuple(alpha.shape) != (S,)):
+    if alpha is not None and (alpha.dtype != torch.float32 or alpha.shape != (S,)):
         raise TypeError(f"alpha must be float32 [{S}]")
-    for t, name in ((la, "la"), (lb, "lb"), (ids, "ids"), (alpha, "alpha")):
-        _require_device(t, name, x.device)
+    _require_all(x.device, (la, "la"), (lb, "lb"), (ids, "ids"), (alpha, "alpha"))
     return S, R
 
 
@@ -497,17 +545,17 @@ def w4a16_lora_linear(x, wq, scales, la, lb, ids, zp=None, bias=None, alpha=None
     torch = _torch()
     dt, M, N, K, out = _linear_args(x, wq, scales, zp, bias, group_size, out)
     S, R = _adapter_args(x, la, lb, ids, alpha, M, N, K)
-    u = torch.empty((M, R), dtype=torch.float32, device=x.device) if save_u else None
-    stream = torch.cuda.current_stream(x.device).cuda_stream
-    with torch.cuda.device(x.device):
-        if workspace is None:
-            workspace = _workspace(x.device, stream, w4a16_lora_workspace_size(M, N, K, group_size, dt, zp is not None,
-                                                                               R, save_u))
-        ws_ptr = None if workspace is None else workspace.data_ptr()
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(lib.w4a16_lora_linear(x.data_ptr(), wq.data_ptr(), scales.data_ptr(), _ptr(zp), _ptr(bias),
-                                     la.data_ptr(), lb.data_ptr(), ids.data_ptr(), _ptr(alpha), out.data_ptr(),
-                                     _ptr(u), M, N, K, group_size, S, R, dt, ws_ptr, ws_bytes, stream))
+    device = x.device
+    u = torch.empty((M, R), dtype=torch.float32, device=device) if save_u else None
+    stream = _raw_stream(device)
+    if workspace is None:
+        workspace = _workspace(device, stream, _size_of(device, lib.w4a16_lora_workspace_size, M, N, K, group_size, dt,
+                                                        int(zp is not None), R, int(save_u)))
+    ws_ptr = None if workspace is None else workspace.data_ptr()
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _invoke(device, lib.w4a16_lora_linear, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), _ptr(zp), _ptr(bias),
+            la.data_ptr(), lb.data_ptr(), ids.data_ptr(), _ptr(alpha), out.data_ptr(), _ptr(u), M, N, K, group_size, S, R,
+            dt, ws_ptr, ws_bytes, stream)
     return (out, u) if save_u else out
 
 
@@ -528,28 +576,29 @@ def w4a16_lora_backward(dy, x, u, wq, scales, la, lb, ids, zp=None, alpha=None, 
     # the projection's own checks (dy stands where its output would)
     dt, M, N, K, _ = _linear_args(x, wq, scales, zp, None, group_size, dy)
     S, R = _adapter_args(x, la, lb, ids, alpha, M, N, K)
-    if u.dtype != torch.float32 or tuple(u.shape) != (M, R):
+    device = x.device
+    if u.dtype != torch.float32 or u.shape != (M, R):
         raise TypeError(f"u must be float32 {(M, R)}, got {u.dtype} {tuple(u.shape)}")
-    _require_device(u, "u", x.device)
+    _require_device(u, "u", device)
     if out is None:
-        out = (torch.empty_like(x) if need_dx else None, torch.empty_like(la), torch.empty_like(lb))
-    dx, dla, dlb = out
-    for t, like, name in ((dx, x, "dx"), (dla, la, "dla"), (dlb, lb, "dlb")):
-        if t is not None and (t.dtype != x.dtype or t.shape != like.shape):
-            raise ValueError(f"{name} must be {x.dtype} {tuple(like.shape)}")
-        _require_device(t, name, x.device)
-    if dla is None or dlb is None:
-        raise ValueError("dla and dlb must be given")
-    stream = torch.cuda.current_stream(x.device).cuda_stream
-    with torch.cuda.device(x.device):
-        if workspace is None:
-            workspace = _workspace(x.device, stream, w4a16_lora_backward_workspace_size(M, N, K, group_size, S, R, dt))
-        ws_ptr = None if workspace is None else workspace.data_ptr()
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(lib.w4a16_lora_backward(dy.data_ptr(), x.data_ptr(), u.data_ptr(), wq.data_ptr(), scales.data_ptr(),
-                                       _ptr(zp), la.data_ptr(), lb.data_ptr(), ids.data_ptr(), _ptr(alpha), _ptr(dx),
-                                       dla.data_ptr(), dlb.data_ptr(), M, N, K, group_size, S, R, dt, ws_ptr, ws_bytes,
-                                       stream))
+        dx, dla, dlb = torch.empty_like(x) if need_dx else None, torch.empty_like(la), torch.empty_like(lb)
+    else:
+        dx, dla, dlb = out
+        if dla is None or dlb is None:
+            raise ValueError("dla and dlb must be given")
+        for t, like, name in ((dx, x, "dx"), (dla, la, "dla"), (dlb, lb, "dlb")):
+            if t is not None and (t.dtype != x.dtype or t.shape != like.shape):
+                raise ValueError(f"{name} must be {x.dtype} {tuple(like.shape)}")
+            _require_device(t, name, device)
+    stream = _raw_stream(device)
+    if workspace is None:
+        workspace = _workspace(device, stream, _size_of(device, lib.w4a16_lora_backward_workspace_size, M, N, K, group_size,
+                                                        S, R, dt))
+    ws_ptr = None if workspace is None else workspace.data_ptr()
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _invoke(device, lib.w4a16_lora_backward, dy.data_ptr(), x.data_ptr(), u.data_ptr(), wq.data_ptr(), scales.data_ptr(),
+            _ptr(zp), la.data_ptr(), lb.data_ptr(), ids.data_ptr(), _ptr(alpha), _ptr(dx), dla.data_ptr(), dlb.data_ptr(),
+            M, N, K, group_size, S, R, dt, ws_ptr, ws_bytes, stream)
     return dx, dla, dlb
 
 
@@ -560,6 +609,7 @@ class AdamwPlan:
 
     def __init__(self, info, table, tensors, device):
         self.info, self.table, self.tensors, self.device = info, table, tensors, device
+        self.info_ref = ctypes.byref(info)
 
     @property
     def state_bits(self) -> int:
@@ -633,11 +683,8 @@ def w4a16_adamw_step(plan: AdamwPlan, *, lr: float, betas=(0.9, 0.999), eps: flo
                      step: int, grad_scale: float = 1.0, seed: int = 0) -> None:
     """One AdamW step (number `step`, from 1) over the plan's tensors, on the current stream.
     Moments in 8 bits are rounded with a dither that seed chooses: give every step another."""
-    torch = _torch()
-    stream = torch.cuda.current_stream(plan.device).cuda_stream
-    with torch.cuda.device(plan.device):
-        _check(lib.w4a16_adamw_step(plan.table.data_ptr(), ctypes.byref(plan.info), lr, betas[0], betas[1], eps,
-                                    weight_decay, step, grad_scale, seed & 0xFFFFFFFF, stream))
+    _invoke(plan.device, lib.w4a16_adamw_step, plan.table.data_ptr(), plan.info_ref, lr, betas[0], betas[1], eps,
+            weight_decay, step, grad_scale, seed & 0xFFFFFFFF, _raw_stream(plan.device))
 
 
 def w4a16_adamw_moments(plan: AdamwPlan, m=None, v=None):
@@ -649,10 +696,9 @@ def w4a16_adamw_moments(plan: AdamwPlan, m=None, v=None):
     if v is None:
         v = torch.empty(plan.blocks * 256, dtype=torch.float32, device=plan.device)
     for t, name in ((m, "m"), (v, "v")):
-        if t.dtype != torch.float32 or tuple(t.shape) != (plan.blocks * 256,):
+        if t.dtype != torch.float32 or t.shape != (plan.blocks * 256,):
             raise ValueError(f"{name} must be float32 [{plan.blocks * 256}]")
         _require_device(t, name, plan.device)
-    stream = torch.cuda.current_stream(plan.device).cuda_stream
-    with torch.cuda.device(plan.device):
-        _check(lib.w4a16_adamw_moments(plan.table.data_ptr(), ctypes.byref(plan.info), m.data_ptr(), v.data_ptr(), stream))
+    _invoke(plan.device, lib.w4a16_adamw_moments, plan.table.data_ptr(), plan.info_ref, m.data_ptr(), v.data_ptr(),
+            _raw_stream(plan.device))
     return m, v
