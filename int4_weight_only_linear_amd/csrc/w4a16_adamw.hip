@@ -31,69 +31,83 @@ namespace w4a16 {
 
 namespace {
 
-constexpr int kBlocksPerWave = kAdamwChunkBlocks / 4;
+// Tensors' pointers come out of the table, so their address space has to be
+// said: the accesses would be flat ones, which also wait for LDS.
+#define W4A16_GLOBAL __attribute__((address_space(1)))
 
 // four consecutive elements as they lie in memory, and their fp32 values
 template <int DT>
 struct Quad {
   using raw = u32x2;
-  __device__ static f32x4 value(const raw& q) {
-    return f32x4{act_to_f32<DT>((uint16_t)q[0]), act_to_f32<DT>((uint16_t)(q[0] >> 16)),
-                 act_to_f32<DT>((uint16_t)q[1]), act_to_f32<DT>((uint16_t)(q[1] >> 16))};
+  using elem = uint16_t;
+  __device__ static f32x4 value(raw q) {
+    const uint32_t a = q[0], b = q[1];
+    return f32x4{act_to_f32<DT>((uint16_t)a), act_to_f32<DT>((uint16_t)(a >> 16)), act_to_f32<DT>((uint16_t)b),
+                 act_to_f32<DT>((uint16_t)(b >> 16))};
   }
   __device__ static raw pack(const f32x4& v) {
     return raw{f32x2_to_act_pair<DT>(v[0], v[1]), f32x2_to_act_pair<DT>(v[2], v[3])};
   }
-  __device__ static float one(const void* p, size_t i) { return act_to_f32<DT>(static_cast<const uint16_t*>(p)[i]); }
-  __device__ static void put(void* p, size_t i, float v) { static_cast<uint16_t*>(p)[i] = f32_to_act<DT>(v); }
+  __device__ static float one(elem e) { return act_to_f32<DT>(e); }
+  __device__ static elem narrow(float v) { return f32_to_act<DT>(v); }
 };
 template <>
 struct Quad<DT_F32> {
   using raw = f32x4;
-  __device__ static f32x4 value(const raw& q) { return q; }
+  using elem = float;
+  __device__ static f32x4 value(raw q) { return q; }
   __device__ static raw pack(const f32x4& v) { return v; }
-  __device__ static float one(const void* p, size_t i) { return static_cast<const float*>(p)[i]; }
-  __device__ static void put(void* p, size_t i, float v) { static_cast<float*>(p)[i] = v; }
+  __device__ static float one(elem e) { return e; }
+  __device__ static elem narrow(float v) { return v; }
 };
 
-// n valid elements from i on (4: a whole quad); `vec`: the tensor takes vector accesses
-template <int DT>
-__device__ __forceinline__ f32x4 load4(const void* p, size_t i, int n, bool vec) {
+// WHOLE: the quad is inside the tensor and takes one vector access;
+// otherwise the first n of its elements, one by one
+template <int DT, bool WHOLE>
+__device__ __forceinline__ f32x4 load4(const void* p, size_t i, int n) {
   using Q = Quad<DT>;
-  if (vec && n == 4) return Q::value(reinterpret_cast<const typename Q::raw*>(p)[i >> 2]);
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if constexpr (WHOLE) {
+    return Q::value(((W4A16_GLOBAL const typename Q::raw*)p)[i >> 2]);
+  } else {
+    f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < n) v[e] = Q::one(p, i + e);
-  return v;
+    for (int e = 0; e < 4; ++e)
+      if (e < n) v[e] = Q::one(((W4A16_GLOBAL const typename Q::elem*)p)[i + e]);
+    return v;
+  }
 }
-template <int DT>
-__device__ __forceinline__ void store4(void* p, size_t i, int n, bool vec, const f32x4& v) {
+template <int DT, bool WHOLE>
+__device__ __forceinline__ void store4(void* p, size_t i, int n, const f32x4& v) {
   using Q = Quad<DT>;
-  if (vec && n == 4) {
-    reinterpret_cast<typename Q::raw*>(p)[i >> 2] = Q::pack(v);
-    return;
+  if constexpr (WHOLE) {
+    ((W4A16_GLOBAL typename Q::raw*)p)[i >> 2] = Q::pack(v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) ((W4A16_GLOBAL typename Q::elem*)p)[i + e] = Q::narrow(v[e]);
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < n) Q::put(p, i + e, v[e]);
 }
-__device__ __forceinline__ uint32_t load_codes(const void* p, size_t i, int n, bool vec) {
-  if (vec && n == 4) return static_cast<const uint32_t*>(p)[i >> 2];
-  uint32_t w = 0;
+template <bool WHOLE>
+__device__ __forceinline__ uint32_t load_codes(const void* p, size_t i, int n) {
+  if constexpr (WHOLE) {
+    return ((W4A16_GLOBAL const uint32_t*)p)[i >> 2];
+  } else {
+    uint32_t w = 0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < n) w |= (uint32_t)static_cast<const uint8_t*>(p)[i + e] << (8 * e);
-  return w;
-}
-__device__ __forceinline__ void store_codes(void* p, size_t i, int n, bool vec, uint32_t w) {
-  if (vec && n == 4) {
-    static_cast<uint32_t*>(p)[i >> 2] = w;
-    return;
+    for (int e = 0; e < 4; ++e)
+      if (e < n) w |= (uint32_t)((W4A16_GLOBAL const uint8_t*)p)[i + e] << (8 * e);
+    return w;
   }
+}
+template <bool WHOLE>
+__device__ __forceinline__ void store_codes(void* p, size_t i, int n, uint32_t w) {
+  if constexpr (WHOLE) {
+    ((W4A16_GLOBAL uint32_t*)p)[i >> 2] = w;
+  } else {
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < n) static_cast<uint8_t*>(p)[i + e] = (uint8_t)(w >> (8 * e));
+    for (int e = 0; e < 4; ++e)
+      if (e < n) ((W4A16_GLOBAL uint8_t*)p)[i + e] = (uint8_t)(w >> (8 * e));
+  }
 }
 
 __device__ __forceinline__ float decode_m(uint32_t w, int e, float ms) {
@@ -105,12 +119,23 @@ __device__ __forceinline__ float decode_r(uint32_t w, int e, float rs) {
   return (c * c) * rs;
 }
 
-// the largest of the wave's values, NaN if one of them is
-__device__ __forceinline__ float wave_max(float v) {
-  const bool nan = __any(v != v);
-#pragma unroll
-  for (int d = 32; d; d >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, d));
-  return nan ? __builtin_nanf("") : v;
+// The largest of the wave's non-negative values by their bits, which order as
+// the values do and put a NaN above them all: four rotations inside the
+// 16-lane rows, then the rows.
+template <int CTRL>
+__device__ __forceinline__ uint32_t rotate(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+__device__ __forceinline__ float wave_max(uint32_t v) {
+  v = max(v, rotate<0x128>(v));
+  v = max(v, rotate<0x124>(v));
+  v = max(v, rotate<0x122>(v));
+  v = max(v, rotate<0x121>(v));
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max((uint32_t)a[0], (uint32_t)a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  v = max((uint32_t)b[0], (uint32_t)b[1]);
+  return __builtin_bit_cast(float, (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
 }
 
 // a published 32-bit integer finaliser (shift, exclusive or, multiply; the
@@ -129,102 +154,123 @@ __device__ __forceinline__ AdamwChunk chunk_of(const void* table, int tensors) {
   return c[blockIdx.x];
 }
 
-template <int PD, int GD, bool EIGHT>
-__global__ __launch_bounds__(256) void adamw_kernel(const void* __restrict__ table, int tensors, AdamwScalars h) {
+// one lane's quad of a block, before and after the step
+template <bool EIGHT>
+struct State {
+  f32x4 p, g, m, v;
+  uint32_t cm, cv;  // 8 bits: codes, and the block's scales
+  float ms, rs;
+};
+
+template <int PD, int GD, bool EIGHT, bool WHOLE>
+__device__ __forceinline__ void load_state(const AdamwTensor& t, int64_t b, int lane, int n, State<EIGHT>& s) {
+  const size_t i = (size_t)b * 256 + 4 * lane;
+  s.p = load4<PD, WHOLE>(t.param, i, n);
+  s.g = load4<GD, WHOLE>(t.grad, i, n);
+  if constexpr (EIGHT) {
+    s.cm = load_codes<WHOLE>(t.m, i, n);
+    s.cv = load_codes<WHOLE>(t.v, i, n);
+    s.ms = ((W4A16_GLOBAL const float*)t.m_scale)[b];
+    s.rs = ((W4A16_GLOBAL const float*)t.v_scale)[b];
+  } else {
+    s.m = load4<DT_F32, WHOLE>(t.m, i, n);
+    s.v = load4<DT_F32, WHOLE>(t.v, i, n);
+  }
+}
+
+template <int PD, bool EIGHT, bool WHOLE>
+__device__ __forceinline__ void step_and_store(const AdamwTensor& t, int64_t b, int lane, int n, const AdamwScalars& h,
+                                               State<EIGHT>& s) {
+  const size_t i = (size_t)b * 256 + 4 * lane;
+  float r[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if constexpr (EIGHT) {
+      s.m[e] = decode_m(s.cm, e, s.ms);
+      r[e] = decode_r(s.cv, e, s.rs);
+      s.v[e] = r[e] * r[e];
+    }
+    const float g = s.g[e] * h.grad_scale;
+    s.m[e] = s.m[e] * h.beta1 + g * h.one_beta1;
+    s.v[e] = s.v[e] * h.beta2 + (g * g) * h.one_beta2;
+    r[e] = __builtin_sqrtf(s.v[e]);
+    s.p[e] = s.p[e] * h.decay - (s.m[e] / (r[e] * h.root + h.eps)) * h.rate;
+  }
+  store4<PD, WHOLE>(t.param, i, n, s.p);
+  if (t.copy) {
+    if (t.copy_dtype == DT_F16)
+      store4<DT_F16, WHOLE>(t.copy, i, n, s.p);
+    else
+      store4<DT_BF16, WHOLE>(t.copy, i, n, s.p);
+  }
+  if constexpr (EIGHT) {
+    uint32_t am = 0, ar = 0;  // elements past the tensor's end are zero
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      am = max(am, __builtin_bit_cast(uint32_t, __builtin_fabsf(s.m[e])));
+      ar = max(ar, __builtin_bit_cast(uint32_t, __builtin_fabsf(r[e])));
+    }
+    const float ms = wave_max(am), rs = wave_max(ar);
+    const float im = ms > 0x1p-100f ? 1.f / ms : 0.f, ir = rs > 0x1p-100f ? 1.f / rs : 0.f;
+    uint32_t cm = 0, cv = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint32_t d = mix32((uint32_t)((t.first_block + b) * 256 + 4 * lane + e) + h.seed);
+      const float qm = __builtin_floorf(__builtin_sqrtf(__builtin_fabsf(s.m[e]) * im) * 127.f + (float)(d & 0xFFFFu) * 0x1p-16f);
+      const float qv = __builtin_floorf(__builtin_sqrtf(r[e] * ir) * 255.f + (float)(d >> 16) * 0x1p-16f);
+      const int c = (int)__builtin_fminf(qm, 127.f);
+      const int u = (int)__builtin_fminf(r[e] > 0.f ? __builtin_fmaxf(qv, 1.f) : qv, 255.f);
+      cm |= (uint32_t)(uint8_t)(s.m[e] < 0.f ? -c : c) << (8 * e);
+      cv |= (uint32_t)(uint8_t)u << (8 * e);
+    }
+    store_codes<WHOLE>(t.m, i, n, cm);
+    store_codes<WHOLE>(t.v, i, n, cv);
+    if (lane == 0) {
+      ((W4A16_GLOBAL float*)t.m_scale)[b] = ms;
+      ((W4A16_GLOBAL float*)t.v_scale)[b] = rs;
+    }
+  } else {
+    store4<DT_F32, WHOLE>(t.m, i, n, s.m);
+    store4<DT_F32, WHOLE>(t.v, i, n, s.v);
+  }
+}
+
+// BPW blocks a wave: one in small tables, so that they fill the CUs, four in
+// large ones, whose loads are all issued before the first step.
+template <int PD, int GD, bool EIGHT, int BPW>
+__global__ __launch_bounds__(256) void adamw_kernel(const void* __restrict__ table, int tensors, const AdamwScalars h) {
   const AdamwChunk ch = chunk_of(table, tensors);
   const AdamwTensor t = static_cast<const AdamwTensor*>(table)[ch.tensor];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const bool vec = t.vec != 0;
+  if (t.vec && ((int64_t)ch.block + 4 * BPW) * 256 <= t.n) {
+    State<EIGHT> s[BPW];
 #pragma unroll
-  for (int k = 0; k < kBlocksPerWave; ++k) {
+    for (int k = 0; k < BPW; ++k) load_state<PD, GD, EIGHT, true>(t, ch.block + wave + 4 * k, lane, 4, s[k]);
+#pragma unroll
+    for (int k = 0; k < BPW; ++k) step_and_store<PD, EIGHT, true>(t, ch.block + wave + 4 * k, lane, 4, h, s[k]);
+    return;
+  }
+  for (int k = 0; k < BPW; ++k) {
     const int64_t b = ch.block + wave + 4 * k;
     const int64_t left = t.n - b * 256;  // elements from this block on
     if (left <= 0) return;
-    const size_t i = (size_t)b * 256 + 4 * lane;
     const int n = (int)min((int64_t)4, max((int64_t)0, left - 4 * lane));
-    f32x4 p = load4<PD>(t.param, i, n, vec);
-    const f32x4 g = load4<GD>(t.grad, i, n, vec);
-    f32x4 m, v, r;
-    if constexpr (EIGHT) {
-      const uint32_t cm = load_codes(t.m, i, n, vec), cv = load_codes(t.v, i, n, vec);
-      const float ms = t.m_scale[b], rs = t.v_scale[b];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        m[e] = decode_m(cm, e, ms);
-        r[e] = decode_r(cv, e, rs);
-        v[e] = r[e] * r[e];
-      }
-    } else {
-      m = load4<DT_F32>(t.m, i, n, vec);
-      v = load4<DT_F32>(t.v, i, n, vec);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float ge = g[e] * h.grad_scale;
-      m[e] = m[e] * h.beta1 + ge * h.one_beta1;
-      v[e] = v[e] * h.beta2 + (ge * ge) * h.one_beta2;
-      r[e] = __builtin_sqrtf(v[e]);
-      p[e] = p[e] * h.decay - (m[e] / (r[e] * h.root + h.eps)) * h.rate;
-    }
-    store4<PD>(t.param, i, n, vec, p);
-    if (t.copy) {
-      if (t.copy_dtype == DT_F16)
-        store4<DT_F16>(t.copy, i, n, vec, p);
-      else
-        store4<DT_BF16>(t.copy, i, n, vec, p);
-    }
-    if constexpr (EIGHT) {
-      float am = 0.f, ar = 0.f;  // elements past the tensor's end are zero
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x = __builtin_fabsf(m[e]);
-        am = am != am || x != x ? __builtin_nanf("") : __builtin_fmaxf(am, x);
-        ar = ar != ar || r[e] != r[e] ? __builtin_nanf("") : __builtin_fmaxf(ar, r[e]);
-      }
-      const float ms = wave_max(am), rs = wave_max(ar);
-      const float im = ms > 0x1p-100f ? 1.f / ms : 0.f, ir = rs > 0x1p-100f ? 1.f / rs : 0.f;
-      uint32_t cm = 0, cv = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t d = mix32((uint32_t)((t.first_block + b) * 256 + 4 * lane + e) + h.seed);
-        const float qm = __builtin_floorf(__builtin_sqrtf(__builtin_fabsf(m[e]) * im) * 127.f + (float)(d & 0xFFFFu) * 0x1p-16f);
-        const float qv = __builtin_floorf(__builtin_sqrtf(r[e] * ir) * 255.f + (float)(d >> 16) * 0x1p-16f);
-        const int c = (int)__builtin_fminf(qm, 127.f);
-        const int u = (int)__builtin_fminf(r[e] > 0.f ? __builtin_fmaxf(qv, 1.f) : qv, 255.f);
-        cm |= (uint32_t)(uint8_t)(m[e] < 0.f ? -c : c) << (8 * e);
-        cv |= (uint32_t)(uint8_t)u << (8 * e);
-      }
-      store_codes(t.m, i, n, vec, cm);
-      store_codes(t.v, i, n, vec, cv);
-      if (lane == 0) {
-        t.m_scale[b] = ms;
-        t.v_scale[b] = rs;
-      }
-    } else {
-      store4<DT_F32>(t.m, i, n, vec, m);
-      store4<DT_F32>(t.v, i, n, vec, v);
-    }
+    State<EIGHT> s;
+    load_state<PD, GD, EIGHT, false>(t, b, lane, n, s);
+    step_and_store<PD, EIGHT, false>(t, b, lane, n, h, s);
   }
 }
 
 // the moments the codes stand for, blocks in the table's order, zero past a tensor's end
+template <int BPW>
 __global__ __launch_bounds__(256) void moments_kernel(const void* __restrict__ table, int tensors, float* __restrict__ mo,
                                                       float* __restrict__ vo) {
   const AdamwChunk ch = chunk_of(table, tensors);
   const AdamwTensor t = static_cast<const AdamwTensor*>(table)[ch.tensor];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const bool vec = t.vec != 0;
-#pragma unroll
-  for (int k = 0; k < kBlocksPerWave; ++k) {
-    const int64_t b = ch.block + wave + 4 * k;
-    const int64_t left = t.n - b * 256;
-    if (left <= 0) return;
-    const size_t i = (size_t)b * 256 + 4 * lane;
-    const int n = (int)min((int64_t)4, max((int64_t)0, left - 4 * lane));
-    const uint32_t cm = load_codes(t.m, i, n, vec), cv = load_codes(t.v, i, n, vec);
-    const float ms = t.m_scale[b], rs = t.v_scale[b];
+  auto block = [&](int64_t b, int n, uint32_t cm, uint32_t cv, float ms, float rs) {
     f32x4 m, v;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -235,39 +281,73 @@ __global__ __launch_bounds__(256) void moments_kernel(const void* __restrict__ t
     const size_t o = ((size_t)(t.first_block + b) * 256 + 4 * lane) >> 2;
     reinterpret_cast<f32x4*>(mo)[o] = m;
     reinterpret_cast<f32x4*>(vo)[o] = v;
+  };
+  auto scale = [&](const float* p, int64_t b) { return ((W4A16_GLOBAL const float*)p)[b]; };
+  if (t.vec && ((int64_t)ch.block + 4 * BPW) * 256 <= t.n) {
+    uint32_t cm[BPW], cv[BPW];
+    float ms[BPW], rs[BPW];
+#pragma unroll
+    for (int k = 0; k < BPW; ++k) {
+      const int64_t b = ch.block + wave + 4 * k;
+      cm[k] = load_codes<true>(t.m, (size_t)b * 256 + 4 * lane, 4);
+      cv[k] = load_codes<true>(t.v, (size_t)b * 256 + 4 * lane, 4);
+      ms[k] = scale(t.m_scale, b);
+      rs[k] = scale(t.v_scale, b);
+    }
+#pragma unroll
+    for (int k = 0; k < BPW; ++k) block(ch.block + wave + 4 * k, 4, cm[k], cv[k], ms[k], rs[k]);
+    return;
+  }
+  for (int k = 0; k < BPW; ++k) {
+    const int64_t b = ch.block + wave + 4 * k;
+    const int64_t left = t.n - b * 256;
+    if (left <= 0) return;
+    const size_t i = (size_t)b * 256 + 4 * lane;
+    const int n = (int)min((int64_t)4, max((int64_t)0, left - 4 * lane));
+    block(b, n, load_codes<false>(t.m, i, n), load_codes<false>(t.v, i, n), scale(t.m_scale, b), scale(t.v_scale, b));
   }
 }
 
-template <int PD, int GD>
-hipError_t launch_bits(const void* table, int tensors, int chunks, int bits, const AdamwScalars& h, hipStream_t s) {
-  if (bits == 8)
-    hipLaunchKernelGGL((adamw_kernel<PD, GD, true>), dim3(chunks), dim3(256), 0, s, table, tensors, h);
+template <int PD, int GD, bool EIGHT>
+hipError_t launch_bpw(const void* table, int tensors, int chunks, int bpw, const AdamwScalars& h, hipStream_t s) {
+  if (bpw == 1)
+    hipLaunchKernelGGL((adamw_kernel<PD, GD, EIGHT, 1>), dim3(chunks), dim3(256), 0, s, table, tensors, h);
   else
-    hipLaunchKernelGGL((adamw_kernel<PD, GD, false>), dim3(chunks), dim3(256), 0, s, table, tensors, h);
+    hipLaunchKernelGGL((adamw_kernel<PD, GD, EIGHT, 4>), dim3(chunks), dim3(256), 0, s, table, tensors, h);
   return hipGetLastError();
 }
+template <int PD, int GD>
+hipError_t launch_bits(const void* table, int tensors, int chunks, int bpw, int bits, const AdamwScalars& h, hipStream_t s) {
+  return bits == 8 ? launch_bpw<PD, GD, true>(table, tensors, chunks, bpw, h, s)
+                   : launch_bpw<PD, GD, false>(table, tensors, chunks, bpw, h, s);
+}
 template <int PD>
-hipError_t launch_grad(const void* table, int tensors, int chunks, int gd, int bits, const AdamwScalars& h, hipStream_t s) {
+hipError_t launch_grad(const void* table, int tensors, int chunks, int bpw, int gd, int bits, const AdamwScalars& h,
+                       hipStream_t s) {
   switch (gd) {
-    case DT_F16: return launch_bits<PD, DT_F16>(table, tensors, chunks, bits, h, s);
-    case DT_BF16: return launch_bits<PD, DT_BF16>(table, tensors, chunks, bits, h, s);
-    default: return launch_bits<PD, DT_F32>(table, tensors, chunks, bits, h, s);
+    case DT_F16: return launch_bits<PD, DT_F16>(table, tensors, chunks, bpw, bits, h, s);
+    case DT_BF16: return launch_bits<PD, DT_BF16>(table, tensors, chunks, bpw, bits, h, s);
+    default: return launch_bits<PD, DT_F32>(table, tensors, chunks, bpw, bits, h, s);
   }
 }
 
 }  // namespace
 
-hipError_t launch_adamw(const void* table, int tensors, int chunks, int param_dtype, int grad_dtype, int bits,
-                        const AdamwScalars& h, hipStream_t s) {
+hipError_t launch_adamw(const void* table, int tensors, int chunks, int blocks_per_wave, int param_dtype, int grad_dtype,
+                        int bits, const AdamwScalars& h, hipStream_t s) {
   switch (param_dtype) {
-    case DT_F16: return launch_grad<DT_F16>(table, tensors, chunks, grad_dtype, bits, h, s);
-    case DT_BF16: return launch_grad<DT_BF16>(table, tensors, chunks, grad_dtype, bits, h, s);
-    default: return launch_grad<DT_F32>(table, tensors, chunks, grad_dtype, bits, h, s);
+    case DT_F16: return launch_grad<DT_F16>(table, tensors, chunks, blocks_per_wave, grad_dtype, bits, h, s);
+    case DT_BF16: return launch_grad<DT_BF16>(table, tensors, chunks, blocks_per_wave, grad_dtype, bits, h, s);
+    default: return launch_grad<DT_F32>(table, tensors, chunks, blocks_per_wave, grad_dtype, bits, h, s);
   }
 }
 
-hipError_t launch_adamw_moments(const void* table, int tensors, int chunks, float* m, float* v, hipStream_t s) {
-  hipLaunchKernelGGL(moments_kernel, dim3(chunks), dim3(256), 0, s, table, tensors, m, v);
+hipError_t launch_adamw_moments(const void* table, int tensors, int chunks, int blocks_per_wave, float* m, float* v,
+                                hipStream_t s) {
+  if (blocks_per_wave == 1)
+    hipLaunchKernelGGL(moments_kernel<1>, dim3(chunks), dim3(256), 0, s, table, tensors, m, v);
+  else
+    hipLaunchKernelGGL(moments_kernel<4>, dim3(chunks), dim3(256), 0, s, table, tensors, m, v);
   return hipGetLastError();
 }
 

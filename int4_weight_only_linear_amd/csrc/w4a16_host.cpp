@@ -1028,20 +1028,25 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
 
 static int elem_bytes(int32_t dtype) { return dtype == W4A16_F32 ? 4 : 2; }
 
-// chunks of a list of tensors, or -1 where a size is out of range
-static int64_t adamw_chunks(const w4a16_adamw_tensor* t, int64_t count) {
-  int64_t chunks = 0;
+// blocks of a list of tensors and the chunks they are cut into, or -1 where a
+// size is out of range
+static int64_t adamw_chunks(const w4a16_adamw_tensor* t, int64_t count, int64_t* blocks) {
+  *blocks = 0;
   for (int64_t i = 0; i < count; ++i) {
     if (t[i].n < 0 || t[i].n > (int64_t(1) << 38)) return -1;
-    const int64_t blocks = (t[i].n + 255) / 256;
-    chunks += (blocks + w4a16::kAdamwChunkBlocks - 1) / w4a16::kAdamwChunkBlocks;
+    *blocks += (t[i].n + 255) / 256;
+    if (*blocks > (int64_t(1) << 40)) return -1;
   }
+  const int64_t per = 4 * w4a16::adamw_blocks_per_wave(*blocks);
+  int64_t chunks = 0;
+  for (int64_t i = 0; i < count; ++i) chunks += ((t[i].n + 255) / 256 + per - 1) / per;
   return chunks > INT32_MAX ? -1 : chunks;
 }
 
 size_t w4a16_adamw_table_size(const w4a16_adamw_tensor* tensors, int64_t count) {
   if (!tensors || count < 1 || count > INT32_MAX) return 0;
-  const int64_t chunks = adamw_chunks(tensors, count);
+  int64_t blocks = 0;
+  const int64_t chunks = adamw_chunks(tensors, count, &blocks);
   return chunks < 0 ? 0 : (size_t)count * sizeof(w4a16::AdamwTensor) + (size_t)chunks * sizeof(w4a16::AdamwChunk);
 }
 
@@ -1054,7 +1059,8 @@ w4a16_status w4a16_adamw_table(const w4a16_adamw_tensor* tensors, int64_t count,
     return fail(W4A16_ERR_INVALID_ARG, "adamw_table: moments are held in 8 or 32 bits, got %d", (int)state_bits);
   if (param_dtype < W4A16_F16 || param_dtype > W4A16_F32 || grad_dtype < W4A16_F16 || grad_dtype > W4A16_F32)
     return fail(W4A16_ERR_INVALID_ARG, "adamw_table: parameters and gradients must be fp16, bf16 or fp32");
-  const int64_t chunks = adamw_chunks(tensors, count);
+  int64_t total = 0;
+  const int64_t chunks = adamw_chunks(tensors, count, &total);
   if (chunks < 0) return fail(W4A16_ERR_INVALID_ARG, "adamw_table: a tensor's size is out of range");
   const size_t need = w4a16_adamw_table_size(tensors, count);
   if (table_bytes < need)
@@ -1091,7 +1097,7 @@ w4a16_status w4a16_adamw_table(const w4a16_adamw_tensor* tensors, int64_t count,
                      aligned(t.v, 4 * sb) && (!t.copy || aligned(t.copy, 8));
     out[i] = w4a16::AdamwTensor{t.param, t.grad, t.m, t.v, t.m_scale, t.v_scale, t.copy, t.n, first, copy_dtype, vec};
     const int64_t blocks = (t.n + 255) / 256;
-    for (int64_t b = 0; b < blocks; b += w4a16::kAdamwChunkBlocks) *ch++ = {(int32_t)i, (int32_t)b};
+    for (int64_t b = 0; b < blocks; b += 4 * w4a16::adamw_blocks_per_wave(total)) *ch++ = {(int32_t)i, (int32_t)b};
     first += blocks;
   }
   *plan = w4a16_adamw_plan{count, chunks, first, state_bits, param_dtype, grad_dtype, 0};
@@ -1131,7 +1137,8 @@ w4a16_status w4a16_adamw_step(const void* table, const w4a16_adamw_plan* plan, d
   h.root = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
   h.grad_scale = (float)grad_scale;
   h.seed = seed * 0x9E3779B9u;
-  const hipError_t e = w4a16::launch_adamw(table, (int)plan->tensors, (int)plan->chunks, plan->param_dtype,
+  const hipError_t e = w4a16::launch_adamw(table, (int)plan->tensors, (int)plan->chunks,
+                                           w4a16::adamw_blocks_per_wave(plan->blocks), plan->param_dtype,
                                            plan->grad_dtype, plan->state_bits, h, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(W4A16_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
   return ok();
@@ -1150,7 +1157,8 @@ w4a16_status w4a16_adamw_moments(const void* table, const w4a16_adamw_plan* plan
   const DeviceInfo* dev = nullptr;
   st = device_info(&dev);
   if (st != W4A16_OK) return st;
-  const hipError_t e = w4a16::launch_adamw_moments(table, (int)plan->tensors, (int)plan->chunks, m, v,
+  const hipError_t e = w4a16::launch_adamw_moments(table, (int)plan->tensors, (int)plan->chunks,
+                                                   w4a16::adamw_blocks_per_wave(plan->blocks), m, v,
                                                    static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(W4A16_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
   return ok();
