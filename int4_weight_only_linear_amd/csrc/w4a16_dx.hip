@@ -336,6 +336,12 @@ hipError_t launch_mw(const DxParams& prm, const LoraTerm& lora, int mw, hipStrea
 
 }  // namespace
 
+// Tile height and split of n: time model in microseconds, fitted to every
+// (height, split) timed on 14 shapes (M 32-2048, N and K 1216-28672, groups of
+// 32; mean error 5.9 %, its picks 2.3 % from the best on average, 13 % at
+// worst): a fixed part and a time per step and round of resident workgroups
+// (64-token tiles: 1.08 us alone on a CU, 1.56 us for two that share one),
+// and for a split its second launch and the partial sums' way through memory.
 DxPlan plan_dx(int64_t M, int64_t N, int64_t K, int cu_count) {
   DxPlan best{};
   double best_t = 0.0;
@@ -343,12 +349,15 @@ DxPlan plan_dx(int64_t M, int64_t N, int64_t K, int cu_count) {
   const int64_t tiles_k = (K + kBKX - 1) / kBKX;
   for (int mw : {4, 2, 1}) {
     const int64_t tiles = (M + 64 * mw - 1) / (64 * mw) * tiles_k;
-    for (int splits = 1; splits <= 16 && splits <= nsteps; ++splits) {
+    for (int splits = 1; splits <= 32 && splits <= nsteps; ++splits) {
       const int sps = (nsteps + splits - 1) / splits;
       if ((nsteps + sps - 1) / sps != splits) continue;
-      const int64_t rounds = (tiles * splits + cu_count - 1) / cu_count;
-      const double t = rounds * (sps * (0.35 + 0.35 * mw) + 2.0) +
-                       (splits > 1 ? 3.0 + (double)(splits + 1) * M * K * 4.0 / 3e6 : 0.0);
+      const int64_t units = tiles * splits;
+      const bool pairs = mw == 1 && units > cu_count;
+      const int64_t rounds = (units + cu_count * (pairs ? 2 : 1) - 1) / (cu_count * (pairs ? 2 : 1));
+      const double step = mw == 4 ? 1.6 : mw == 2 ? 1.19 : pairs ? 1.56 : 1.08;
+      const double fixed = mw == 4 ? 2.3 : mw == 2 ? 1.5 : 0.0;
+      const double t = rounds * (fixed + sps * step) + (splits > 1 ? 4.2 + 0.387e-6 * splits * (double)M * (double)K * 4.0 : 0.0);
       if (best.tiles == 0 || t < best_t) {
         best_t = t;
         best = DxPlan{mw, splits, sps, (int)tiles_k, (int)tiles};
