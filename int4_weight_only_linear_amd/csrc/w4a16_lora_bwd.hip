@@ -28,32 +28,52 @@ __global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int job = blockIdx.x;
   if (job < a.S) {
-    int* const counts = reinterpret_cast<int*>(lds);  // [4] below, [4] own, per wave
+    // batches of 8 x 256 ids, a batch's loads all issued at once (one load and
+    // two barriers per 256 ids made this the launch's critical path)
+    constexpr int B = 8;
+    int* const counts = reinterpret_cast<int*>(lds);  // [B][4] own per wave, [4] below
     const int s = job;
+    int id[B];
+    auto load = [&](int m0) {
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const int m = m0 + 256 * i + tid;
+        id[i] = m < a.M ? a.ids[m] : -1;
+      }
+    };
     int below = 0;
-    for (int m0 = 0; m0 < a.M; m0 += 256) {
-      const int m = m0 + tid, id = m < a.M ? a.ids[m] : -1;
-      below += __popcll(__ballot(id >= 0 && id < s));
+    for (int m0 = 0; m0 < a.M; m0 += 256 * B) {
+      load(m0);
+#pragma unroll
+      for (int i = 0; i < B; ++i) below += __popcll(__ballot(id[i] >= 0 && id[i] < s));
     }
-    if (lane == 0) counts[wave] = below;
+    if (lane == 0) counts[4 * B + wave] = below;
     __syncthreads();
-    const int before_all = counts[0] + counts[1] + counts[2] + counts[3];
+    const int before_all = counts[4 * B] + counts[4 * B + 1] + counts[4 * B + 2] + counts[4 * B + 3];
     const int first = (before_all + 31) / 32 * 32 + 32 * s;
     int at = first;
-    for (int m0 = 0; m0 < a.M; m0 += 256) {
-      const int m = m0 + tid;
-      const bool own = m < a.M && a.ids[m] == s;
-      const uint64_t mask = __ballot(own);
+    for (int m0 = 0; m0 < a.M; m0 += 256 * B) {
+      if (a.M > 256 * B) load(m0);  // (a single batch is still here)
+      uint64_t mask[B];
+#pragma unroll
+      for (int i = 0; i < B; ++i) mask[i] = __ballot(id[i] == s);
       __syncthreads();
-      if (lane == 0) counts[4 + wave] = __popcll(mask);
-      __syncthreads();
-      int before = 0, all = 0;
-      for (int w = 0; w < 4; ++w) {
-        before += w < wave ? counts[4 + w] : 0;
-        all += counts[4 + w];
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < B; ++i) counts[4 * i + wave] = __popcll(mask[i]);
       }
-      if (own) a.order[at + before + __popcll(mask & ((1ull << lane) - 1))] = m;
-      at += all;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        int before = at;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int n = counts[4 * i + w];
+          before += w < wave ? n : 0;
+          at += n;
+        }
+        if (id[i] == s) a.order[before + __popcll(mask[i] & ((1ull << lane) - 1))] = m0 + 256 * i + tid;
+      }
     }
     // nothing up to where the next adapter begins (the last: to the end; the
     // first: from the beginning, which is its own)
@@ -68,36 +88,47 @@ __global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n
   job -= a.S;
   if (job < a.S * tiles_n) {
     // lb[s][n0 + i][r] -> lb_t[s][r][n0 + i]
-    const int s = job / tiles_n, n0 = (job - s * tiles_n) * kTile;
-    const int rows = min(kTile, a.N - n0);
+    const int s = job / tiles_n, n0 = (job - s * tiles_n) * kTile, R8 = a.R >> 3;
     const uint16_t* src = a.lb + ((size_t)s * a.N + n0) * a.R;
-    for (int i = tid; i < kTile * a.R; i += 256) {
-      const int n = i / a.R, r = i - n * a.R;
-      lds[r * (kTile + 2) + n] = n < rows ? src[i] : 0;
+#pragma unroll 4
+    for (int i = tid; i < kTile * R8; i += 256) {
+      const int n = i / R8, r = 8 * (i - n * R8);
+      const u32x4 w = n0 + n < a.N ? *reinterpret_cast<const u32x4*>(src + 8 * i) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) lds[(r + e) * (kTile + 2) + n] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
     }
     __syncthreads();
     uint16_t* dst = a.lb_t + (size_t)s * a.R * a.np + n0;
-    for (int i = tid; i < a.R * kTile; i += 256) {
-      const int r = i / kTile, n = i - r * kTile;
-      if (n0 + n < a.np) dst[(size_t)r * a.np + n] = lds[r * (kTile + 2) + n];
+    for (int i = tid; i < a.R * (kTile / 8); i += 256) {  // (np is a multiple of the tile)
+      const int r = i / (kTile / 8), n = 8 * (i % (kTile / 8));
+      const uint32_t* l = reinterpret_cast<const uint32_t*>(lds + r * (kTile + 2) + n);
+      *reinterpret_cast<u32x4*>(dst + (size_t)r * a.np + n) = u32x4{l[0], l[1], l[2], l[3]};
     }
     return;
   }
   job -= a.S * tiles_n;
   if (job < a.S * tiles_k) {
     // la[s][r][k0 + i] -> la_t[s][k0 + i][r]
-    const int s = job / tiles_k, k0 = (job - s * tiles_k) * kTile;
-    const int cols = min(kTile, a.K - k0);
+    const int s = job / tiles_k, k0 = (job - s * tiles_k) * kTile, R8 = a.R >> 3;
     const uint16_t* src = a.la + (size_t)s * a.R * a.K + k0;
-    for (int i = tid; i < a.R * kTile; i += 256) {
-      const int r = i / kTile, k = i - r * kTile;
-      if (k < cols) lds[r * (kTile + 2) + k] = src[(size_t)r * a.K + k];
+#pragma unroll 4
+    for (int i = tid; i < a.R * (kTile / 8); i += 256) {
+      const int r = i / (kTile / 8), k = 8 * (i % (kTile / 8));
+      if (k0 + k >= a.K) continue;  // K is a multiple of 8
+      const u32x4 w = *reinterpret_cast<const u32x4*>(src + (size_t)r * a.K + k);
+      uint32_t* l = reinterpret_cast<uint32_t*>(lds + r * (kTile + 2) + k);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) l[e] = w[e];
     }
     __syncthreads();
     uint16_t* dst = a.la_t + ((size_t)s * a.K + k0) * a.R;
-    for (int i = tid; i < cols * a.R; i += 256) {
-      const int k = i / a.R, r = i - k * a.R;
-      dst[i] = lds[r * (kTile + 2) + k];
+    for (int i = tid; i < min(kTile, a.K - k0) * R8; i += 256) {
+      const int k = i / R8, r = 8 * (i - k * R8);
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = (uint32_t)lds[(r + 2 * e) * (kTile + 2) + k] | ((uint32_t)lds[(r + 2 * e + 1) * (kTile + 2) + k] << 16);
+      *reinterpret_cast<u32x4*>(dst + 8 * i) = u32x4{w[0], w[1], w[2], w[3]};
     }
     return;
   }
@@ -137,8 +168,9 @@ __global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n
     uint32_t* const sz = reinterpret_cast<uint32_t*>(lds);  // [64][33]
     const int gb = (a.dx.G + 31) / 32, n0 = job / gb * 64, g0 = (job - job / gb * gb) * 32;
     const int groups = min(32, a.dx.G - g0);
-    for (int i = tid; i < 64 * 32; i += 256) {
-      const int n = n0 + (i >> 5), g = i & 31;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = tid + 256 * j, n = n0 + (i >> 5), g = i & 31;
       if (g < groups) {
         uint32_t v = 0u;
         if (n < a.N) {
@@ -227,27 +259,33 @@ __global__ __launch_bounds__(256) void operand_kernel(const OperandArgs a, int r
   }
 }
 
-// columns per lane: with 64 ranks, four (eight would spill the accumulators)
+// columns per lane: with 64 ranks, four (eight would spill the accumulators);
+// then two waves side by side share a step's operands, which they find in L1
 constexpr int outer_cpl(int rc) { return rc == 4 ? 4 : 8; }
+constexpr int outer_cw(int rc) { return rc == 4 ? 2 : 1; }
+constexpr int outer_cols(int rc) { return 16 * outer_cpl(rc) * outer_cw(rc); }
 
-// A workgroup owns 16 CPL columns of one problem, 16 RC ranks, one adapter and
-// a range of its tokens; its eight waves take steps of 32 places in turn.  The
+// A workgroup owns 128 columns of one problem, 16 RC ranks, one adapter and a
+// range of its tokens; its eight waves, CW beside each other, take steps of 32
+// places in turn.  The
 // tokens are the MFMA's reduction (16x16x32): a lane loads CPL columns of 8
 // tokens (a step later in flight) and pairs the tokens' halves with v_perm
 // into the A operands of its columns; the B operands, value and
 // remainder of w, come ready by rank and place.  Nothing is rounded but the
-// result.  The waves are added through four LDS buffers in two passes, always
-// in the same order; where an adapter has more tokens than one workgroup
+// result.  The waves are added through LDS buffers in two passes, always in
+// the same order; where an adapter has more tokens than one workgroup
 // takes, the ranges' fp32 sums go through the workspace and the last to arrive
 // adds them in range order.
 template <int DT, int RC>
 __global__ __launch_bounds__(512) void outer_kernel(const OuterArgs a, const OuterPlan pl) {
-  constexpr int CPL = outer_cpl(RC), BC = 16 * CPL, BR = 16 * RC, LD = BC + 4, WAVES = 8, STRIDE = 32 * WAVES;
+  constexpr int CPL = outer_cpl(RC), CW = outer_cw(RC), BC = outer_cols(RC), BR = 16 * RC, LD = BC + 4;
+  constexpr int TW = 8 / CW, STRIDE = 32 * TW, BUFS = TW / 2;
   typedef uint32_t cols_t __attribute__((ext_vector_type(CPL / 2)));
-  __shared__ __attribute__((aligned(16))) float sum[4 * BR * LD];
+  __shared__ __attribute__((aligned(16))) float sum[BUFS * BR * LD];
   __shared__ uint32_t last_flag;
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave8 = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = wave8 / CW, cw = wave8 % CW;  // turn among the steps, place among the columns
   const int col = lane & 15, q = lane >> 4;
   const bool second = (int)blockIdx.x >= pl.tiles[0];
   const OuterProblem& p = second ? a.p[1] : a.p[0];
@@ -265,38 +303,39 @@ __global__ __launch_bounds__(512) void outer_kernel(const OuterArgs a, const Out
   for (int t = 0; t < CPL; ++t)
 #pragma unroll
     for (int rc = 0; rc < RC; ++rc) acc[t][rc] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const uint16_t* vcol = p.v + min(c0 + CPL * col, p.ld - CPL);
+  const uint16_t* vcol = p.v + min(c0 + 16 * CPL * cw + CPL * col, p.ld - CPL);
   const uint16_t* wrow[RC];
 #pragma unroll
   for (int rc = 0; rc < RC; ++rc) wrow[rc] = p.op + (size_t)min(r0 + 16 * rc + col, a.R - 1) * a.places;
   const size_t lo_at = (size_t)a.R * a.places;
 
-  // places of an adapter's last step past its tokens are -1: their v is zero
+  // The tokens of a step's places are read two steps ahead and its rows one:
+  // the rows' addresses never wait.  (Places past the tokens hold -1.)
   struct Step {
-    int m[8];
     cols_t v[8];
     u32x4 hi[RC], lo[RC];
   };
-  auto load = [&](int t0, Step& st) {
-    const int4 m0 = *reinterpret_cast<const int4*>(a.order + t0 + 8 * q);
-    const int4 m1 = *reinterpret_cast<const int4*>(a.order + t0 + 8 * q + 4);
-    const int m[8] = {m0.x, m0.y, m0.z, m0.w, m1.x, m1.y, m1.z, m1.w};
+  const int t_last = start + (count + 31) / 32 * 32 - 32;  // the adapter's last step
+  auto load_tokens = [&](int t0, int (&m)[8]) {
+    const int at = min(t0, t_last) + 8 * q;
+    const int4 m0 = *reinterpret_cast<const int4*>(a.order + at), m1 = *reinterpret_cast<const int4*>(a.order + at + 4);
+    m[0] = m0.x, m[1] = m0.y, m[2] = m0.z, m[3] = m0.w, m[4] = m1.x, m[5] = m1.y, m[6] = m1.z, m[7] = m1.w;
+  };
+  auto load = [&](int t0, const int (&m)[8], Step& st) {
+    const int at = min(t0, t_last) + 8 * q;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      st.m[e] = m[e];
-      st.v[e] = *reinterpret_cast<const cols_t*>(vcol + (size_t)max(m[e], 0) * p.ld);
-    }
+    for (int e = 0; e < 8; ++e) st.v[e] = *reinterpret_cast<const cols_t*>(vcol + (size_t)max(m[e], 0) * p.ld);
 #pragma unroll
     for (int rc = 0; rc < RC; ++rc) {
-      st.hi[rc] = *reinterpret_cast<const u32x4*>(wrow[rc] + t0 + 8 * q);
-      st.lo[rc] = *reinterpret_cast<const u32x4*>(wrow[rc] + lo_at + t0 + 8 * q);
+      st.hi[rc] = *reinterpret_cast<const u32x4*>(wrow[rc] + at);
+      st.lo[rc] = *reinterpret_cast<const u32x4*>(wrow[rc] + lo_at + at);
     }
   };
-  auto multiply = [&](Step& st, bool last) {
-    if (last) {  // wave-uniform: only an adapter's last step holds empty places
+  auto multiply = [&](Step& st, int t0) {
+    if (t0 + 32 > t_end) {  // wave-uniform: only an adapter's last step holds empty places
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (st.m[e] < 0) st.v[e] = cols_t{};
+        if (t0 + 8 * q + e >= t_end) st.v[e] = cols_t{};
     }
 #pragma unroll
     for (int t = 0; t < CPL; ++t) {
@@ -315,21 +354,26 @@ __global__ __launch_bounds__(512) void outer_kernel(const OuterArgs a, const Out
   int t0 = t_begin + 32 * wave;
   if (t0 < t_end) {
     Step x, y;
-    load(t0, x);
+    int mx[8], my[8];
+    load_tokens(t0, mx);
+    load_tokens(t0 + STRIDE, my);
+    load(t0, mx, x);
     for (;;) {
-      if (t0 + STRIDE < t_end) load(t0 + STRIDE, y);
-      multiply(x, t0 + 32 > t_end);
+      load(t0 + STRIDE, my, y);
+      load_tokens(t0 + 2 * STRIDE, mx);
+      multiply(x, t0);
       t0 += STRIDE;
       if (t0 >= t_end) break;
-      if (t0 + STRIDE < t_end) load(t0 + STRIDE, x);
-      multiply(y, t0 + 32 > t_end);
+      load(t0 + STRIDE, mx, x);
+      load_tokens(t0 + 2 * STRIDE, my);
+      multiply(y, t0);
       t0 += STRIDE;
       if (t0 >= t_end) break;
     }
   }
   // acc[t][rc][e]: column CPL (4 q + e) + t, rank 16 rc + col
   auto put = [&](bool add) {
-    float* const buf = sum + (wave & 3) * (BR * LD);
+    float* const buf = sum + (wave % BUFS) * (BR * LD) + 16 * CPL * cw;
 #pragma unroll
     for (int rc = 0; rc < RC; ++rc)
 #pragma unroll
@@ -342,13 +386,14 @@ __global__ __launch_bounds__(512) void outer_kernel(const OuterArgs a, const Out
           *d = v;
         }
   };
-  if (wave < 4) put(false);
+  if (wave < BUFS) put(false);
   __syncthreads();
-  if (wave >= 4) put(true);
+  if (wave >= BUFS) put(true);
   __syncthreads();
   auto total = [&](int r, int c) {
     const float* d = sum + r * LD + c;
-    return (d[0] + d[BR * LD]) + (d[2 * BR * LD] + d[3 * BR * LD]);
+    if constexpr (BUFS == 2) return d[0] + d[BR * LD];
+    return (d[0] + d[BR * LD]) + (d[(BUFS - 2) * BR * LD] + d[(BUFS - 1) * BR * LD]);
   };
   if (ranges > 1) {
     // slots of an adapter with several ranges: from 2 floor(start / tokens),
@@ -370,7 +415,8 @@ __global__ __launch_bounds__(512) void outer_kernel(const OuterArgs a, const Out
       for (int sp = 0; sp < ranges; ++sp) v += load_coherent(a.partial + ((slot + sp) * tiles + place) * (BR * BC) + i);
       float* d = sum + (i / BC) * LD + i % BC;
       d[0] = v;
-      d[BR * LD] = d[2 * BR * LD] = d[3 * BR * LD] = 0.f;
+#pragma unroll
+      for (int k = 1; k < BUFS; ++k) d[k * BR * LD] = 0.f;
     }
     __syncthreads();
   }
@@ -421,7 +467,7 @@ OuterPlan plan_outer(int64_t M, int64_t C0, int64_t C1, int S, int R, int cu_cou
   const int blocks = (R + 15) / 16;
   p.rc = blocks > 2 ? 4 : blocks;
   p.rgroups = (blocks + p.rc - 1) / p.rc;
-  const int cols = 16 * outer_cpl(p.rc);
+  const int cols = outer_cols(p.rc);
   p.tiles[0] = (int)((C0 + cols - 1) / cols);
   p.tiles[1] = (int)((C1 + cols - 1) / cols);
   // about one workgroup per CU when one adapter has all tokens (a range costs
@@ -435,7 +481,7 @@ size_t outer_partial_bytes(const OuterPlan& p, int64_t places) {
   if (p.splits <= 1) return 0;
   // starts lie below order_places(M, S): 32 per adapter past the tokens, and an
   // adapter of several ranges has more than `tokens` >= 256 of them
-  return (size_t)(2 * (places / p.tokens) + 2 + p.splits) * (size_t)(p.tiles[0] + p.tiles[1]) * p.rgroups * (16 * p.rc * 16 * outer_cpl(p.rc)) * sizeof(float);
+  return (size_t)(2 * (places / p.tokens) + 2 + p.splits) * (size_t)(p.tiles[0] + p.tiles[1]) * p.rgroups * (16 * p.rc * outer_cols(p.rc)) * sizeof(float);
 }
 size_t outer_counter_bytes(const OuterPlan& p, int S) {
   return (size_t)S * (size_t)(p.tiles[0] + p.tiles[1]) * p.rgroups * sizeof(uint32_t);
