@@ -164,35 +164,28 @@ __global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n
   }
   job -= tail_blocks;
   if (job < const_blocks) {
-    // 64 rows x 32 groups through LDS: scale bits and zero point of each
-    uint32_t* const sz = reinterpret_cast<uint32_t*>(lds);  // [64][33]
-    const int gb = (a.dx.G + 31) / 32, n0 = job / gb * 64, g0 = (job - job / gb * gb) * 32;
-    const int groups = min(32, a.dx.G - g0);
+    // 16 rows x 32 groups through LDS: scale bits and zero point of each
+    uint32_t* const sz = reinterpret_cast<uint32_t*>(lds);  // [16][33]
+    const int G = a.dx.G, gb = (G + 31) / 32, n0 = job / gb * 16, g0 = (job - job / gb * gb) * 32;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int i = tid + 256 * j, n = n0 + (i >> 5), g = i & 31;
-      if (g < groups) {
-        uint32_t v = 0u;
-        if (n < a.N) {
-          const uint32_t z = a.dx.zp ? (a.dx.zp[(size_t)(n >> 3) * a.dx.G + g0 + g] >> (4 * (n & 7))) & 15u : 8u;
-          v = a.dx.scales[(size_t)n * a.dx.G + g0 + g] | (z << 16);
-        }
-        sz[(i >> 5) * 33 + g] = v;
-      }
+    for (int j = 0; j < 2; ++j) {
+      const int row = (tid >> 5) + 8 * j, n = min(n0 + row, a.N - 1), g = min(g0 + (tid & 31), G - 1);
+      const uint32_t sc = a.dx.scales[(size_t)n * G + g];
+      const uint32_t z = a.dx.zp ? (a.dx.zp[(size_t)(n >> 3) * G + g] >> (4 * (n & 7))) & 15u : 8u;
+      sz[row * 33 + (tid & 31)] = n0 + row < a.N ? sc | (z << 16) : 0u;
     }
     __syncthreads();
-    for (int i = tid; i < 32 * groups; i += 256) {
-      const int g = i >> 5, q = i & 31;  // group, pair of rows
-      const uint32_t a0 = sz[2 * q * 33 + g], a1 = sz[(2 * q + 1) * 33 + g];
-      const size_t at = (size_t)(g0 + g) * a.np / 2 + n0 / 2 + q;
-      if (a.dx.dtype == DT_F16) {
-        constexpr uint32_t NEG = Magic<DT_F16>::neg;
-        static_cast<u32x2*>(a.dx.constants)[at] = u32x2{(a0 & 0xFFFFu) | (a1 << 16), (NEG | (a0 >> 16)) | ((NEG | (a1 >> 16)) << 16)};
-      } else {
-        const GroupConst<DT_BF16> c0 = group_const<DT_BF16, true>((uint16_t)a0, a0 >> 16);
-        const GroupConst<DT_BF16> c1 = group_const<DT_BF16, true>((uint16_t)a1, a1 >> 16);
-        static_cast<f32x4*>(a.dx.constants)[at] = f32x4{c0.s_f32, c0.c_f32, c1.s_f32, c1.c_f32};
-      }
+    const int g = tid >> 3, q = tid & 7;  // group, pair of rows
+    if (g0 + g >= G) return;
+    const uint32_t a0 = sz[2 * q * 33 + g], a1 = sz[(2 * q + 1) * 33 + g];
+    const size_t at = (size_t)(g0 + g) * a.np / 2 + n0 / 2 + q;
+    if (a.dx.dtype == DT_F16) {
+      constexpr uint32_t NEG = Magic<DT_F16>::neg;
+      static_cast<u32x2*>(a.dx.constants)[at] = u32x2{(a0 & 0xFFFFu) | (a1 << 16), (NEG | (a0 >> 16)) | ((NEG | (a1 >> 16)) << 16)};
+    } else {
+      const GroupConst<DT_BF16> c0 = group_const<DT_BF16, true>((uint16_t)a0, a0 >> 16);
+      const GroupConst<DT_BF16> c1 = group_const<DT_BF16, true>((uint16_t)a1, a1 >> 16);
+      static_cast<f32x4*>(a.dx.constants)[at] = f32x4{c0.s_f32, c0.c_f32, c1.s_f32, c1.c_f32};
     }
     return;
   }
@@ -448,7 +441,7 @@ hipError_t launch_prep(const PrepArgs& a, hipStream_t s) {
   const int tiles_n = (a.np + kTile - 1) / kTile, tiles_k = (a.K + kTile - 1) / kTile;
   const int pad_blocks = a.dy_pad ? (int)std::min<int64_t>(2048, ((int64_t)a.M * a.np + 255) / 256) : 0;
   const int tail_blocks = a.dx.wq_tail ? (8 * a.K + 1023) / 1024 : 0;  // four words a thread
-  const int const_blocks = a.dx.constants ? a.np / 64 * ((a.dx.G + 31) / 32) : 0;
+  const int const_blocks = a.dx.constants ? a.np / 16 * ((a.dx.G + 31) / 32) : 0;
   const int64_t jobs = (int64_t)a.S * (1 + tiles_n + tiles_k) + pad_blocks + tail_blocks + const_blocks + 1;
   if (jobs > INT32_MAX) return hipErrorInvalidValue;
   hipLaunchKernelGGL(prep_kernel, dim3((unsigned)jobs), dim3(256), 0, s, a, tiles_n, tiles_k, pad_blocks, tail_blocks, const_blocks);
