@@ -312,6 +312,15 @@ __device__ __forceinline__ GroupConst<DT> group_const(uint16_t s_bits, uint32_t 
   return g;
 }
 
+// Workgroups are dispatched round-robin over the XCDs; give each XCD a
+// contiguous range of work units instead.
+constexpr int kXcds = 8;
+__device__ __forceinline__ int xcd_unit(int b, int units) {
+  const int q = units / kXcds, r = units % kXcds;
+  const int xcd = b % kXcds, local = b / kXcds;
+  return xcd < r ? xcd * (q + 1) + local : r * (q + 1) + (xcd - r) * q + local;
+}
+
 // s_waitcnt vmcnt(0): every vector memory access of this wave has completed
 // (gfx9 counts stores in vmcnt too).  expcnt and lgkmcnt fields left at their
 // maxima, so only vmcnt is waited for.

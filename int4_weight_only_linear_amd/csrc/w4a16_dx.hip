@@ -46,12 +46,6 @@ struct DxParams {
   int nsteps, tiles_k, units, splits, steps_per_split;
 };
 
-// consecutive work units -- the same tokens, neighbouring k -- on one XCD
-__device__ __forceinline__ int xcd_unit(int b, int units) {
-  const int q = units / 8, r = units % 8, xcd = b % 8, local = b / 8;
-  return xcd < r ? xcd * (q + 1) + local : r * (q + 1) + (xcd - r) * q + local;
-}
-
 // A wave-uniform global address in scalar registers: loads then take it with a
 // 32-bit lane offset, without 64-bit vector address arithmetic.
 typedef __attribute__((address_space(1))) const char g_char;
@@ -84,7 +78,7 @@ __global__ __launch_bounds__(kThreads) void dx_kernel(const DxParams p, const Lo
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int j = lane & 31, h = lane >> 5;
-  const int unit = xcd_unit(blockIdx.x, p.units);
+  const int unit = xcd_unit(blockIdx.x, p.units);  // the same tokens, neighbouring k on one XCD
   const int tile = unit / p.splits, split = unit - tile * p.splits;
   const int mt = tile / p.tiles_k, kt = tile - mt * p.tiles_k;
   const int m0 = mt * BM, k0 = kt * kBKX;

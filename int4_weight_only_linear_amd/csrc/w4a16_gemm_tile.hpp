@@ -46,18 +46,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBK = 128;         // k per step: one stored run of every row
 constexpr int kXRowBytes = 256;  // one staged x row: 128 k of 16-bit values
-constexpr int kXcds = 8;
 
 typedef __attribute__((address_space(3))) unsigned char lds_u8;
 typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
-
-// Workgroups are dispatched round-robin over the XCDs; give each XCD a
-// contiguous range of work units instead.
-__device__ __forceinline__ int xcd_unit(int b, int units) {
-  const int q = units / kXcds, r = units % kXcds;
-  const int xcd = b % kXcds, local = b / kXcds;
-  return xcd < r ? xcd * (q + 1) + local : r * (q + 1) + (xcd - r) * q + local;
-}
 
 template <int DT, int GS, bool ASYM, int MB, int CB, bool DENSE, bool LORA>
 __device__ __forceinline__ void gemm_tile(const GemmParams& p, const LoraTerm& lora) {

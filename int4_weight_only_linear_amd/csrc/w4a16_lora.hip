@@ -16,10 +16,10 @@ constexpr int shrink_depth(int tt, int rc) { return tt + rc > 8 ? 1 : (tt + rc >
 
 // A workgroup owns a tile of 16 TT tokens, 16 RC ranks and one K range, and of
 // the adapters that the tile's tokens name, in the order of their first token,
-// every `turns`-th (blockIdx.z): an adapter's rows are read once per tile,
-// several adapters of a tile side by side.  (The tile is the fastest index:
-// with one adapter only the first turn has work, and its workgroups spread
-// over all XCDs; as multiples of the turns they all fell on one, 6-9x slower.)
+// every `turns`-th: an adapter's rows are read once per tile, several adapters
+// of a tile side by side.  Each XCD takes a run of work units, tile by tile of
+// one K range, so that the tiles find the range of an adapter's rows in their
+// L2; turns come last, since with one adapter only the first has work.
 // The waves take the range's chunks in turn.  The tokens are the MFMA's A
 // rows, the adapter's ranks its B columns, both loaded straight from their
 // rows (16 bytes a lane); the waves are added through LDS in wave order, and
@@ -34,10 +34,16 @@ __global__ __launch_bounds__(64 * shrink_waves(TT, RC)) void shrink_kernel(
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int col = lane & 15, row4 = lane >> 4;
-  const int m0 = blockIdx.x * BM;
-  const int rg = blockIdx.z / turns, turn = blockIdx.z - rg * turns;
-  const int r0 = rg * BR;
-  float* const out = u + (size_t)blockIdx.y * M * R;
+  // unit = ((turn * rank groups + rank group) * splits + split) * tiles + tile
+  const int tiles = (M + BM - 1) / BM, rgroups = (R + BR - 1) / BR;
+  const int per_turn = gridDim.x / turns;  // units of a turn: rank groups x splits x tiles
+  const int turn = blockIdx.x / per_turn;
+  int unit = xcd_unit(blockIdx.x - turn * per_turn, per_turn);
+  const int tile = unit % tiles;
+  unit /= tiles;
+  const int splits = per_turn / (tiles * rgroups), split = unit % splits;
+  const int m0 = tile * BM, r0 = unit / splits * BR;
+  float* const out = u + (size_t)split * M * R;
 
   const bool token = lane < BM && m0 + lane < M;
   const int mine = token ? ids[m0 + lane] : -1;
@@ -52,7 +58,7 @@ __global__ __launch_bounds__(64 * shrink_waves(TT, RC)) void shrink_kernel(
   const uint16_t* xrow[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) xrow[t] = x + (size_t)min(m0 + 16 * t + col, M - 1) * K;
-  const int c_begin = blockIdx.y * chunks_per_split;
+  const int c_begin = split * chunks_per_split;
   const int c_end = min((K + 31) >> 5, c_begin + chunks_per_split);
 
   uint64_t todo = __ballot(named);
@@ -140,7 +146,9 @@ template <int DT, int TT, int RC>
 hipError_t launch_t(const ShrinkArgs& a, const ShrinkPlan& p, float* out, hipStream_t s) {
   const int64_t tiles = (a.M + 16 * TT - 1) / (16 * TT);
   const int turns = std::min(a.S, TT == 1 ? 16 : 8);  // (adapters of a tile: at most its tokens)
-  const dim3 grid((unsigned)tiles, p.splits, (a.R + 16 * RC - 1) / (16 * RC) * turns);
+  const int64_t units = tiles * p.splits * ((a.R + 16 * RC - 1) / (16 * RC)) * turns;
+  if (units > INT32_MAX) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)units);
   hipLaunchKernelGGL((shrink_kernel<DT, TT, RC>), grid, dim3(64 * shrink_waves(TT, RC)), 0, s,
                      static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.down), a.ids, out, (int)a.M,
                      (int)a.K, a.S, a.R, p.chunks_per_split, turns);
