@@ -148,6 +148,20 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
   return x ^ (x >> 16);
 }
 
+// Square root of 2^-100 <= x <= 2^100, rounded to nearest: the hardware's
+// reciprocal square root, then one Newton step whose residual x - s^2 is exact
+// in one fma.  (Compared with the compiler's correctly rounded one for every
+// fp32 value of the range: equal.  It takes 9 issue slots where that one, for
+// all of fp32, takes 17; with three of those per element the 8-bit step was
+// bound by instructions: 504 us for 143 M elements, 434 us so, 5.3 TB/s.)
+__device__ __forceinline__ float sqrt_mid(float x) {
+  const float r = __builtin_amdgcn_rsqf(x), s = x * r;
+  return __builtin_fmaf(__builtin_fmaf(-s, s, x), 0.5f * r, s);
+}
+// the same for 0 <= x <= 2^100 where only (a multiple of it plus a dither)'s
+// whole part counts: below 2^-100 as good as zero
+__device__ __forceinline__ float sqrt_code(float x) { return x >= 0x1p-100f ? sqrt_mid(x) : 0.f; }
+
 // the chunk of this workgroup: its tensor and its first block there
 __device__ __forceinline__ AdamwChunk chunk_of(const void* table, int tensors) {
   const AdamwChunk* c = reinterpret_cast<const AdamwChunk*>(static_cast<const AdamwTensor*>(table) + tensors);
@@ -183,6 +197,7 @@ __device__ __forceinline__ void step_and_store(const AdamwTensor& t, int64_t b, 
                                                State<EIGHT>& s) {
   const size_t i = (size_t)b * 256 + 4 * lane;
   float r[4];
+  uint32_t far = 0;  // how far v's bits lie above those of 2^-100 (wrapping below it)
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     if constexpr (EIGHT) {
@@ -193,8 +208,25 @@ __device__ __forceinline__ void step_and_store(const AdamwTensor& t, int64_t b, 
     const float g = s.g[e] * h.grad_scale;
     s.m[e] = s.m[e] * h.beta1 + g * h.one_beta1;
     s.v[e] = s.v[e] * h.beta2 + (g * g) * h.one_beta2;
-    r[e] = __builtin_sqrtf(s.v[e]);
-    s.p[e] = s.p[e] * h.decay - (s.m[e] / (r[e] * h.root + h.eps)) * h.rate;
+    const float v = s.v[e];
+    far = max(far, __builtin_bit_cast(uint32_t, v) - __builtin_bit_cast(uint32_t, 0x1p-100f));
+  }
+  // 8 bits: the short forms where every v of the wave is in their range (no
+  // zeros, infinities or NaN); the quotient only goes into p, which a last
+  // place of the update does not reach
+  constexpr uint32_t span = __builtin_bit_cast(uint32_t, 0x1p100f) - __builtin_bit_cast(uint32_t, 0x1p-100f);
+  if (EIGHT && __all(far <= span)) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      r[e] = sqrt_mid(s.v[e]);
+      s.p[e] = s.p[e] * h.decay - (s.m[e] * __builtin_amdgcn_rcpf(r[e] * h.root + h.eps)) * h.rate;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      r[e] = __builtin_sqrtf(s.v[e]);
+      s.p[e] = s.p[e] * h.decay - (s.m[e] / (r[e] * h.root + h.eps)) * h.rate;
+    }
   }
   store4<PD, WHOLE>(t.param, i, n, s.p);
   if (t.copy) {
@@ -216,8 +248,8 @@ __device__ __forceinline__ void step_and_store(const AdamwTensor& t, int64_t b, 
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint32_t d = mix32((uint32_t)((t.first_block + b) * 256 + 4 * lane + e) + h.seed);
-      const float qm = __builtin_floorf(__builtin_sqrtf(__builtin_fabsf(s.m[e]) * im) * 127.f + (float)(d & 0xFFFFu) * 0x1p-16f);
-      const float qv = __builtin_floorf(__builtin_sqrtf(r[e] * ir) * 255.f + (float)(d >> 16) * 0x1p-16f);
+      const float qm = __builtin_floorf(sqrt_code(__builtin_fabsf(s.m[e]) * im) * 127.f + (float)(d & 0xFFFFu) * 0x1p-16f);
+      const float qv = __builtin_floorf(sqrt_code(r[e] * ir) * 255.f + (float)(d >> 16) * 0x1p-16f);
       const int c = (int)__builtin_fminf(qm, 127.f);
       const int u = (int)__builtin_fminf(r[e] > 0.f ? __builtin_fmaxf(qv, 1.f) : qv, 255.f);
       cm |= (uint32_t)(uint8_t)(s.m[e] < 0.f ? -c : c) << (8 * e);

@@ -142,6 +142,44 @@ def test_moments_in_8_bits(param, grad, shift):
         first += blocks[i]
 
 
+@pytest.mark.parametrize("scale", [1.0, 1e-3, 1e-18, 0.0])
+def test_codes_are_the_plain_sequence_of_fp32_operations(scale):
+    # every code and scale, bit for bit, of the step written as single fp32
+    # operations (numpy rounds each once); 1e-18: moments near the end of fp32
+    n = 256 * 200
+    rng = np.random.default_rng(11)
+    g = (rng.normal(0, 1, n) * np.exp(rng.normal(0, 2, n)) * scale).astype(np.float32)
+    g[:256 * 20:3] = 0
+    cm, cv = rng.integers(-127, 128, n).astype(np.int8), rng.integers(0, 256, n).astype(np.uint8)
+    ms, rs = (rng.uniform(0.1, 1, n // 256).astype(np.float32) * np.float32(scale) for _ in range(2))
+    cm[:256 * 10], cv[:256 * 10] = 0, 0
+    dev = lambda a: torch.from_numpy(a.copy()).cuda()  # noqa: E731
+    t = [dev(a) for a in (cm, cv, ms, rs)]
+    step(L.w4a16_adamw_plan([torch.zeros(n, device="cuda")], [dev(g)], [t[0]], [t[1]], m_scales=[t[2]], v_scales=[t[3]]),
+         seed=77)
+    f, h = np.float32, HYPER
+    spread = lambda a: np.repeat(a, 256)  # noqa: E731
+    with np.errstate(all="ignore"):
+        c = cm.astype(f) * f(1 / 127)
+        m = (c * np.abs(c)) * spread(ms)
+        c = cv.astype(f) * f(1 / 255)
+        r = (c * c) * spread(rs)
+        v = r * r
+        gs = g * f(h["grad_scale"])
+        m = m * f(h["beta1"]) + gs * f(1 - h["beta1"])
+        v = v * f(h["beta2"]) + (gs * gs) * f(1 - h["beta2"])
+        r = np.sqrt(v)
+        m2, r2 = np.abs(m).reshape(-1, 256).max(1), r.reshape(-1, 256).max(1)
+        inv = lambda a: spread(np.where(a > f(2.0 ** -100), f(1) / a, f(0)).astype(f))  # noqa: E731
+        dm, dv = A.adamw_dither(np.arange(n), 77)
+        qm = np.minimum(np.floor(np.sqrt(np.abs(m) * inv(m2)) * f(127) + dm.astype(f)), f(127))
+        qv = np.floor(np.sqrt(r * inv(r2)) * f(255) + dv.astype(f))
+        qv = np.minimum(np.where(r > 0, np.maximum(qv, f(1)), qv), f(255))
+    assert np.array_equal(t[2].cpu().numpy(), m2) and np.array_equal(t[3].cpu().numpy(), r2)
+    assert np.array_equal(t[0].cpu().numpy(), np.where(m < 0, -qm, qm).astype(np.int8))
+    assert np.array_equal(t[1].cpu().numpy(), qv.astype(np.uint8))
+
+
 def zeros8(n):
     b = (n + 255) // 256
     z = lambda k, dt: torch.zeros(k, dtype=dt, device="cuda")  # noqa: E731
