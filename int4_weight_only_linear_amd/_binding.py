@@ -332,38 +332,40 @@ def _workspace(device, stream_ptr: int, nbytes: int):
 
 def _linear_args(x, wq, scales, zp, bias, group_size, out):
     torch = _torch()
+    dtype = x.dtype
     dt = _act_code(x)
     if x.dim() != 2:
         raise ValueError("x must be 2-D [M, K]")
     M, K = x.shape
-    if wq.dim() != 2 or wq.dtype not in (torch.int32, getattr(torch, "uint32", torch.int32)):
+    words = (torch.int32, getattr(torch, "uint32", torch.int32))
+    if wq.dim() != 2 or wq.dtype not in words:
         raise TypeError(f"wq must be a 2-D int32 or uint32 tensor, got {wq.dtype}")
-    N = wq.shape[0]
-    if wq.shape[1] * 8 != K:
+    N, J = wq.shape
+    if J * 8 != K:
         raise ValueError(f"wq is {tuple(wq.shape)}, expected [N, K/8] with K={K}")
-    if scales.dtype != x.dtype:
-        raise TypeError(f"scales must be {x.dtype}, got {scales.dtype}")
+    if scales.dtype != dtype:
+        raise TypeError(f"scales must be {dtype}, got {scales.dtype}")
     if group_size <= 0 or K % group_size:
         raise ValueError(f"K={K} is not a multiple of group_size={group_size}")
     G = K // group_size
     if scales.shape != (N, G):
         raise ValueError(f"scales are {tuple(scales.shape)}, expected {(N, G)}")
     if zp is not None:
-        if zp.dtype not in (torch.int32, getattr(torch, "uint32", torch.int32)):
+        if zp.dtype not in words:
             raise RuntimeError(_ZP_MSG.format(zp.dtype))
         if zp.shape != (N // 8, G) or N % 8:
             raise ValueError(f"zp is {tuple(zp.shape)}, expected {(N // 8, G)} (N % 8 == 0)")
     if bias is not None:
-        if bias.dtype != x.dtype or tuple(bias.shape) != (N,):
-            raise ValueError(f"bias must be {x.dtype} [{N}]")
+        if bias.dtype != dtype or bias.shape != (N,):
+            raise ValueError(f"bias must be {dtype} [{N}]")
     device = x.device
     _require_device(x, "x", device)
     _require_all(device, (wq, "wq"), (scales, "scales"), (zp, "zp"), (bias, "bias"))
     if out is None:
-        out = torch.empty((M, N), dtype=x.dtype, device=device)
+        out = x.new_empty((M, N))
     else:
-        if out.dtype != x.dtype or out.shape != (M, N):
-            raise ValueError(f"out must be {x.dtype} [{M}, {N}]")
+        if out.dtype != dtype or out.shape != (M, N):
+            raise ValueError(f"out must be {dtype} [{M}, {N}]")
         _require_device(out, "out", device)
     return dt, M, N, K, out
 

@@ -258,22 +258,12 @@ size_t workspace_for(int64_t M, int64_t N, int64_t K, int32_t group, int32_t dty
 
 bool log_enabled() { return w4a16::tuning().log; }
 
-w4a16_status linear_impl(const void* x, const int32_t* wq, const void* scales, const int32_t* zp,
-                         const void* bias, void* y, int64_t M, int64_t N, int64_t K,
-                         int32_t group_size, int32_t dtype, void* workspace,
-                         size_t workspace_bytes, void* stream, int32_t path,
-                         const w4a16::LoraTerm* lora = nullptr) {
-  w4a16_status st = w4a16_check_args(x, wq, scales, zp, bias, y, M, N, K, group_size, dtype);
-  if (st != W4A16_OK) return st;
-  const GroupMap gm = group_map(group_size, K);
-  group_size = gm.kgroup;  // from here on, the kernels' group
-  if (path < W4A16_PATH_AUTO || path > W4A16_PATH_GEMM)
-    return fail(W4A16_ERR_INVALID_ARG, "unknown path %d", (int)path);
-  if (M == 0) return ok();
-  const DeviceInfo* dev = nullptr;
-  st = device_info(&dev);
-  if (st != W4A16_OK) return st;
-  const w4a16_path p = resolve_path(M, N, K, group_size, dtype, zp != nullptr, path);
+// the launch of a checked problem (M > 0) on the path p
+w4a16_status linear_run(const DeviceInfo* dev, w4a16_path p, const GroupMap& gm, const void* x, const int32_t* wq,
+                        const void* scales, const int32_t* zp, const void* bias, void* y, int64_t M, int64_t N,
+                        int64_t K, int32_t dtype, void* workspace, size_t workspace_bytes, void* stream,
+                        const w4a16::LoraTerm* lora) {
+  const int32_t group_size = gm.kgroup;  // the kernels' group
   if (p == W4A16_PATH_GEMV && M > W4A16_GEMV_MAX_M)
     return fail(W4A16_ERR_UNSUPPORTED, "the decode kernel takes M <= %d, got M=%lld",
                 W4A16_GEMV_MAX_M, (long long)M);
@@ -319,6 +309,23 @@ w4a16_status linear_impl(const void* x, const int32_t* wq, const void* scales, c
   }
   if (e != hipSuccess) return fail(W4A16_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
   return ok();
+}
+
+w4a16_status linear_impl(const void* x, const int32_t* wq, const void* scales, const int32_t* zp,
+                         const void* bias, void* y, int64_t M, int64_t N, int64_t K,
+                         int32_t group_size, int32_t dtype, void* workspace,
+                         size_t workspace_bytes, void* stream, int32_t path) {
+  w4a16_status st = w4a16_check_args(x, wq, scales, zp, bias, y, M, N, K, group_size, dtype);
+  if (st != W4A16_OK) return st;
+  const GroupMap gm = group_map(group_size, K);
+  if (path < W4A16_PATH_AUTO || path > W4A16_PATH_GEMM)
+    return fail(W4A16_ERR_INVALID_ARG, "unknown path %d", (int)path);
+  if (M == 0) return ok();
+  const DeviceInfo* dev = nullptr;
+  st = device_info(&dev);
+  if (st != W4A16_OK) return st;
+  const w4a16_path p = resolve_path(M, N, K, gm.kgroup, dtype, zp != nullptr, path);
+  return linear_run(dev, p, gm, x, wq, scales, zp, bias, y, M, N, K, dtype, workspace, workspace_bytes, stream, nullptr);
 }
 
 // the CU count that plans are made for: the current device's, or MI355X's
@@ -368,9 +375,20 @@ w4a16_path lora_path(int64_t M, int64_t N, int64_t K, int32_t group, int32_t dty
 }
 
 // the workspace of w4a16_lora_linear: the projection's own (its counter region
-// always kept, so that one workspace serves every entry point), then u
-size_t lora_u_offset(int64_t M, int64_t N, int64_t K, int32_t kgroup, int32_t dtype, bool asym, w4a16_path p, int cus) {
-  return round256(std::max(w4a16::kCounterBytes, workspace_for(M, N, K, kgroup, dtype, asym, p, cus)));
+// always kept, so that one workspace serves every entry point), then the K
+// ranges' sums of u, and u itself where the caller does not keep it
+struct LoraPlan {
+  w4a16_path path;
+  w4a16::ShrinkPlan shrink;
+  size_t u_at, bytes;
+};
+LoraPlan plan_lora(int64_t M, int64_t N, int64_t K, int32_t kgroup, int32_t dtype, bool asym, int R, bool save_u, int cus) {
+  LoraPlan p;
+  p.path = lora_path(M, N, K, kgroup, dtype, asym);
+  p.shrink = w4a16::plan_shrink(M, K, R, cus, p.path == W4A16_PATH_GEMV);
+  p.u_at = round256(std::max(w4a16::kCounterBytes, workspace_for(M, N, K, kgroup, dtype, asym, p.path, cus)));
+  p.bytes = p.u_at + round256((size_t)(p.shrink.splits + (save_u ? 0 : 1)) * (size_t)M * (size_t)R * sizeof(float));
+  return p;
 }
 
 // the workspace of w4a16_lora_backward, by byte offsets behind the counter
@@ -836,13 +854,7 @@ size_t w4a16_lora_workspace_size(int64_t M, int64_t N, int64_t K, int32_t group_
                                  int32_t has_zp, int64_t R, int32_t save_u) {
   if (M <= 0 || N <= 0 || K <= 0 || !group_ok(group_size, K) || K % group_size || R < 8 || R % 8 || R > w4a16::kMaxRank)
     return 0;
-  const int cus = planning_cus();
-  const int kgroup = group_map(group_size, K).kgroup;
-  const w4a16_path p = lora_path(M, N, K, kgroup, dtype, has_zp);
-  const w4a16::ShrinkPlan sp = w4a16::plan_shrink(M, K, (int)R, cus, p == W4A16_PATH_GEMV);
-  // the K ranges' sums, and u itself where the caller does not keep it
-  return lora_u_offset(M, N, K, kgroup, dtype, has_zp != 0, p, cus) +
-         round256((size_t)(sp.splits + (save_u ? 0 : 1)) * (size_t)M * (size_t)R * sizeof(float));
+  return plan_lora(M, N, K, group_map(group_size, K).kgroup, dtype, has_zp != 0, (int)R, save_u != 0, planning_cus()).bytes;
 }
 
 w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* scales, const int32_t* zp,
@@ -867,19 +879,18 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
   const DeviceInfo* dev = nullptr;
   st = device_info(&dev);
   if (st != W4A16_OK) return st;
-  const size_t need = w4a16_lora_workspace_size(M, N, K, group_size, dtype, zp != nullptr, R, u != nullptr);
-  if (workspace == nullptr || workspace_bytes < need)
-    return fail(W4A16_ERR_WORKSPACE, "lora_linear: workspace of %zu bytes needed, got %zu%s", need, workspace_bytes,
+  const GroupMap gm = group_map(group_size, K);
+  const LoraPlan plan = plan_lora(M, N, K, gm.kgroup, dtype, zp != nullptr, (int)R, u != nullptr, dev->cu_count);
+  if (workspace == nullptr || workspace_bytes < plan.bytes)
+    return fail(W4A16_ERR_WORKSPACE, "lora_linear: workspace of %zu bytes needed, got %zu%s", plan.bytes, workspace_bytes,
                 workspace ? "" : " (NULL)");
   if (!aligned(workspace, 256)) return fail(W4A16_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
-  const int kgroup = group_map(group_size, K).kgroup;
-  const w4a16_path p = lora_path(M, N, K, kgroup, dtype, zp != nullptr);
-  const size_t at = lora_u_offset(M, N, K, kgroup, dtype, zp != nullptr, p, dev->cu_count);
-  const w4a16::ShrinkPlan sp = w4a16::plan_shrink(M, K, (int)R, dev->cu_count, p == W4A16_PATH_GEMV);
+  const w4a16_path p = plan.path;
+  const w4a16::ShrinkPlan& sp = plan.shrink;
   // Decode: the epilogue adds the K ranges' sums itself, which saves a launch
   // (a few floats per output).  Above it every tile of the GEMM reads all of
   // its tokens' u, so the ranges are added once, before it.
-  float* const part = reinterpret_cast<float*>(static_cast<char*>(workspace) + at);
+  float* const part = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.u_at);
   float* const sums = u ? u : (p == W4A16_PATH_GEMV ? nullptr : part + (size_t)sp.splits * M * R);
   const w4a16::ShrinkArgs sa{x, la, ids, part, sums, M, K, (int)S, (int)R, dtype};
   const hipError_t e = w4a16::launch_shrink(sa, sp, static_cast<hipStream_t>(stream));
@@ -892,7 +903,7 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
   t.S = (int)S;
   t.R = (int)R;
   t.usplits = sums ? 1 : sp.splits;
-  return linear_impl(x, wq, scales, zp, bias, y, M, N, K, group_size, dtype, workspace, at, stream, p, &t);
+  return linear_run(dev, p, gm, x, wq, scales, zp, bias, y, M, N, K, dtype, workspace, plan.u_at, stream, &t);
 }
 
 size_t w4a16_lora_backward_workspace_size(int64_t M, int64_t N, int64_t K, int32_t group_size, int64_t S, int64_t R,
