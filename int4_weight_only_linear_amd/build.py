@@ -104,14 +104,8 @@ _THIN = re.compile(r"<(_Z\S*gemm_(?:lora_)?kernelILi\d+ELi\d+ELb(\d)ELi1ELi(\d)E
 _META = ("global_load_ushort", "global_load_short_d16", "global_load_dword", "global_load_sshort")
 
 
-def check_thin_tile_waits(obj: str) -> int:
-    """The 32-token GEMM tiles keep the step after next in flight across the
-    step barrier with a partial wait, vmcnt(WP * CB + 2): that count is right
-    only if the last vector memory instructions before the barrier are that
-    step's WP * CB 16-byte weight loads and two x loads into LDS (its
-    metadata before them).  Checks it in the disassembly of this build's own
-    gfx950 code (one object file); returns the number of barriers checked,
-    raises if one breaks it."""
+def _disassembly(obj: str) -> str:
+    """The gfx950 code of an object file of this build, as llvm-objdump text."""
     with tempfile.TemporaryDirectory() as d:
         fat, co = os.path.join(d, "fatbin"), os.path.join(d, "code.o")
         for cmd in ([_llvm_tool("llvm-objcopy"), f"--dump-section=.hip_fatbin={fat}", obj, os.path.join(d, "host.o")],
@@ -123,7 +117,18 @@ def check_thin_tile_waits(obj: str) -> int:
         r = subprocess.run([_llvm_tool("llvm-objdump"), "-d", f"--mcpu={ARCH}", co], capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"llvm-objdump failed:\n{r.stderr}")
-    return thin_tile_waits_in(r.stdout)
+    return r.stdout
+
+
+def check_thin_tile_waits(obj: str) -> int:
+    """The 32-token GEMM tiles keep the step after next in flight across the
+    step barrier with a partial wait, vmcnt(WP * CB + 2): that count is right
+    only if the last vector memory instructions before the barrier are that
+    step's WP * CB 16-byte weight loads and two x loads into LDS (its
+    metadata before them).  Checks it in the disassembly of this build's own
+    gfx950 code (one object file); returns the number of barriers checked,
+    raises if one breaks it."""
+    return thin_tile_waits_in(_disassembly(obj))
 
 
 def thin_tile_waits_in(disassembly: str) -> int:
@@ -160,6 +165,54 @@ def thin_tile_waits_in(disassembly: str) -> int:
     return checked
 
 
+_DX = re.compile(r"<(_Z\S*dx_kernelILi\d+ELi\d\S*)>:")
+
+
+def check_dx_waits(obj: str) -> int:
+    """The backward dx kernel waits at its step barrier for everything but the
+    weight words and constants just loaded, vmcnt(12) or vmcnt(10): right only
+    if those are the last vector memory instructions before the barrier, and
+    the loads of dy into LDS, issued after the barrier before, stand in front of
+    them.  Checks it in the disassembly of this build's own gfx950 code (one
+    object file); returns the number of barriers checked, raises if one breaks
+    it."""
+    return dx_waits_in(_disassembly(obj))
+
+
+def dx_waits_in(disassembly: str) -> int:
+    """The check of check_dx_waits on llvm-objdump text."""
+    checked, kernel, vm, prev, partial = 0, None, [], "", False
+    for line in disassembly.splitlines():
+        m = _DX.search(line)
+        if m or line.endswith(">:"):
+            kernel, vm, prev, partial = (m.group(1) if m else None), [], "", False
+            continue
+        if kernel is None or not line.startswith("\t"):
+            continue
+        ins = line.strip().split("//")[0].strip()
+        op = ins.split(" ")[0]
+        if op.startswith(("global_", "buffer_", "flat_", "scratch_")):
+            vm.append(op)
+        elif op == "s_barrier":
+            w = re.match(r"s_waitcnt vmcnt\((\d+)\)", prev)
+            n = int(w.group(1)) if w else 0
+            if n:
+                dy, words = vm[:-n], vm[-n:]
+                if (n not in (10, 12) or len(words) != n or words.count("global_load_dword") != 8
+                        or words.count("global_load_dwordx4") != n - 8 or any(o != "global_load_lds_dwordx4" for o in dy)):
+                    raise RuntimeError(f"{kernel}: '{prev}' before a step barrier, but the vector memory instructions "
+                                       f"since the last one are {vm}")
+                checked += 1
+            vm, partial = [], n > 0
+        elif op.startswith(("s_cbranch", "s_branch")):
+            # the loop's end: no word may be loaded ahead of the next barrier's group
+            if partial and any(o != "global_load_lds_dwordx4" for o in vm):
+                raise RuntimeError(f"{kernel}: {vm} between the last step barrier of the loop and its end")
+            partial = False
+        prev = ins
+    return checked
+
+
 def _link(objs, lib: str) -> None:
     tmp = lib + ".tmp"
     cmd = [_hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
@@ -179,6 +232,8 @@ def build(verbose: bool = False) -> str:
     for src in ("w4a16_gemm.hip", "w4a16_gemm_lora.hip"):
         if check_thin_tile_waits(objs[SOURCES.index(src)]) == 0:
             raise RuntimeError(f"no partial-wait step barrier found in the 32-token GEMM tiles of {src}")
+    if check_dx_waits(objs[SOURCES.index("w4a16_dx.hip")]) == 0:
+        raise RuntimeError("no partial-wait step barrier found in w4a16_dx.hip")
     _link(objs[:len(SOURCES)], LIB)
     _link(objs[len(SOURCES):], CEILINGS_LIB)
     if verbose:
