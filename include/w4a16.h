@@ -338,7 +338,8 @@ size_t w4a16_dense_workspace_size(int64_t M, int64_t N, int64_t K, int32_t dtype
  * below 65504 there.
  * Workspace: always needed (w4a16_lora_workspace_size), 256-byte aligned,
  * under w4a16_linear's rules: zero-filled before its first use, then
- * reusable by calls of any entry point on the same stream.
+ * reusable by calls of any entry point on the same stream; it must not overlap
+ * an input or an output.
  * Errors: those of w4a16_linear; W4A16_ERR_INVALID_ARG for S < 1 or a rank
  * that is no positive multiple of 8, W4A16_ERR_UNSUPPORTED for one above 128. */
 size_t w4a16_lora_workspace_size(int64_t M, int64_t N, int64_t K, int32_t group_size, int32_t dtype,
@@ -407,7 +408,8 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
  * share their types (param, grad: W4A16_F16, W4A16_BF16 or W4A16_F32; copy:
  * W4A16_F16 or W4A16_BF16).  n may be 0.  Pointers are aligned to their
  * elements; four-element alignment of all of a tensor's pointers is faster.
- * A tensor's buffers must not overlap one another.
+ * What a step writes must not overlap, within a tensor or between two, nor a
+ * gradient (which tensors may share).
  * Errors: W4A16_ERR_INVALID_ARG, W4A16_ERR_ALIGNMENT, W4A16_ERR_WORKSPACE (a
  * table too small); nothing is written then. */
 typedef struct w4a16_adamw_tensor {
@@ -432,7 +434,7 @@ w4a16_status w4a16_adamw_table(const w4a16_adamw_tensor* tensors, int64_t count,
                                size_t table_bytes, w4a16_adamw_plan* plan);
 
 /* The step (device): asynchronous on `stream`; the numbers are taken when it
- * is called.  Needs betas in [0, 1), eps >= 0, step >= 1 and finite rates. */
+ * is called.  Needs betas in [0, 1), eps >= 0, step >= 1 and the rest finite. */
 w4a16_status w4a16_adamw_step(const void* table, const w4a16_adamw_plan* plan, double lr, double beta1, double beta2,
                               double eps, double weight_decay, int64_t step, double grad_scale, uint32_t seed,
                               void* stream);

@@ -18,8 +18,10 @@
 #include <cstdlib>
 #include <algorithm>
 #include <cstring>
+#include <exception>
 #include <mutex>
 #include <string>
+#include <vector>
 
 #include "w4a16_adamw.h"
 #include "w4a16_internal.h"
@@ -852,7 +854,8 @@ w4a16_status w4a16_linear_dense(const void* x, const void* w, const void* bias, 
 
 size_t w4a16_lora_workspace_size(int64_t M, int64_t N, int64_t K, int32_t group_size, int32_t dtype,
                                  int32_t has_zp, int64_t R, int32_t save_u) {
-  if (M <= 0 || N <= 0 || K <= 0 || !group_ok(group_size, K) || K % group_size || R < 8 || R % 8 || R > w4a16::kMaxRank)
+  if (M <= 0 || N <= 0 || K <= 0 || !group_ok(group_size, K) || K % group_size || R < 8 || R % 8 || R > w4a16::kMaxRank ||
+      (dtype != W4A16_F16 && dtype != W4A16_BF16))
     return 0;
   return plan_lora(M, N, K, group_map(group_size, K).kgroup, dtype, has_zp != 0, (int)R, save_u != 0, planning_cus()).bytes;
 }
@@ -885,6 +888,10 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
     return fail(W4A16_ERR_WORKSPACE, "lora_linear: workspace of %zu bytes needed, got %zu%s", plan.bytes, workspace_bytes,
                 workspace ? "" : " (NULL)");
   if (!aligned(workspace, 256)) return fail(W4A16_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  if (overlaps_adapters(workspace, plan.bytes, la, lb, ids, alpha, M, N, K, S, R) ||
+      overlap(workspace, plan.bytes, y, ybytes) || overlap(workspace, plan.bytes, u, ubytes) ||
+      overlap(workspace, plan.bytes, x, act_bytes(M * K)) || overlap(workspace, plan.bytes, wq, (size_t)N * (K / 8) * 4))
+    return fail(W4A16_ERR_INVALID_ARG, "lora_linear: the workspace must not overlap an input or an output");
   const w4a16_path p = plan.path;
   const w4a16::ShrinkPlan& sp = plan.shrink;
   // Decode: the epilogue adds the K ranges' sums itself, which saves a launch
@@ -959,6 +966,10 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
     return fail(W4A16_ERR_WORKSPACE, "lora_backward: workspace of %zu bytes needed, got %zu%s", p.bytes, workspace_bytes,
                 workspace ? "" : " (NULL)");
   if (!aligned(workspace, 256)) return fail(W4A16_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+  bool inside = overlaps_adapters(workspace, p.bytes, la, lb, ids, alpha, M, N, K, S, R);
+  for (const auto& o : out) inside |= overlap(workspace, p.bytes, o.p, o.n);
+  for (const auto& i : in) inside |= overlap(workspace, p.bytes, i.p, i.n);
+  if (inside) return fail(W4A16_ERR_INVALID_ARG, "lora_backward: the workspace must not overlap an input or an output");
   char* const ws = static_cast<char*>(workspace);
   auto at = [&](size_t o) { return static_cast<void*>(ws + o); };
   const bool pad = p.np != N;
@@ -1079,6 +1090,13 @@ w4a16_status w4a16_adamw_table(const w4a16_adamw_tensor* tensors, int64_t count,
   if (!aligned(table, 8)) return fail(W4A16_ERR_ALIGNMENT, "adamw_table: the table must be 8-byte aligned");
   const int pb = elem_bytes(param_dtype), gb = elem_bytes(grad_dtype), sb = state_bits == 8 ? 1 : 4;
   // first every tensor is checked, then the table is written
+  struct Range { uintptr_t begin, end; int64_t tensor; };
+  std::vector<Range> ranges;  // that a step writes
+  try {
+    ranges.reserve((size_t)count * 6);
+  } catch (const std::exception&) {
+    return fail(W4A16_ERR_UNSUPPORTED, "adamw_table: no host memory to check %lld tensors", (long long)count);
+  }
   for (int64_t i = 0; i < count; ++i) {
     const w4a16_adamw_tensor& t = tensors[i];
     if (t.n == 0) continue;
@@ -1089,15 +1107,29 @@ w4a16_status w4a16_adamw_table(const w4a16_adamw_tensor* tensors, int64_t count,
     if (!aligned(t.param, pb) || !aligned(t.grad, gb) || !aligned(t.m, sb) || !aligned(t.v, sb) ||
         (t.copy && !aligned(t.copy, 2)) || (state_bits == 8 && (!aligned(t.m_scale, 4) || !aligned(t.v_scale, 4))))
       return fail(W4A16_ERR_ALIGNMENT, "adamw_table: a pointer of tensor %lld is not aligned to its elements", (long long)i);
-    const struct { const void* p; size_t n; } own[7] = {
+    const struct { const void* p; size_t n; } own[6] = {
         {t.param, (size_t)t.n * pb}, {t.m, (size_t)t.n * sb}, {t.v, (size_t)t.n * sb},
         {state_bits == 8 ? t.m_scale : nullptr, (size_t)((t.n + 255) / 256) * 4},
         {state_bits == 8 ? t.v_scale : nullptr, (size_t)((t.n + 255) / 256) * 4},
-        {t.copy, (size_t)t.n * 2}, {t.grad, (size_t)t.n * gb}};
-    for (int a = 0; a < 7; ++a)
-      for (int b = 0; b < a; ++b)
-        if (overlap(own[a].p, own[a].n, own[b].p, own[b].n))
-          return fail(W4A16_ERR_INVALID_ARG, "adamw_table: buffers of tensor %lld overlap", (long long)i);
+        {t.copy, (size_t)t.n * 2}};
+    for (int a = 0; a < 6; ++a) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(own[a].p);
+      if (own[a].p) ranges.push_back({at, at + own[a].n, i});
+    }
+  }
+  // no element is written by two of them, none is read as a gradient
+  std::sort(ranges.begin(), ranges.end(), [](const Range& a, const Range& b) { return a.begin < b.begin; });
+  for (size_t i = 1; i < ranges.size(); ++i)
+    if (ranges[i].begin < ranges[i - 1].end)
+      return fail(W4A16_ERR_INVALID_ARG, "adamw_table: buffers of tensors %lld and %lld overlap", (long long)ranges[i - 1].tensor,
+                  (long long)ranges[i].tensor);
+  for (int64_t i = 0; i < count; ++i) {
+    if (tensors[i].n == 0) continue;
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(tensors[i].grad), end = begin + (size_t)tensors[i].n * gb;
+    const auto r = std::lower_bound(ranges.begin(), ranges.end(), end, [](const Range& a, uintptr_t e) { return a.begin < e; });
+    if (r != ranges.begin() && (r - 1)->end > begin)
+      return fail(W4A16_ERR_INVALID_ARG, "adamw_table: the gradient of tensor %lld and a buffer of tensor %lld overlap",
+                  (long long)i, (long long)(r - 1)->tensor);
   }
   w4a16::AdamwTensor* out = static_cast<w4a16::AdamwTensor*>(table);
   w4a16::AdamwChunk* ch = reinterpret_cast<w4a16::AdamwChunk*>(out + count);
@@ -1131,7 +1163,7 @@ w4a16_status w4a16_adamw_step(const void* table, const w4a16_adamw_plan* plan, d
   w4a16_status st = check_adamw_plan("adamw_step", table, plan);
   if (st != W4A16_OK) return st;
   if (!(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps >= 0) || step < 1 || !std::isfinite(lr) ||
-      !std::isfinite(weight_decay) || !std::isfinite(eps))
+      !std::isfinite(weight_decay) || !std::isfinite(eps) || !std::isfinite(grad_scale))
     return fail(W4A16_ERR_INVALID_ARG, "adamw_step: need betas in [0, 1), eps >= 0, finite rates and step >= 1");
   if (plan->chunks == 0) return ok();
   const DeviceInfo* dev = nullptr;
