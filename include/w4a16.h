@@ -335,7 +335,9 @@ size_t w4a16_dense_workspace_size(int64_t M, int64_t N, int64_t K, int32_t dtype
  * and lb 16-byte, u 16-byte, ids and alpha 4-byte aligned.  y and u must not
  * overlap any input or each other.  Above the decode threshold alpha * u is
  * carried as two values of the activation dtype, so with fp16 it has to stay
- * below 65504 there.
+ * below 65504 there.  Infinite or NaN values of an adapter reach its own tokens
+ * only (where tokens of several adapters share a tile, an infinite element of
+ * B may reach them as NaN).
  * Workspace: always needed (w4a16_lora_workspace_size), 256-byte aligned,
  * under w4a16_linear's rules: zero-filled before its first use, then
  * reusable by calls of any entry point on the same stream; it must not overlap

@@ -94,6 +94,7 @@ __device__ __forceinline__ void split_hi_lo(const float (&v)[8], u32x4& hi, u32x
 // few registers and whose tokens are mostly of one request, take one k-sub at
 // a time.
 //   acc[rb][cb]: tokens m0 + 32 rb + (lane & 31), features nw0 + 32 cb + ...
+typedef uint16_t uint16x2_t __attribute__((ext_vector_type(2)));
 template <int DT, int MB, int CB>
 __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int m0, int nw0, int lane, int turn, int turns,
                                            f32x16 (&acc)[MB][CB]) {
@@ -163,7 +164,33 @@ __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int 
     }
     return n;
   };
+  // Other adapters' tokens of a block take part with zeros, which an infinite
+  // or NaN factor would turn into NaN.  Where an item holds one, it is taken
+  // out of the product and made of finite numbers that overflow for the
+  // adapter's own tokens: + and - max * 2^127, in bf16 whose products pass
+  // fp32's range; zeros stay zeros.  (Selecting sums by token instead keeps
+  // them in vector registers: up to 1150 spilled.  The test costs 8 operations
+  // a fragment, nothing where all tokens are the adapter's.)
   auto multiply = [&](const Item& it) {
+    uint64_t others = 0;
+#pragma unroll
+    for (int rb = 0; rb < MB; ++rb)
+      if (it.own[rb]) others |= __ballot(m0 + 32 * rb + j < M) & ~it.own[rb];
+    bool broken = false;
+    constexpr uint32_t INF = DT == DT_F16 ? 0x7C00 : 0x7F80;
+    if (others) {
+      uint16x2_t top = {0, 0};
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t word = it.w[ks][cb][e] & 0x7FFF7FFFu;
+            top = __builtin_elementwise_max(top, __builtin_bit_cast(uint16x2_t, word));
+          }
+      broken = __ballot(top[0] >= (uint16_t)INF || top[1] >= (uint16_t)INF) != 0;
+    }
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
       if (it.r0 + 16 * ks >= t.R) continue;
@@ -177,8 +204,23 @@ __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int 
           split_hi_lo<DT>(v, hi, lo);
 #pragma unroll
           for (int cb = 0; cb < CB; ++cb) {
-            acc[rb][cb] = mfma32x32x16<DT>(it.w[ks][cb], hi, acc[rb][cb]);
-            acc[rb][cb] = mfma32x32x16<DT>(it.w[ks][cb], lo, acc[rb][cb]);
+            u32x4 w = it.w[ks][cb];
+            if (broken) {
+              u32x4 bad;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t word = w[e];
+                const uint32_t mask = ((((word & 0x7FFF7FFFu) + (0x80008000u - 0x10001u * INF)) & 0x80008000u) >> 15) * 0xFFFFu;
+                w[e] = word & ~mask;
+                bad[e] = mask & 0x7F7F7F7Fu;
+              }
+              const bool own = (it.own[rb] >> lane) & 1;
+              const uint32_t big = own ? 0x7F007F00u : 0u, low = own ? 0xFF00FF00u : 0u;
+              acc[rb][cb] = mfma32x32x16<DT_BF16>(bad, u32x4{big, big, big, big}, acc[rb][cb]);
+              acc[rb][cb] = mfma32x32x16<DT_BF16>(bad, u32x4{low, low, low, low}, acc[rb][cb]);
+            }
+            acc[rb][cb] = mfma32x32x16<DT>(w, hi, acc[rb][cb]);
+            acc[rb][cb] = mfma32x32x16<DT>(w, lo, acc[rb][cb]);
           }
         }
     }

@@ -247,3 +247,24 @@ def test_refusals():
         ok(out=(None, case.t_la, torch.empty_like(case.t_lb)))
     with pytest.raises(L.W4A16Error, match="WORKSPACE"):
         ok(workspace=torch.zeros(4096, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dt", [O.F16, O.BF16])
+@pytest.mark.parametrize("M", [40, 150, 700])
+def test_a_broken_adapter_stays_with_its_tokens(M, dt):
+    # infinities and NaN in an adapter's factors: the other tokens' dx and the
+    # other adapters' gradients keep their bits
+    case = Grad(M, 192, 512, 64, dt, True, 4, 24, "mixed")
+    d = case.d
+    run = lambda la, lb: L.w4a16_lora_backward(case.t_dy, d.x, case.t_u, d.wq, d.s, la, lb, case.t_ids, d.zp,  # noqa: E731
+                                               case.t_alpha, group_size=64)
+    dx, dla, dlb = run(case.t_la, case.t_lb)
+    for value, down in ((float("inf"), True), (float("nan"), True), (float("nan"), False)):
+        la, lb = case.t_la.clone(), case.t_lb.clone()
+        (la if down else lb)[2, 7, 5] = value
+        gx, ga, gb = run(la, lb)
+        clean = case.t_ids != 2
+        assert torch.equal(gx[clean], dx[clean])
+        others = [0, 1, 3]
+        assert torch.equal(ga[others], dla[others]) and torch.equal(gb[others], dlb[others])
+        assert not torch.isfinite(gx[~clean]).all(dim=1).any()

@@ -206,3 +206,22 @@ def test_refusals():
     # no tokens: nothing to do
     y = ok(x=d.x[:0], ids=case.t_ids[:0])
     assert y.shape == (0, 64)
+
+
+@pytest.mark.parametrize("dt", [O.F16, O.BF16])
+@pytest.mark.parametrize("M", [9, 50, 150, 700])
+def test_a_broken_adapter_stays_with_its_tokens(M, dt):
+    # infinities and NaN in adapters that some tokens name: everyone else's
+    # outputs keep their bits, on every kernel and tile
+    case = LoraCase(M, 192, 512, 64, dt, False, True, 4, 24, "mixed", seed=9)
+    y = case.run()
+    for value, up in ((float("inf"), True), (float("nan"), True), (float("nan"), False)):
+        la, lb = case.t_la.clone(), case.t_lb.clone()
+        (lb if up else la)[2, 7, 5] = value
+        (lb if up else la)[1] = value
+        d = case.d
+        got = L.w4a16_lora_linear(d.x, d.wq, d.s, la, lb, case.t_ids, d.zp, d.bias, case.t_alpha, group_size=64)
+        clean = torch.from_numpy((case.ids != 1) & (case.ids != 2)).cuda()
+        assert torch.equal(got[clean], y[clean]), (value, up)
+        assert not torch.isfinite(got[case.t_ids == 1]).any()
+        assert not torch.isfinite(got[case.t_ids == 2]).all(dim=1).any()
