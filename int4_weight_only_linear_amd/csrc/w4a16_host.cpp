@@ -378,18 +378,21 @@ w4a16_path lora_path(int64_t M, int64_t N, int64_t K, int32_t group, int32_t dty
 
 // the workspace of w4a16_lora_linear: the projection's own (its counter region
 // always kept, so that one workspace serves every entry point), then the K
-// ranges' sums of u, and u itself where the caller does not keep it
+// ranges' sums of u (one range goes to the caller's u where it is kept), and
+// alpha * u as operands for the matrix tiles
 struct LoraPlan {
   w4a16_path path;
   w4a16::ShrinkPlan shrink;
-  size_t u_at, bytes;
+  size_t u_at, op_at, bytes;
 };
 LoraPlan plan_lora(int64_t M, int64_t N, int64_t K, int32_t kgroup, int32_t dtype, bool asym, int R, bool save_u, int cus) {
   LoraPlan p;
   p.path = lora_path(M, N, K, kgroup, dtype, asym);
   p.shrink = w4a16::plan_shrink(M, K, R, cus, p.path == W4A16_PATH_GEMV);
   p.u_at = round256(std::max(w4a16::kCounterBytes, workspace_for(M, N, K, kgroup, dtype, asym, p.path, cus)));
-  p.bytes = p.u_at + round256((size_t)(p.shrink.splits + (save_u ? 0 : 1)) * (size_t)M * (size_t)R * sizeof(float));
+  const size_t plane = (size_t)M * (size_t)R * sizeof(float);
+  p.op_at = p.u_at + round256(save_u && p.shrink.splits == 1 ? 0 : (size_t)p.shrink.splits * plane);
+  p.bytes = p.op_at + (p.path == W4A16_PATH_GEMV ? 0 : round256(plane));
   return p;
 }
 
@@ -896,20 +899,21 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
   const w4a16::ShrinkPlan& sp = plan.shrink;
   // Decode: the epilogue adds the K ranges' sums itself, which saves a launch
   // (a few floats per output).  Above it every tile of the GEMM reads all of
-  // its tokens' u, so the ranges are added once, before it.
+  // its tokens' alpha * u as operands, made once, before it.
   float* const part = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.u_at);
-  float* const sums = u ? u : (p == W4A16_PATH_GEMV ? nullptr : part + (size_t)sp.splits * M * R);
-  const w4a16::ShrinkArgs sa{x, la, ids, part, sums, M, K, (int)S, (int)R, dtype};
+  uint16_t* const op = p == W4A16_PATH_GEMV ? nullptr : reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + plan.op_at);
+  const w4a16::ShrinkArgs sa{x, la, ids, part, u, op, alpha, M, K, (int)S, (int)R, dtype};
   const hipError_t e = w4a16::launch_shrink(sa, sp, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(W4A16_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
   w4a16::LoraTerm t;
   t.ids = ids;
   t.up = lb;
-  t.u = sums ? sums : part;
+  t.u = u ? u : part;
   t.alpha = alpha;
+  t.op = op;
   t.S = (int)S;
   t.R = (int)R;
-  t.usplits = sums ? 1 : sp.splits;
+  t.usplits = u ? 1 : sp.splits;
   return linear_run(dev, p, gm, x, wq, scales, zp, bias, y, M, N, K, dtype, workspace, plan.u_at, stream, &t);
 }
 
@@ -1003,17 +1007,17 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
     prep.dx.dtype = dtype;
   }
   const uint16_t* const dyr = pad ? prep.dy_pad : prep.dy;
-  float* const g = static_cast<float*>(at(p.g));
+  uint16_t* const g = static_cast<uint16_t*>(at(p.g));
   e = w4a16::launch_prep(prep, s);
   if (e == hipSuccess) {
     // g / alpha = dy . B: the transposed lb in the first factor's place
-    const w4a16::ShrinkArgs sa{dyr, prep.lb_t, ids, static_cast<float*>(at(p.part)), nullptr, M, p.np, (int)S, (int)R, dtype};
+    const w4a16::ShrinkArgs sa{dyr, prep.lb_t, ids, static_cast<float*>(at(p.part)), nullptr, nullptr, nullptr, M, p.np, (int)S, (int)R, dtype};
     e = w4a16::launch_shrink(sa, p.shrink, s);
   }
   uint16_t* const op[2] = {static_cast<uint16_t*>(at(p.op[0])), static_cast<uint16_t*>(at(p.op[1]))};
   if (e == hipSuccess) {
     const w4a16::OperandArgs pa{static_cast<const float*>(at(p.part)), u, ids, prep.order, alpha, g, {op[0], op[1]},
-                                (int)M, (int)R, p.shrink.splits, (int)p.places, dtype};
+                                (int)M, (int)S, (int)R, p.shrink.splits, (int)p.places, dtype};
     e = w4a16::launch_operands(pa, s);
   }
   if (e == hipSuccess && dx) {
@@ -1022,8 +1026,7 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
     w4a16::LoraTerm t;
     t.ids = ids;
     t.up = prep.la_t;
-    t.u = g;
-    t.alpha = alpha;
+    t.op = g;
     t.S = (int)S;
     t.R = (int)R;
     e = w4a16::launch_dx(da, p.dx, t, s);

@@ -9,6 +9,8 @@ namespace w4a16 {
 
 namespace {
 
+typedef uint16_t u16x4 __attribute__((ext_vector_type(4)));
+
 // waves of a workgroup, and 32-k chunks a wave loads before it multiplies
 // (about 100 registers of loads in flight)
 constexpr int shrink_waves(int tt, int rc) { return tt + rc > 4 ? 8 : 16; }
@@ -28,7 +30,7 @@ constexpr int shrink_depth(int tt, int rc) { return tt + rc > 8 ? 1 : (tt + rc >
 template <int DT, int TT, int RC>
 __global__ __launch_bounds__(64 * shrink_waves(TT, RC)) void shrink_kernel(
     const uint16_t* __restrict__ x, const uint16_t* __restrict__ down, const int32_t* __restrict__ ids,
-    float* __restrict__ u, int M, int K, int S, int R, int chunks_per_split, int turns) {
+    float* __restrict__ u, uint16_t* __restrict__ op, const float* __restrict__ alpha, int M, int K, int S, int R, int chunks_per_split, int turns) {
   constexpr int WAVES = shrink_waves(TT, RC), DEPTH = shrink_depth(TT, RC), BM = 16 * TT, BR = 16 * RC;
   __shared__ __attribute__((aligned(16))) float red[WAVES * 256 * RC];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -119,15 +121,22 @@ __global__ __launch_bounds__(64 * shrink_waves(TT, RC)) void shrink_kernel(
 #pragma unroll
           for (int w = 0; w < WAVES; ++w) v += red[w * (16 * BR) + i];
           out[(size_t)(m0 + m) * R + r] = v;
+          if (op) {  // (one K range)
+            uint16_t* const d = op + (size_t)(m0 + m) * 2 * R + r;
+            split_hi_lo<DT>(alpha ? v * alpha[a] : v, d[0], d[R]);
+          }
         }
       }
     }
   }
 }
 
-// u = the K ranges' sums in range order; n a multiple of 4
-__global__ __launch_bounds__(256) void shrink_reduce_kernel(const float* __restrict__ part, float* __restrict__ u,
-                                                            int64_t n, int splits) {
+// u = the K ranges' sums in range order, and alpha * u as operands (each where
+// wanted); n = M R
+template <int DT>
+__global__ __launch_bounds__(256) void shrink_reduce_kernel(const float* __restrict__ part, const int32_t* __restrict__ ids,
+                                                            const float* __restrict__ alpha, float* __restrict__ u,
+                                                            uint16_t* __restrict__ op, int64_t n, int splits, int S, int R) {
   const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
   if (i >= n) return;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
@@ -139,7 +148,21 @@ __global__ __launch_bounds__(256) void shrink_reduce_kernel(const float* __restr
     for (int k = 0; k < 4; ++k)
       if (s0 + k < splits) v += p[k];
   }
-  *reinterpret_cast<f32x4*>(u + i) = v;
+  if (u) *reinterpret_cast<f32x4*>(u + i) = v;
+  if (!op) return;
+  const int64_t m = i / R;
+  const int r = (int)(i - m * R), a = ids[m];
+  const float k = alpha && a >= 0 && a < S ? alpha[a] : 1.f;
+  u16x4 h, l;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    uint16_t hi, lo;
+    split_hi_lo<DT>(k * v[e], hi, lo);
+    h[e] = hi, l[e] = lo;
+  }
+  uint16_t* const d = op + (size_t)m * 2 * R + r;
+  *reinterpret_cast<u16x4*>(d) = h;
+  *reinterpret_cast<u16x4*>(d + R) = l;
 }
 
 template <int DT, int TT, int RC>
@@ -150,8 +173,8 @@ hipError_t launch_t(const ShrinkArgs& a, const ShrinkPlan& p, float* out, hipStr
   if (units > INT32_MAX) return hipErrorInvalidValue;
   const dim3 grid((unsigned)units);
   hipLaunchKernelGGL((shrink_kernel<DT, TT, RC>), grid, dim3(64 * shrink_waves(TT, RC)), 0, s,
-                     static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.down), a.ids, out, (int)a.M,
-                     (int)a.K, a.S, a.R, p.chunks_per_split, turns);
+                     static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.down), a.ids, out,
+                     p.splits == 1 ? a.op : nullptr, a.alpha, (int)a.M, (int)a.K, a.S, a.R, p.chunks_per_split, turns);
   return hipGetLastError();
 }
 
@@ -187,9 +210,11 @@ ShrinkPlan plan_shrink(int64_t M, int64_t K, int R, int cu_count, bool few) {
 hipError_t launch_shrink(const ShrinkArgs& a, const ShrinkPlan& p, hipStream_t s) {
   float* const out = p.splits > 1 && a.u ? a.part : (a.u ? a.u : a.part);
   const hipError_t e = a.dtype == DT_F16 ? launch_dt<DT_F16>(a, p, out, s) : launch_dt<DT_BF16>(a, p, out, s);
-  if (e != hipSuccess || p.splits == 1 || !a.u) return e;
+  if (e != hipSuccess || p.splits == 1 || !(a.u || a.op)) return e;
   const int64_t n = a.M * a.R;
-  hipLaunchKernelGGL(shrink_reduce_kernel, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, s, a.part, a.u, n, p.splits);
+  auto kern = a.dtype == DT_F16 ? shrink_reduce_kernel<DT_F16> : shrink_reduce_kernel<DT_BF16>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, s, a.part, a.ids, a.alpha, a.u, a.op, n,
+                     p.splits, a.S, a.R);
   return hipGetLastError();
 }
 

@@ -81,6 +81,11 @@ __device__ __forceinline__ void split_hi_lo(const float (&v)[8], u32x4& hi, u32x
   hi = u32x4{h[0], h[1], h[2], h[3]};
   lo = u32x4{l[0], l[1], l[2], l[3]};
 }
+template <int DT>
+__device__ __forceinline__ void split_hi_lo(float v, uint16_t& hi, uint16_t& lo) {
+  hi = (uint16_t)f32x2_to_act_pair<DT>(v, 0.f);
+  lo = (uint16_t)f32x2_to_act_pair<DT>(v - act_to_f32<DT>(hi), 0.f);
+}
 
 // The GEMM tile's adapter term, as more k of its product: for every adapter
 // that a token of the tile names (in the order of their first tokens),
@@ -117,16 +122,14 @@ __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int 
   struct Item {
     int a, r0;           // adapter (-1: no more), first rank (of both halves)
     uint64_t own[MB];    // lanes whose token is the adapter's
-    float alpha;
     u32x4 w[KS][CB];
-    f32x4 u[KS][MB][2];
+    u32x4 u[KS][MB][2];  // alpha * u: value and remainder
   };
   // the item after `it`: the next ranks of its adapter, or the next adapter
   auto next = [&](const Item& it) {
     Item n;
     n.a = it.a;
     n.r0 = it.r0 + 16 * KS;
-    n.alpha = it.alpha;
 #pragma unroll
     for (int rb = 0; rb < MB; ++rb) n.own[rb] = it.own[rb];
     if (n.r0 >= t.R) {
@@ -143,7 +146,6 @@ __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int 
           todo[rb] &= ~n.own[rb];
         }
       } while (count++ % turns != turn);
-      n.alpha = lora_alpha(t, n.a);
     }
     // (R is a multiple of 8: a last k-sub may lie past it, wholly or its upper half)
 #pragma unroll
@@ -157,9 +159,9 @@ __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int 
       for (int rb = 0; rb < MB; ++rb)
         if (n.own[rb]) {
           const bool own = in && ((n.own[rb] >> lane) & 1);
-          const float* src = t.u + (size_t)(m0 + 32 * rb + j) * t.R + r + 8 * h;
-          n.u[ks][rb][0] = own ? *reinterpret_cast<const f32x4*>(src) : f32x4{0.f, 0.f, 0.f, 0.f};
-          n.u[ks][rb][1] = own ? *reinterpret_cast<const f32x4*>(src + 4) : f32x4{0.f, 0.f, 0.f, 0.f};
+          const uint16_t* src = t.op + (size_t)(m0 + 32 * rb + j) * 2 * t.R + r + 8 * h;
+          n.u[ks][rb][0] = own ? *reinterpret_cast<const u32x4*>(src) : u32x4{0u, 0u, 0u, 0u};
+          n.u[ks][rb][1] = own ? *reinterpret_cast<const u32x4*>(src + t.R) : u32x4{0u, 0u, 0u, 0u};
         }
     }
     return n;
@@ -197,11 +199,6 @@ __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int 
 #pragma unroll
       for (int rb = 0; rb < MB; ++rb)
         if (it.own[rb]) {
-          float v[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = it.u[ks][rb][e >> 2][e & 3] * it.alpha;
-          u32x4 hi, lo;
-          split_hi_lo<DT>(v, hi, lo);
 #pragma unroll
           for (int cb = 0; cb < CB; ++cb) {
             u32x4 w = it.w[ks][cb];
@@ -219,8 +216,8 @@ __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int 
               acc[rb][cb] = mfma32x32x16<DT_BF16>(bad, u32x4{big, big, big, big}, acc[rb][cb]);
               acc[rb][cb] = mfma32x32x16<DT_BF16>(bad, u32x4{low, low, low, low}, acc[rb][cb]);
             }
-            acc[rb][cb] = mfma32x32x16<DT>(w, hi, acc[rb][cb]);
-            acc[rb][cb] = mfma32x32x16<DT>(w, lo, acc[rb][cb]);
+            acc[rb][cb] = mfma32x32x16<DT>(w, it.u[ks][rb][0], acc[rb][cb]);
+            acc[rb][cb] = mfma32x32x16<DT>(w, it.u[ks][rb][1], acc[rb][cb]);
           }
         }
     }

@@ -192,7 +192,7 @@ __global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n
   for (int i = tid; i < a.zero_words; i += 256) a.zero[i] = 0u;
 }
 
-// Workgroups below row_blocks sum g's K ranges row by row; the others take 64
+// Workgroups below row_blocks sum g's K ranges token by token; the others take 64
 // places of one problem each and transpose its rows through LDS into operands.
 // (the sum over K ranges, four at a time so that their loads overlap)
 __device__ __forceinline__ f32x4 sum_ranges(const float* src, int64_t plane, int splits) {
@@ -214,9 +214,22 @@ __global__ __launch_bounds__(256) void operand_kernel(const OperandArgs a, int r
   const int tid = threadIdx.x;
   const int64_t n = (int64_t)a.M * a.R;
   if ((int)blockIdx.x < row_blocks) {
-    const int64_t i = ((int64_t)blockIdx.x * 256 + tid) * 4;
+    // eight ranks of a token (none is read of a token without an adapter)
+    const int64_t i = ((int64_t)blockIdx.x * 256 + tid) * 8;
     if (i >= n) return;
-    *reinterpret_cast<f32x4*>(a.g + i) = sum_ranges(a.part + i, n, a.splits);
+    const int64_t m = i / a.R;
+    const int s = a.ids[m];
+    if (s < 0 || s >= a.S) return;
+    const float alpha = a.alpha ? a.alpha[s] : 1.f;
+    const f32x4 g[2] = {sum_ranges(a.part + i, n, a.splits), sum_ranges(a.part + i + 4, n, a.splits)};
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = g[e >> 2][e & 3] * alpha;
+    u32x4 hi, lo;
+    split_hi_lo<DT>(v, hi, lo);
+    uint16_t* const d = a.g + 2 * m * a.R + (i - m * a.R);
+    *reinterpret_cast<u32x4*>(d) = hi;
+    *reinterpret_cast<u32x4*>(d + a.R) = lo;
     return;
   }
   const int job = blockIdx.x - row_blocks;
@@ -449,7 +462,7 @@ hipError_t launch_prep(const PrepArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_operands(const OperandArgs& a, hipStream_t s) {
-  const int row_blocks = (int)(((int64_t)a.M * a.R / 4 + 255) / 256), place_blocks = (a.places + kTile - 1) / kTile;
+  const int row_blocks = (int)(((int64_t)a.M * a.R / 8 + 255) / 256), place_blocks = (a.places + kTile - 1) / kTile;
   auto kern = a.dtype == DT_F16 ? operand_kernel<DT_F16> : operand_kernel<DT_BF16>;
   hipLaunchKernelGGL(kern, dim3(row_blocks + 2 * place_blocks), dim3(256), 0, s, a, row_blocks, place_blocks);
   return hipGetLastError();

@@ -43,17 +43,18 @@ struct PrepArgs {
 };
 hipError_t launch_prep(const PrepArgs& a, hipStream_t s);
 
-// g[m][r] = sum of its K ranges, and alpha * g and alpha * u as MFMA operands:
-// value and remainder in the activation dtype (split_hi_lo), by rank and place
+// alpha * g (the sum of its K ranges) and alpha * u as MFMA operands, value and
+// remainder in the activation dtype (split_hi_lo): both by rank and place, and
+// alpha * g by token
 struct OperandArgs {
   const float* part;    // [splits][M][R]
   const float* u;       // [M][R]
   const int32_t* ids;
   const int32_t* order;
   const float* alpha;   // [S] or NULL
-  float* g;             // [M][R]
+  uint16_t* g;          // [M][2][R]
   uint16_t* op[2];      // of g and of u: [2][R][places]
-  int M, R, splits, places, dtype;
+  int M, S, R, splits, places, dtype;
 };
 hipError_t launch_operands(const OperandArgs& a, hipStream_t s);
 
