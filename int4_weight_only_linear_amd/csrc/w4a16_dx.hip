@@ -274,7 +274,19 @@ static_for<0, 4>([&](auto kc) {
     if (s < s_end) step(s, w0, d0, w1, d1, b1, std::false_type{});
     wait_vm_all();  // no load into LDS in flight past the loop
   }
-  lora_steps<DT, MW, 4>(lora, p.M, p.K, m0 + 32 * MW * wm, k0 + 128 * wk, lane, split, p.splits, acc);
+  {
+    // rows of 256 tokens take all four buffers, 128 to an array (the halves of
+    // the tile that the waves own); shorter tiles one array each
+    static_assert(128 * 256 <= kWBytes && (BM != 256 || 128 * 256 <= BM * 128), "rows of the tile's tokens");
+    constexpr bool four = BM == 256;
+    lora_stage(lora, p.M, m0, BM, tid, kThreads,
+               [&](int m) { return four && m >= 128 ? w1 + 256 * (m - 128) : w0 + 256 * m; },
+               [&](int m) { return !four ? w1 + 256 * m : m >= 128 ? d1 + 256 * (m - 128) : d0 + 256 * m; });
+    const int first = 32 * MW * wm;
+    const lds_u8* hi = four ? (wm ? w1 : w0) : w0 + 256 * first;
+    const lds_u8* lo = four ? (wm ? d1 : d0) : w1 + 256 * first;
+    lora_steps<DT, MW, 4>(lora, p.M, p.K, m0 + first, k0 + 128 * wk, lane, split, p.splits, hi, lo, acc);
+  }
 
   // acc[mb][kb][4a + e]: token m0 + 32 (MW wm + mb) + j, k = k0 + 128 wk + 32 kb + 8a + 4h + e
 #pragma unroll

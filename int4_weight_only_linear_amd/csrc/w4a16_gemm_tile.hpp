@@ -463,7 +463,11 @@ __device__ __forceinline__ void gemm_tile(const GemmParams& p, const LoraTerm& l
 
   // ---- adapters beside the projection: more k of the same product, spread
   // over the K ranges' accumulators
-  if constexpr (LORA) lora_steps<DT, MB, CB>(lora, p.M, p.N, m0, nw0, lane, split, p.splits, acc);
+  if constexpr (LORA) {
+    static_assert(kXRowBytes == 256, "lora_stage's rows");
+    lora_stage(lora, p.M, m0, BM, tid, kThreads, [&](int m) { return buf0 + 256 * m; }, [&](int m) { return buf1 + 256 * m; });
+    lora_steps<DT, MB, CB>(lora, p.M, p.N, m0, nw0, lane, split, p.splits, buf0, buf1, acc);
+  }
 
   // ---- split-K: store the partial tile; the last unit of the tile sums them
   // in split order (cross-workgroup hand-off as described at store_coherent).

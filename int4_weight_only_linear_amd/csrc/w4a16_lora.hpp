@@ -87,24 +87,57 @@ __device__ __forceinline__ void split_hi_lo(float v, uint16_t& hi, uint16_t& lo)
   lo = (uint16_t)f32x2_to_act_pair<DT>(v - act_to_f32<DT>(hi), 0.f);
 }
 
+typedef __attribute__((address_space(3))) unsigned char lds_bytes;
+typedef __attribute__((address_space(3))) u32x4 lds_piece;
+typedef uint16_t uint16x2_t __attribute__((ext_vector_type(2)));
+
+// A tile's rows of t.op into LDS: 256 bytes a token, values from hi(token) and
+// remainders from lo(token), eight ranks (piece p) at p ^ (token & 15), so that
+// the operand reads of 16 tokens touch 16 different banks of 16 bytes.  Rows of
+// tokens without an adapter hold anything (lora_steps reads none of them).
+// Begins and ends with a barrier.
+template <typename Hi, typename Lo>
+__device__ __forceinline__ void lora_stage(const LoraTerm& t, int M, int m0, int tokens, int tid, int threads, Hi&& hi,
+                                           Lo&& lo) {
+  constexpr int B = 8;  // pieces in flight per thread
+  const int pieces = t.R >> 3, total = tokens * 2 * pieces;
+  __syncthreads();  // the buffers are free
+  for (int i0 = tid; i0 < total; i0 += threads * B) {
+    u32x4 v[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int i = min(i0 + b * threads, total - 1), m = i / (2 * pieces), p = i - m * 2 * pieces;
+      v[b] = *reinterpret_cast<const u32x4*>(t.op + (size_t)min(m0 + m, M - 1) * 2 * t.R + 8 * p);
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int i = min(i0 + b * threads, total - 1), m = i / (2 * pieces), p = i - m * 2 * pieces;
+      *(lds_piece*)((p < pieces ? hi(m) : lo(m)) + 16 * ((p < pieces ? p : p - pieces) ^ (m & 15))) = v[b];
+    }
+  }
+  __syncthreads();
+}
+
 // The GEMM tile's adapter term, as more k of its product: for every adapter
 // that a token of the tile names (in the order of their first tokens),
 // ceil(R / 16) k-subs whose A operand is the wave's rows of up_a and whose B
-// operand is alpha * u of the adapter's own tokens, zero for the others; token
-// blocks without such a token are left out.  The K ranges of a split tile take
-// the adapters in turns, and the operands of the next two k-subs are loaded
-// while two are multiplied: a tile of many adapters is otherwise a chain of
-// memory round trips (16 adapters of rank 32 among 67 tokens, 19456 x 2560:
-// 28 us of 48, now 11 of 31).  The large tiles, whose accumulators leave
-// few registers and whose tokens are mostly of one request, take one k-sub at
-// a time.
+// operand is alpha * u of the adapter's own tokens (from LDS), zero for the
+// others; token blocks without such a token are left out.  The K ranges of a
+// split tile take the adapters in turns.  A tile of many adapters is a chain
+// of items (KS k-subs of one adapter), so the rows of the next two are on
+// their way while one is multiplied.  Bound by the adapters' rows, read after
+// the weights, and by a wave's instructions: 67 tokens of 16 adapters, ranks of
+// 32, 2560 x 19456, fp16: 20.8 us without adapters, 22 with one per K range,
+// 29 with all (48 before operands were split once, staged and prefetched);
+// 1476 tokens of ten adapters mixed, ranks of 128, 256 x 5584: 112 -> 91 us
+// by the LDS and the prefetch.  1920 tokens of one adapter, ranks of 64,
+// 14336 x 4096: within 2 % of the product alone.
 //   acc[rb][cb]: tokens m0 + 32 rb + (lane & 31), features nw0 + 32 cb + ...
-typedef uint16_t uint16x2_t __attribute__((ext_vector_type(2)));
+//   hi, lo: rows of token m0 (lora_stage)
 template <int DT, int MB, int CB>
 __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int m0, int nw0, int lane, int turn, int turns,
-                                           f32x16 (&acc)[MB][CB]) {
-  constexpr bool DEEP = MB * CB <= 8;  // registers for operands in flight beside the accumulators
-  constexpr int KS = DEEP ? 2 : 1;      // k-subs of an item
+                                           const lds_bytes* hi, const lds_bytes* lo, f32x16 (&acc)[MB][CB]) {
+  constexpr int KS = MB * CB <= 8 ? 2 : 1;  // registers beside the accumulators
   const int j = lane & 31, h = lane >> 5;
   int id[MB];
   uint64_t todo[MB];
@@ -113,58 +146,43 @@ __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int 
     id[rb] = lora_id(t, M, m0 + 32 * rb + j);
     todo[rb] = __ballot(id[rb] >= 0);
   }
-  const uint16_t* up = static_cast<const uint16_t*>(t.up) + 8 * h;
+  const uint16_t* const up = static_cast<const uint16_t*>(t.up);
   uint32_t row[CB];
 #pragma unroll
   for (int cb = 0; cb < CB; ++cb) row[cb] = (uint32_t)min(nw0 + 32 * cb + j, N - 1);
   int count = 0;  // adapters of the tile seen so far
 
   struct Item {
-    int a, r0;           // adapter (-1: no more), first rank (of both halves)
-    uint64_t own[MB];    // lanes whose token is the adapter's
+    int a, r0;  // adapter (-1: no more), first rank (of both halves)
     u32x4 w[KS][CB];
-    u32x4 u[KS][MB][2];  // alpha * u: value and remainder
   };
-  // the item after `it`: the next ranks of its adapter, or the next adapter
-  auto next = [&](const Item& it) {
-    Item n;
-    n.a = it.a;
-    n.r0 = it.r0 + 16 * KS;
-#pragma unroll
-    for (int rb = 0; rb < MB; ++rb) n.own[rb] = it.own[rb];
-    if (n.r0 >= t.R) {
-      n.r0 = 0;
+  // The item after ranks r0 of adapter a: its next ranks, or the next adapter.
+  // The loads stand behind no branch (valid addresses throughout, zeros put in
+  // by multiply): behind one their number is unknown, and every wait would be
+  // for all of them.
+  auto next = [&](int a, int r0, Item& n) {
+    r0 += 16 * KS;
+    if (a < 0 || r0 >= t.R) {
+      r0 = 0;
       do {
-        n.a = -1;
+        a = -1;
 #pragma unroll
         for (int rb = MB - 1; rb >= 0; --rb)
-          if (todo[rb]) n.a = __builtin_amdgcn_readlane(id[rb], __builtin_ctzll(todo[rb]));
-        if (n.a < 0) return n;
+          if (todo[rb]) a = __builtin_amdgcn_readlane(id[rb], __builtin_ctzll(todo[rb]));
+        if (a < 0) break;
 #pragma unroll
-        for (int rb = 0; rb < MB; ++rb) {
-          n.own[rb] = __ballot(id[rb] == n.a);
-          todo[rb] &= ~n.own[rb];
-        }
+        for (int rb = 0; rb < MB; ++rb) todo[rb] &= ~__ballot(id[rb] == a);
       } while (count++ % turns != turn);
     }
-    // (R is a multiple of 8: a last k-sub may lie past it, wholly or its upper half)
+    n.a = a;
+    n.r0 = r0;
+    const uint16_t* const rows = up + (size_t)max(a, 0) * N * t.R;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      const int r = n.r0 + 16 * ks;
-      const bool in = r + 8 * h < t.R;
+      const int r = min(r0 + 16 * ks + 8 * h, t.R - 8);
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb)
-        n.w[ks][cb] = in ? *reinterpret_cast<const u32x4*>(up + ((size_t)n.a * N + row[cb]) * t.R + r) : u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int rb = 0; rb < MB; ++rb)
-        if (n.own[rb]) {
-          const bool own = in && ((n.own[rb] >> lane) & 1);
-          const uint16_t* src = t.op + (size_t)(m0 + 32 * rb + j) * 2 * t.R + r + 8 * h;
-          n.u[ks][rb][0] = own ? *reinterpret_cast<const u32x4*>(src) : u32x4{0u, 0u, 0u, 0u};
-          n.u[ks][rb][1] = own ? *reinterpret_cast<const u32x4*>(src + t.R) : u32x4{0u, 0u, 0u, 0u};
-        }
+      for (int cb = 0; cb < CB; ++cb) n.w[ks][cb] = *reinterpret_cast<const u32x4*>(rows + (size_t)row[cb] * t.R + r);
     }
-    return n;
   };
   // Other adapters' tokens of a block take part with zeros, which an infinite
   // or NaN factor would turn into NaN.  Where an item holds one, it is taken
@@ -172,69 +190,75 @@ __device__ __forceinline__ void lora_steps(const LoraTerm& t, int M, int N, int 
   // adapter's own tokens: + and - max * 2^127, in bf16 whose products pass
   // fp32's range; zeros stay zeros.  (Selecting sums by token instead keeps
   // them in vector registers: up to 1150 spilled.  The test costs 8 operations
-  // a fragment, nothing where all tokens are the adapter's.)
+  // a fragment.)
   auto multiply = [&](const Item& it) {
-    uint64_t others = 0;
-#pragma unroll
-    for (int rb = 0; rb < MB; ++rb)
-      if (it.own[rb]) others |= __ballot(m0 + 32 * rb + j < M) & ~it.own[rb];
-    bool broken = false;
     constexpr uint32_t INF = DT == DT_F16 ? 0x7C00 : 0x7F80;
-    if (others) {
-      uint16x2_t top = {0, 0};
+    uint16x2_t top = {0, 0};
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
+    for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int cb = 0; cb < CB; ++cb)
+      for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t word = it.w[ks][cb][e] & 0x7FFF7FFFu;
-            top = __builtin_elementwise_max(top, __builtin_bit_cast(uint16x2_t, word));
-          }
-      broken = __ballot(top[0] >= (uint16_t)INF || top[1] >= (uint16_t)INF) != 0;
-    }
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t word = it.w[ks][cb][e] & 0x7FFF7FFFu;
+          top = __builtin_elementwise_max(top, __builtin_bit_cast(uint16x2_t, word));
+        }
+    const bool broken = __ballot(top[0] >= (uint16_t)INF || top[1] >= (uint16_t)INF) != 0;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
+      // R is a multiple of 8: a last k-sub may lie past it, wholly or its upper half
       if (it.r0 + 16 * ks >= t.R) continue;
+      const int piece = (it.r0 >> 3) + 2 * ks + h;
+      const bool in = 8 * piece < t.R;
+      u32x4 w[CB], bad[CB];
 #pragma unroll
-      for (int rb = 0; rb < MB; ++rb)
-        if (it.own[rb]) {
+      for (int cb = 0; cb < CB; ++cb) {
+        w[cb] = in ? it.w[ks][cb] : u32x4{0u, 0u, 0u, 0u};
+        if (broken) {
 #pragma unroll
-          for (int cb = 0; cb < CB; ++cb) {
-            u32x4 w = it.w[ks][cb];
-            if (broken) {
-              u32x4 bad;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t word = w[e];
-                const uint32_t mask = ((((word & 0x7FFF7FFFu) + (0x80008000u - 0x10001u * INF)) & 0x80008000u) >> 15) * 0xFFFFu;
-                w[e] = word & ~mask;
-                bad[e] = mask & 0x7F7F7F7Fu;
-              }
-              const bool own = (it.own[rb] >> lane) & 1;
-              const uint32_t big = own ? 0x7F007F00u : 0u, low = own ? 0xFF00FF00u : 0u;
-              acc[rb][cb] = mfma32x32x16<DT_BF16>(bad, u32x4{big, big, big, big}, acc[rb][cb]);
-              acc[rb][cb] = mfma32x32x16<DT_BF16>(bad, u32x4{low, low, low, low}, acc[rb][cb]);
-            }
-            acc[rb][cb] = mfma32x32x16<DT>(w, it.u[ks][rb][0], acc[rb][cb]);
-            acc[rb][cb] = mfma32x32x16<DT>(w, it.u[ks][rb][1], acc[rb][cb]);
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t word = w[cb][e];
+            const uint32_t mask = ((((word & 0x7FFF7FFFu) + (0x80008000u - 0x10001u * INF)) & 0x80008000u) >> 15) * 0xFFFFu;
+            w[cb][e] = word & ~mask;
+            bad[cb][e] = mask & 0x7F7F7F7Fu;
           }
         }
+      }
+#pragma unroll
+      for (int rb = 0; rb < MB; ++rb) {
+        const bool own = id[rb] == it.a;
+        if (__ballot(own) == 0) continue;
+        const int at = (32 * rb + j) * 256 + 16 * (piece ^ (j & 15));
+        u32x4 x = *(const lds_piece*)(hi + at), y = *(const lds_piece*)(lo + at);
+        if (!(own && in)) x = y = u32x4{0u, 0u, 0u, 0u};
+        if (broken) {
+          const uint32_t big = own ? 0x7F007F00u : 0u, low = own ? 0xFF00FF00u : 0u;
+#pragma unroll
+          for (int cb = 0; cb < CB; ++cb) {
+            acc[rb][cb] = mfma32x32x16<DT_BF16>(bad[cb], u32x4{big, big, big, big}, acc[rb][cb]);
+            acc[rb][cb] = mfma32x32x16<DT_BF16>(bad[cb], u32x4{low, low, low, low}, acc[rb][cb]);
+          }
+        }
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb) {
+          acc[rb][cb] = mfma32x32x16<DT>(w[cb], x, acc[rb][cb]);
+          acc[rb][cb] = mfma32x32x16<DT>(w[cb], y, acc[rb][cb]);
+        }
+      }
     }
   };
-  Item none{};
-  none.r0 = t.R;
-  Item p = next(none);
-  if constexpr (!DEEP) {
-    for (; p.a >= 0; p = next(p)) multiply(p);
-    return;
-  }
+  Item p, q, r;
+  next(-1, 0, p);
+  next(p.a, p.r0, q);
   while (p.a >= 0) {
-    const Item q = next(p);
+    next(q.a, q.r0, r);
     multiply(p);
     if (q.a < 0) break;
-    p = next(q);
+    next(r.a, r.r0, p);
     multiply(q);
+    if (r.a < 0) break;
+    next(p.a, p.r0, q);
+    multiply(r);
   }
 }
 
