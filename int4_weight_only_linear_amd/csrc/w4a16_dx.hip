@@ -20,7 +20,7 @@
 // Bound by instructions beside the matrix cores, one wave on each SIMD, as the
 // forward GEMM: 1920 tokens, 4096 x 28672: 417-427 us, 1060-1080 TFLOP/s, the
 // matrix cores busy 53-56 % of the time, and 14 us for the sum of its two ranges
-// of n; 1921 tokens, 4096 x 6144, fp16: 109 us, 890 TFLOP/s; 128 tokens, 4096 x
+// of n; 1921 tokens, 4096 x 6144, fp16: 109-116 us, 830-890 TFLOP/s; 128 tokens, 4096 x
 // 4096: 19-20 us and 4.4, latency: eight ranges of eight steps.
 #include <algorithm>
 
