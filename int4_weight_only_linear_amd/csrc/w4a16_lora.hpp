@@ -133,8 +133,9 @@ __device__ __forceinline__ void lora_stage(const LoraTerm& t, int M, int m0, int
 // 32, 2560 x 19456, fp16: 20.8 us without adapters, 22 with one per K range,
 // 29 with all (48 before operands were split once, staged and prefetched);
 // 1476 tokens of ten adapters mixed, ranks of 128, 256 x 5584: 112 -> 91 us
-// by the LDS and the prefetch.  1920 tokens of one adapter, ranks of 64,
-// 14336 x 4096: within 2 % of the product alone.
+// by the LDS and the prefetch (15 without adapters).  1920 tokens of one
+// adapter, ranks of 64, 14336 x 4096: 213 us, 208 without; of six, ranks of 16,
+// 4096 x 28672: 419 us, 391 without.
 //   acc[rb][cb]: tokens m0 + 32 rb + (lane & 31), features nw0 + 32 cb + ...
 //   hi, lo: rows of token m0 (lora_stage)
 template <int DT, int MB, int CB>
