@@ -619,17 +619,18 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(small_wave
   }
 
   // ---- 4. reduce the waves in order, then the K ranges ----
-  // (low-rank adapters: each wave adds its tokens' term to its own sums)
-  auto add_lora = [&]() {
-    lora_wave_add<DT>(p.lora, p.M, p.N, n0, wave, nwaves, lane, [&](int m, int row, float v) {
-      red[wave * 256 + (m & 3) * 64 + 16 * (m >> 2) + row] += v;
+  // (low-rank adapters, with the first K range: each wave adds its tokens' term
+  // to its own sums; token m is register m & 3 of 16-lane row m >> 2)
+  if (p.lora.ids && split == 0)
+    lora_wave_add<DT>(p.lora, p.M, p.N, n0, wave, nwaves, lane, [&](int m, float v) {
+#pragma unroll
+      for (int r = 0; r < (ONE ? 1 : 4); ++r)
+        if ((m & 3) == r && (m >> 2) == row4) acc[r] += v;
     });
-  };
   if constexpr (ONE) {
     if (p.splits == 1) {
       // one token, one K range: the sums are register 0 of lanes 0..15
       red[wave * 256 + lane] = acc[0];
-      if (p.lora.ids) add_lora();
       __syncthreads();
       const int nn = n0 + tid;
       if (tid < kGemvRowsPerTile && nn < p.N) {
@@ -646,7 +647,6 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(small_wave
     // 0..15 (the general path's order: waves in order, then bias, rounding)
 #pragma unroll
     for (int r = 0; r < 4; ++r) red[wave * 256 + r * 64 + lane] = acc[r];
-    if (p.lora.ids) add_lora();
     __syncthreads();
     const int m = tid >> 4, nn = n0 + (tid & 15);
     if (tid < 16 * p.M && nn < p.N) {
@@ -659,7 +659,6 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(small_wave
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) red[wave * 256 + r * 64 + lane] = acc[r];
-  if (p.lora.ids && split == 0) add_lora();
   __syncthreads();
   finish_tile<DT>(p, red, nwaves, 256, tile, split, &last_flag);
 }
@@ -1006,22 +1005,25 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(one_waves_
     }
   }
 #pragma unroll
-  for (int r = 0; r < SLOTS; ++r) {
-    if constexpr (MT == 8) {
-      // rows 0 + 2 (tokens 0..3) and 1 + 3 (tokens 4..7), in lanes 0..31
-      const float v = halves_sum(acc[r]);
-      if (lane < 32) red_of(wave)[(4 * row4 + r) * 16 + col] = v;
-    } else {
-      const float v = rows_sum(acc[r]);
-      if (lane < 16) red_of(wave)[r * 16 + lane] = v;
-    }
-  }
-  // low-rank adapters: each wave adds its tokens' term to its own sums (of the
-  // first K range)
+  for (int r = 0; r < SLOTS; ++r)  // eight tokens: rows 0 + 2 (tokens 0..3) and 1 + 3 (tokens 4..7), in lanes 0..31
+    acc[r] = MT == 8 ? halves_sum(acc[r]) : rows_sum(acc[r]);
+  // low-rank adapters, with the first K range: each wave adds its tokens' term
+  // to its own sums
   if constexpr (!MOE) {
     if (moe.lora.ids && blockIdx.y == 0)
-      lora_wave_add<DT>(moe.lora, M, N, n0, wave, nwaves, lane,
-                        [&](int m, int row, float v) { red_of(wave)[m * 16 + row] += v; });
+      lora_wave_add<DT>(moe.lora, M, N, n0, wave, nwaves, lane, [&](int m, float v) {
+#pragma unroll
+        for (int r = 0; r < SLOTS; ++r)
+          if (MT == 8 ? (m & 3) == r && (m >> 2) == row4 : m == r) acc[r] += v;
+      });
+  }
+#pragma unroll
+  for (int r = 0; r < SLOTS; ++r) {
+    if constexpr (MT == 8) {
+      if (lane < 32) red_of(wave)[(4 * row4 + r) * 16 + col] = acc[r];
+    } else {
+      if (lane < 16) red_of(wave)[r * 16 + lane] = acc[r];
+    }
   }
   __syncthreads();
   // 16 M outputs (a workgroup of one wave covers eight tokens in two passes)

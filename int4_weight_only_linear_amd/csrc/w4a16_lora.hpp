@@ -23,10 +23,12 @@ __device__ __forceinline__ float lora_alpha(const LoraTerm& t, int a) { return t
 
 // The decode kernels' term, in fp32 throughout.  Token m belongs to the wave
 // m % waves, which adds the term of the tile's 16 rows n0.. to its own sums
-// before the waves are added (add(m, row, value), lanes 0..15): no further
-// barrier, and every wave's loads are under way at once.  A lane takes every
-// fourth run of eight ranks of one row; the K ranges of u are read four at a
-// time, so that their loads overlap.
+// before the waves are added: no further barrier, and every wave's loads are
+// under way at once.  add(m, value) is called by all lanes with the term of
+// row lane & 15, so that the lanes that hold token m's sums add it in their
+// registers (in LDS they would have to wait for other lanes' stores).  A lane
+// takes every fourth run of eight ranks of one row; the K ranges of u are read
+// four at a time, so that their loads overlap.
 // Bound by that one chain of loads: 3 us of 15.3 with 16 tokens of 16 adapters,
 // ranks of 16, 4096 x 6144 (12.3 without adapters; spread over the projection's
 // K ranges as well 15.1).
@@ -65,7 +67,7 @@ __device__ __forceinline__ void lora_wave_add(const LoraTerm& t, int M, int N, i
     }
     s += __shfl_xor(s, 16);
     s += __shfl_xor(s, 32);
-    if (lane < 16) add(m, lane, s * alpha);
+    add(m, s * alpha);
   }
 }
 
