@@ -88,7 +88,13 @@ struct GemvParams {
   int topk, experts, x_per_slot;
   size_t w_estride, s_estride, z_estride;  // words / halves / words per expert
   int slots;  // workgroups along z: 1, or the expert slots
-  LoraTerm lora;  // low-rank adapters beside the projection (ids NULL: none)
+};
+// Low-rank adapters beside the projection have instances of their own: inside
+// the plain ones they cost up to 2.4 % even where no adapter is given (seven
+// waves per SIMD instead of eight, twice the scalar registers; 14336 x 4096, bf16,
+// groups of 32, one token: 8.59 -> 8.79 us; 4096 x 28672, fp16, eight: 26.1 -> 26.4).
+struct GemvLoraParams : GemvParams {
+  LoraTerm lora;
 };
 
 // One 16-byte global->LDS load per active lane: lane l reads base + off and
@@ -242,11 +248,11 @@ constexpr int small_waves_per_simd(int kpw, bool one, int gs, int xpt) {
 // in SGPRs when the wave starts instead of after a scalar load from the
 // argument segment (gfx950 preloads plain arguments, not the parameter
 // struct).  The other fields that the loads need are derived from them.
-template <int DT, int GS, bool ASYM, int KPW, int XPT, bool ONE, bool MOE, bool WGSZ>
+template <int DT, int GS, bool ASYM, int KPW, int XPT, bool ONE, bool MOE, bool WGSZ, class Params>
 __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(small_waves_per_simd(KPW, ONE, GS, XPT)))) void gemv_small_kernel(const uint16_t* a_x, const uint32_t* a_wq,
                                                           const uint16_t* a_scales, const uint32_t* a_zp,
                                                           int a_M, int a_N, int a_K, int a_sG, int a_gmul,
-                                                          int a_kps, const GemvParams params) {
+                                                          int a_kps, const Params params) {
   constexpr int CPG = GS / 32;          // 32-k chunks per group (1, 2, 4)
   constexpr int SPT = (32 * KPW) / GS > 0 ? (32 * KPW) / GS : 1;  // scale loads per lane
   static_assert(!WGSZ || (ONE && DT == DT_BF16 && GS == 128 && KPW == 8), "WGSZ instance");
@@ -621,12 +627,14 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(small_wave
   // ---- 4. reduce the waves in order, then the K ranges ----
   // (low-rank adapters, with the first K range: each wave adds its tokens' term
   // to its own sums; token m is register m & 3 of 16-lane row m >> 2)
-  if (p.lora.ids && split == 0)
-    lora_wave_add<DT>(p.lora, p.M, p.N, n0, wave, nwaves, lane, [&](int m, float v) {
+  if constexpr (std::is_same_v<Params, GemvLoraParams>) {
+    if (split == 0)
+      lora_wave_add<DT>(params.lora, p.M, p.N, n0, wave, nwaves, lane, [&](int m, float v) {
 #pragma unroll
-      for (int r = 0; r < (ONE ? 1 : 4); ++r)
-        if ((m & 3) == r && (m >> 2) == row4) acc[r] += v;
-    });
+        for (int r = 0; r < (ONE ? 1 : 4); ++r)
+          if ((m & 3) == r && (m >> 2) == row4) acc[r] += v;
+      });
+  }
   if constexpr (ONE) {
     if (p.splits == 1) {
       // one token, one K range: the sums are register 0 of lanes 0..15
@@ -776,20 +784,25 @@ struct OneArgs {
   float* partial;
   uint32_t* counters;
   int splits, runs_per_split;
-  LoraTerm lora;  // low-rank adapters beside the projection (ids NULL: none)
+};
+struct OneLoraArgs : OneArgs {
+  LoraTerm lora;  // low-rank adapters beside the projection
 };
 
 // PART: the last wave's run may be shorter (otherwise every run is whole and
 // the masks and clamps below compile away).  MODE: ONE_PLAIN, ONE_MOE
 // (expert-indexed, MT == 1) or ONE_SPLIT (K ranges; a plain launch computes
 // its runs from the wave index alone, with no wait for an argument load
-// before the weight addresses).
-enum { ONE_PLAIN = 0, ONE_MOE = 1, ONE_SPLIT = 2 };
-template <int DT, int GS, bool ASYM, int KPW, int MT, bool PART, int MODE>
+// before the weight addresses); ONE_LORA and ONE_LORA_SPLIT: the plain and the
+// split one with low-rank adapters.
+enum { ONE_PLAIN = 0, ONE_MOE = 1, ONE_SPLIT = 2, ONE_LORA = 3, ONE_LORA_SPLIT = 4 };
+template <int DT, int GS, bool ASYM, int KPW, int MT, bool PART, int MODE, class Args>
 __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(one_waves_per_simd(KPW, GS, MT)))) void gemv_one_kernel(
     const uint16_t* a_x, const uint32_t* a_wq, const uint16_t* a_scales, const uint32_t* a_zp, int N, int K,
-    int sG, int M, const uint16_t* bias, uint16_t* y, const OneArgs moe) {
-  constexpr bool MOE = MODE == ONE_MOE, SPLIT = MODE == ONE_SPLIT;
+    int sG, int M, const uint16_t* bias, uint16_t* y, const Args moe) {
+  constexpr bool MOE = MODE == ONE_MOE, SPLIT = MODE == ONE_SPLIT || MODE == ONE_LORA_SPLIT;
+  constexpr bool LORA = MODE == ONE_LORA || MODE == ONE_LORA_SPLIT;
+  static_assert(std::is_same_v<Args, std::conditional_t<LORA, OneLoraArgs, OneArgs>>, "arguments of the mode");
   constexpr int CPG = GS / 32;            // 32-k chunks per group
   constexpr int NC = 4 * KPW;             // chunks of a run
   constexpr int NGW = NC / CPG;           // groups of a run
@@ -1004,13 +1017,18 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(one_waves_
       acc[r] = __builtin_fmaf(sv, v, __builtin_fmaf(szc, xsum[r][t], acc[r]));
     }
   }
+  // Up to four tokens the sums are formed before any is stored (14336 x 4096,
+  // group 64, four tokens: 10.5 us; one by one 12.7); eight one by one (2048 x
+  // 1536, group 32: 4.62 us; before any 4.74).
+  constexpr bool FIRST = LORA || MT <= 4;
+  if constexpr (FIRST) {
 #pragma unroll
-  for (int r = 0; r < SLOTS; ++r)  // eight tokens: rows 0 + 2 (tokens 0..3) and 1 + 3 (tokens 4..7), in lanes 0..31
-    acc[r] = MT == 8 ? halves_sum(acc[r]) : rows_sum(acc[r]);
+    for (int r = 0; r < SLOTS; ++r) acc[r] = MT == 8 ? halves_sum(acc[r]) : rows_sum(acc[r]);
+  }
   // low-rank adapters, with the first K range: each wave adds its tokens' term
   // to its own sums
-  if constexpr (!MOE) {
-    if (moe.lora.ids && blockIdx.y == 0)
+  if constexpr (LORA) {
+    if (!SPLIT || blockIdx.y == 0)
       lora_wave_add<DT>(moe.lora, M, N, n0, wave, nwaves, lane, [&](int m, float v) {
 #pragma unroll
         for (int r = 0; r < SLOTS; ++r)
@@ -1020,7 +1038,9 @@ __global__ __launch_bounds__(1024) __attribute__((amdgpu_waves_per_eu(one_waves_
 #pragma unroll
   for (int r = 0; r < SLOTS; ++r) {
     if constexpr (MT == 8) {
-      if (lane < 32) red_of(wave)[(4 * row4 + r) * 16 + col] = acc[r];
+      // rows 0 + 2 (tokens 0..3) and 1 + 3 (tokens 4..7), in lanes 0..31
+      const float v = FIRST ? acc[r] : halves_sum(acc[r]);
+      if (lane < 32) red_of(wave)[(4 * row4 + r) * 16 + col] = v;
     } else {
       if (lane < 16) red_of(wave)[r * 16 + lane] = acc[r];
     }
@@ -1203,9 +1223,13 @@ constexpr int small_xpt(int kpw, bool one) {
 
 // the small kernel is instantiated per k-steps per wave, so that its
 // branch-free path covers every wave whose run is complete
-template <int DT, int GS, bool ASYM, bool MOE>
-static hipError_t launch_small(const GemvParams& prm, const GemvPlan& plan, dim3 grid, dim3 block,
+template <int DT, int GS, bool ASYM, bool MOE, class Params>
+static hipError_t launch_small(const Params& prm, const GemvPlan& plan, dim3 grid, dim3 block,
                                hipStream_t s) {
+  auto go = [&](auto kern) {
+    hipLaunchKernelGGL(kern, grid, block, plan.lds_bytes, s, prm.x, prm.wq, prm.scales, prm.zp, prm.M, prm.N, prm.K, prm.sG,
+                       prm.gmul, prm.ksteps_per_split, prm);
+  };
   const bool one = plan.kpw == 8 && prm.M == 1;
   // three or four tokens at 8 k-steps (K too long for 4 without a split)
   // stage up to 8 x segments per lane
@@ -1225,45 +1249,46 @@ static hipError_t launch_small(const GemvParams& prm, const GemvPlan& plan, dim3
       if (one) {
         if constexpr (DT == DT_BF16 && GS == 128) {
           if (wgsz) {
-            hipLaunchKernelGGL((gemv_small_kernel<DT, GS, ASYM, 8, small_xpt(8, true), true, MOE, true>), grid, block, plan.lds_bytes, s, prm.x, prm.wq, prm.scales, prm.zp, prm.M, prm.N, prm.K, prm.sG, prm.gmul, prm.ksteps_per_split, prm);
+            go(gemv_small_kernel<DT, GS, ASYM, 8, small_xpt(8, true), true, MOE, true, Params>);
             break;
           }
         }
-        hipLaunchKernelGGL((gemv_small_kernel<DT, GS, ASYM, 8, small_xpt(8, true), true, MOE, false>), grid, block, plan.lds_bytes, s, prm.x, prm.wq, prm.scales, prm.zp, prm.M, prm.N, prm.K, prm.sG, prm.gmul, prm.ksteps_per_split, prm);
+        go(gemv_small_kernel<DT, GS, ASYM, 8, small_xpt(8, true), true, MOE, false, Params>);
       } else if (x8) {
         if constexpr (!MOE)
-          hipLaunchKernelGGL((gemv_small_kernel<DT, GS, ASYM, 8, 8, false, MOE, false>), grid, block, plan.lds_bytes, s, prm.x, prm.wq, prm.scales, prm.zp, prm.M, prm.N, prm.K, prm.sG, prm.gmul, prm.ksteps_per_split, prm);
+          go(gemv_small_kernel<DT, GS, ASYM, 8, 8, false, MOE, false, Params>);
       } else {
-        hipLaunchKernelGGL((gemv_small_kernel<DT, GS, ASYM, 8, small_xpt(8, false), false, MOE, false>), grid, block, plan.lds_bytes, s, prm.x, prm.wq, prm.scales, prm.zp, prm.M, prm.N, prm.K, prm.sG, prm.gmul, prm.ksteps_per_split, prm);
+        go(gemv_small_kernel<DT, GS, ASYM, 8, small_xpt(8, false), false, MOE, false, Params>);
       }
       break;
-    case 4: hipLaunchKernelGGL((gemv_small_kernel<DT, GS, ASYM, 4, small_xpt(4, false), false, MOE, false>), grid, block, plan.lds_bytes, s, prm.x, prm.wq, prm.scales, prm.zp, prm.M, prm.N, prm.K, prm.sG, prm.gmul, prm.ksteps_per_split, prm); break;
-    case 2: hipLaunchKernelGGL((gemv_small_kernel<DT, GS, ASYM, 2, small_xpt(2, false), false, MOE, false>), grid, block, plan.lds_bytes, s, prm.x, prm.wq, prm.scales, prm.zp, prm.M, prm.N, prm.K, prm.sG, prm.gmul, prm.ksteps_per_split, prm); break;
-    case 1: hipLaunchKernelGGL((gemv_small_kernel<DT, GS, ASYM, 1, small_xpt(1, false), false, MOE, false>), grid, block, plan.lds_bytes, s, prm.x, prm.wq, prm.scales, prm.zp, prm.M, prm.N, prm.K, prm.sG, prm.gmul, prm.ksteps_per_split, prm); break;
+    case 4: go(gemv_small_kernel<DT, GS, ASYM, 4, small_xpt(4, false), false, MOE, false, Params>); break;
+    case 2: go(gemv_small_kernel<DT, GS, ASYM, 2, small_xpt(2, false), false, MOE, false, Params>); break;
+    case 1: go(gemv_small_kernel<DT, GS, ASYM, 1, small_xpt(1, false), false, MOE, false, Params>); break;
     default: return hipErrorInvalidConfiguration;
   }
   return hipGetLastError();
 }
 
 template <int DT, int GS, bool ASYM>
-static hipError_t launch_t(const GemvParams& prm, const GemvPlan& plan, int launch_tiles, hipStream_t s) {
+static hipError_t launch_t(const GemvParams& prm, const LoraTerm* lora, const GemvPlan& plan, int launch_tiles, hipStream_t s) {
   dim3 grid(launch_tiles, plan.splits, prm.slots);
   dim3 block(plan.waves * 64);
+  if (lora) return launch_small<DT, GS, ASYM, false>(GemvLoraParams{prm, *lora}, plan, grid, block, s);
   return prm.moe_ids ? launch_small<DT, GS, ASYM, true>(prm, plan, grid, block, s)
                      : launch_small<DT, GS, ASYM, false>(prm, plan, grid, block, s);
 }
 
 template <int DT, int GS>
-static hipError_t launch_z(const GemvParams& prm, const GemvPlan& plan, int lt, hipStream_t s) {
-  return prm.zp ? launch_t<DT, GS, true>(prm, plan, lt, s) : launch_t<DT, GS, false>(prm, plan, lt, s);
+static hipError_t launch_z(const GemvParams& prm, const LoraTerm* lora, const GemvPlan& plan, int lt, hipStream_t s) {
+  return prm.zp ? launch_t<DT, GS, true>(prm, lora, plan, lt, s) : launch_t<DT, GS, false>(prm, lora, plan, lt, s);
 }
 
 template <int DT>
-static hipError_t launch_g(const GemvParams& prm, int group, const GemvPlan& plan, int lt, hipStream_t s) {
+static hipError_t launch_g(const GemvParams& prm, const LoraTerm* lora, int group, const GemvPlan& plan, int lt, hipStream_t s) {
   switch (group) {
-    case 32: return launch_z<DT, 32>(prm, plan, lt, s);
-    case 64: return launch_z<DT, 64>(prm, plan, lt, s);
-    case 128: return launch_z<DT, 128>(prm, plan, lt, s);
+    case 32: return launch_z<DT, 32>(prm, lora, plan, lt, s);
+    case 64: return launch_z<DT, 64>(prm, lora, plan, lt, s);
+    case 128: return launch_z<DT, 128>(prm, lora, plan, lt, s);
     default: return hipErrorInvalidValue;
   }
 }
@@ -1282,18 +1307,24 @@ static hipError_t launch_one_k(const LinearArgs& a, const GemvPlan& plan, hipStr
     const int runs = (int)((a.K / kGemvKStep + KPW - 1) / KPW);
     const bool part = (int64_t)runs * KPW * kGemvKStep != a.K || plan.one_splits * plan.one_waves != runs;
     OneArgs om{};
-    if (lora) om.lora = *lora;
     om.splits = plan.one_splits;
     om.runs_per_split = plan.one_waves;
     if (plan.one_splits > 1) {
       om.counters = static_cast<uint32_t*>(workspace);
       om.partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
     }
-    auto kern = plan.one_splits > 1
-                    ? (part ? gemv_one_kernel<DT, GS, ASYM, KPW, MT, true, ONE_SPLIT>
-                            : gemv_one_kernel<DT, GS, ASYM, KPW, MT, false, ONE_SPLIT>)
-                    : (part ? gemv_one_kernel<DT, GS, ASYM, KPW, MT, true, ONE_PLAIN>
-                            : gemv_one_kernel<DT, GS, ASYM, KPW, MT, false, ONE_PLAIN>);
+    const dim3 grid(plan.tiles, plan.one_splits, moe ? (unsigned)moe->slots : 1u), block(64 * plan.one_waves);
+    auto go = [&](auto mode, const auto& args) {
+      constexpr int MODE = decltype(mode)::value;
+      using Args = std::decay_t<decltype(args)>;
+      auto kern = part ? gemv_one_kernel<DT, GS, ASYM, KPW, MT, true, MODE, Args>
+                       : gemv_one_kernel<DT, GS, ASYM, KPW, MT, false, MODE, Args>;
+      hipLaunchKernelGGL(kern, grid, block, plan.one_lds_bytes, s,
+                         static_cast<const uint16_t*>(a.x), reinterpret_cast<const uint32_t*>(a.wq),
+                         static_cast<const uint16_t*>(a.scales), reinterpret_cast<const uint32_t*>(a.zp), (int)a.N,
+                         (int)a.K, a.sG, (int)a.M, static_cast<const uint16_t*>(a.bias), static_cast<uint16_t*>(a.y),
+                         args);
+    };
     if (moe) {
       if constexpr (MT == 1) {
         om.ids = moe->ids;
@@ -1304,18 +1335,16 @@ static hipError_t launch_one_k(const LinearArgs& a, const GemvPlan& plan, hipStr
         om.w_estride = (size_t)a.N * (size_t)(a.K / 8);
         om.s_estride = (size_t)a.N * (size_t)a.sG;
         om.z_estride = (size_t)(a.N / 8) * (size_t)a.sG;
-        kern = part ? gemv_one_kernel<DT, GS, ASYM, KPW, MT, true, ONE_MOE>
-                    : gemv_one_kernel<DT, GS, ASYM, KPW, MT, false, ONE_MOE>;
+        go(std::integral_constant<int, ONE_MOE>{}, om);
       } else {
         return hipErrorInvalidConfiguration;
       }
+    } else if (lora) {
+      const OneLoraArgs la{om, *lora};
+      plan.one_splits > 1 ? go(std::integral_constant<int, ONE_LORA_SPLIT>{}, la) : go(std::integral_constant<int, ONE_LORA>{}, la);
+    } else {
+      plan.one_splits > 1 ? go(std::integral_constant<int, ONE_SPLIT>{}, om) : go(std::integral_constant<int, ONE_PLAIN>{}, om);
     }
-    const dim3 grid(plan.tiles, plan.one_splits, moe ? (unsigned)moe->slots : 1u), block(64 * plan.one_waves);
-    hipLaunchKernelGGL(kern, grid, block, plan.one_lds_bytes, s,
-                       static_cast<const uint16_t*>(a.x), reinterpret_cast<const uint32_t*>(a.wq),
-                       static_cast<const uint16_t*>(a.scales), reinterpret_cast<const uint32_t*>(a.zp), (int)a.N,
-                       (int)a.K, a.sG, (int)a.M, static_cast<const uint16_t*>(a.bias), static_cast<uint16_t*>(a.y),
-                       om);
     return hipGetLastError();
   }
 }
@@ -1383,7 +1412,6 @@ hipError_t launch_gemv(const LinearArgs& a, const GemvPlan& plan, void* workspac
               moe->slots > kMaxGridZ))
     return hipErrorInvalidConfiguration;
   GemvParams prm;
-  if (lora) prm.lora = *lora;
   prm.yscale = 1.0f;
   prm.moe_ids = nullptr;
   prm.moe_weights = nullptr;
@@ -1443,8 +1471,8 @@ hipError_t launch_gemv(const LinearArgs& a, const GemvPlan& plan, void* workspac
   for (int t0 = 0; t0 < plan.tiles; t0 += chunk) {
     prm.tile_base = t0;
     const int lt = min(chunk, plan.tiles - t0);
-    const hipError_t e = a.dtype == DT_F16 ? launch_g<DT_F16>(prm, a.group, plan, lt, stream)
-                                           : launch_g<DT_BF16>(prm, a.group, plan, lt, stream);
+    const hipError_t e = a.dtype == DT_F16 ? launch_g<DT_F16>(prm, lora, a.group, plan, lt, stream)
+                                           : launch_g<DT_BF16>(prm, lora, a.group, plan, lt, stream);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
