@@ -260,12 +260,8 @@ size_t workspace_for(int64_t M, int64_t N, int64_t K, int32_t group, int32_t dty
 
 bool log_enabled() { return w4a16::tuning().log; }
 
-// the launch of a checked problem (M > 0) on the path p
-w4a16_status linear_run(const DeviceInfo* dev, w4a16_path p, const GroupMap& gm, const void* x, const int32_t* wq,
-                        const void* scales, const int32_t* zp, const void* bias, void* y, int64_t M, int64_t N,
-                        int64_t K, int32_t dtype, void* workspace, size_t workspace_bytes, void* stream,
-                        const w4a16::LoraTerm* lora) {
-  const int32_t group_size = gm.kgroup;  // the kernels' group
+// the sizes that the path p takes
+w4a16_status check_path(w4a16_path p, int64_t M, int64_t N, int64_t K) {
   if (p == W4A16_PATH_GEMV && M > W4A16_GEMV_MAX_M)
     return fail(W4A16_ERR_UNSUPPORTED, "the decode kernel takes M <= %d, got M=%lld",
                 W4A16_GEMV_MAX_M, (long long)M);
@@ -279,6 +275,17 @@ w4a16_status linear_run(const DeviceInfo* dev, w4a16_path p, const GroupMap& gm,
                 "the prefill kernel addresses weights and activations with 32-bit byte "
                 "offsets: N*K/2 and M*K*2 must be below 4 GiB (M=%lld N=%lld K=%lld)",
                 (long long)M, (long long)N, (long long)K);
+  return ok();
+}
+
+// the launch of a checked problem (M > 0) on the path p
+w4a16_status linear_run(const DeviceInfo* dev, w4a16_path p, const GroupMap& gm, const void* x, const int32_t* wq,
+                        const void* scales, const int32_t* zp, const void* bias, void* y, int64_t M, int64_t N,
+                        int64_t K, int32_t dtype, void* workspace, size_t workspace_bytes, void* stream,
+                        const w4a16::LoraTerm* lora) {
+  const int32_t group_size = gm.kgroup;  // the kernels' group
+  const w4a16_status st = check_path(p, M, N, K);
+  if (st != W4A16_OK) return st;
   const size_t need = workspace_for(M, N, K, group_size, dtype, zp != nullptr, p, dev->cu_count);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need))
     return fail(W4A16_ERR_WORKSPACE, "workspace of %zu bytes needed, got %zu%s", need,
@@ -882,10 +889,13 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
              (zp && overlap(u, ubytes, zp, (size_t)(N / 8) * (K / group_size) * 4)) ||
              (bias && overlap(u, ubytes, bias, act_bytes(N))))))
     return fail(W4A16_ERR_INVALID_ARG, "lora_linear: y and u must not overlap any input or each other");
+  const GroupMap gm = group_map(group_size, K);
+  // (before u is formed, so that a refused call has launched nothing)
+  st = check_path(lora_path(M, N, K, gm.kgroup, dtype, zp != nullptr), M, N, K);
+  if (st != W4A16_OK) return st;
   const DeviceInfo* dev = nullptr;
   st = device_info(&dev);
   if (st != W4A16_OK) return st;
-  const GroupMap gm = group_map(group_size, K);
   const LoraPlan plan = plan_lora(M, N, K, gm.kgroup, dtype, zp != nullptr, (int)R, u != nullptr, dev->cu_count);
   if (workspace == nullptr || workspace_bytes < plan.bytes)
     return fail(W4A16_ERR_WORKSPACE, "lora_linear: workspace of %zu bytes needed, got %zu%s", plan.bytes, workspace_bytes,
