@@ -903,7 +903,10 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
   if (!aligned(workspace, 256)) return fail(W4A16_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
   if (overlaps_adapters(workspace, plan.bytes, la, lb, ids, alpha, M, N, K, S, R) ||
       overlap(workspace, plan.bytes, y, ybytes) || overlap(workspace, plan.bytes, u, ubytes) ||
-      overlap(workspace, plan.bytes, x, act_bytes(M * K)) || overlap(workspace, plan.bytes, wq, (size_t)N * (K / 8) * 4))
+      overlap(workspace, plan.bytes, x, act_bytes(M * K)) || overlap(workspace, plan.bytes, wq, (size_t)N * (K / 8) * 4) ||
+      overlap(workspace, plan.bytes, scales, act_bytes(N * (K / group_size))) ||
+      overlap(workspace, plan.bytes, zp, (size_t)(N / 8) * (K / group_size) * 4) ||
+      overlap(workspace, plan.bytes, bias, act_bytes(N)))
     return fail(W4A16_ERR_INVALID_ARG, "lora_linear: the workspace must not overlap an input or an output");
   const w4a16_path p = plan.path;
   const w4a16::ShrinkPlan& sp = plan.shrink;
