@@ -154,8 +154,11 @@ __device__ __forceinline__ uint32_t mix32(uint32_t x) {
 // reciprocal square root, then one Newton step whose residual x - s^2 is exact
 // in one fma.  (Compared with the compiler's correctly rounded one for every
 // fp32 value of the range: equal.  It takes 9 issue slots where that one, for
-// all of fp32, takes 17; with three of those per element the 8-bit step was
-// bound by instructions: 504 us for 143 M elements, 434 us so, 5.3 TB/s.)
+// all of fp32, takes 17, three times an element: 143 M elements with bf16
+// gradients and copies 610 us with that one, 545 us so.  The update's quotient
+// stays a division: m times the hardware's reciprocal takes 520 us there, and
+// nothing less in a step without copies, but p would no longer be the plain
+// sequence's.)
 __device__ __forceinline__ float sqrt_mid(float x) {
   const float r = __builtin_amdgcn_rsqf(x), s = x * r;
   return __builtin_fmaf(__builtin_fmaf(-s, s, x), 0.5f * r, s);
@@ -213,23 +216,18 @@ __device__ __forceinline__ void step_and_store(const AdamwTensor& t, int64_t b, 
     const float v = s.v[e];
     far = max(far, __builtin_bit_cast(uint32_t, v) - __builtin_bit_cast(uint32_t, 0x1p-100f));
   }
-  // 8 bits: the short forms where every v of the wave is in their range (no
-  // zeros, infinities or NaN); the quotient only goes into p, which a last
-  // place of the update does not reach
+  // 8 bits: the short square root where every v of the wave is in its range (no
+  // zeros, infinities or NaN); the bits are the same either way
   constexpr uint32_t span = __builtin_bit_cast(uint32_t, 0x1p100f) - __builtin_bit_cast(uint32_t, 0x1p-100f);
   if (EIGHT && __all(far <= span)) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      r[e] = sqrt_mid(s.v[e]);
-      s.p[e] = s.p[e] * h.decay - (s.m[e] * __builtin_amdgcn_rcpf(r[e] * h.root + h.eps)) * h.rate;
-    }
+    for (int e = 0; e < 4; ++e) r[e] = sqrt_mid(s.v[e]);
   } else {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      r[e] = __builtin_sqrtf(s.v[e]);
-      s.p[e] = s.p[e] * h.decay - (s.m[e] / (r[e] * h.root + h.eps)) * h.rate;
-    }
+    for (int e = 0; e < 4; ++e) r[e] = __builtin_sqrtf(s.v[e]);
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) s.p[e] = s.p[e] * h.decay - (s.m[e] / (r[e] * h.root + h.eps)) * h.rate;
   store4<PD, WHOLE>(t.param, i, n, s.p);
   if (t.copy) {
     if (t.copy_dtype == DT_F16)
