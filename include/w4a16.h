@@ -334,8 +334,9 @@ size_t w4a16_dense_workspace_size(int64_t M, int64_t N, int64_t K, int32_t dtype
  * other arguments, their layout and their alignment as for w4a16_linear; la
  * and lb 16-byte, u 16-byte, ids and alpha 4-byte aligned.  y and u must not
  * overlap any input or each other.  Above the decode threshold alpha * u is
- * carried as two values of the activation dtype, so with fp16 it has to stay
- * below 65504 there.  Infinite or NaN values of an adapter reach its own tokens
+ * carried as two values of the activation dtype: to 16 bits with bf16, with
+ * fp16 (as multiples of a power of two for each token) to 2^-23 of the token's
+ * largest, whatever its size.  Infinite or NaN values of an adapter reach its own tokens
  * only (where tokens of several adapters share a tile, an infinite element of
  * B may reach them as NaN).
  * Workspace: always needed (w4a16_lora_workspace_size), 256-byte aligned,
@@ -365,7 +366,8 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
  * zeros, and tokens without an adapter add to dx only.  u is w4a16_lora_linear's
  * (its rows of tokens without an adapter are not read).  dx may be NULL (not
  * wanted).  The sums over tokens run in a fixed order: equal inputs give equal
- * bits.  With fp16, alpha * u and g have to stay below 65504.
+ * bits.  alpha * u and g are carried as in w4a16_lora_linear (with fp16, in dla
+ * and dlb, to 2^-23 of a rank's largest among 32 tokens).
  * x, wq, la, lb, dy, u, dx, dla, dlb 16-byte aligned, the others as for
  * w4a16_lora_linear; outputs must not overlap any input or each other; S at
  * most 65535, N*K/2 below 4 GiB.

@@ -390,7 +390,7 @@ w4a16_path lora_path(int64_t M, int64_t N, int64_t K, int32_t group, int32_t dty
 struct LoraPlan {
   w4a16_path path;
   w4a16::ShrinkPlan shrink;
-  size_t u_at, op_at, bytes;
+  size_t u_at, op_at, shift_at, bytes;
 };
 LoraPlan plan_lora(int64_t M, int64_t N, int64_t K, int32_t kgroup, int32_t dtype, bool asym, int R, bool save_u, int cus) {
   LoraPlan p;
@@ -399,7 +399,8 @@ LoraPlan plan_lora(int64_t M, int64_t N, int64_t K, int32_t kgroup, int32_t dtyp
   p.u_at = round256(std::max(w4a16::kCounterBytes, workspace_for(M, N, K, kgroup, dtype, asym, p.path, cus)));
   const size_t plane = (size_t)M * (size_t)R * sizeof(float);
   p.op_at = p.u_at + round256(save_u && p.shrink.splits == 1 ? 0 : (size_t)p.shrink.splits * plane);
-  p.bytes = p.op_at + (p.path == W4A16_PATH_GEMV ? 0 : round256(plane));
+  p.shift_at = p.op_at + (p.path == W4A16_PATH_GEMV ? 0 : round256(plane));
+  p.bytes = p.shift_at + (p.path == W4A16_PATH_GEMV || dtype != W4A16_F16 ? 0 : round256((size_t)M * 4));
   return p;
 }
 
@@ -411,7 +412,8 @@ struct BackwardPlan {
   w4a16::OuterPlan outer;
   w4a16::DxPlan dx;
   int64_t places;  // of the tokens' order
-  size_t zeros, order, start, count, la_t, lb_t, dy_pad, part, g, op[2], outer_part, dx_part, tail_w, constants, bytes;
+  size_t zeros, order, start, count, la_t, lb_t, dy_pad, part, g, op[2], g_shift, op_shift[2], outer_part, dx_part, tail_w,
+      constants, bytes;
   size_t zero_bytes;  // the outer products' counters, zero when they start
 };
 BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K, int32_t group_size, int64_t S, int64_t R, int32_t dtype, int cus) {
@@ -438,6 +440,9 @@ BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K, int32_t group_size, 
   p.part = take((size_t)p.shrink.splits * (size_t)M * (size_t)R * 4);
   p.g = take((size_t)M * (size_t)R * 4);
   for (size_t& o : p.op) o = take(act_bytes(2 * R * p.places));
+  const bool shifted = dtype == W4A16_F16;
+  p.g_shift = take(shifted ? (size_t)M * 4 : 0);
+  for (size_t& o : p.op_shift) o = take(shifted ? (size_t)w4a16::shift_row(R) * (size_t)(p.places / 32) : 0);
   // the two are not in use at the same time, but both stay clear of the rest
   p.outer_part = take(w4a16::outer_partial_bytes(p.outer, p.places));
   p.dx_part = take(w4a16::dx_partial_bytes(p.dx, M, K));
@@ -915,7 +920,8 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
   // its tokens' alpha * u as operands, made once, before it.
   float* const part = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.u_at);
   uint16_t* const op = p == W4A16_PATH_GEMV ? nullptr : reinterpret_cast<uint16_t*>(static_cast<char*>(workspace) + plan.op_at);
-  const w4a16::ShrinkArgs sa{x, la, ids, part, u, op, alpha, M, K, (int)S, (int)R, dtype};
+  int32_t* const shift = op && dtype == W4A16_F16 ? reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + plan.shift_at) : nullptr;
+  const w4a16::ShrinkArgs sa{x, la, ids, part, u, op, shift, alpha, M, K, (int)S, (int)R, dtype};
   const hipError_t e = w4a16::launch_shrink(sa, sp, static_cast<hipStream_t>(stream));
   if (e != hipSuccess) return fail(W4A16_ERR_LAUNCH, "kernel launch failed: %s", hipGetErrorString(e));
   w4a16::LoraTerm t;
@@ -924,6 +930,7 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
   t.u = u ? u : part;
   t.alpha = alpha;
   t.op = op;
+  t.shift = shift;
   t.S = (int)S;
   t.R = (int)R;
   t.usplits = u ? 1 : sp.splits;
@@ -1024,13 +1031,15 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
   e = w4a16::launch_prep(prep, s);
   if (e == hipSuccess) {
     // g / alpha = dy . B: the transposed lb in the first factor's place
-    const w4a16::ShrinkArgs sa{dyr, prep.lb_t, ids, static_cast<float*>(at(p.part)), nullptr, nullptr, nullptr, M, p.np, (int)S, (int)R, dtype};
+    const w4a16::ShrinkArgs sa{dyr, prep.lb_t, ids, static_cast<float*>(at(p.part)), nullptr, nullptr, nullptr, nullptr, M, p.np, (int)S, (int)R, dtype};
     e = w4a16::launch_shrink(sa, p.shrink, s);
   }
   uint16_t* const op[2] = {static_cast<uint16_t*>(at(p.op[0])), static_cast<uint16_t*>(at(p.op[1]))};
+  int32_t* const g_shift = static_cast<int32_t*>(at(p.g_shift));
+  int8_t* const op_shift[2] = {static_cast<int8_t*>(at(p.op_shift[0])), static_cast<int8_t*>(at(p.op_shift[1]))};
   if (e == hipSuccess) {
-    const w4a16::OperandArgs pa{static_cast<const float*>(at(p.part)), u, ids, prep.order, alpha, g, {op[0], op[1]},
-                                (int)M, (int)S, (int)R, p.shrink.splits, (int)p.places, dtype};
+    const w4a16::OperandArgs pa{static_cast<const float*>(at(p.part)), u, ids, prep.order, alpha, g, {op[0], op[1]}, g_shift,
+                                {op_shift[0], op_shift[1]}, (int)M, (int)S, (int)R, p.shrink.splits, (int)p.places, dtype};
     e = w4a16::launch_operands(pa, s);
   }
   if (e == hipSuccess && dx) {
@@ -1040,14 +1049,15 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
     t.ids = ids;
     t.up = prep.la_t;
     t.op = g;
+    t.shift = g_shift;
     t.S = (int)S;
     t.R = (int)R;
     e = w4a16::launch_dx(da, p.dx, t, s);
   }
   if (e == hipSuccess) {
     w4a16::OuterArgs oa;
-    oa.p[0] = {static_cast<const uint16_t*>(x), op[0], static_cast<uint16_t*>(dla), (int)K, (int)K, 1};
-    oa.p[1] = {dyr, op[1], static_cast<uint16_t*>(dlb), (int)p.np, (int)N, 0};
+    oa.p[0] = {static_cast<const uint16_t*>(x), op[0], op_shift[0], static_cast<uint16_t*>(dla), (int)K, (int)K, 1};
+    oa.p[1] = {dyr, op[1], op_shift[1], static_cast<uint16_t*>(dlb), (int)p.np, (int)N, 0};
     oa.order = prep.order;
     oa.start = prep.start;
     oa.count = prep.count;

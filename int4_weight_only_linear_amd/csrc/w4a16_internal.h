@@ -30,13 +30,15 @@ struct LinearArgs {
 // w4a16_lora.hpp): token m's adapter ids[m] (outside [0, S): none), the stack
 // up[S][N][R], and for the decode kernels u[usplits][M][R] in fp32 and alpha[S]
 // (NULL: 1), for the matrix tiles op [M][2][R], alpha * u as two values of the
-// activation dtype (split_hi_lo), all from shrink_kernel.
+// activation dtype (split_hi_lo), with fp16 times 2^shift[m] (op_shift), all
+// from shrink_kernel.
 struct LoraTerm {
   const int32_t* ids = nullptr;  // NULL: no adapters
   const void* up = nullptr;
   const float* u = nullptr;
   const float* alpha = nullptr;
   const uint16_t* op = nullptr;
+  const int32_t* shift = nullptr;  // fp16 only
   int S = 0, R = 0, usplits = 1;
 };
 // u[m][r] = sum over k of x[m, k] * down[ids[m]][r, k]
@@ -47,6 +49,7 @@ struct ShrinkArgs {
   float* part;         // [splits][M][R]: the K ranges' sums
   float* u;            // [M][R], or NULL: not wanted
   uint16_t* op;        // [M][2][R]: alpha * u as operands, or NULL: not wanted
+  int32_t* shift;      // [M]: their shifts (fp16, with op)
   const float* alpha;  // [S] or NULL
   int64_t M, K;
   int S, R, dtype;

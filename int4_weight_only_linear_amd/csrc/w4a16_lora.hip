@@ -127,9 +127,11 @@ __global__ __launch_bounds__(64 * shrink_waves(TT, RC)) void shrink_kernel(
 #pragma unroll
           for (int w = 0; w < WAVES; ++w) v += red[w * (16 * BR) + i];
           out[(size_t)(m0 + m) * R + r] = v;
-          if (op) {  // (one K range)
-            uint16_t* const d = op + (size_t)(m0 + m) * 2 * R + r;
-            split_hi_lo<DT>(alpha ? v * alpha[a] : v, d[0], d[R]);
+          if constexpr (DT == DT_BF16) {
+            if (op) {  // (one K range)
+              uint16_t* const d = op + (size_t)(m0 + m) * 2 * R + r;
+              split_hi_lo<DT>(alpha ? v * alpha[a] : v, d[0], d[R]);
+            }
           }
         }
       }
@@ -138,15 +140,21 @@ __global__ __launch_bounds__(64 * shrink_waves(TT, RC)) void shrink_kernel(
 }
 
 // u = the K ranges' sums in range order, and alpha * u as operands (each where
-// wanted); n = M R.  (A launch of its own: 2.3 us for 67 tokens of 32 ranks,
-// 5.2 for 1920 of 64.)
+// wanted); n = M R.  Four ranks a lane, a token 2^lanes_log2 lanes, which find
+// its largest value together.  (A launch of its own: 2.3 us for 67 tokens of 32
+// ranks, 5.2 for 1920 of 64.)
 template <int DT>
 __global__ __launch_bounds__(256) void shrink_reduce_kernel(const float* __restrict__ part, const int32_t* __restrict__ ids,
-                                                            const float* __restrict__ alpha, float* __restrict__ u,
-                                                            uint16_t* __restrict__ op, int64_t n, int splits, int S, int R) {
-  const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 4;
-  if (i >= n) return;
+                                                            const float* __restrict__ alpha, float* u, uint16_t* __restrict__ op,
+                                                            int32_t* __restrict__ shift, int64_t n, int lanes_log2, int splits,
+                                                            int S, int R) {
+  const int64_t lane = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, m = lane >> lanes_log2;
+  const int r = 4 * (int)(lane & ((1 << lanes_log2) - 1));
+  const int64_t i = m * R + r;
+  if (m * R >= n) return;  // (a token's lanes together)
+  const bool in = r < R;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  if (in)
   for (int s0 = 0; s0 < splits; s0 += 4) {  // four at a time, so that their loads overlap
     f32x4 p[4];
 #pragma unroll
@@ -155,16 +163,27 @@ __global__ __launch_bounds__(256) void shrink_reduce_kernel(const float* __restr
     for (int k = 0; k < 4; ++k)
       if (s0 + k < splits) v += p[k];
   }
-  if (u) *reinterpret_cast<f32x4*>(u + i) = v;
+  if (u && in) *reinterpret_cast<f32x4*>(u + i) = v;
   if (!op) return;
-  const int64_t m = i / R;
-  const int r = (int)(i - m * R), a = ids[m];
+  const int a = ids[m];
   const float k = alpha && a >= 0 && a < S ? alpha[a] : 1.f;
+  v *= k;
+  if constexpr (DT == DT_F16) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = max(top, magnitude_bits(v[e]));
+    for (int b = 0; b < lanes_log2; ++b) top = max(top, (uint32_t)__shfl_xor((int)top, 1 << b));
+    const int sh = op_shift(top);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(v[e], sh);
+    if (r == 0) shift[m] = sh;
+  }
+  if (!in) return;
   u16x4 h, l;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     uint16_t hi, lo;
-    split_hi_lo<DT>(k * v[e], hi, lo);
+    split_hi_lo<DT>(v[e], hi, lo);
     h[e] = hi, l[e] = lo;
   }
   uint16_t* const d = op + (size_t)m * 2 * R + r;
@@ -181,7 +200,7 @@ hipError_t launch_t(const ShrinkArgs& a, const ShrinkPlan& p, float* out, hipStr
   const dim3 grid((unsigned)units);
   hipLaunchKernelGGL((shrink_kernel<DT, TT, RC>), grid, dim3(64 * shrink_waves(TT, RC)), 0, s,
                      static_cast<const uint16_t*>(a.x), static_cast<const uint16_t*>(a.down), a.ids, out,
-                     p.splits == 1 ? a.op : nullptr, a.alpha, (int)a.M, (int)a.K, a.S, a.R, p.chunks_per_split, turns);
+                     p.splits == 1 && DT == DT_BF16 ? a.op : nullptr, a.alpha, (int)a.M, (int)a.K, a.S, a.R, p.chunks_per_split, turns);
   return hipGetLastError();
 }
 
@@ -219,11 +238,16 @@ ShrinkPlan plan_shrink(int64_t M, int64_t K, int R, int cu_count, bool few) {
 hipError_t launch_shrink(const ShrinkArgs& a, const ShrinkPlan& p, hipStream_t s) {
   float* const out = p.splits > 1 && a.u ? a.part : (a.u ? a.u : a.part);
   const hipError_t e = a.dtype == DT_F16 ? launch_dt<DT_F16>(a, p, out, s) : launch_dt<DT_BF16>(a, p, out, s);
-  if (e != hipSuccess || p.splits == 1 || !(a.u || a.op)) return e;
+  // one K range: u is there, and bf16's operands; fp16's need a token's largest
+  // value, which several workgroups hold (1920 tokens, 1024 x 4096: 34 -> 37 us)
+  const bool u_done = p.splits == 1, op_done = u_done && a.dtype == DT_BF16;
+  if (e != hipSuccess || !((a.u && !u_done) || (a.op && !op_done))) return e;
   const int64_t n = a.M * a.R;
+  int lanes_log2 = 1;
+  while ((4 << lanes_log2) < a.R) ++lanes_log2;
   auto kern = a.dtype == DT_F16 ? shrink_reduce_kernel<DT_F16> : shrink_reduce_kernel<DT_BF16>;
-  hipLaunchKernelGGL(kern, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, s, a.part, a.ids, a.alpha, a.u, a.op, n,
-                     p.splits, a.S, a.R);
+  hipLaunchKernelGGL(kern, dim3((unsigned)(((a.M << lanes_log2) + 255) / 256)), dim3(256), 0, s, out, a.ids, a.alpha,
+                     u_done ? nullptr : a.u, a.op, a.shift, n, lanes_log2, p.splits, a.S, a.R);
   return hipGetLastError();
 }
 

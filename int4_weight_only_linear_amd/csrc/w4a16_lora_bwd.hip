@@ -194,8 +194,10 @@ __global__ __launch_bounds__(256) void prep_kernel(const PrepArgs a, int tiles_n
   for (int i = tid; i < a.zero_words; i += 256) a.zero[i] = 0u;
 }
 
-// Workgroups below row_blocks sum g's K ranges token by token; the others take 64
-// places of one problem each and transpose its rows through LDS into operands.
+// Workgroups below row_blocks sum g's K ranges token by token (eight ranks a
+// lane, a token 2^lanes_log2 lanes, which find its largest value together); the
+// others take 64 places of one problem each and transpose its rows through LDS
+// into operands.
 // Bound by the sum over g's K ranges, read twice: 3.1 us for 128 tokens of 16
 // ranks, 12 us for 1920 of 64 (16 ranges).
 // (the sum over K ranges, four at a time so that their loads overlap)
@@ -213,25 +215,39 @@ __device__ __forceinline__ f32x4 sum_ranges(const float* src, int64_t plane, int
 }
 
 template <int DT>
-__global__ __launch_bounds__(256) void operand_kernel(const OperandArgs a, int row_blocks, int place_blocks) {
+__global__ __launch_bounds__(256) void operand_kernel(const OperandArgs a, int row_blocks, int place_blocks, int lanes_log2) {
   __shared__ float lds[kMaxRank * (kTile + 1)];
   const int tid = threadIdx.x;
   const int64_t n = (int64_t)a.M * a.R;
   if ((int)blockIdx.x < row_blocks) {
     // eight ranks of a token (none is read of a token without an adapter)
-    const int64_t i = ((int64_t)blockIdx.x * 256 + tid) * 8;
-    if (i >= n) return;
-    const int64_t m = i / a.R;
+    const int64_t at = (int64_t)blockIdx.x * 256 + tid, m = at >> lanes_log2;
+    const int r = 8 * (int)(at & ((1 << lanes_log2) - 1));
+    if (m >= a.M) return;  // (a token's lanes together)
     const int s = a.ids[m];
     if (s < 0 || s >= a.S) return;
     const float alpha = a.alpha ? a.alpha[s] : 1.f;
-    const f32x4 g[2] = {sum_ranges(a.part + i, n, a.splits), sum_ranges(a.part + i + 4, n, a.splits)};
-    float v[8];
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (r < a.R) {
+      const float* src = a.part + m * a.R + r;
+      const f32x4 g[2] = {sum_ranges(src, n, a.splits), sum_ranges(src + 4, n, a.splits)};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = g[e >> 2][e & 3] * alpha;
+      for (int e = 0; e < 8; ++e) v[e] = g[e >> 2][e & 3] * alpha;
+    }
+    if constexpr (DT == DT_F16) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, magnitude_bits(v[e]));
+      for (int b = 0; b < lanes_log2; ++b) top = max(top, (uint32_t)__shfl_xor((int)top, 1 << b));
+      const int sh = op_shift(top);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __builtin_ldexpf(v[e], sh);
+      if (r == 0) a.g_shift[m] = sh;
+    }
+    if (r >= a.R) return;
     u32x4 hi, lo;
     split_hi_lo<DT>(v, hi, lo);
-    uint16_t* const d = a.g + 2 * m * a.R + (i - m * a.R);
+    uint16_t* const d = a.g + 2 * m * a.R + r;
     *reinterpret_cast<u32x4*>(d) = hi;
     *reinterpret_cast<u32x4*>(d + a.R) = lo;
     return;
@@ -255,12 +271,30 @@ __global__ __launch_bounds__(256) void operand_kernel(const OperandArgs a, int r
   }
   __syncthreads();
   uint16_t* const out = second ? a.op[1] : a.op[0];
-  for (int i = tid; i < a.R * (kTile / 8); i += 256) {
+  const int ranks = DT == DT_F16 ? (a.R + 63) / 64 * 64 : a.R;  // (shifts of ranks past R: zero)
+  for (int i = tid; i < ranks * (kTile / 8); i += 256) {
     const int r = i / (kTile / 8), pl = 8 * (i - r * (kTile / 8));
     if (p0 + pl >= a.places) continue;  // places is a multiple of 32
+    int8_t* const shift = (second ? a.op_shift[1] : a.op_shift[0]) + (size_t)((p0 + pl) / 32) * ((a.R + 63) / 64 * 64) + shift_at(r);
+    if (DT == DT_F16 && r >= a.R) {
+      *shift = 0;
+      continue;
+    }
     float v[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = lds[r * (kTile + 1) + pl + e];
+    if constexpr (DT == DT_F16) {
+      // 32 places are four lanes, which take this turn together
+      uint32_t top = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = max(top, magnitude_bits(v[e]));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+      top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+      const int sh = op_shift(top);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = __builtin_ldexpf(v[e], sh);
+      if ((i & 3) == 0) *shift = (int8_t)(sh / 16);
+    }
     u32x4 hi, lo;
     split_hi_lo<DT>(v, hi, lo);
     uint16_t* const d = out + (size_t)r * a.places + p0 + pl;
@@ -288,7 +322,7 @@ constexpr int outer_cols(int rc) { return 16 * outer_cpl(rc) * outer_cw(rc); }
 // adds them in range order.
 //
 // Bound by the rows of x and dy, and by the operands that every 128 columns
-// read again: 1920 tokens of one adapter, 64 ranks, 4096 and 28672 columns: 50 us
+// read again: 1920 tokens of one adapter, 64 ranks, 4096 and 28672 columns: 44 us
 // for 126 MB (66 with one wave for 64 columns and tokens read one step ahead);
 // 1921 tokens of three, 16 ranks, 4096 and 6144 columns: 10.9 us; 128 tokens 4.9.
 template <int DT, int RC>
@@ -319,16 +353,35 @@ __global__ __launch_bounds__(512) void outer_kernel(const OuterArgs a, const Out
 #pragma unroll
     for (int rc = 0; rc < RC; ++rc) acc[t][rc] = f32x4{0.f, 0.f, 0.f, 0.f};
   const uint16_t* vcol = p.v + min(c0 + 16 * CPL * cw + CPL * col, p.ld - CPL);
-  const uint16_t* wrow[RC];
-#pragma unroll
-  for (int rc = 0; rc < RC; ++rc) wrow[rc] = p.op + (size_t)min(r0 + 16 * rc + col, a.R - 1) * a.places;
   const size_t lo_at = (size_t)a.R * a.places;
+  // fp16: the sums of a lane's ranks (a byte each) at the shifts of the last
+  // step's operands
+  constexpr bool SHIFTED = DT == DT_F16;
+  const int8_t* const shifts = p.shift + r0 / 64 * 64;
+  const uint32_t shift_step = (uint32_t)((a.R + 63) / 64 * 64);  // bytes of 32 places (all of them below 4 GiB)
+  uint32_t shift = 0;
+  auto rescale = [&](uint32_t to) {
+    if (__builtin_expect(__ballot(to != shift) == 0, 1)) return;
+#pragma unroll
+    for (int rc = 0; rc < RC; ++rc) {
+      // (r0 is a multiple of 16 RC, so a group of ranks lies inside 64)
+      const int by = 16 * ((int8_t)(to >> (8 * rc)) - (int8_t)(shift >> (8 * rc)));
+#pragma unroll
+      for (int t = 0; t < CPL; ++t) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[t][rc][e] = __builtin_ldexpf(acc[t][rc][e], by);
+        __builtin_amdgcn_sched_barrier(0);  // (few registers beside the accumulators)
+      }
+    }
+    shift = to;
+  };
 
   // The tokens of a step's places are read two steps ahead and its rows one:
   // the rows' addresses never wait.  (Places past the tokens hold -1.)
   struct Step {
     cols_t v[8];
     u32x4 hi[RC], lo[RC];
+    uint32_t shift;
   };
   const int t_last = start + (count + 31) / 32 * 32 - 32;  // the adapter's last step
   auto load_tokens = [&](int t0, int (&m)[8]) {
@@ -340,11 +393,16 @@ __global__ __launch_bounds__(512) void outer_kernel(const OuterArgs a, const Out
     const int at = min(t0, t_last) + 8 * q;
 #pragma unroll
     for (int e = 0; e < 8; ++e) st.v[e] = *reinterpret_cast<const cols_t*>(vcol + (size_t)max(m[e], 0) * p.ld);
+    int c = col;
+    asm("" : "+v"(c));  // the ranks' rows are formed here (kept over the loop they would spill)
 #pragma unroll
     for (int rc = 0; rc < RC; ++rc) {
-      st.hi[rc] = *reinterpret_cast<const u32x4*>(wrow[rc] + at);
-      st.lo[rc] = *reinterpret_cast<const u32x4*>(wrow[rc] + lo_at + at);
+      const uint16_t* row = p.op + (size_t)min(r0 + 16 * rc + c, a.R - 1) * a.places + at;
+      st.hi[rc] = *reinterpret_cast<const u32x4*>(row);
+      st.lo[rc] = *reinterpret_cast<const u32x4*>(row + lo_at);
     }
+    if constexpr (SHIFTED)
+      st.shift = *reinterpret_cast<const uint32_t*>(shifts + ((uint32_t)(min(t0, t_last) / 32) * shift_step + 4u * (uint32_t)col));
   };
   auto multiply = [&](Step& st, int t0) {
     if (t0 + 32 > t_end) {  // wave-uniform: only an adapter's last step holds empty places
@@ -352,6 +410,7 @@ __global__ __launch_bounds__(512) void outer_kernel(const OuterArgs a, const Out
       for (int e = 0; e < 8; ++e)
         if (t0 + 8 * q + e >= t_end) st.v[e] = cols_t{};
     }
+    if constexpr (SHIFTED) rescale(st.shift);
 #pragma unroll
     for (int t = 0; t < CPL; ++t) {
       const uint32_t sel = (t & 1) ? 0x07060302u : 0x05040100u;
@@ -386,6 +445,7 @@ __global__ __launch_bounds__(512) void outer_kernel(const OuterArgs a, const Out
       if (t0 >= t_end) break;
     }
   }
+  if constexpr (SHIFTED) rescale(0u);
   // acc[t][rc][e]: column CPL (4 q + e) + t, rank 16 rc + col
   auto put = [&](bool add) {
     float* const buf = sum + (wave % BUFS) * (BR * LD) + 16 * CPL * cw;
@@ -471,9 +531,11 @@ hipError_t launch_prep(const PrepArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_operands(const OperandArgs& a, hipStream_t s) {
-  const int row_blocks = (int)(((int64_t)a.M * a.R / 8 + 255) / 256), place_blocks = (a.places + kTile - 1) / kTile;
+  int lanes_log2 = 0;
+  while ((8 << lanes_log2) < a.R) ++lanes_log2;
+  const int row_blocks = (int)((((int64_t)a.M << lanes_log2) + 255) / 256), place_blocks = (a.places + kTile - 1) / kTile;
   auto kern = a.dtype == DT_F16 ? operand_kernel<DT_F16> : operand_kernel<DT_BF16>;
-  hipLaunchKernelGGL(kern, dim3(row_blocks + 2 * place_blocks), dim3(256), 0, s, a, row_blocks, place_blocks);
+  hipLaunchKernelGGL(kern, dim3(row_blocks + 2 * place_blocks), dim3(256), 0, s, a, row_blocks, place_blocks, lanes_log2);
   return hipGetLastError();
 }
 

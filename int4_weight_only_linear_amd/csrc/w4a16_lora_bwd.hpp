@@ -43,9 +43,14 @@ struct PrepArgs {
 };
 hipError_t launch_prep(const PrepArgs& a, hipStream_t s);
 
+// where rank r's shift stands among those of 32 places
+__host__ __device__ inline int shift_at(int r) { return r / 64 * 64 + r % 16 * 4 + r % 64 / 16; }
+inline int64_t shift_row(int64_t R) { return (R + 63) / 64 * 64; }
+
 // alpha * g (the sum of its K ranges) and alpha * u as MFMA operands, value and
 // remainder in the activation dtype (split_hi_lo): both by rank and place, and
-// alpha * g by token
+// alpha * g by token.  With fp16 times a power of two (op_shift): of a token in
+// g, of a rank over 32 places (one adapter's, and a step of outer_kernel) in op.
 struct OperandArgs {
   const float* part;    // [splits][M][R]
   const float* u;       // [M][R]
@@ -54,6 +59,8 @@ struct OperandArgs {
   const float* alpha;   // [S] or NULL
   uint16_t* g;          // [M][2][R]
   uint16_t* op[2];      // of g and of u: [2][R][places]
+  int32_t* g_shift;     // [M], fp16 only
+  int8_t* op_shift[2];  // [places / 32][R to 64]: shifts / 16, four ranks 16 apart together (shift_at); fp16 only
   int M, S, R, splits, places, dtype;
 };
 hipError_t launch_operands(const OperandArgs& a, hipStream_t s);
@@ -62,6 +69,7 @@ hipError_t launch_operands(const OperandArgs& a, hipStream_t s);
 struct OuterProblem {
   const uint16_t* v;   // [M][ld]
   const uint16_t* op;  // [2][R][places]
+  const int8_t* shift; // OperandArgs' op_shift
   uint16_t* out;       // [S][R][C] (by_rank) or [S][C][R]
   int ld, C, by_rank;
 };
