@@ -638,7 +638,8 @@ def w4a16_adamw_plan(params, grads, exp_avgs, exp_avg_sqs, *, m_scales=None, v_s
     exp_avgs / exp_avg_sqs are float32 (moments in 32 bits), or int8 / uint8 with
     m_scales / v_scales float32 [ceil(n / 256)] (moments in 8 bits; zeros to begin
     with).  copies: float16 or bfloat16 copies of the parameters, written by every
-    step.  The plan keeps the tensors; they must stay where they are."""
+    step (None for a parameter that has none).  The plan keeps the tensors; they
+    must stay where they are."""
     torch = _torch()
     params, grads, ms, vs = list(params), list(grads), list(exp_avgs), list(exp_avg_sqs)
     count = len(params)
@@ -654,11 +655,12 @@ def w4a16_adamw_plan(params, grads, exp_avgs, exp_avg_sqs, *, m_scales=None, v_s
         if len(got) != count:
             raise ValueError(f"{len(got)} {name} for {count} params")
     device = params[0].device
+    copy_type = next((c.dtype for c in cps if c is not None), None)  # any of them may be None
     want_m, want_v = (torch.int8, torch.uint8) if eight else (torch.float32, torch.float32)
     rows = (AdamwTensor * count)()
     for i, (p, g, m, v, a, b, c) in enumerate(zip(params, grads, ms, vs, msc, vsc, cps)):
         n = p.numel()
-        if p.dtype != params[0].dtype or g.dtype != grads[0].dtype or (c is not None and c.dtype != cps[0].dtype):
+        if p.dtype != params[0].dtype or g.dtype != grads[0].dtype or (c is not None and c.dtype != copy_type):
             raise TypeError(f"tensor {i}: all tensors of a plan share their types")
         if m.dtype != want_m or v.dtype != want_v:
             raise TypeError(f"tensor {i}: moments must be {want_m} and {want_v}, got {m.dtype} and {v.dtype}")
@@ -671,7 +673,7 @@ def w4a16_adamw_plan(params, grads, exp_avgs, exp_avg_sqs, *, m_scales=None, v_s
                         (c, "copy")):
             _require_device(t, f"tensor {i}: {name}", device)
         rows[i] = AdamwTensor(p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), _ptr(a), _ptr(b), _ptr(c), n)
-    copy_dtype = W4A16_BF16 if copies is None else _act_code(cps[0])
+    copy_dtype = W4A16_BF16 if copy_type is None else _act_code(next(c for c in cps if c is not None))
     size = int(lib.w4a16_adamw_table_size(rows, count))
     host = np.zeros((size + 7) // 8, dtype=np.int64)
     info = AdamwPlanInfo()
