@@ -293,7 +293,9 @@ def _raw_stream(device) -> int:
 
 
 # workspace sizes by (entry point, device, sizes): the plan behind one is the
-# same for every call of these sizes until the tuning variables are read again
+# same for every call of these sizes until the tuning variables are read again.
+# A serving process meets many token counts: started afresh at this many.
+_SIZES_MAX = 4096
 _sizes: dict = {}
 
 
@@ -304,6 +306,8 @@ def _size_of(device, fn, *args) -> int:
         torch = _torch()
         with torch.cuda.device(device):
             n = int(fn(*args))
+        if len(_sizes) >= _SIZES_MAX:
+            _sizes.clear()
         _sizes[key] = n
     return n
 
