@@ -370,7 +370,7 @@ w4a16_status w4a16_lora_linear(const void* x, const int32_t* wq, const void* sca
  * and dlb, to 2^-23 of a rank's largest among 32 tokens).
  * x, wq, la, lb, dy, u, dx, dla, dlb 16-byte aligned, the others as for
  * w4a16_lora_linear; outputs must not overlap any input or each other; S at
- * most 65535, N*K/2 below 4 GiB.
+ * most 65535, N*K/2 below 4 GiB, N at most 2^23 - 64.
  * Workspace: w4a16_lora_backward_workspace_size bytes, always needed, under
  * the rules above.  It holds the transposed factors (S*R*(K+N) values), the
  * scales and zero points in the kernel's order and the partial sums. */

@@ -960,6 +960,9 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
   if (S > 65535) return fail(W4A16_ERR_UNSUPPORTED, "lora_backward: at most 65535 adapters, got %lld", (long long)S);
   if ((uint64_t)N * (uint64_t)K / 2 > 0xFFFFFFFFull)
     return fail(W4A16_ERR_UNSUPPORTED, "lora_backward: N*K/2 must be below 4 GiB (N=%lld K=%lld)", (long long)N, (long long)K);
+  // a tile's 256 rows of dy (of N rounded up to 64) lie below 4 GiB
+  if (N > (1 << 23) - 64)
+    return fail(W4A16_ERR_UNSUPPORTED, "lora_backward: N above %d is not supported, got %lld", (1 << 23) - 64, (long long)N);
   if (M > 0 && !u) return fail(W4A16_ERR_INVALID_ARG, "lora_backward: u must not be NULL");
   if (!dla || !dlb) return fail(W4A16_ERR_INVALID_ARG, "lora_backward: dla and dlb must not be NULL");
   if ((dy && !aligned(dy, 16)) || (u && !aligned(u, 16)) || (dx && !aligned(dx, 16)) || !aligned(dla, 16) || !aligned(dlb, 16))
