@@ -997,6 +997,12 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
   for (const auto& o : out) inside |= overlap(workspace, p.bytes, o.p, o.n);
   for (const auto& i : in) inside |= overlap(workspace, p.bytes, i.p, i.n);
   if (inside) return fail(W4A16_ERR_INVALID_ARG, "lora_backward: the workspace must not overlap an input or an output");
+  if (log_enabled())
+    std::fprintf(stderr,
+                 "[w4a16] lora_backward M=%lld N=%lld K=%lld g=%d %s %s S=%lld R=%lld dx bm=%d splits=%d sums tokens=%d splits=%d\n",
+                 (long long)M, (long long)N, (long long)K, group_size, dtype == W4A16_F16 ? "f16" : "bf16",
+                 zp ? "asym" : "sym", (long long)S, (long long)R, dx ? 64 * p.dx.mw : 0, dx ? p.dx.splits : 0,
+                 p.outer.tokens, p.outer.splits);
   char* const ws = static_cast<char*>(workspace);
   auto at = [&](size_t o) { return static_cast<void*>(ws + o); };
   const bool pad = p.np != N;
