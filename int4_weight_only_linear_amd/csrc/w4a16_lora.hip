@@ -153,20 +153,22 @@ __global__ __launch_bounds__(256) void shrink_reduce_kernel(const float* __restr
   const int64_t i = m * R + r;
   if (m * R >= n) return;  // (a token's lanes together)
   const bool in = r < R;
+  // (alpha's two loads on their way beside the sums')
+  const int a = op ? ids[m] : -1;
+  const float k = alpha && a >= 0 && a < S ? alpha[a] : 1.f;
+  const float* const src = part + (in ? i : m * R);
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  if (in)
   for (int s0 = 0; s0 < splits; s0 += 4) {  // four at a time, so that their loads overlap
     f32x4 p[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) p[k] = *reinterpret_cast<const f32x4*>(part + min(s0 + k, splits - 1) * n + i);
+    for (int k = 0; k < 4; ++k) p[k] = *reinterpret_cast<const f32x4*>(src + min(s0 + k, splits - 1) * n);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (s0 + k < splits) v += p[k];
   }
   if (u && in) *reinterpret_cast<f32x4*>(u + i) = v;
   if (!op) return;
-  const int a = ids[m];
-  const float k = alpha && a >= 0 && a < S ? alpha[a] : 1.f;
+  if (!in) v = f32x4{0.f, 0.f, 0.f, 0.f};
   v *= k;
   if constexpr (DT == DT_F16) {
     uint32_t top = 0;
