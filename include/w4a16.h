@@ -343,6 +343,7 @@ size_t w4a16_dense_workspace_size(int64_t M, int64_t N, int64_t K, int32_t dtype
  * under w4a16_linear's rules: zero-filled before its first use, then
  * reusable by calls of any entry point on the same stream; it must not overlap
  * an input or an output.
+ * A refused call has launched nothing.
  * Errors: those of w4a16_linear; W4A16_ERR_INVALID_ARG for S < 1 or a rank
  * that is no positive multiple of 8, W4A16_ERR_UNSUPPORTED for one above 128. */
 size_t w4a16_lora_workspace_size(int64_t M, int64_t N, int64_t K, int32_t group_size, int32_t dtype,
@@ -401,14 +402,20 @@ w4a16_status w4a16_lora_backward(const void* dy, const void* x, const float* u, 
  * (floor of the exact code plus a dither in [0, 1)); the dither is a hash of
  * seed and of the element's place (block number in the table * 256 + place in
  * the block, modulo 2^32), so a step is a function of its arguments.  Give
- * every step another seed.  All-zero moments are all-zero codes and scales.  A
+ * every step another seed.  The mean of a code is exact, the mean of a v it
+ * stands for, its fourth power, is not: with beta2 = 0.999 and gradients of
+ * constant size the v of an element whose sqrt(v) is a tenth of its block's
+ * largest comes out 2 % high, a hundredth 7 %, a thousandth 25 %, 0.0003 of it
+ * 50 % (its updates are 1, 3, 11 and 18 % smaller).  All-zero moments are all-zero codes and scales.  A
  * gradient that is not finite makes its element, and in 8 bits the moments of
  * its block, NaN or infinite: check gradients before the step.
  *
  * w4a16_adamw_table (host) checks the tensors and lays out the table that the
  * steps read, w4a16_adamw_table_size bytes in host memory; the caller copies
  * it to device memory (8-byte aligned) and keeps it, and the tensors where
- * they are, for as long as it calls w4a16_adamw_step.  All tensors of a table
+ * they are, for as long as it calls w4a16_adamw_step: a step reads the gradients
+ * at the addresses that the table was made with, so keep them in place (set them
+ * to zero, not free) or lay the table out again.  All tensors of a table
  * share their types (param, grad: W4A16_F16, W4A16_BF16 or W4A16_F32; copy:
  * W4A16_F16 or W4A16_BF16).  n may be 0.  Pointers are aligned to their
  * elements; four-element alignment of all of a tensor's pointers is faster.
@@ -438,7 +445,8 @@ w4a16_status w4a16_adamw_table(const w4a16_adamw_tensor* tensors, int64_t count,
                                size_t table_bytes, w4a16_adamw_plan* plan);
 
 /* The step (device): asynchronous on `stream`; the numbers are taken when it
- * is called.  Needs betas in [0, 1), eps >= 0, step >= 1 and the rest finite. */
+ * is called, so a captured graph repeats its step, rates and seed at every
+ * replay: leave steps out of graphs that are replayed for several steps.  Needs betas in [0, 1), eps >= 0, step >= 1 and the rest finite. */
 w4a16_status w4a16_adamw_step(const void* table, const w4a16_adamw_plan* plan, double lr, double beta1, double beta2,
                               double eps, double weight_decay, int64_t step, double grad_scale, uint32_t seed,
                               void* stream);

@@ -547,7 +547,8 @@ def w4a16_lora_linear(x, wq, scales, la, lb, ids, zp=None, bias=None, alpha=None
     """y = x . dequant(wq, scales, zp)^T (+ bias) + alpha_a * (x . A_a^T) . B_a^T with token
     m's adapter a = ids[m] out of the stacks la [S, R, K] and lb [S, N, R] (an id outside
     [0, S): no adapter).  With save_u returns (y, u), u = x . A_a^T in float32 [M, R] for
-    w4a16_lora_backward."""
+    w4a16_lora_backward.  Not recorded by autograd: y requires no gradient, whatever la, lb
+    and x do; a training step calls w4a16_lora_backward itself."""
     torch = _torch()
     dt, M, N, K, out = _linear_args(x, wq, scales, zp, bias, group_size, out)
     S, R = _adapter_args(x, la, lb, ids, alpha, M, N, K)
@@ -573,7 +574,7 @@ def w4a16_lora_backward(dy, x, u, wq, scales, la, lb, ids, zp=None, alpha=None, 
                         need_dx: bool = True, out=None, workspace=None):
     """Gradients of w4a16_lora_linear: (dx, dla, dlb) for dy [M, N], with x and the u that the
     forward call kept (save_u).  dx is None where need_dx is false.  out: (dx or None, dla, dlb)
-    to write into."""
+    to write into: overwritten, not added to."""
     torch = _torch()
     if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0] or dy.shape[1] != wq.shape[0]:
         raise ValueError(f"dy is {tuple(dy.shape)}, expected {(x.shape[0], wq.shape[0])}")
@@ -642,8 +643,9 @@ def w4a16_adamw_plan(params, grads, exp_avgs, exp_avg_sqs, *, m_scales=None, v_s
     exp_avgs / exp_avg_sqs are float32 (moments in 32 bits), or int8 / uint8 with
     m_scales / v_scales float32 [ceil(n / 256)] (moments in 8 bits; zeros to begin
     with).  copies: float16 or bfloat16 copies of the parameters, written by every
-    step (None for a parameter that has none).  The plan keeps the tensors; they
-    must stay where they are."""
+    step (None for a parameter that has none).  The plan keeps the tensors, and every
+    step reads and writes them where they are now: gradients that are allocated anew
+    (set to None between steps) need a new plan, or are copied into the plan's."""
     torch = _torch()
     params, grads, ms, vs = list(params), list(grads), list(exp_avgs), list(exp_avg_sqs)
     count = len(params)
@@ -690,7 +692,8 @@ def w4a16_adamw_plan(params, grads, exp_avgs, exp_avg_sqs, *, m_scales=None, v_s
 def w4a16_adamw_step(plan: AdamwPlan, *, lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
                      step: int, grad_scale: float = 1.0, seed: int = 0) -> None:
     """One AdamW step (number `step`, from 1) over the plan's tensors, on the current stream.
-    Moments in 8 bits are rounded with a dither that seed chooses: give every step another."""
+    Moments in 8 bits are rounded with a dither that seed chooses: give every step another.
+    A captured graph repeats the numbers it was captured with."""
     _invoke(plan.device, lib.w4a16_adamw_step, plan.table.data_ptr(), plan.info_ref, lr, betas[0], betas[1], eps,
             weight_decay, step, grad_scale, seed & 0xFFFFFFFF, _raw_stream(plan.device))
 

@@ -23,8 +23,8 @@
 // elements a lane, so a block's largest value is a wave reduction and every
 // access of a full block is one vector load or store.  The step is bound by
 // the memory it moves: 35.7 M elements with 32-bit moments 185 us (5.4 TB/s),
-// 143 M with 8-bit moments 430 us (5.3 TB/s) and 249 us for their decoded
-// moments; a copy reaches 5.2.  One layer's 0.8 M elements: 6.3 us, latency.
+// 143 M with 8-bit moments 440 us (5.2 TB/s) and 248 us for their decoded
+// moments; a copy reaches 5.2.  One layer's 0.8 M elements: 6.6 us, latency.
 #include "w4a16_adamw.h"
 #include "w4a16_device.hpp"
 #include "w4a16_internal.h"

@@ -350,8 +350,10 @@ hipError_t launch_mw(const DxParams& prm, const LoraTerm& lora, int mw, hipStrea
 
 // Tile height and split of n: time model in microseconds, fitted to every
 // (height, split) timed on 14 shapes (M 32-2048, N and K 1216-28672, groups of
-// 32; mean error 5.9 %, its picks 2.3 % from the best on average, 13 % at
-// worst): a fixed part and a time per step and round of resident workgroups
+// 32, all in bf16; mean error 5.9 %, its picks 2.3 % from the best on average,
+// 13 % at worst; fp16, whose dequantisation takes other instructions, uses the
+// same model unswept: 1921 x 4096 x 6144 takes 125 us where it gives 108): a
+// fixed part and a time per step and round of resident workgroups
 // (64-token tiles: 1.08 us alone on a CU, 1.56 us for two that share one),
 // and for a split its second launch and the partial sums' way through memory.
 DxPlan plan_dx(int64_t M, int64_t N, int64_t K, int cu_count) {

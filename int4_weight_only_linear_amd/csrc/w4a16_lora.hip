@@ -141,7 +141,7 @@ __global__ __launch_bounds__(64 * shrink_waves(TT, RC)) void shrink_kernel(
 
 // u = the K ranges' sums in range order, and alpha * u as operands (each where
 // wanted); n = M R.  Four ranks a lane, a token 2^lanes_log2 lanes, which find
-// its largest value together.  (A launch of its own: 2.3 us for 67 tokens of 32
+// its largest value together.  (A launch of its own: 2.3-4 us for 67 tokens of 32
 // ranks, 5.2 for 1920 of 64.)
 template <int DT>
 __global__ __launch_bounds__(256) void shrink_reduce_kernel(const float* __restrict__ part, const int32_t* __restrict__ ids,
