@@ -1,4 +1,4 @@
-"""The decode kernels of this build (CPU only): adapters live in instances of
+"""The compiled decode kernels (CPU only): adapters live in instances of
 their own, and every kernel the host code launches by name is in the device
 code (a name that the two passes of the compiler spell differently, such as one
 with an unnamed type in it, aborts at its first launch)."""
