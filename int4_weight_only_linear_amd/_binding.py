@@ -548,7 +548,9 @@ def w4a16_lora_linear(x, wq, scales, la, lb, ids, zp=None, bias=None, alpha=None
     m's adapter a = ids[m] out of the stacks la [S, R, K] and lb [S, N, R] (an id outside
     [0, S): no adapter).  With save_u returns (y, u), u = x . A_a^T in float32 [M, R] for
     w4a16_lora_backward.  Not recorded by autograd: y requires no gradient, whatever la, lb
-    and x do; a training step calls w4a16_lora_backward itself."""
+    and x do; a training step calls w4a16_lora_backward itself.  workspace: zero-filled uint8 of
+    w4a16_lora_workspace_size; without one a buffer kept per stream is used, which a later, larger
+    call replaces, so calls captured in a graph bring their own."""
     torch = _torch()
     dt, M, N, K, out = _linear_args(x, wq, scales, zp, bias, group_size, out)
     S, R = _adapter_args(x, la, lb, ids, alpha, M, N, K)
@@ -574,7 +576,8 @@ def w4a16_lora_backward(dy, x, u, wq, scales, la, lb, ids, zp=None, alpha=None, 
                         need_dx: bool = True, out=None, workspace=None):
     """Gradients of w4a16_lora_linear: (dx, dla, dlb) for dy [M, N], with x and the u that the
     forward call kept (save_u).  dx is None where need_dx is false.  out: (dx or None, dla, dlb)
-    to write into: overwritten, not added to."""
+    to write into: overwritten, not added to.  workspace: as for w4a16_lora_linear, of
+    w4a16_lora_backward_workspace_size."""
     torch = _torch()
     if dy.dim() != 2 or x.dim() != 2 or dy.shape[0] != x.shape[0] or dy.shape[1] != wq.shape[0]:
         raise ValueError(f"dy is {tuple(dy.shape)}, expected {(x.shape[0], wq.shape[0])}")
