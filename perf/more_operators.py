@@ -1,0 +1,385 @@
+"""Measured cases of the experts' operators: routing of tokens to experts with
+its gradient, quantisation of activations to 8-bit floating point, and matrix
+products of 8-bit weights with a scale for each block of 128, for one layer
+and for the experts that the routing names.
+
+``run`` computes a case in its plain form (elementary torch operations in 32
+bits, in 64 where experts are ranked, rounded once at the end), or, where
+``own`` is true, with the framework's entry points.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+SIZE = {"f16": 2, "bf16": 2, "f32": 4}
+BLOCK = 128
+
+
+def listed():
+    def route(name, M, E, topk, score, dtype, bias=False, groups=1, topk_groups=1, group_top=1, renormalize=False,
+              scale=1.0, op="route"):
+        return dict(name=name, op=op, M=M, E=E, topk=topk, score=score, dtype=dtype, bias=bias, groups=groups,
+                    topk_groups=topk_groups, group_top=group_top, renormalize=renormalize, scale=scale)
+
+    def linear(name, M, K, N, dtype="bf16", e8m0=False, bias=False, transpose=False):
+        return dict(name=name, op="linear", M=M, K=K, N=N, dtype=dtype, e8m0=e8m0, bias=bias, transpose=transpose)
+
+    def moe(name, M, E, topk, K, N, dtype="bf16", e8m0=False, per_slot=False, weights=True, transpose=False):
+        return dict(name=name, op="moe", M=M, E=E, topk=topk, K=K, N=N, dtype=dtype, e8m0=e8m0, per_slot=per_slot,
+                    weights=weights, transpose=transpose)
+
+    return [
+        # the next tokens of four requests: latency alone
+        route("route_4", 4, 64, 6, "softmax", "bf16", renormalize=True),
+        # a large prefill step, scores with a bias for balance and a choice of groups before the choice of experts
+        route("route_16384", 16384, 256, 8, "sigmoid", "f32", bias=True, groups=8, topk_groups=4, group_top=2,
+              renormalize=True, scale=2.5),
+        # an odd training step of a small router
+        route("route_bwd_1921", 1921, 60, 4, "softmax", "bf16", op="route_bwd"),
+        # a large training step's router
+        route("route_bwd_16384", 16384, 256, 8, "sigmoid", "f32", bias=True, groups=8, topk_groups=4, group_top=2,
+              renormalize=True, scale=2.5, op="route_bwd"),
+        # an odd batch's activations, quantised once for several products
+        dict(name="quantize_67", op="quantize", M=67, K=2560, dtype="f16"),
+        # a large step's wide activations: memory rate
+        dict(name="quantize_8192", op="quantize", M=8192, K=14336, dtype="bf16"),
+        # one user's next token through the attention output projection: latency alone
+        linear("linear_1", 1, 4096, 4096),
+        # an odd batch through a down projection, fp16, power-of-two scales and a bias
+        linear("linear_67", 67, 14336, 4096, dtype="f16", e8m0=True, bias=True),
+        # a prefill step through gate + up
+        linear("linear_1920", 1920, 4096, 28672),
+        # the gradient of a training step's input: an odd number of tokens through the weights the other way
+        linear("linear_dx_1921", 1921, 6144, 4096, transpose=True),
+        # eight users decode: nearly every slot meets an expert of its own
+        moe("moe_8", 8, 128, 8, 2048, 1536),
+        # a prefill step's experts
+        moe("moe_2048", 2048, 64, 8, 4096, 2048),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(("route", "route_bwd", "quantize", "linear", "linear", "moe", "moe"))
+    if op in ("route", "route_bwd"):
+        groups = rng.choice((1, 1, 2, 4, 8))
+        E = groups * _log(rng, max(2, 8 // groups), 256 // groups)
+        kept = rng.randint(max(1, groups // 2), groups)
+        topk = rng.randint(1, min(8, kept * (E // groups)))
+        return dict(op=op, M=_log(rng, 1, 16384), E=E, topk=topk, score=rng.choice(("softmax", "sigmoid")),
+                    dtype=rng.choice(("f16", "bf16", "f32")), bias=rng.random() < 0.5, groups=groups, topk_groups=kept,
+                    group_top=rng.choice((1, 2)) if groups > 1 else 1, renormalize=rng.random() < 0.6,
+                    scale=rng.choice((1.0, 1.0, 2.5)))
+    dtype = rng.choice(("f16", "bf16"))
+    if op == "quantize":
+        return dict(op=op, M=_log(rng, 1, 8192), K=_log(rng, 16, 14336), dtype=dtype)
+    case = dict(op=op, dtype=dtype, e8m0=rng.random() < 0.4, transpose=rng.random() < 0.3)
+    if op == "linear":
+        case |= dict(M=_log(rng, 1, 2048), K=_log(rng, 128, 14336), N=_log(rng, 64, 7168), bias=rng.random() < 0.3)
+    else:
+        E = _log(rng, 4, 128)
+        topk = rng.randint(1, min(8, E))
+        per_slot = rng.random() < 0.4
+        case |= dict(E=E, topk=topk, K=_log(rng, 128, 4096), N=_log(rng, 64, 2048), per_slot=per_slot,
+                     weights=rng.random() < 0.6, M=_log(rng, 1, max(1, min(2048, 131072 // E // (topk if per_slot else 1)))))
+    # a row of the weights holds a multiple of 16 codes
+    row = "N" if case["transpose"] else "K"
+    case[row] = (case[row] + 15) // 16 * 16
+    return case
+
+
+# ------------------------------------------------------------- inputs ---
+
+def _router_logits(gen, dev, M, E):
+    # experts differ in how often they are wanted
+    return torch.randn((M, E), generator=gen, device=dev) * 1.5 + torch.randn(E, generator=gen, device=dev) * 0.5
+
+
+def _prepare_route(case, gen, dev):
+    M, E = case["M"], case["E"]
+    state = dict(case=case, logits=_router_logits(gen, dev, M, E).to(DTYPES[case["dtype"]]),
+                 bias=torch.randn(E, generator=gen, device=dev) * 0.05 if case["bias"] else None)
+    if case["op"] == "route_bwd":
+        # the forward pass's choice and the gradient of its weights
+        state["ids"] = _plain_route(state)[1]
+        state["dw"] = torch.randn((M, case["topk"]), generator=gen, device=dev)
+    return state
+
+
+def _prepare_weights(case, gen, dev):
+    """Codes of normal weights that fill the range of each block of 128 x 128, and the blocks' scales."""
+    lead = (case["E"],) if case["op"] == "moe" else ()
+    rows, cols = (case["K"], case["N"]) if case["transpose"] else (case["N"], case["K"])
+    w = torch.empty(lead + (rows, cols), dtype=torch.float8_e4m3fn, device=dev)
+    for part in w if lead else (w,):
+        part.copy_(torch.randn((rows, cols), generator=gen, device=dev).mul_(107.0).clamp_(-448.0, 448.0))
+    blocks = lead + ((rows + BLOCK - 1) // BLOCK, (cols + BLOCK - 1) // BLOCK)
+    if case["e8m0"]:
+        scales = torch.randint(112, 116, blocks, generator=gen, device=dev, dtype=torch.uint8).view(torch.float8_e8m0fnu)
+    else:
+        scales = (torch.rand(blocks, generator=gen, device=dev) + 0.5) * (0.02 / 107.0)
+    return w, scales
+
+
+def _activations(gen, dev, M, K, dtype):
+    # a few channels are far larger than the others
+    return (torch.randn((M, K), generator=gen, device=dev) * torch.exp(torch.randn(K, generator=gen, device=dev) * 0.7)).to(dtype)
+
+
+def prepare(case, seed):
+    dev = torch.device("cuda")
+    gen = torch.Generator(device=dev).manual_seed(seed)
+    op, dt = case["op"], DTYPES[case["dtype"]]
+    if op in ("route", "route_bwd"):
+        return _prepare_route(case, gen, dev)
+    if op == "quantize":
+        return dict(case=case, x=_activations(gen, dev, case["M"], case["K"], dt))
+    w, scales = _prepare_weights(case, gen, dev)
+    state = dict(case=case, w=w, scales=scales)
+    M, N = case["M"], case["N"]
+    if op == "linear":
+        return state | dict(x=_activations(gen, dev, M, case["K"], dt),
+                            bias=(torch.randn(N, generator=gen, device=dev) * 0.1).to(dt) if case["bias"] else None)
+    topk = case["topk"]
+    top = torch.sort(torch.softmax(_router_logits(gen, dev, M, case["E"]), 1), dim=1, descending=True, stable=True)
+    return state | dict(x=_activations(gen, dev, M * topk if case["per_slot"] else M, case["K"], dt),
+                        ids=top.indices[:, :topk].to(torch.int32).contiguous(),
+                        weights=top.values[:, :topk].contiguous() if case["weights"] else None)
+
+
+# --------------------------------------------------------- plain form ---
+
+def _scores(case, l):
+    if case["score"] == "sigmoid":
+        return 1.0 / (1.0 + torch.exp(-l))
+    e = torch.exp(l - l.amax(1, keepdim=True))
+    return e / e.sum(1, keepdim=True)
+
+
+def _plain_route(s):
+    case, l = s["case"], s["logits"].double()
+    M, E = l.shape
+    score = _scores(case, l)
+    groups, top = case["groups"], case["group_top"]
+    # scores grow with the logits: without a bias the logits rank the experts
+    key = score + s["bias"].double() if s["bias"] is not None else (l if top == 1 else score)
+    if groups > 1:
+        best = torch.sort(key.view(M, groups, E // groups), dim=2, descending=True).values[:, :, :top].sum(2)
+        order = torch.sort(best, dim=1, descending=True, stable=True).indices[:, :case["topk_groups"]]
+        kept = torch.zeros_like(best, dtype=torch.bool).scatter_(1, order, True)
+        key = torch.where(kept.repeat_interleave(E // groups, 1), key, -math.inf)
+    ids = torch.sort(key, dim=1, descending=True, stable=True).indices[:, :case["topk"]]
+    w = score.gather(1, ids)
+    if case["renormalize"]:
+        w = w / w.sum(1, keepdim=True)
+    return (w * case["scale"]).float(), ids.to(torch.int32)
+
+
+def _plain_route_bwd(s):
+    case, l, dw, ids = s["case"], s["logits"].float(), s["dw"] * s["case"]["scale"], s["ids"].long()
+    score = _scores(case, l)
+    picked = score.gather(1, ids)
+    if case["renormalize"]:
+        total = picked.sum(1, keepdim=True)
+        dw = (dw - (picked / total * dw).sum(1, keepdim=True)) / total
+    ds = torch.zeros_like(score).scatter_(1, ids, dw)
+    if case["score"] == "softmax":
+        dl = score * (ds - (score * ds).sum(1, keepdim=True))
+    else:
+        dl = ds * score / (1.0 + torch.exp(l))
+    return dl.to(s["logits"].dtype)
+
+
+def _plain_quantize(x):
+    """Codes [M, K'] and scales [M, blocks], K' a multiple of 128 and the blocks of four; and the codes' values with
+    their scales, in 32 bits."""
+    M, K = x.shape
+    blocks = (K + 4 * BLOCK - 1) // (4 * BLOCK) * 4
+    v = torch.zeros((M, blocks * BLOCK), dtype=torch.float32, device=x.device)
+    v[:, :K] = x.float()
+    v = v.view(M, blocks, BLOCK)
+    # the smallest power of two that brings the block's largest value to 448 = 1.75 * 2^8 or below
+    part, exponent = torch.frexp(v.abs().amax(2))
+    exponent = torch.where(part > 0, exponent - 9 + (part > 0.875).int(), 0).clamp(min=-127)
+    scales = (exponent + 127).to(torch.uint8).view(torch.float8_e8m0fnu)
+    inverse = ((127 - exponent) << 23).view(torch.float32)  # 2^-exponent
+    codes = (v * inverse[:, :, None]).to(torch.float8_e4m3fn)
+    values = codes.float() * scales.float()[:, :, None]
+    columns = (K + BLOCK - 1) // BLOCK * BLOCK
+    return codes.view(M, -1)[:, :columns].contiguous(), scales, values.view(M, -1)[:, :K]
+
+
+def _weights(s):
+    """[..., K, N] in 32 bits."""
+    w, scales = s["w"], s["scales"].float()
+    scales = scales.repeat_interleave(BLOCK, -1)[..., :w.shape[-1]].repeat_interleave(BLOCK, -2)[..., :w.shape[-2], :]
+    w = w.float() * scales
+    return w if s["case"]["transpose"] else w.transpose(-1, -2)
+
+
+def _plain_linear(s):
+    y = _plain_quantize(s["x"])[2] @ _weights(s)
+    if s["bias"] is not None:
+        y = y + s["bias"].float()
+    return y.to(s["x"].dtype)
+
+
+def _plain_moe(s):
+    # every row through every expert, and of each slot its own expert's result
+    case, ids = s["case"], s["ids"].long()
+    M, E, topk, K, N = case["M"], case["E"], case["topk"], case["K"], case["N"]
+    every = _plain_quantize(s["x"])[2] @ _weights(s).permute(1, 0, 2).reshape(K, E * N)
+    every = every.view(M, topk if case["per_slot"] else 1, E, N).expand(M, topk, E, N)
+    y = every.gather(2, ids.view(M, topk, 1, 1).expand(M, topk, 1, N)).view(M * topk, N)
+    if s["weights"] is not None:
+        y = y * s["weights"].view(M * topk, 1)
+    return y.to(s["x"].dtype)
+
+
+# ----------------------------------------------------------------- run ---
+
+def run(state):
+    s, case = state, state["case"]
+    op = case["op"]
+    if not own:
+        if op == "quantize":
+            return _plain_quantize(s["x"])[:2]
+        return {"route": _plain_route, "route_bwd": _plain_route_bwd, "linear": _plain_linear, "moe": _plain_moe}[op](s)
+    import int4_weight_only_linear_amd as L
+    if op == "route":
+        return L.w4a16_route(s["logits"], case["topk"], s["bias"], score=case["score"], groups=case["groups"],
+                             topk_groups=case["topk_groups"], group_top=case["group_top"],
+                             renormalize=case["renormalize"], scale=case["scale"])
+    if op == "route_bwd":
+        return L.w4a16_route_backward(s["dw"], s["logits"], s["ids"], score=case["score"],
+                                      renormalize=case["renormalize"], scale=case["scale"])
+    if op == "quantize":
+        return L.w4a16_fp8_quantize(s["x"])
+    if op == "linear":
+        return L.w4a16_fp8_linear(s["x"], s["w"], s["scales"], s["bias"], transpose=case["transpose"])
+    return L.w4a16_fp8_moe_linear(s["x"], s["w"], s["scales"], s["ids"], s["weights"], transpose=case["transpose"],
+                                  x_per_slot=case["per_slot"])
+
+
+# ---------------------------------------------------------------- work ---
+
+def work(case):
+    op, M = case["op"], case["M"]
+    if op in ("route", "route_bwd"):
+        E, topk, size = case["E"], case["topk"], SIZE[case["dtype"]]
+        back = op == "route_bwd"
+        return {"bytes": M * (E * size * (2 if back else 1) + 8 * topk) + (4 * E if case["bias"] and not back else 0),
+                "flops": M * (10 * E + topk * (10 if back else E))}
+    K = case["K"]
+    blocks = (K + 4 * BLOCK - 1) // (4 * BLOCK) * 4
+    if op == "quantize":
+        return {"bytes": M * (2 * K + (K + BLOCK - 1) // BLOCK * BLOCK + blocks), "flops": 4 * M * K}
+    N = case["N"]
+    weights = N * K + ((N + BLOCK - 1) // BLOCK) * ((K + BLOCK - 1) // BLOCK) * (1 if case["e8m0"] else 4)
+    if op == "linear":
+        return {"bytes": weights + 2 * M * (K + N) + (2 * N if case["bias"] else 0), "flops": 2 * M * N * K}
+    slots, E = M * case["topk"], case["E"]
+    # the experts that so many evenly drawn slots name
+    used = max(1, min(E, slots, round(E * (1 - (1 - case["topk"] / E) ** M))))
+    rows = slots if case["per_slot"] else M
+    return {"bytes": used * weights + 2 * rows * K + 2 * slots * N + slots * (8 if case["weights"] else 4),
+            "flops": 2 * slots * N * K}
+
+
+# --------------------------------------------------------------- exact ---
+
+def _power(e):
+    """2^e in 64 bits for whole e."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def _exact_values(x):
+    """What each element of x is rounded to: with 2^e the smallest power of two for which the largest of its 128 is at
+    most 448 * 2^e, the nearest multiple of the step that three mantissa bits leave (ties to even), in 64 bits."""
+    M, K = x.shape
+    blocks = (K + BLOCK - 1) // BLOCK
+    v = torch.nn.functional.pad(x.double(), (0, blocks * BLOCK - K)).view(M, blocks, BLOCK)
+    top = v.abs().amax(2, keepdim=True)
+    e = torch.ceil(torch.log2(top.clamp(min=1e-300) / 448.0))
+    e = torch.where(448.0 * _power(e - 1) >= top, e - 1, e)  # (a logarithm next to a whole number)
+    e = torch.where(448.0 * _power(e) < top, e + 1, e)
+    e = torch.where(top > 0, e.clamp(min=-127.0), 0.0)
+    u = v / _power(e)
+    step = _power(torch.floor(torch.log2(u.abs().clamp(min=2.0 ** -6))) - 3)
+    u = torch.round(u / step) * step
+    return u.view(M, -1), e.view(M, blocks), (u * _power(e)).view(M, -1)[:, :K]
+
+
+def _exact_weights(w, scales):
+    i = torch.arange(w.shape[0], device=w.device) // BLOCK
+    j = torch.arange(w.shape[1], device=w.device) // BLOCK
+    return w.double() * scales.double()[i][:, j]
+
+
+def _exact_route(s):
+    case, l = s["case"], s["logits"].double()
+    M, E = l.shape
+    if case["score"] == "softmax":
+        e = torch.exp(l - l.amax(1, keepdim=True))
+        p = e / e.sum(1, keepdim=True)
+    else:
+        p = torch.sigmoid(l)
+    if case["op"] == "route_bwd":
+        # the weights' Jacobian with respect to the scores, then the scores' with respect to the logits
+        chosen = torch.nn.functional.one_hot(s["ids"].long(), E).double()
+        q, dw = (chosen * p[:, None]).sum(2), s["dw"].double() * case["scale"]
+        if case["renormalize"]:
+            t = q.sum(1, keepdim=True)
+            dw = dw / t - (dw * q).sum(1, keepdim=True) / t ** 2
+        ds = (chosen * dw[:, :, None]).sum(1)
+        return p * ds - p * (p * ds).sum(1, keepdim=True) if case["score"] == "softmax" else ds * p * torch.sigmoid(-l)
+    return p
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op = case["op"]
+    if op == "route_bwd":
+        return _exact_route(s)
+    if op == "route":
+        # the experts chosen one after another: the first of the largest keys of the groups that are left in
+        l = s["logits"].double()
+        p = _exact_route(s)
+        key = p + s["bias"].double() if s["bias"] is not None else (l if case["group_top"] == 1 else p)
+        G = case["groups"]
+        if G > 1:
+            group = torch.topk(key.view(len(l), G, -1), case["group_top"], dim=2).values.sum(2)
+            left = torch.zeros_like(group, dtype=torch.bool)
+            for _ in range(case["topk_groups"]):
+                left.scatter_(1, torch.where(left, -math.inf, group).max(1, keepdim=True).indices, True)
+            key = torch.where(left[:, :, None], key.view(len(l), G, -1), -math.inf).view(len(l), -1)
+        picked = []
+        for _ in range(case["topk"]):
+            i = (key == key.amax(1, keepdim=True)).int().argmax(1, keepdim=True)
+            picked.append(i)
+            key = key.scatter(1, i, -math.inf)
+        w = p.gather(1, torch.cat(picked, 1))
+        return (w / w.sum(1, keepdim=True) if case["renormalize"] else w) * case["scale"], None
+    u, e, x = _exact_values(s["x"])
+    if op == "quantize":
+        blocks = (case["K"] + 4 * BLOCK - 1) // (4 * BLOCK) * 4
+        return u, torch.nn.functional.pad(_power(e), (0, blocks - e.shape[1]), value=1.0)
+    turn = (lambda w: w) if case["transpose"] else (lambda w: w.T)
+    if op == "linear":
+        y = x @ turn(_exact_weights(s["w"], s["scales"]))
+        return y if s["bias"] is None else y + s["bias"].double()
+    topk = case["topk"]
+    ids = s["ids"].reshape(-1)
+    y = torch.zeros((len(ids), case["N"]), dtype=torch.float64, device=x.device)
+    for a in range(case["E"]):
+        slots = torch.nonzero(ids == a).view(-1)
+        if len(slots):
+            rows = slots if case["per_slot"] else slots // topk
+            y[slots] = x[rows] @ turn(_exact_weights(s["w"][a], s["scales"][a]))
+    return y if s["weights"] is None else y * s["weights"].double().reshape(-1, 1)
