@@ -206,7 +206,7 @@ def _plain_quantize(x):
     v = v.view(M, blocks, BLOCK)
     # the smallest power of two that brings the block's largest value to 448 = 1.75 * 2^8 or below
     part, exponent = torch.frexp(v.abs().amax(2))
-    exponent = torch.where(part > 0, exponent - 9 + (part > 0.875).int(), 0).clamp(min=-127)
+    exponent = torch.where(part > 0, exponent - 9 + (part > 0.875).int(), 0).clamp(min=-126)
     scales = (exponent + 127).to(torch.uint8).view(torch.float8_e8m0fnu)
     inverse = ((127 - exponent) << 23).view(torch.float32)  # 2^-exponent
     codes = (v * inverse[:, :, None]).to(torch.float8_e4m3fn)
@@ -309,7 +309,7 @@ def _exact_values(x):
     e = torch.ceil(torch.log2(top.clamp(min=1e-300) / 448.0))
     e = torch.where(448.0 * _power(e - 1) >= top, e - 1, e)  # (a logarithm next to a whole number)
     e = torch.where(448.0 * _power(e) < top, e + 1, e)
-    e = torch.where(top > 0, e.clamp(min=-127.0), 0.0)
+    e = torch.where(top > 0, e.clamp(min=-126.0), 0.0)
     u = v / _power(e)
     step = _power(torch.floor(torch.log2(u.abs().clamp(min=2.0 ** -6))) - 3)
     u = torch.round(u / step) * step
