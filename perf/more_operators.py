@@ -260,10 +260,10 @@ def run(state):
         return L.w4a16_route_backward(s["dw"], s["logits"], s["ids"], score=case["score"],
                                       renormalize=case["renormalize"], scale=case["scale"])
     if op == "quantize":
-        return L.w4a16_fp8_quantize(s["x"])
+        return L.w4a16_minifloat_quantize(s["x"])
     if op == "linear":
-        return L.w4a16_fp8_linear(s["x"], s["w"], s["scales"], s["bias"], transpose=case["transpose"])
-    return L.w4a16_fp8_moe_linear(s["x"], s["w"], s["scales"], s["ids"], s["weights"], transpose=case["transpose"],
+        return L.w4a16_minifloat_linear(s["x"], s["w"], s["scales"], s["bias"], transpose=case["transpose"])
+    return L.w4a16_minifloat_moe_linear(s["x"], s["w"], s["scales"], s["ids"], s["weights"], transpose=case["transpose"],
                                   x_per_slot=case["per_slot"])
 
 
