@@ -81,8 +81,13 @@ typedef enum w4a16_status {
   W4A16_ERR_WORKSPACE = 6     /* workspace missing or smaller than w4a16_workspace_size */
 } w4a16_status;
 
-/* W4A16_F32: the optimiser's tensors only, never activations */
-typedef enum w4a16_dtype { W4A16_F16 = 0, W4A16_BF16 = 1, W4A16_F32 = 2 } w4a16_dtype;
+/* Activations are fp16 or bf16.  W4A16_F32: the optimiser's tensors, a router's
+ * logits and 8-bit weights' scales; W4A16_E4M3: 8-bit codes (OCP e4m3: no
+ * infinities, largest value 448); W4A16_E8M0: scales that are powers of two, held
+ * as exponent + 127 (255: NaN). */
+typedef enum w4a16_dtype {
+  W4A16_F16 = 0, W4A16_BF16 = 1, W4A16_F32 = 2, W4A16_E4M3 = 3, W4A16_E8M0 = 4
+} w4a16_dtype;
 
 typedef enum w4a16_path {
   W4A16_PATH_AUTO = 0,  /* pick by M, N, K, group and dtype */
@@ -455,6 +460,108 @@ w4a16_status w4a16_adamw_step(const void* table, const w4a16_adamw_plan* plan, d
  * state): m, v fp32 [plan->blocks * 256], 16-byte aligned, the tensors' blocks
  * in the table's order, zeros past a tensor's last element. */
 w4a16_status w4a16_adamw_moments(const void* table, const w4a16_adamw_plan* plan, float* m, float* v, void* stream);
+
+/* -------------------------------------------------- routing to experts ---
+ * The router's choice for w4a16_moe_linear and w4a16_minifloat_moe_linear.  For token
+ * m with the logits l = logits[m, :] of E experts:
+ *   s_e   = softmax(l)_e (W4A16_SCORE_SOFTMAX) or 1 / (1 + exp(-l_e)) (W4A16_SCORE_SIGMOID)
+ *   key_e = s_e + bias_e            (bias: for balance; it moves the choice only)
+ * The experts form `groups` groups of E / groups neighbours.  A group's key is
+ * the sum of its group_top (1 or 2) largest keys; the topk_groups groups of the
+ * largest keys stay in (groups = 1: every expert does).  Of their experts the
+ * topk with the largest keys are chosen, in falling order; equal keys go to the
+ * lower index, among groups too.  With i_j the j-th of them:
+ *   weights[m, j] = scale * s_{i_j}                                   (renormalize == 0)
+ *                 = scale * s_{i_j} / (sum over k of s_{i_k})         (renormalize != 0)
+ *   ids[m, j]     = i_j
+ * Keys are formed and compared in 64 bits (without a bias, and with group_top 1,
+ * the logits themselves are compared: scores grow with them); weights are
+ * rounded once, to fp32.
+ *   logits fp16, bf16 or fp32 [M, E]   bias fp32 [E] or NULL
+ *   weights fp32 [M, topk]             ids int32 [M, topk]
+ * An expert whose logit is -infinity or NaN, or whose key is, is never chosen:
+ * slots that none is left for get id -1 (a zero row of the experts' products)
+ * and weight 0.  A NaN logit makes all weights of its row NaN.  Where logits are
+ * +infinity, softmax shares 1 among them.  A sum of scores that is zero gives
+ * zero weights.
+ * E at most 1024, topk at most 64, groups at most 64 and M at most 2^25
+ * (W4A16_ERR_UNSUPPORTED above); topk at most topk_groups * E / groups.
+ * Pointers are aligned to their elements; outputs overlap nothing. */
+#define W4A16_SCORE_SOFTMAX 0
+#define W4A16_SCORE_SIGMOID 1
+w4a16_status w4a16_route(const void* logits, const float* bias, float* weights, int32_t* ids, int64_t M, int64_t E,
+                         int64_t topk, int64_t groups, int64_t topk_groups, int64_t group_top, int32_t dtype,
+                         int32_t score, int32_t renormalize, double scale, void* stream);
+
+/* The gradient of w4a16_route's weights with respect to the logits (the choice
+ * is constant; the bias has none).  With g = scale * dweights[m, :], p_j the
+ * chosen scores, S their sum and c = sum over j of g_j p_j / S:
+ *   d s_{i_j} = g_j                   (renormalize == 0), (g_j - c) / S (renormalize != 0)
+ *   d l_e = s_e (d s_e - sum over k of s_k d s_k)   softmax
+ *         = d s_e s_e (1 - s_e)                     sigmoid
+ * in fp32, rounded once to the logits' type.  ids as w4a16_route wrote them (any
+ * choice is taken: an id outside [0, E) adds nothing, one that is there twice
+ * counts twice).  Every element of dlogits [M, E] is written; -infinite logits
+ * get zero, a row with a NaN logit NaN. */
+w4a16_status w4a16_route_backward(const float* dweights, const void* logits, const int32_t* ids, void* dlogits,
+                                  int64_t M, int64_t E, int64_t topk, int32_t dtype, int32_t score,
+                                  int32_t renormalize, double scale, void* stream);
+
+/* ------------------------------------------ 8-bit floating-point weights ---
+ * Layers whose weights are e4m3 codes with one scale for each block of 128 x 128
+ * beside the 4-bit ones.  Activations are quantised with one scale for each
+ * token and block of 128 k:
+ *   2^e = the smallest power of two, at least 2^-126, for which the block's
+ *         largest finite |x| is at most 448 * 2^e (1 where that is zero)
+ *   code = x / 2^e rounded once, to nearest-even, to e4m3
+ * Infinite and NaN values become NaN codes and leave the others as they are.
+ *   x      fp16 or bf16 [M, K]
+ *   codes  e4m3 [M, K'], K' = K rounded up to 128, zeros behind K
+ *   scales e8m0 [M, B], B = ceil(K / 512) * 4: of K's blocks, then 1
+ * codes 16-byte, scales 4-byte, x 2-byte aligned (16-byte aligned rows are faster);
+ * M at most 2^30, K at most 2^24, M * B * 128 at most 2^34. */
+w4a16_status w4a16_minifloat_quantize(const void* x, void* codes, uint8_t* scales, int64_t M, int64_t K, int32_t dtype,
+                                void* stream);
+
+/* y = x' . w'^T (+ bias), x' the quantised x and w' the scaled weights:
+ *   y[m, n] = sum over blocks b of x_scales[m, b] w_scales[n / 128, b]
+ *                 * (sum over k in b of x_codes[m, k] w[n, k])  + bias[n]
+ *   x        fp16 or bf16 [M, K] (x_dtype == dtype, x_scales NULL: quantised by
+ *            the call, in its workspace), or codes [M, K'] with their x_scales as
+ *            w4a16_minifloat_quantize writes them (x_dtype W4A16_E4M3)
+ *   w        e4m3 [N, K], w_scales fp32 or e8m0 [ceil(N / 128), ceil(K / 128)]
+ *   bias act [N] or NULL, y act [M, N] (dtype)
+ * transpose != 0: w is [K, N] and w_scales [ceil(K / 128), ceil(N / 128)], so
+ * that a layer's own weights give the gradient of its input: x = dy [M, K], K the
+ * layer's outputs.  (The weights are frozen, as the 4-bit ones.)
+ * The length of a row of w (K, or N where transposed) is a multiple of 16.
+ * Products are exact; the matrix unit adds those of eight neighbouring k at the
+ * largest one's exponent and drops what lies more than 13 bits below it, and adds
+ * these sums in fp32.  Outputs are rounded once.
+ * Workspace: w4a16_minifloat_linear_workspace_size bytes (0: none), 256-byte aligned,
+ * under w4a16_linear's rules.  w and codes 16-byte, scales 4-byte (e8m0 w_scales
+ * any), the others 2-byte aligned; y and the workspace overlap nothing. */
+size_t w4a16_minifloat_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t x_dtype, int32_t transpose);
+w4a16_status w4a16_minifloat_linear(const void* x, const uint8_t* x_scales, const void* w, const void* w_scales,
+                              const void* bias, void* y, int64_t M, int64_t N, int64_t K, int32_t x_dtype,
+                              int32_t scale_dtype, int32_t dtype, int32_t transpose, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* The same product with the experts of a routed batch, from one token to
+ * prefill: for token m and slot j, s = m * topk + j, e = topk_ids[m, j]:
+ *   y[s, :] = topk_weights[m, j] * (x'_row . w'_e^T + bias_e)
+ * rounded once; x_row = x[m], or x[s] where x_per_slot != 0 (x is [M * topk, K]).
+ *   w e4m3 [E, N, K] (transposed: [E, K, N]), w_scales [E, ...] of them, bias act
+ *   [E, N] or NULL; topk_ids int32 [M, topk] (an id outside [0, E) gives a zero
+ *   row), topk_weights fp32 [M, topk] or NULL (1); y act [M * topk, N]
+ * E at most 1024, M * topk at most 2^30.  The rest as for w4a16_minifloat_linear. */
+size_t w4a16_minifloat_moe_workspace_size(int64_t M, int64_t topk, int64_t E, int64_t N, int64_t K, int32_t x_dtype,
+                                    int32_t transpose, int32_t x_per_slot);
+w4a16_status w4a16_minifloat_moe_linear(const void* x, const uint8_t* x_scales, const void* w, const void* w_scales,
+                                  const void* bias, const int32_t* topk_ids, const float* topk_weights, void* y,
+                                  int64_t M, int64_t topk, int64_t E, int64_t N, int64_t K, int32_t x_dtype,
+                                  int32_t scale_dtype, int32_t dtype, int32_t transpose, int32_t x_per_slot,
+                                  void* workspace, size_t workspace_bytes, void* stream);
 
 /* The 4-bit codes q[N, K] (uint8, 0..15) unpacked on the device from wq. */
 w4a16_status w4a16_unpack_device(const int32_t* wq, uint8_t* q, int64_t N, int64_t K,

@@ -13,4 +13,6 @@ from ._binding import (  # noqa: F401
     w4a16_lora_backward, w4a16_lora_backward_workspace_size, w4a16_lora_linear, w4a16_lora_workspace_size,
     AdamwPlan, W4A16_F32, w4a16_adamw_moments, w4a16_adamw_plan, w4a16_adamw_step,
     w4a16_linear_noalloc, NOALLOC_SCRATCH_BYTES,
+    W4A16_E4M3, W4A16_E8M0, w4a16_minifloat_linear, w4a16_minifloat_linear_workspace_size, w4a16_minifloat_moe_linear,
+    w4a16_minifloat_moe_workspace_size, w4a16_minifloat_quantize, w4a16_route, w4a16_route_backward,
 )

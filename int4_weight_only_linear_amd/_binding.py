@@ -21,6 +21,9 @@ W4A16_OK = 0
 W4A16_F16 = 0
 W4A16_BF16 = 1
 W4A16_F32 = 2
+W4A16_E4M3 = 3
+W4A16_E8M0 = 4
+SCORES = {"softmax": 0, "sigmoid": 1}
 PATH_AUTO, PATH_GEMV, PATH_GEMM = 0, 1, 2
 GEMV_MAX_M = 16
 ABI_VERSION = 4
@@ -102,6 +105,15 @@ SIGNATURES["w4a16_adamw_table"] = (_c_int, [ctypes.POINTER(AdamwTensor), _c_i64,
 SIGNATURES["w4a16_adamw_step"] = (_c_int, [_vp, ctypes.POINTER(AdamwPlanInfo), _c_dbl, _c_dbl, _c_dbl, _c_dbl, _c_dbl,
                                            _c_i64, _c_dbl, ctypes.c_uint32, _vp])
 SIGNATURES["w4a16_adamw_moments"] = (_c_int, [_vp, ctypes.POINTER(AdamwPlanInfo), _vp, _vp, _vp])
+
+
+SIGNATURES["w4a16_route"] = (_c_int, [_vp] * 4 + [_c_i64] * 6 + [_c_i32, _c_i32, _c_i32, _c_dbl, _vp])
+SIGNATURES["w4a16_route_backward"] = (_c_int, [_vp] * 4 + [_c_i64] * 3 + [_c_i32, _c_i32, _c_i32, _c_dbl, _vp])
+SIGNATURES["w4a16_minifloat_quantize"] = (_c_int, [_vp, _vp, _vp, _c_i64, _c_i64, _c_i32, _vp])
+SIGNATURES["w4a16_minifloat_linear_workspace_size"] = (_c_sz, [_c_i64, _c_i64, _c_i64, _c_i32, _c_i32])
+SIGNATURES["w4a16_minifloat_linear"] = (_c_int, [_vp] * 6 + [_c_i64] * 3 + [_c_i32] * 4 + [_vp, _c_sz, _vp])
+SIGNATURES["w4a16_minifloat_moe_workspace_size"] = (_c_sz, [_c_i64] * 5 + [_c_i32] * 3)
+SIGNATURES["w4a16_minifloat_moe_linear"] = (_c_int, [_vp] * 8 + [_c_i64] * 5 + [_c_i32] * 5 + [_vp, _c_sz, _vp])
 
 
 class W4A16Error(RuntimeError):
@@ -716,3 +728,200 @@ def w4a16_adamw_moments(plan: AdamwPlan, m=None, v=None):
     _invoke(plan.device, lib.w4a16_adamw_moments, plan.table.data_ptr(), plan.info_ref, m.data_ptr(), v.data_ptr(),
             _raw_stream(plan.device))
     return m, v
+
+
+# --------------------------------------------------- routing to experts ---
+
+def _score_code(score) -> int:
+    if score not in SCORES:
+        raise ValueError(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+    return SCORES[score]
+
+
+def w4a16_route(logits, topk: int, bias=None, *, score: str = "softmax", groups: int = 1, topk_groups: int = 1,
+                group_top: int = 1, renormalize: bool = False, scale: float = 1.0, out=None):
+    """(weights float32 [M, topk], ids int32 [M, topk]) of the topk experts of each token, from
+    the router's logits [M, E] (float16, bfloat16 or float32): the largest softmax or sigmoid
+    scores, plus bias (float32 [E], moves the choice only), of the topk_groups of `groups` groups
+    of experts whose group_top (1 or 2) largest sum highest; ties to the lower index.  weights:
+    the scores without the bias, divided by their sum with renormalize, times scale.  Experts of
+    logit -inf are never chosen: id -1, weight 0 where none is left.  Not recorded by autograd:
+    a training step calls w4a16_route_backward.  out: (weights, ids) to write into."""
+    torch = _torch()
+    code = _float_code(logits, "logits")
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D [M, E]")
+    M, E = logits.shape
+    if bias is not None and (bias.dtype != torch.float32 or bias.shape != (E,)):
+        raise TypeError(f"bias must be float32 [{E}]")
+    device = logits.device
+    _require_device(logits, "logits", device)
+    if out is None:
+        weights, ids = logits.new_empty((M, topk), dtype=torch.float32), logits.new_empty((M, topk), dtype=torch.int32)
+    else:
+        weights, ids = out
+        if weights.dtype != torch.float32 or ids.dtype != torch.int32 or weights.shape != (M, topk) or ids.shape != (M, topk):
+            raise ValueError(f"out must be float32 and int32 {(M, topk)}")
+    _require_all(device, (bias, "bias"), (weights, "weights"), (ids, "ids"))
+    _invoke(device, lib.w4a16_route, logits.data_ptr(), _ptr(bias), weights.data_ptr(), ids.data_ptr(), M, E, topk, groups,
+            topk_groups, group_top, code, _score_code(score), int(bool(renormalize)), scale, _raw_stream(device))
+    return weights, ids
+
+
+def w4a16_route_backward(dweights, logits, ids, *, score: str = "softmax", renormalize: bool = False, scale: float = 1.0,
+                         out=None):
+    """dlogits [M, E], in the logits' dtype: the gradient of w4a16_route's weights for dweights
+    float32 [M, topk], with its logits and the ids that it chose.  score, renormalize and scale as
+    given there."""
+    torch = _torch()
+    code = _float_code(logits, "logits")
+    if logits.dim() != 2 or ids.dim() != 2 or ids.shape[0] != logits.shape[0]:
+        raise ValueError(f"logits must be [M, E] and ids [M, topk], got {tuple(logits.shape)} and {tuple(ids.shape)}")
+    (M, E), topk = logits.shape, ids.shape[1]
+    if ids.dtype != torch.int32 or dweights.dtype != torch.float32 or dweights.shape != ids.shape:
+        raise TypeError(f"dweights must be float32 and ids int32 {(M, topk)}")
+    device = logits.device
+    if out is None:
+        out = torch.empty_like(logits)
+    elif out.dtype != logits.dtype or out.shape != logits.shape:
+        raise ValueError(f"out must be {logits.dtype} {tuple(logits.shape)}")
+    _require_device(logits, "logits", device)
+    _require_all(device, (dweights, "dweights"), (ids, "ids"), (out, "out"))
+    _invoke(device, lib.w4a16_route_backward, dweights.data_ptr(), logits.data_ptr(), ids.data_ptr(), out.data_ptr(), M, E,
+            topk, code, _score_code(score), int(bool(renormalize)), scale, _raw_stream(device))
+    return out
+
+
+# --------------------------------------- 8-bit floating-point weights ---
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def w4a16_minifloat_quantize(x, *, out=None):
+    """(codes float8_e4m3fn [M, K'], scales float8_e8m0fnu [M, B]) of x [M, K] (float16 or
+    bfloat16): one power-of-two scale for each token and 128 k; K' is K rounded up to 128 (zeros
+    behind K), B = ceil(K / 512) * 4.  out: (codes, scales) to write into."""
+    torch = _torch()
+    code = _act_code(x)
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D [M, K]")
+    M, K = x.shape
+    device = x.device
+    _require_device(x, "x", device)
+    shapes = (M, _blocks(K) * 128), (M, (K + 511) // 512 * 4)
+    if out is None:
+        codes = x.new_empty(shapes[0], dtype=torch.float8_e4m3fn)
+        scales = x.new_empty(shapes[1], dtype=torch.float8_e8m0fnu)
+    else:
+        codes, scales = out
+        if codes.dtype != torch.float8_e4m3fn or scales.dtype != torch.float8_e8m0fnu or (codes.shape, scales.shape) != shapes:
+            raise ValueError(f"out must be float8_e4m3fn {shapes[0]} and float8_e8m0fnu {shapes[1]}")
+        _require_all(device, (codes, "codes"), (scales, "scales"))
+    _invoke(device, lib.w4a16_minifloat_quantize, x.data_ptr(), codes.data_ptr(), scales.data_ptr(), M, K, code, _raw_stream(device))
+    return codes, scales
+
+
+def _fp8_args(x, w, scales, bias, transpose, x_scales, dtype, rows, lead):
+    """Checks of both products; lead: () or (E,).  Returns (output dtype, its code, x's code,
+    the scales' code, N, K)."""
+    torch = _torch()
+    if w.dim() != 2 + len(lead) or w.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"w must be float8_e4m3fn with {2 + len(lead)} dimensions, got {w.dtype} {tuple(w.shape)}")
+    if scales.dtype not in (torch.float32, torch.float8_e8m0fnu):
+        raise TypeError(f"scales must be float32 or float8_e8m0fnu, got {scales.dtype}")
+    K, N = w.shape[-2:] if transpose else w.shape[:-3:-1]
+    if scales.shape != lead + (_blocks(w.shape[-2]), _blocks(w.shape[-1])):
+        raise ValueError(f"scales are {tuple(scales.shape)}, expected {lead + (_blocks(w.shape[-2]), _blocks(w.shape[-1]))}")
+    if x.dim() != 2 or (rows is not None and x.shape[0] != rows):
+        raise ValueError(f"x must be 2-D [{'M' if rows is None else rows}, K], got {tuple(x.shape)}")
+    if x.dtype == torch.float8_e4m3fn:
+        x_code, dtype = W4A16_E4M3, torch.bfloat16 if dtype is None else dtype
+        if dtype not in (torch.float16, torch.bfloat16):
+            raise TypeError(f"dtype must be float16 or bfloat16, got {dtype}")
+        if x.shape[1] != _blocks(K) * 128:
+            raise ValueError(f"codes are {tuple(x.shape)}, expected {_blocks(K) * 128} columns for K={K}")
+        if x_scales is None or x_scales.dtype != torch.float8_e8m0fnu or x_scales.shape != (x.shape[0], (K + 511) // 512 * 4):
+            raise ValueError(f"codes need x_scales, float8_e8m0fnu {(x.shape[0], (K + 511) // 512 * 4)}")
+    else:
+        x_code = _act_code(x)
+        if x_scales is not None or dtype not in (None, x.dtype):
+            raise ValueError("x_scales and another dtype go with float8_e4m3fn codes")
+        dtype = x.dtype
+        if x.shape[1] != K:
+            raise ValueError(f"x is {tuple(x.shape)}, expected {K} columns")
+    if bias is not None and (bias.dtype != dtype or bias.shape != lead + (N,)):
+        raise ValueError(f"bias must be {dtype} {lead + (N,)}")
+    device = x.device
+    _require_device(x, "x", device)
+    _require_all(device, (w, "w"), (scales, "scales"), (bias, "bias"), (x_scales, "x_scales"))
+    return (dtype, W4A16_F16 if dtype == torch.float16 else W4A16_BF16, x_code,
+            W4A16_F32 if scales.dtype == torch.float32 else W4A16_E8M0, N, K)
+
+
+def _fp8_out(x, out, dtype, shape):
+    if out is None:
+        return x.new_empty(shape, dtype=dtype)
+    if out.dtype != dtype or out.shape != shape:
+        raise ValueError(f"out must be {dtype} {shape}")
+    _require_device(out, "out", x.device)
+    return out
+
+
+def w4a16_minifloat_linear_workspace_size(M, N, K, x_dtype, transpose=False) -> int:
+    return int(lib.w4a16_minifloat_linear_workspace_size(M, N, K, x_dtype, int(bool(transpose))))
+
+
+def w4a16_minifloat_linear(x, w, scales, bias=None, *, transpose: bool = False, x_scales=None, dtype=None, out=None,
+                     workspace=None):
+    """y = x . (w * scales)^T (+ bias): w float8_e4m3fn [N, K] with scales float32 or float8_e8m0fnu
+    [ceil(N / 128), ceil(K / 128)]; x float16 or bfloat16 [M, K], quantised as by
+    w4a16_minifloat_quantize, or its codes with x_scales (y then of dtype, bfloat16 by default).  With
+    transpose w is [K, N], y = x . (w * scales): w4a16_minifloat_linear(dy, w, scales, transpose=True) is
+    the gradient of a layer's input.  Not recorded by autograd.  workspace: as for
+    w4a16_lora_linear, of w4a16_minifloat_linear_workspace_size."""
+    dtype, dt, x_code, s_code, N, K = _fp8_args(x, w, scales, bias, transpose, x_scales, dtype, None, ())
+    M, device = x.shape[0], x.device
+    out = _fp8_out(x, out, dtype, (M, N))
+    stream, transpose = _raw_stream(device), int(bool(transpose))
+    if workspace is None:
+        workspace = _workspace(device, stream, _size_of(device, lib.w4a16_minifloat_linear_workspace_size, M, N, K, x_code, transpose))
+    ws_ptr = None if workspace is None else workspace.data_ptr()
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _invoke(device, lib.w4a16_minifloat_linear, x.data_ptr(), _ptr(x_scales), w.data_ptr(), scales.data_ptr(), _ptr(bias),
+            out.data_ptr(), M, N, K, x_code, s_code, dt, transpose, ws_ptr, ws_bytes, stream)
+    return out
+
+
+def w4a16_minifloat_moe_workspace_size(M, topk, E, N, K, x_dtype, transpose=False, x_per_slot=False) -> int:
+    return int(lib.w4a16_minifloat_moe_workspace_size(M, topk, E, N, K, x_dtype, int(bool(transpose)), int(bool(x_per_slot))))
+
+
+def w4a16_minifloat_moe_linear(x, w, scales, topk_ids, topk_weights=None, bias=None, *, transpose: bool = False,
+                         x_per_slot: bool = False, x_scales=None, dtype=None, out=None, workspace=None):
+    """w4a16_minifloat_linear with each slot's expert: y[m * topk + j] = topk_weights[m, j] * (x_row .
+    (w_e * scales_e)^T + bias_e), e = topk_ids[m, j] (outside [0, E): a zero row), from stacks
+    w [E, N, K], scales [E, ceil(N / 128), ceil(K / 128)] and bias [E, N]; x is [M, K], or
+    [M * topk, K] with x_per_slot.  topk_ids int32 and topk_weights float32 [M, topk] as w4a16_route
+    gives them.  With transpose w is [E, K, N].  Returns [M * topk, N]."""
+    torch = _torch()
+    if topk_ids.dim() != 2 or topk_ids.dtype != torch.int32:
+        raise TypeError("topk_ids must be int32 [M, topk]")
+    M, topk = topk_ids.shape
+    E = w.shape[0]
+    dtype, dt, x_code, s_code, N, K = _fp8_args(x, w, scales, bias, transpose, x_scales, dtype, M * topk if x_per_slot else M, (E,))
+    if topk_weights is not None and (topk_weights.dtype != torch.float32 or topk_weights.shape != (M, topk)):
+        raise ValueError(f"topk_weights must be float32 {(M, topk)}")
+    device = x.device
+    _require_all(device, (topk_ids, "topk_ids"), (topk_weights, "topk_weights"))
+    out = _fp8_out(x, out, dtype, (M * topk, N))
+    stream, transpose, x_per_slot = _raw_stream(device), int(bool(transpose)), int(bool(x_per_slot))
+    if workspace is None:
+        workspace = _workspace(device, stream, _size_of(device, lib.w4a16_minifloat_moe_workspace_size, M, topk, E, N, K, x_code,
+                                                        transpose, x_per_slot))
+    ws_ptr = None if workspace is None else workspace.data_ptr()
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _invoke(device, lib.w4a16_minifloat_moe_linear, x.data_ptr(), _ptr(x_scales), w.data_ptr(), scales.data_ptr(), _ptr(bias),
+            topk_ids.data_ptr(), _ptr(topk_weights), out.data_ptr(), M, topk, E, N, K, x_code, s_code, dt, transpose, x_per_slot,
+            ws_ptr, ws_bytes, stream)
+    return out

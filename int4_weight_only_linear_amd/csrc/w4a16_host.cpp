@@ -24,6 +24,7 @@
 #include <vector>
 
 #include "w4a16_adamw.h"
+#include "w4a16_host.hpp"
 #include "w4a16_internal.h"
 #include "w4a16_lora_bwd.hpp"
 
@@ -84,76 +85,21 @@ void reload_tuning() {
 
 namespace {
 
+using w4a16::DeviceInfo;
+using w4a16::act_bytes;
+using w4a16::aligned;
+using w4a16::device_info;
+using w4a16::fail;
+using w4a16::ok;
+using w4a16::overlap;
+using w4a16::planning_cus;
+using w4a16::round256;
+
 thread_local std::string g_last_error;
-
-w4a16_status fail(w4a16_status st, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_last_error = buf;
-  return st;
-}
-
-w4a16_status ok() {
-  g_last_error.clear();
-  return W4A16_OK;
-}
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// [a, a + na) and [b, b + nb) overlap
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b || na == 0 || nb == 0) return false;
-  const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
-  return pa < pb + nb && pb < pa + na;
-}
-
-// ---- per-device properties, filled once per device ------------------------
-struct DeviceInfo {
-  bool ready = false;
-  hipError_t err = hipSuccess;
-  bool gfx950 = false;
-  int cu_count = 0;
-  char arch[64] = {0};
-  // this device's copy of `scratch` (w4a16_linear_noalloc), set up on the
-  // entry point's first call on the device
-  bool scratch_ready = false;
-  void* scratch_ptr = nullptr;
-};
 
 constexpr int kMaxDevices = 64;
 DeviceInfo g_devices[kMaxDevices];
 std::mutex g_device_mutex;
-
-w4a16_status device_info(const DeviceInfo** out) {
-  int dev = -1;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return fail(W4A16_ERR_DEVICE, "hipGetDevice failed: %s", hipGetErrorString(e));
-  if (dev < 0 || dev >= kMaxDevices) return fail(W4A16_ERR_DEVICE, "device ordinal %d out of range", dev);
-  DeviceInfo& d = g_devices[dev];
-  {
-    std::lock_guard<std::mutex> lock(g_device_mutex);
-    if (!d.ready) {
-      hipDeviceProp_t prop;
-      d.err = hipGetDeviceProperties(&prop, dev);
-      if (d.err == hipSuccess) {
-        std::snprintf(d.arch, sizeof(d.arch), "%s", prop.gcnArchName);
-        d.cu_count = prop.multiProcessorCount;
-        d.gfx950 = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 &&
-                   (prop.gcnArchName[6] == '\0' || prop.gcnArchName[6] == ':');
-      }
-      d.ready = true;
-    }
-  }
-  if (d.err != hipSuccess)
-    return fail(W4A16_ERR_DEVICE, "hipGetDeviceProperties failed: %s", hipGetErrorString(d.err));
-  if (!d.gfx950)
-    return fail(W4A16_ERR_UNSUPPORTED, "libw4a16 supports gfx950 only; this device is %s", d.arch);
-  *out = &d;
-  return W4A16_OK;
-}
 
 // ---- scratch of the allocation-free entry point ----------------------------
 // w4a16_linear_noalloc takes its split-K workspace (completion counters, then
@@ -189,8 +135,6 @@ w4a16_status scratch_for(DeviceInfo& d, int dev, hipStream_t stream, void** out)
   *out = d.scratch_ptr;
   return W4A16_OK;
 }
-
-size_t act_bytes(int64_t n) { return (size_t)n * 2; }
 
 bool valid_group(int32_t g) { return g == 32 || g == 64 || g == 128; }
 
@@ -337,20 +281,6 @@ w4a16_status linear_impl(const void* x, const int32_t* wq, const void* scales, c
   return linear_run(dev, p, gm, x, wq, scales, zp, bias, y, M, N, K, dtype, workspace, workspace_bytes, stream, nullptr);
 }
 
-// the CU count that plans are made for: the current device's, or MI355X's
-// where none is visible
-int planning_cus() {
-  int cus = kPlanningCUs, dev = -1;
-  if (hipGetDevice(&dev) == hipSuccess && dev >= 0 && dev < kMaxDevices) {
-    const DeviceInfo* d = nullptr;
-    if (device_info(&d) == W4A16_OK) cus = d->cu_count;
-    g_last_error.clear();
-  }
-  return cus;
-}
-
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-
 // ---- low-rank adapters ------------------------------------------------------
 w4a16_status check_adapters(const char* what, const void* la, const void* lb, const int32_t* ids,
                             const float* alpha, int64_t M, int64_t N, int64_t K, int64_t S, int64_t R) {
@@ -453,6 +383,63 @@ BackwardPlan plan_backward(int64_t M, int64_t N, int64_t K, int32_t group_size, 
 }
 
 }  // namespace
+
+namespace w4a16 {
+
+w4a16_status fail(w4a16_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return st;
+}
+
+w4a16_status ok() {
+  g_last_error.clear();
+  return W4A16_OK;
+}
+
+w4a16_status device_info(const DeviceInfo** out) {
+  int dev = -1;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return fail(W4A16_ERR_DEVICE, "hipGetDevice failed: %s", hipGetErrorString(e));
+  if (dev < 0 || dev >= kMaxDevices) return fail(W4A16_ERR_DEVICE, "device ordinal %d out of range", dev);
+  DeviceInfo& d = g_devices[dev];
+  {
+    std::lock_guard<std::mutex> lock(g_device_mutex);
+    if (!d.ready) {
+      hipDeviceProp_t prop;
+      d.err = (int)hipGetDeviceProperties(&prop, dev);
+      if (d.err == hipSuccess) {
+        std::snprintf(d.arch, sizeof(d.arch), "%s", prop.gcnArchName);
+        d.cu_count = prop.multiProcessorCount;
+        d.gfx950 = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 &&
+                   (prop.gcnArchName[6] == '\0' || prop.gcnArchName[6] == ':');
+      }
+      d.ready = true;
+    }
+  }
+  if (d.err != hipSuccess)
+    return fail(W4A16_ERR_DEVICE, "hipGetDeviceProperties failed: %s", hipGetErrorString((hipError_t)d.err));
+  if (!d.gfx950)
+    return fail(W4A16_ERR_UNSUPPORTED, "libw4a16 supports gfx950 only; this device is %s", d.arch);
+  *out = &d;
+  return W4A16_OK;
+}
+
+int planning_cus() {
+  int cus = kPlanningCUs, dev = -1;
+  if (hipGetDevice(&dev) == hipSuccess && dev >= 0 && dev < kMaxDevices) {
+    const DeviceInfo* d = nullptr;
+    if (device_info(&d) == W4A16_OK) cus = d->cu_count;
+    g_last_error.clear();
+  }
+  return cus;
+}
+
+}  // namespace w4a16
 
 extern "C" {
 
