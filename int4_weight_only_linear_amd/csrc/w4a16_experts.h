@@ -64,13 +64,20 @@ struct Fp8Args {
   int64_t M, N, K;         // M: tokens, or slots
   int dtype;               // of y and bias
   bool e8m0, transpose;
-  // experts (NULL ids: one layer)
-  const int32_t* ids = nullptr;    // [slots]
+  // experts (NULL start: one layer)
   const float* slot_weights = nullptr;
   const int32_t* start = nullptr;  // the order's
   const int32_t* order = nullptr;
   int E = 1, topk = 1;             // x row of slot s: s / topk, or s (topk 1)
+  float* part = nullptr;           // fp8_partial_bytes
 };
-hipError_t launch_fp8_gemm(const Fp8Args& a, hipStream_t s);
+// tiles of bm tokens (experts: slots) x bn features, and K ranges of `steps` steps
+struct Fp8Tiles {
+  int bm, bn, tiles_m, tiles_n, splits, steps;
+};
+constexpr int64_t kMaxFp8Tiles = int64_t(1) << 22;  // of a launch: its threads stay below 2^32
+Fp8Tiles plan_fp8_tiles(int64_t M, int64_t N, int64_t K, int E, bool experts, int cus);
+size_t fp8_partial_bytes(const Fp8Tiles& t, int64_t M, int64_t N);
+hipError_t launch_fp8_gemm(const Fp8Args& a, const Fp8Tiles& t, hipStream_t s);
 
 }  // namespace w4a16

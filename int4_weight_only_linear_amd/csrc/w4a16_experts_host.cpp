@@ -62,8 +62,10 @@ w4a16_status check_fp8_sizes(const char* what, int64_t rows, int64_t N, int64_t 
   if ((transpose ? N : K) % 16)
     return fail(W4A16_ERR_UNSUPPORTED, "%s: a row of the weights must hold a multiple of 16 codes, got %lld", what,
                 (long long)(transpose ? N : K));
-  if (rows > kMaxRows || N > w4a16::kMaxK || K > w4a16::kMaxK || rows * K > kMaxValues)
-    return fail(W4A16_ERR_UNSUPPORTED, "%s: too large (rows=%lld N=%lld K=%lld)", what, (long long)rows, (long long)N, (long long)K);
+  // codes of x and of one layer's (expert's) weights are addressed with 32-bit offsets
+  if (rows > kMaxRows || N > w4a16::kMaxK || K > w4a16::kMaxK || rows * fp8_columns(K) > 0xFFFFFFFFll || N * K > 0xFFFFFFFFll)
+    return fail(W4A16_ERR_UNSUPPORTED, "%s: too large: M * K and N * K must be below 4 Gi (M=%lld N=%lld K=%lld)", what, (long long)rows,
+                (long long)N, (long long)K);
   return ok();
 }
 
@@ -79,13 +81,15 @@ bool any_overlap(const Buffer (&a)[A], const Buffer (&b)[B]) {
   return false;
 }
 
-// Workspace of a product: behind the region that every entry point leaves zero,
-// the quantised x, then the experts' order.
+// A product's tiles, and its workspace: behind the region that every entry point
+// leaves zero, the quantised x, the experts' order, and the K ranges' sums.
 struct Fp8Plan {
-  size_t codes, scales, start, order, bytes;
+  w4a16::Fp8Tiles tiles;
+  size_t codes, scales, start, order, part, bytes;
 };
-Fp8Plan plan_fp8(int64_t rows, int64_t K, int32_t x_dtype, int64_t slots, int64_t E) {
+Fp8Plan plan_fp8(int64_t rows, int64_t slots, int64_t E, int64_t N, int64_t K, int32_t x_dtype, bool experts, int cus) {
   Fp8Plan p{};
+  p.tiles = w4a16::plan_fp8_tiles(slots, N, K, (int)E, experts, cus);
   size_t at = w4a16::kCounterBytes;
   auto take = [&](size_t n) {
     const size_t was = at;
@@ -95,8 +99,9 @@ Fp8Plan plan_fp8(int64_t rows, int64_t K, int32_t x_dtype, int64_t slots, int64_
   const bool quantize = x_dtype != W4A16_E4M3;
   p.codes = take(quantize ? (size_t)(rows * fp8_columns(K)) : 0);
   p.scales = take(quantize ? (size_t)(rows * fp8_scales(K)) : 0);
-  p.start = take(E ? (size_t)(E + 2) * 4 : 0);
-  p.order = take((size_t)slots * 4);
+  p.start = take(experts ? (size_t)(E + 2) * 4 : 0);
+  p.order = take(experts ? (size_t)slots * 4 : 0);
+  p.part = take(w4a16::fp8_partial_bytes(p.tiles, slots, N));
   p.bytes = at == w4a16::kCounterBytes ? 0 : at;
   return p;
 }
@@ -115,7 +120,7 @@ w4a16_status fp8_product(const char* what, const void* x, const uint8_t* x_scale
                          int64_t E, int64_t N, int64_t K, int32_t x_dtype, int32_t scale_dtype, int32_t dtype,
                          int32_t transpose, bool per_slot, bool experts, void* workspace, size_t workspace_bytes, void* stream) {
   const int64_t slots = M * topk, rows = per_slot ? slots : M;
-  w4a16_status st = check_fp8_sizes(what, slots, N, K, x_dtype, scale_dtype, dtype, transpose);
+  w4a16_status st = check_fp8_sizes(what, rows, N, K, x_dtype, scale_dtype, dtype, transpose);
   if (st != W4A16_OK) return st;
   if (M == 0) return ok();
   const bool codes = x_dtype == W4A16_E4M3;
@@ -142,7 +147,9 @@ w4a16_status fp8_product(const char* what, const void* x, const uint8_t* x_scale
   const DeviceInfo* dev = nullptr;
   st = device_info(&dev);
   if (st != W4A16_OK) return st;
-  const Fp8Plan p = plan_fp8(rows, K, x_dtype, experts ? slots : 0, experts ? E : 0);
+  const Fp8Plan p = plan_fp8(rows, slots, E, N, K, x_dtype, experts, dev->cu_count);
+  if ((int64_t)p.tiles.tiles_m * p.tiles.tiles_n * p.tiles.splits > w4a16::kMaxFp8Tiles)
+    return fail(W4A16_ERR_UNSUPPORTED, "%s: too large (M=%lld N=%lld)", what, (long long)slots, (long long)N);
   st = check_workspace(what, workspace, workspace_bytes, p.bytes);
   if (st != W4A16_OK) return st;
   const Buffer ws[] = {{workspace, p.bytes}};
@@ -180,14 +187,14 @@ w4a16_status fp8_product(const char* what, const void* x, const uint8_t* x_scale
     int32_t* const order = reinterpret_cast<int32_t*>(base + p.order);
     const hipError_t e = w4a16::launch_expert_order(ids, start, order, (int)slots, (int)E, s);
     if (e != hipSuccess) return launched(e);
-    a.ids = ids;
     a.slot_weights = slot_weights;
     a.start = start;
     a.order = order;
     a.E = (int)E;
     a.topk = per_slot ? 1 : (int)topk;
   }
-  return launched(w4a16::launch_fp8_gemm(a, s));
+  a.part = reinterpret_cast<float*>(base + p.part);
+  return launched(w4a16::launch_fp8_gemm(a, p.tiles, s));
 }
 
 }  // namespace
@@ -267,8 +274,8 @@ w4a16_status w4a16_minifloat_quantize(const void* x, void* codes, uint8_t* scale
 
 size_t w4a16_minifloat_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t x_dtype, int32_t transpose) {
   (void)transpose;
-  if (M <= 0 || N <= 0 || K <= 0 || M > kMaxRows || K > w4a16::kMaxK) return 0;
-  return plan_fp8(M, K, x_dtype, 0, 0).bytes;
+  if (M <= 0 || N <= 0 || K <= 0 || M > kMaxRows || N > w4a16::kMaxK || K > w4a16::kMaxK) return 0;
+  return plan_fp8(M, M, 1, N, K, x_dtype, false, w4a16::planning_cus()).bytes;
 }
 
 w4a16_status w4a16_minifloat_linear(const void* x, const uint8_t* x_scales, const void* w, const void* w_scales, const void* bias,
@@ -282,9 +289,9 @@ size_t w4a16_minifloat_moe_workspace_size(int64_t M, int64_t topk, int64_t E, in
                                     int32_t transpose, int32_t x_per_slot) {
   (void)transpose;
   if (M <= 0 || topk <= 0 || E <= 0 || N <= 0 || K <= 0 || M > kMaxRows || topk > kMaxRows / M || E > w4a16::kMaxExperts ||
-      K > w4a16::kMaxK)
+      N > w4a16::kMaxK || K > w4a16::kMaxK)
     return 0;
-  return plan_fp8(x_per_slot ? M * topk : M, K, x_dtype, M * topk, E).bytes;
+  return plan_fp8(x_per_slot ? M * topk : M, M * topk, E, N, K, x_dtype, true, w4a16::planning_cus()).bytes;
 }
 
 w4a16_status w4a16_minifloat_moe_linear(const void* x, const uint8_t* x_scales, const void* w, const void* w_scales,

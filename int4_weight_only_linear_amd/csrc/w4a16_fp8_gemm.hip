@@ -17,6 +17,9 @@ typedef __attribute__((address_space(3))) const u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) i32x2 lds_i32x2;
 typedef __attribute__((address_space(1))) const void global_void;
 
+typedef __attribute__((address_space(4))) const float const_float;
+typedef __attribute__((address_space(4))) const uint32_t const_u32;
+
 struct Fp8Params {
   const uint8_t* x;
   const uint8_t* xs;
@@ -24,29 +27,35 @@ struct Fp8Params {
   const void* ws;
   const uint16_t* bias;
   uint16_t* y;
+  float* part;        // K split: [splits][M][N] sums, or NULL
   const float* slot_weights;
-  const int32_t* start;
+  const int32_t* start;  // experts: the order, or NULL (one layer)
   const int32_t* order;
   int M, N, K, E, topk;
-  int steps;          // blocks of 128 k
   int xrow, xsrow;    // bytes of a row of codes and of scales
   int wsrow;          // scales in a row of ws
   int64_t wexpert, wsexpert;  // codes and scales of an expert
   int tiles_m, tiles_n;
+  int steps;          // of a K range
   bool wide;          // y's rows take 8-byte stores
+  bool f16;
 };
 
-// A[i][k] . B[k][j] over 128 k, accumulated in fp32, with one power of two for
-// each row of A and column of B (byte 0 of a scale, its exponent + 127).  Lane l
-// holds row (column) l % 16 of the operands, both with the same 32 of the 128 k,
-// and D[i][j] for j = l % 16, i = 4 (l / 16) + r.
+// A[i][k] . B[k][j] over 64 k, accumulated in fp32, with one power of two for
+// each row of A and column of B and 32 k (byte 0 of a scale, its exponent +
+// 127).  Lane l holds row (column) l % 32 of the operands, k = 32 (l / 32) ..,
+// and D[i][j] for j = l % 32, i = 8 (r / 4) + 4 (l / 32) + r % 4.
 // The unit adds the products of eight consecutive k of a lane at the largest
 // one's exponent and drops what lies more than 13 bits below it; those sums, and
-// the accumulator, are added in fp32.  (Measured; the older 16x16x32 form does
-// the same at half the rate.)
-__device__ __forceinline__ f32x4 mfma_fp8(i32x8 a, i32x8 b, f32x4 c, int sa, int sb) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, sa, 0, sb);
+// the accumulator, are added in fp32.  (Measured; the older forms without scales
+// do the same at half the rate.)  With this shape scaling costs nothing beside
+// the products: 4.93 PFLOP/s alone, where 16 x 16 x 128 reaches 4.5.
+__device__ __forceinline__ f32x16 mfma_fp8(i32x8 a, i32x8 b, f32x16 c, int sa, int sb) {
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, sa, 0, sb);
 }
+
+// s_waitcnt vmcnt(n) alone
+constexpr int wait_vm(int n) { return 0x0F70 | (n & 15) | ((n >> 4) << 14); }
 
 // The bucket of the order (expert e, or E for the slots that name none) in
 // which tile t of BM slots lies, its first place there and how many it has.
@@ -77,23 +86,45 @@ __device__ __forceinline__ bool find_tile(const int32_t* start, int E, int t, in
   return false;
 }
 
-template <int DT, bool E8M0, bool TR, bool EXPERTS, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void fp8_gemm_kernel(Fp8Params p) {
-  constexpr int WAVES = (BM / WM) * (BN / WN), TM = WM / 16, TN = WN / 16;
-  static_assert(128 % WN == 0 && BM % WM == 0 && BN % 128 == 0, "a wave's features share a scale");
-  constexpr int XP = BM / 8, WP = BN / 8;  // KiB of a step's x and w
-  __shared__ __attribute__((aligned(1024))) unsigned char sx0[XP * 1024], sx1[XP * 1024];
-  __shared__ __attribute__((aligned(1024))) unsigned char sw0[WP * 1024], sw1[WP * 1024];
-  lds_u8 *const lx0 = (lds_u8*)sx0, *const lx1 = (lds_u8*)sx1, *const lw0 = (lds_u8*)sw0, *const lw1 = (lds_u8*)sw1;
+// A workgroup owns BM tokens (or slots of one expert) x BN features and one K
+// range, in steps of BK bytes of a row; its waves own WM x WN of it each.  A
+// step's rows of x and w go straight from memory to LDS, NS - 1 steps ahead; the
+// one barrier of a step says that everyone's pieces of it have landed and that
+// the stage before it may be written over.
+template <bool E8M0, bool TR, int BM, int BN, int WM, int WN, int BK, int NS, int WAVES_PER_SIMD>
+__global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp8_tile_kernel(Fp8Params p) {
+  constexpr int WAVES = (BM / WM) * (BN / WN), TM = WM / 32, TN = WN / 32, KK = BK / 64;
+  constexpr int GROUP = 512 / BK;  // steps of a word of x's scales
+  static_assert(128 % WN == 0 && BN % 128 == 0, "a wave's features share a scale");
+  static_assert(GROUP % NS == 0, "a step's stage is known at compile time");
+  constexpr int XP = BM * BK / 1024, WP = BN * BK / 1024;  // KiB of a stage
+  constexpr int XQ = XP / WAVES, WQ = WP / WAVES, LOADS = XQ + WQ;
+  static_assert(XP % WAVES == 0 && WP % WAVES == 0, "every wave issues as many loads");
+  // an array for each stage, so that the compiler knows that loads into one do not touch the others
+  __shared__ __attribute__((aligned(1024))) unsigned char st0[(XP + WP) * 1024], st1[(XP + WP) * 1024];
+  __shared__ __attribute__((aligned(1024))) unsigned char st2[NS > 2 ? (XP + WP) * 1024 : 16], st3[NS > 3 ? (XP + WP) * 1024 : 16];
+  auto stage_at = [&](auto I) {
+    constexpr int i = decltype(I)::value % NS;
+    if constexpr (i == 0) return (lds_u8*)st0;
+    else if constexpr (i == 1) return (lds_u8*)st1;
+    else if constexpr (i == 2) return (lds_u8*)st2;
+    else return (lds_u8*)st3;
+  };
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = lane & 15, quad = lane >> 4;
+  const int col = lane & 31, half = lane >> 5;
+  const bool experts = p.start != nullptr;
 
-  const int unit = xcd_unit(blockIdx.x, gridDim.x);
-  const int tm = EXPERTS ? unit / p.tiles_n : unit % p.tiles_m, tn = EXPERTS ? unit % p.tiles_n : unit / p.tiles_m;
+  // one layer: the tiles of one K range and feature block are neighbours, so that an XCD reads its weights
+  // once; experts: the tiles of a few slots are, which share their expert's weights and rows of x
+  const int tiles = p.tiles_m * p.tiles_n;
+  int unit = xcd_unit(blockIdx.x, gridDim.x);
+  const int split = unit / tiles;
+  unit -= split * tiles;
+  const int tm = experts ? unit / p.tiles_n : unit % p.tiles_m, tn = experts ? unit % p.tiles_n : unit / p.tiles_m;
   const int n0 = tn * BN;
   int expert = 0, first = tm * BM, count = min(BM, p.M - first);
-  if constexpr (EXPERTS) {
+  if (experts) {
     if (!find_tile(p.start, p.E, tm, BM, expert, first, count)) return;
     if (expert == p.E) {  // no expert: zeros
       for (int i = threadIdx.x; i < count * BN; i += 64 * WAVES) {
@@ -103,195 +134,316 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN)) void fp8_gemm_kernel(Fp
       return;
     }
   }
-  // the slot (dense: token) of place r of the tile; places past the last repeat it
+  // the slot (one layer: token) of place r of the tile, and its row of x; places past the last repeat it
   auto slot_of = [&](int r) {
     const int at = first + min(r, count - 1);
-    return EXPERTS ? p.order[at] : at;
+    return experts ? p.order[at] : at;
   };
+  auto row_of = [&](int r) {
+    const int s = slot_of(r);
+    return (uint32_t)(experts ? s / p.topk : s);
+  };
+  const int k_steps = (p.K + BK - 1) / BK, s_begin = split * p.steps, steps = min(p.steps, k_steps - s_begin);
 
-  // ---- staging: piece q is 1 KiB, 16 bytes a lane, written in lane order
-  // x, and w not transposed: 16 rows, half q % 2 of a step's 128 k; a wave's
-  // operand of the same rows is then its lanes' own 16 bytes of both halves
-  constexpr int XQ = (XP + WAVES - 1) / WAVES, WQ = (WP + WAVES - 1) / WAVES;
-  const uint8_t* xsrc[XQ];
-  const uint8_t* wsrc[WQ];
+  // ---- staging: a load fills 1 KiB, 16 bytes a lane in lane order: whole pieces of rows, since lanes that
+  // take turns over rows get a quarter of the rate.  The 16-byte piece c of a row lies at c ^ turn(row),
+  // so that an operand's reads, 32 rows of one piece, meet all banks.
+  constexpr int PL = BK / 16;  // pieces of a row
+  auto turn = [](int row) { return BK == 128 ? (row >> 1) & 7 : (row >> 2) & 3; };
+  uint32_t xoff[XQ], woff[WQ];
   const uint8_t* const we = p.w + expert * p.wexpert;
+  auto piece_row = [&](int i) { return (wave + WAVES * i) * (64 / PL) + lane / PL; };
 #pragma unroll
-  for (int i = 0; i < XQ; ++i) {
-    const int q = min(wave + WAVES * i, XP - 1);
-    xsrc[i] = p.x + (size_t)(slot_of(16 * (q >> 1) + col) / (EXPERTS ? p.topk : 1)) * p.xrow + 64 * (q & 1) + 16 * quad;
-  }
-  // transposed: a piece is 1024 / BN rows of k; the 16-byte piece c of row r
-  // lies at c ^ (r % 8), so that eight rows of one c are in different banks
-  constexpr int RL = BN / 16;  // lanes of a row
+  for (int i = 0; i < XQ; ++i)
+    xoff[i] = row_of(piece_row(i)) * (uint32_t)p.xrow + 16 * ((lane % PL) ^ turn(piece_row(i)));
+  // transposed: rows of k, of BN features; the piece c of row r lies at c ^ (r % 8)
+  constexpr int RL = BN / 16;
+  auto k_row = [&](int i) { return (wave + WAVES * i) * (64 / RL) + lane / RL; };
 #pragma unroll
   for (int i = 0; i < WQ; ++i) {
-    const int q = min(wave + WAVES * i, WP - 1);
-    if constexpr (TR) {
-      const int r = q * (64 / RL) + lane / RL, c = (lane % RL) ^ (r & 7);
-      wsrc[i] = we + min(n0 + 16 * c, p.N - 16);
-    } else {
-      wsrc[i] = we + (size_t)min(n0 + 16 * (q >> 1) + col, p.N - 1) * p.K;
-    }
+    if constexpr (TR)
+      woff[i] = (uint32_t)k_row(i) * (uint32_t)p.N + min(n0 + 16 * ((lane % RL) ^ (k_row(i) & 7)), p.N - 16);
+    else
+      woff[i] = (uint32_t)min(n0 + piece_row(i), p.N - 1) * (uint32_t)p.K + 16 * ((lane % PL) ^ turn(piece_row(i)));
   }
-  auto stage = [&](int s, lds_u8* lx, lds_u8* lw) {
+  auto stage = [&](int at, auto I) {
+    lds_u8 *const dx = stage_at(I) + wave * 1024, *const dw = stage_at(I) + (XP + wave) * 1024;
+    const int s = s_begin + min(at, steps - 1);  // (past the last step: loaded again, never used)
+    const uint8_t* const xb = p.x + (size_t)s * BK;
+    const uint8_t* const wb = we + (size_t)s * (TR ? (size_t)p.N * BK : (size_t)BK);
+    const int left = p.K - s * BK;
 #pragma unroll
-    for (int i = 0; i < XQ; ++i)
-      if (XP % WAVES == 0 || wave + WAVES * i < XP)
-        __builtin_amdgcn_global_load_lds((global_void*)(xsrc[i] + (size_t)s * 128), lx + (wave + WAVES * i) * 1024, 16, 0, 0);
+    for (int i = 0; i < XQ; ++i) {
+      uint32_t off = xoff[i];
+      asm("" : "+v"(off));  // (32-bit offsets stay offsets: as pointers they would take twice the registers)
+      __builtin_amdgcn_global_load_lds((global_void*)(xb + off), dx + WAVES * i * 1024, 16, 0, 0);
+    }
 #pragma unroll
-    for (int i = 0; i < WQ; ++i)
-      if (WP % WAVES == 0 || wave + WAVES * i < WP) {
-        const int q = wave + WAVES * i;
+    for (int i = 0; i < WQ; ++i) {
+      uint32_t off = woff[i];
+      asm("" : "+v"(off));
+      if (left < BK) {
         // past the last k: bytes of the same feature, which meet zero codes of x
-        const uint8_t* src;
-        if constexpr (TR) src = wsrc[i] + (size_t)min(s * 128 + q * (64 / RL) + lane / RL, p.K - 1) * p.N;
-        else src = wsrc[i] + min(s * 128 + 64 * (q & 1) + 16 * quad, p.K - 16);
-        __builtin_amdgcn_global_load_lds((global_void*)src, lw + q * 1024, 16, 0, 0);
+        if constexpr (TR) off -= (uint32_t)max(k_row(i) - (left - 1), 0) * (uint32_t)p.N;
+        else off -= (uint32_t)max(16 * ((lane % PL) ^ turn(piece_row(i))) - (left - 16), 0);
       }
+      __builtin_amdgcn_global_load_lds((global_void*)(wb + off), dw + WAVES * i * 1024, 16, 0, 0);
+    }
   };
 
-  // ---- scales
+  // ---- operands of 64 k
   const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
-  const uint8_t* xssrc[TM];
+  const uint32_t at0 = col * BK + (((2 * half) ^ turn(col)) << 4);
+  auto operand = [&](const lds_u8* rows, int kk) {
+    const uint32_t at = at0 ^ (64 * kk);
+    const u32x4 u = *(lds_u32x4*)(rows + at), v = *(lds_u32x4*)(rows + (at ^ 16));
+    return i32x8{(int)u[0], (int)u[1], (int)u[2], (int)u[3], (int)v[0], (int)v[1], (int)v[2], (int)v[3]};
+  };
+  // transposed: sixteen lanes read eight rows of k of sixteen features, and each gets a feature's eight
+  const int sub = (lane & 15) >> 1;
+  const uint32_t trow = (32 * half + sub) * BN, tcol = ((wn / 16 + ((lane >> 4) & 1)) ^ sub) * 16 + 8 * (lane & 1);
+  auto operand_t = [&](lds_u8* rows, int n, int kk) {
+    i32x8 a;
 #pragma unroll
-  for (int t = 0; t < TM; ++t)
-    xssrc[t] = p.xs + (size_t)(slot_of(wm + 16 * t + col) / (EXPERTS ? p.topk : 1)) * p.xsrow;
-  const int nb = min(n0 + wn, p.N - 1) >> 7;
-  auto scale_at = [&](int s) {
-    return expert * p.wsexpert + (TR ? (int64_t)s * p.wsrow + nb : (int64_t)nb * p.wsrow + s);
+    for (int j = 0; j < 4; ++j) {
+      const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(rows + trow + (64 * kk + 8 * j) * BN + (tcol ^ (32 * n))));
+      a[2 * j] = v[0], a[2 * j + 1] = v[1];
+    }
+    return a;
   };
 
-  f32x4 acc[TN][TM];
+  // ---- scales.  x's, a word of four blocks for each token, go to the matrix unit as they are.  So does the
+  // power of two of an fp32 scale of w; its rest, 1 <= |unit| < 2, is the unit that the accumulators are kept
+  // in, changed by one product for each of them and block, half of what adding scaled sums takes.
+  uint32_t xsoff[TM], xs[TM], xs_next[TM];
+  const uint8_t* const xs_base = p.xs + s_begin * BK / 128;
+  const int xs_last = p.xsrow - 4 - s_begin * BK / 128;
+#pragma unroll
+  for (int t = 0; t < TM; ++t) {
+    xsoff[t] = row_of(wm + 32 * t + col) * (uint32_t)p.xsrow;
+    xs_next[t] = *reinterpret_cast<const uint32_t*>(xs_base + xsoff[t]);
+  }
+  const int nb = __builtin_amdgcn_readfirstlane(min(n0 + wn, p.N - 1) >> 7);
+  auto scale_at = [&](int s) {  // of local step s, at most the last
+    const int b = (s_begin + min(s, steps - 1)) * BK / 128;
+    return expert * p.wsexpert + (TR ? (int64_t)b * p.wsrow + nb : (int64_t)nb * p.wsrow + b);
+  };
+  float unit_of = 1.f, ratio = 1.f, ws_next = 0.f;
+  if constexpr (!E8M0) ws_next = *(const_float*)(static_cast<const float*>(p.ws) + scale_at(0));
+  int sa = 127;
+  auto next_scale = [&](int s) {
+    if constexpr (E8M0) {
+      // (a word at a time: it holds the byte, so it lies in the same allocation)
+      const uintptr_t at = reinterpret_cast<uintptr_t>(static_cast<const uint8_t*>(p.ws) + scale_at(s));
+      sa = (int)(*(const_u32*)(at & ~(uintptr_t)3) >> (8 * (at & 3))) & 255;
+    } else {
+      const uint32_t bits = __builtin_bit_cast(uint32_t, ws_next), field = (bits >> 23) & 255;
+      float u = __builtin_bit_cast(float, (bits & 0x807FFFFFu) | 0x3F800000u);
+      sa = (int)field;
+      if (field == 255) u = ws_next, sa = 127;      // infinite or NaN
+      if (field == 0) u = ws_next * 0x1p126f, sa = 1;  // below the normal numbers
+      if (u == 0.f) {
+        ratio = 1.f, sa = -1;  // (the block adds nothing)
+      } else {
+        ratio = unit_of / u, unit_of = u;
+      }
+    }
+  };
+
+  f32x16 acc[TN][TM];
 #pragma unroll
   for (int n = 0; n < TN; ++n)
 #pragma unroll
-    for (int t = 0; t < TM; ++t) acc[n][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < TM; ++t) acc[n][t] = f32x16{};
 
-  uint32_t xs[TM];
-  auto compute = [&](int s, const lds_u8* lx, const lds_u8* lw) {
-    if ((s & 3) == 0) {
-#pragma unroll
-      for (int t = 0; t < TM; ++t) xs[t] = *reinterpret_cast<const uint32_t*>(xssrc[t] + s);
-    }
-    int sb[TM];
-#pragma unroll
-    for (int t = 0; t < TM; ++t) sb[t] = (int)(xs[t] >> (8 * (s & 3)));
-    float wsf = 1.f;
-    int sa = 127;
-    if constexpr (E8M0) sa = static_cast<const uint8_t*>(p.ws)[scale_at(s)];
-    else wsf = static_cast<const float*>(p.ws)[scale_at(s)];
-    i32x8 b[TM];
-    auto operand = [&](const lds_u8* base) {
-      const u32x4 lo = *(lds_u32x4*)(base + 16 * lane), hi = *(lds_u32x4*)(base + 1024 + 16 * lane);
-      return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-    };
-#pragma unroll
-    for (int t = 0; t < TM; ++t) b[t] = operand(lx + (wm / 16 + t) * 2048);
-#pragma unroll
-    for (int n = 0; n < TN; ++n) {
-      i32x8 a;
-      if constexpr (TR) {
-        // rows 64 (j / 2) + 16 quad + 8 (j % 2) + 0..7 of column wn + 16 n + col: sixteen lanes read eight
-        // rows of sixteen columns, and each gets a column
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 64 * (j >> 1) + 16 * quad + 8 * (j & 1) + (col >> 1), c = (wn / 16 + n) ^ (r & 7);
-          const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_i32x2*)(const_cast<lds_u8*>(lw) + r * BN + 16 * c + 8 * (col & 1)));
-          a[2 * j] = v[0], a[2 * j + 1] = v[1];
-        }
-      } else {
-        a = operand(lw + (wn / 16 + n) * 2048);
-      }
+  auto step = [&](int s0, auto I, auto TAIL) {
+    constexpr int i = decltype(I)::value, block = i * BK / 128;
+    constexpr bool tail = decltype(TAIL)::value, first_of_block = i * BK % 128 == 0;
+    lds_u8 *const cx = stage_at(I), *const cw = cx + XP * 1024;
+    const int s = s0 + i;
+    // this wave's pieces of the step have landed when at most the loads issued after them are under way: NS - 2
+    // later stages, and x's scales where they were issued behind the step's own stage
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(wait_vm((NS - 2) * LOADS + (i > 0 && i < NS ? TM : 0)));
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+    stage(s + NS - 1, std::integral_constant<int, i + NS - 1>{});
+    if constexpr (first_of_block) next_scale(s);
+    if constexpr (!E8M0 && (i + 1) * BK % 128 == 0) ws_next = *(const_float*)(static_cast<const float*>(p.ws) + scale_at(s + 1));
+    if constexpr (i == 0) {
 #pragma unroll
       for (int t = 0; t < TM; ++t) {
-        if constexpr (E8M0) {
-          acc[n][t] = mfma_fp8(a, b[t], acc[n][t], sa, sb[t]);
-        } else {
-          const f32x4 v = mfma_fp8(a, b[t], f32x4{0.f, 0.f, 0.f, 0.f}, 127, sb[t]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[n][t][e] = __builtin_fmaf(v[e], wsf, acc[n][t][e]);
-        }
+        xs[t] = xs_next[t];
+        uint32_t off = xsoff[t];
+        asm("" : "+v"(off));
+        xs_next[t] = *reinterpret_cast<const uint32_t*>(xs_base + min((s + GROUP) * BK / 128, xs_last) + off);
       }
     }
+    if (tail && s >= steps) return;
+    if constexpr (E8M0) asm("" : "+s"(sa));  // (a branch that may be taken keeps the steps apart: gathered, they spill)
+    if (sa < 0) return;
+    int sb[TM];
+#pragma unroll
+    for (int t = 0; t < TM; ++t) sb[t] = (int)(xs[t] >> (8 * block));
+    i32x8 a[TN][KK], b[TM][KK];
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) a[n][kk] = TR ? operand_t(cw, n, kk) : operand(cw + (wn + 32 * n) * BK, kk);
+#pragma unroll
+    for (int t = 0; t < TM; ++t)
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) b[t][kk] = operand(cx + (wm + 32 * t) * BK, kk);
+    static_for<0, TM * TN>([&](auto J) {
+      constexpr int t = decltype(J)::value / TN, n = decltype(J)::value % TN;
+      f32x16& c = acc[n][t];
+      if constexpr (!E8M0 && first_of_block) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) c[e] *= ratio;
+      }
+#pragma unroll
+      for (int kk = 0; kk < KK; ++kk) c = mfma_fp8(a[n][kk], b[t][kk], c, sa, sb[t]);
+      __builtin_amdgcn_sched_barrier(0);  // (one tile's products beside the next one's change of unit)
+    });
   };
-  auto barrier = [&] {
-    __builtin_amdgcn_s_waitcnt(0);  // own pieces have landed, own reads are done
-    __syncthreads();
-  };
+  static_for<0, NS - 1>([&](auto I) { stage(decltype(I)::value, I); });
+  int s0 = 0;
+  for (; s0 + GROUP <= steps; s0 += GROUP) static_for<0, GROUP>([&](auto I) { step(s0, I, std::false_type{}); });
+  if (s0 < steps) static_for<0, GROUP>([&](auto I) { step(s0, I, std::true_type{}); });
+  __builtin_amdgcn_s_waitcnt(0);  // (no load may land in LDS after the workgroup's end)
 
-  stage(0, lx0, lw0);
-  for (int s = 0; s < p.steps; s += 2) {
-    barrier();
-    if (s + 1 < p.steps) stage(s + 1, lx1, lw1);
-    compute(s, lx0, lw0);
-    if (s + 1 < p.steps) {
-      barrier();
-      if (s + 2 < p.steps) stage(s + 2, lx0, lw0);
-      compute(s + 1, lx1, lw1);
+  auto store = [&](auto type) {
+    constexpr int DT = decltype(type)::value;
+#pragma unroll
+    for (int t = 0; t < TM; ++t) {
+      const int r = wm + 32 * t + col;
+      if (r >= count) continue;
+      const int slot = slot_of(r);
+      const float k = experts && p.slot_weights ? p.slot_weights[slot] : 1.f;
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int f = n0 + wn + 32 * n + 8 * g + 4 * half;
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = E8M0 ? acc[n][t][4 * g + e] : acc[n][t][4 * g + e] * unit_of;
+          if (p.part) {
+            float* const out = p.part + ((size_t)split * p.M + slot) * p.N + f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (f + e < p.N) out[e] = v[e];
+            continue;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (p.bias && f + e < p.N) v[e] += act_to_f32<DT>(p.bias[(size_t)expert * p.N + f + e]);
+            v[e] *= k;
+          }
+          uint16_t* const out = p.y + (size_t)slot * p.N + f;
+          if (p.wide && f < p.N) {
+            *reinterpret_cast<u32x2*>(out) = u32x2{f32x2_to_act_pair<DT>(v[0], v[1]), f32x2_to_act_pair<DT>(v[2], v[3])};
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (f + e < p.N) out[e] = f32_to_act<DT>(v[e]);
+          }
+        }
     }
-  }
+  };
+  if (p.f16) store(std::integral_constant<int, DT_F16>{});
+  else store(std::integral_constant<int, DT_BF16>{});
+}
 
+// y = the K ranges' sums in range order, and the bias
+template <int DT>
+__global__ __launch_bounds__(256) void fp8_sum_kernel(const float* __restrict__ part, const uint16_t* __restrict__ bias,
+                                                      uint16_t* __restrict__ y, int64_t values, int N, int splits) {
+  for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < values; i += (int64_t)gridDim.x * 1024) {
+    if (N % 4 == 0) {
+      f32x4 v = {0.f, 0.f, 0.f, 0.f};
+      for (int s0 = 0; s0 < splits; s0 += 4) {  // four at a time, so that their loads overlap
+        f32x4 q[4];
 #pragma unroll
-  for (int t = 0; t < TM; ++t) {
-    const int r = wm + 16 * t + col;
-    if (r >= count) continue;
-    const int slot = slot_of(r);
-    const float k = EXPERTS && p.slot_weights ? p.slot_weights[slot] : 1.f;
+        for (int k = 0; k < 4; ++k) q[k] = *reinterpret_cast<const f32x4*>(part + (int64_t)min(s0 + k, splits - 1) * values + i);
 #pragma unroll
-    for (int n = 0; n < TN; ++n) {
-      const int f = n0 + wn + 16 * n + 4 * quad;
-      float v[4];
+        for (int k = 0; k < 4; ++k)
+          if (s0 + k < splits) v += q[k];
+      }
+      const int n = (int)(i % N);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[e] = acc[n][t][e];
-        if (p.bias && f + e < p.N) v[e] += act_to_f32<DT>(p.bias[(size_t)expert * p.N + f + e]);
-        v[e] *= k;
+        if (bias) v[e] += act_to_f32<DT>(bias[n + e]);
+        y[i + e] = f32_to_act<DT>(v[e]);
       }
-      uint16_t* const out = p.y + (size_t)slot * p.N + f;
-      if (p.wide && f < p.N) {
-        *reinterpret_cast<u32x2*>(out) = u32x2{f32x2_to_act_pair<DT>(v[0], v[1]), f32x2_to_act_pair<DT>(v[2], v[3])};
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (f + e < p.N) out[e] = f32_to_act<DT>(v[e]);
+    } else {
+      for (int64_t j = i; j < min(i + 4, values); ++j) {
+        float v = 0.f;
+        for (int s = 0; s < splits; ++s) v += part[s * values + j];
+        if (bias) v += act_to_f32<DT>(bias[j % N]);
+        y[j] = f32_to_act<DT>(v);
       }
     }
   }
 }
 
-template <int DT, bool E8M0, bool TR, bool EXPERTS, int BM, int BN, int WM, int WN>
-hipError_t launch_tile(const Fp8Args& a, Fp8Params p, hipStream_t s) {
-  p.tiles_n = (int)((a.N + BN - 1) / BN);
-  // every bucket of the order may end with a part of a tile
-  p.tiles_m = EXPERTS ? (int)(a.M / BM + std::min<int64_t>(a.M, a.E + 1)) : (int)((a.M + BM - 1) / BM);
-  const int64_t units = (int64_t)p.tiles_m * p.tiles_n;
-  if (units > INT32_MAX) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((fp8_gemm_kernel<DT, E8M0, TR, EXPERTS, BM, BN, WM, WN>), dim3((unsigned)units),
+template <bool E8M0, bool TR, int BM, int BN, int WM, int WN, int BK, int NS, int WPS>
+void launch_tile(const Fp8Params& p, int64_t units, hipStream_t s) {
+  hipLaunchKernelGGL((fp8_tile_kernel<E8M0, TR, BM, BN, WM, WN, BK, NS, WPS>), dim3((unsigned)units),
                      dim3(64 * (BM / WM) * (BN / WN)), 0, s, p);
-  return hipGetLastError();
 }
 
-template <int DT, bool E8M0, bool TR, bool EXPERTS>
-hipError_t launch_shape(const Fp8Args& a, const Fp8Params& p, hipStream_t s) {
-  const int64_t tokens = EXPERTS ? a.M / a.E : a.M;  // of a product
-  if (tokens <= 16) return launch_tile<DT, E8M0, TR, EXPERTS, 16, 128, 16, 32>(a, p, s);
-  return launch_tile<DT, E8M0, TR, EXPERTS, 128, 128, 64, 64>(a, p, s);
+template <bool E8M0, bool TR>
+void launch_kind(const Fp8Params& p, int bm, int64_t units, hipStream_t s) {
+  switch (bm) {
+    case 256: return launch_tile<E8M0, TR, 256, 256, 128, 64, 64, 4, 2>(p, units, s);
+    case 128: return launch_tile<E8M0, TR, 128, 128, 64, 64, 128, 2, 2>(p, units, s);
+    case 96: return launch_tile<E8M0, TR, 96, 128, 96, 32, 128, 2, 2>(p, units, s);
+    case 64: return launch_tile<E8M0, TR, 64, 128, 64, 32, 128, 2, 3>(p, units, s);
+    default: return launch_tile<E8M0, TR, 32, 128, 32, 32, 128, 2, 3>(p, units, s);
+  }
 }
 
-template <int DT, bool E8M0, bool TR>
-hipError_t launch_kind(const Fp8Args& a, const Fp8Params& p, hipStream_t s) {
-  return a.ids ? launch_shape<DT, E8M0, TR, true>(a, p, s) : launch_shape<DT, E8M0, TR, false>(a, p, s);
-}
-template <int DT>
-hipError_t launch_type(const Fp8Args& a, const Fp8Params& p, hipStream_t s) {
-  if (a.e8m0) return a.transpose ? launch_kind<DT, true, true>(a, p, s) : launch_kind<DT, true, false>(a, p, s);
-  return a.transpose ? launch_kind<DT, false, true>(a, p, s) : launch_kind<DT, false, false>(a, p, s);
-}
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-hipError_t launch_fp8_gemm(const Fp8Args& a, hipStream_t s) {
+Fp8Tiles plan_fp8_tiles(int64_t M, int64_t N, int64_t K, int E, bool experts, int cus) {
+  Fp8Tiles t{};
+  const int64_t tokens = experts ? ceil_div(M, E) : M;  // of a product, about
+  if (tokens <= 32) t.bm = 32;
+  else if (tokens <= 64) t.bm = 64;
+  else if (tokens <= 96 && !experts) t.bm = 96;
+  else t.bm = 128;
+  // 256 x 256 where that still gives every CU a tile in full rounds
+  if (t.bm == 128) {
+    const int64_t wide = ceil_div(tokens, 256) * ceil_div(N, 256) * (experts ? E : 1);
+    if (tokens > 128 && wide >= 2 * cus) t.bm = 256;
+  }
+  t.bn = t.bm == 256 ? 256 : 128;
+  t.tiles_n = (int)ceil_div(N, t.bn);
+  // every bucket of the order may end with a part of a tile
+  t.tiles_m = (int)(experts ? M / t.bm + std::min<int64_t>(M, E + 1) : ceil_div(M, t.bm));
+  const int bk = t.bm == 256 ? 64 : 128, steps = (int)ceil_div(K, bk);
+  t.splits = 1;
+  t.steps = steps;
+  const int64_t tiles = (int64_t)t.tiles_m * t.tiles_n;
+  if (!experts && t.bm < 256) {
+    // fewer tiles than two a CU: ranges of K, of four blocks or more
+    const int64_t want = std::min<int64_t>(2 * cus / std::max<int64_t>(tiles, 1), steps / 4);
+    if (want > 1) {
+      t.steps = (int)ceil_div(ceil_div(steps, want), 4) * 4;  // (whole words of x's scales)
+      t.splits = (int)ceil_div(steps, t.steps);
+    }
+  }
+  return t;
+}
+
+size_t fp8_partial_bytes(const Fp8Tiles& t, int64_t M, int64_t N) {
+  return t.splits > 1 ? (size_t)t.splits * (size_t)M * (size_t)N * sizeof(float) : 0;
+}
+
+hipError_t launch_fp8_gemm(const Fp8Args& a, const Fp8Tiles& t, hipStream_t s) {
   Fp8Params p{};
   p.x = a.x;
   p.xs = a.xs;
@@ -299,6 +451,7 @@ hipError_t launch_fp8_gemm(const Fp8Args& a, hipStream_t s) {
   p.ws = a.ws;
   p.bias = static_cast<const uint16_t*>(a.bias);
   p.y = static_cast<uint16_t*>(a.y);
+  p.part = t.splits > 1 ? a.part : nullptr;
   p.slot_weights = a.slot_weights;
   p.start = a.start;
   p.order = a.order;
@@ -307,15 +460,30 @@ hipError_t launch_fp8_gemm(const Fp8Args& a, hipStream_t s) {
   p.K = (int)a.K;
   p.E = a.E;
   p.topk = a.topk;
-  p.steps = (int)(fp8_columns(a.K) / kFp8Block);
   p.xrow = (int)fp8_columns(a.K);
   p.xsrow = (int)fp8_scales(a.K);
-  const int64_t nb = (a.N + kFp8Block - 1) / kFp8Block;
-  p.wsrow = a.transpose ? (int)nb : p.steps;
+  const int64_t nb = ceil_div(a.N, kFp8Block), kb = ceil_div(a.K, kFp8Block);
+  p.wsrow = (int)(a.transpose ? nb : kb);
   p.wexpert = a.N * a.K;
-  p.wsexpert = nb * p.steps;
+  p.wsexpert = nb * kb;
+  p.tiles_m = t.tiles_m;
+  p.tiles_n = t.tiles_n;
+  p.steps = t.steps;
   p.wide = a.N % 4 == 0 && (reinterpret_cast<uintptr_t>(a.y) & 7) == 0;
-  return a.dtype == DT_F16 ? launch_type<DT_F16>(a, p, s) : launch_type<DT_BF16>(a, p, s);
+  p.f16 = a.dtype == DT_F16;
+  const int64_t units = (int64_t)t.tiles_m * t.tiles_n * t.splits;
+  if (units > kMaxFp8Tiles) return hipErrorInvalidValue;
+  if (a.e8m0) a.transpose ? launch_kind<true, true>(p, t.bm, units, s) : launch_kind<true, false>(p, t.bm, units, s);
+  else a.transpose ? launch_kind<false, true>(p, t.bm, units, s) : launch_kind<false, false>(p, t.bm, units, s);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && t.splits > 1) {
+    const int64_t values = a.M * a.N;
+    const dim3 grid((unsigned)std::min<int64_t>(ceil_div(values, 1024), 4096));
+    if (p.f16) hipLaunchKernelGGL((fp8_sum_kernel<DT_F16>), grid, dim3(256), 0, s, a.part, p.bias, p.y, values, p.N, t.splits);
+    else hipLaunchKernelGGL((fp8_sum_kernel<DT_BF16>), grid, dim3(256), 0, s, a.part, p.bias, p.y, values, p.N, t.splits);
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 }  // namespace w4a16
