@@ -80,4 +80,11 @@ Fp8Tiles plan_fp8_tiles(int64_t M, int64_t N, int64_t K, int E, bool experts, in
 size_t fp8_partial_bytes(const Fp8Tiles& t, int64_t M, int64_t N);
 hipError_t launch_fp8_gemm(const Fp8Args& a, const Fp8Tiles& t, hipStream_t s);
 
+// Few tokens (experts: few slots for each): whether they are decoded, one
+// launch that takes x as it is where its rows are 16-byte aligned (x_dtype
+// DT_F16 or DT_BF16; a.x is not read), or codes (any other), and the slots' ids
+// without an order.
+bool fp8_decodes(int64_t M, int64_t N, int64_t K, int E, bool experts, bool transpose);
+hipError_t launch_fp8_decode(const Fp8Args& a, const void* x, int x_dtype, const int32_t* ids, hipStream_t s);
+
 }  // namespace w4a16

@@ -84,12 +84,15 @@ bool any_overlap(const Buffer (&a)[A], const Buffer (&b)[B]) {
 // A product's tiles, and its workspace: behind the region that every entry point
 // leaves zero, the quantised x, the experts' order, and the K ranges' sums.
 struct Fp8Plan {
+  bool decode;
   w4a16::Fp8Tiles tiles;
   size_t codes, scales, start, order, part, bytes;
 };
-Fp8Plan plan_fp8(int64_t rows, int64_t slots, int64_t E, int64_t N, int64_t K, int32_t x_dtype, bool experts, int cus) {
+Fp8Plan plan_fp8(int64_t rows, int64_t slots, int64_t E, int64_t N, int64_t K, int32_t x_dtype, bool transpose, bool experts,
+                 int cus) {
   Fp8Plan p{};
-  p.tiles = w4a16::plan_fp8_tiles(slots, N, K, (int)E, experts, cus);
+  p.decode = w4a16::fp8_decodes(slots, N, K, (int)E, experts, transpose);
+  if (!p.decode) p.tiles = w4a16::plan_fp8_tiles(slots, N, K, (int)E, experts, cus);
   size_t at = w4a16::kCounterBytes;
   auto take = [&](size_t n) {
     const size_t was = at;
@@ -99,8 +102,8 @@ Fp8Plan plan_fp8(int64_t rows, int64_t slots, int64_t E, int64_t N, int64_t K, i
   const bool quantize = x_dtype != W4A16_E4M3;
   p.codes = take(quantize ? (size_t)(rows * fp8_columns(K)) : 0);
   p.scales = take(quantize ? (size_t)(rows * fp8_scales(K)) : 0);
-  p.start = take(experts ? (size_t)(E + 2) * 4 : 0);
-  p.order = take(experts ? (size_t)slots * 4 : 0);
+  p.start = take(experts && !p.decode ? (size_t)(E + 2) * 4 : 0);
+  p.order = take(experts && !p.decode ? (size_t)slots * 4 : 0);
   p.part = take(w4a16::fp8_partial_bytes(p.tiles, slots, N));
   p.bytes = at == w4a16::kCounterBytes ? 0 : at;
   return p;
@@ -147,7 +150,7 @@ w4a16_status fp8_product(const char* what, const void* x, const uint8_t* x_scale
   const DeviceInfo* dev = nullptr;
   st = device_info(&dev);
   if (st != W4A16_OK) return st;
-  const Fp8Plan p = plan_fp8(rows, slots, E, N, K, x_dtype, experts, dev->cu_count);
+  const Fp8Plan p = plan_fp8(rows, slots, E, N, K, x_dtype, transpose != 0, experts, dev->cu_count);
   if ((int64_t)p.tiles.tiles_m * p.tiles.tiles_n * p.tiles.splits > w4a16::kMaxFp8Tiles)
     return fail(W4A16_ERR_UNSUPPORTED, "%s: too large (M=%lld N=%lld)", what, (long long)slots, (long long)N);
   st = check_workspace(what, workspace, workspace_bytes, p.bytes);
@@ -164,7 +167,9 @@ w4a16_status fp8_product(const char* what, const void* x, const uint8_t* x_scale
   w4a16::Fp8Args a{};
   a.x = static_cast<const uint8_t*>(x);
   a.xs = x_scales;
-  if (!codes) {
+  // (rows of K % 16 == 0 values: aligned where the first one is)
+  const bool in_place = p.decode && !codes && aligned(x, 16);
+  if (!codes && !in_place) {
     uint8_t* const q = reinterpret_cast<uint8_t*>(base + p.codes);
     uint8_t* const qs = reinterpret_cast<uint8_t*>(base + p.scales);
     const hipError_t e = w4a16::launch_fp8_quantize(x, q, qs, rows, K, dtype, s);
@@ -182,16 +187,18 @@ w4a16_status fp8_product(const char* what, const void* x, const uint8_t* x_scale
   a.dtype = dtype;
   a.e8m0 = scale_dtype == W4A16_E8M0;
   a.transpose = transpose != 0;
+  a.slot_weights = slot_weights;
+  a.E = (int)E;
+  a.topk = per_slot ? 1 : (int)topk;
+  if (p.decode)
+    return launched(w4a16::launch_fp8_decode(a, in_place ? x : a.x, in_place ? dtype : (int)W4A16_E4M3, ids, s));
   if (experts) {
     int32_t* const start = reinterpret_cast<int32_t*>(base + p.start);
     int32_t* const order = reinterpret_cast<int32_t*>(base + p.order);
     const hipError_t e = w4a16::launch_expert_order(ids, start, order, (int)slots, (int)E, s);
     if (e != hipSuccess) return launched(e);
-    a.slot_weights = slot_weights;
     a.start = start;
     a.order = order;
-    a.E = (int)E;
-    a.topk = per_slot ? 1 : (int)topk;
   }
   a.part = reinterpret_cast<float*>(base + p.part);
   return launched(w4a16::launch_fp8_gemm(a, p.tiles, s));
@@ -273,9 +280,8 @@ w4a16_status w4a16_minifloat_quantize(const void* x, void* codes, uint8_t* scale
 }
 
 size_t w4a16_minifloat_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t x_dtype, int32_t transpose) {
-  (void)transpose;
   if (M <= 0 || N <= 0 || K <= 0 || M > kMaxRows || N > w4a16::kMaxK || K > w4a16::kMaxK) return 0;
-  return plan_fp8(M, M, 1, N, K, x_dtype, false, w4a16::planning_cus()).bytes;
+  return plan_fp8(M, M, 1, N, K, x_dtype, transpose != 0, false, w4a16::planning_cus()).bytes;
 }
 
 w4a16_status w4a16_minifloat_linear(const void* x, const uint8_t* x_scales, const void* w, const void* w_scales, const void* bias,
@@ -287,11 +293,10 @@ w4a16_status w4a16_minifloat_linear(const void* x, const uint8_t* x_scales, cons
 
 size_t w4a16_minifloat_moe_workspace_size(int64_t M, int64_t topk, int64_t E, int64_t N, int64_t K, int32_t x_dtype,
                                     int32_t transpose, int32_t x_per_slot) {
-  (void)transpose;
   if (M <= 0 || topk <= 0 || E <= 0 || N <= 0 || K <= 0 || M > kMaxRows || topk > kMaxRows / M || E > w4a16::kMaxExperts ||
       N > w4a16::kMaxK || K > w4a16::kMaxK)
     return 0;
-  return plan_fp8(x_per_slot ? M * topk : M, M * topk, E, N, K, x_dtype, true, w4a16::planning_cus()).bytes;
+  return plan_fp8(x_per_slot ? M * topk : M, M * topk, E, N, K, x_dtype, transpose != 0, true, w4a16::planning_cus()).bytes;
 }
 
 w4a16_status w4a16_minifloat_moe_linear(const void* x, const uint8_t* x_scales, const void* w, const void* w_scales,

@@ -87,29 +87,20 @@ __device__ __forceinline__ bool find_tile(const int32_t* start, int E, int t, in
 }
 
 // A workgroup owns BM tokens (or slots of one expert) x BN features and one K
-// range, in steps of BK bytes of a row; its waves own WM x WN of it each.  A
-// step's rows of x and w go straight from memory to LDS, NS - 1 steps ahead; the
+// range, in steps of a block of 128 k; its waves own WM x WN of it each.  A
+// step's rows of x and w go straight from memory to LDS, one step ahead; the
 // one barrier of a step says that everyone's pieces of it have landed and that
 // the stage before it may be written over.
-template <bool E8M0, bool TR, int BM, int BN, int WM, int WN, int BK, int NS, int WAVES_PER_SIMD>
+template <bool E8M0, bool TR, int BM, int BN, int WM, int WN, int WAVES_PER_SIMD>
 __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp8_tile_kernel(Fp8Params p) {
-  constexpr int WAVES = (BM / WM) * (BN / WN), TM = WM / 32, TN = WN / 32, KK = BK / 64;
-  constexpr int GROUP = 512 / BK;  // steps of a word of x's scales
+  constexpr int WAVES = (BM / WM) * (BN / WN), TM = WM / 32, TN = WN / 32, BK = kFp8Block;
   static_assert(128 % WN == 0 && BN % 128 == 0, "a wave's features share a scale");
-  static_assert(GROUP % NS == 0, "a step's stage is known at compile time");
   constexpr int XP = BM * BK / 1024, WP = BN * BK / 1024;  // KiB of a stage
-  constexpr int XQ = XP / WAVES, WQ = WP / WAVES, LOADS = XQ + WQ;
+  constexpr int XQ = XP / WAVES, WQ = WP / WAVES;
   static_assert(XP % WAVES == 0 && WP % WAVES == 0, "every wave issues as many loads");
-  // an array for each stage, so that the compiler knows that loads into one do not touch the others
+  // an array for each stage, so that the compiler knows that loads into one do not touch the other
   __shared__ __attribute__((aligned(1024))) unsigned char st0[(XP + WP) * 1024], st1[(XP + WP) * 1024];
-  __shared__ __attribute__((aligned(1024))) unsigned char st2[NS > 2 ? (XP + WP) * 1024 : 16], st3[NS > 3 ? (XP + WP) * 1024 : 16];
-  auto stage_at = [&](auto I) {
-    constexpr int i = decltype(I)::value % NS;
-    if constexpr (i == 0) return (lds_u8*)st0;
-    else if constexpr (i == 1) return (lds_u8*)st1;
-    else if constexpr (i == 2) return (lds_u8*)st2;
-    else return (lds_u8*)st3;
-  };
+  auto stage_at = [&](auto I) { return decltype(I)::value % 2 ? (lds_u8*)st1 : (lds_u8*)st0; };
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 31, half = lane >> 5;
@@ -149,7 +140,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
   // take turns over rows get a quarter of the rate.  The 16-byte piece c of a row lies at c ^ turn(row),
   // so that an operand's reads, 32 rows of one piece, meet all banks.
   constexpr int PL = BK / 16;  // pieces of a row
-  auto turn = [](int row) { return BK == 128 ? (row >> 1) & 7 : (row >> 2) & 3; };
+  auto turn = [](int row) { return (row >> 1) & 7; };
   uint32_t xoff[XQ], woff[WQ];
   const uint8_t* const we = p.w + expert * p.wexpert;
   auto piece_row = [&](int i) { return (wave + WAVES * i) * (64 / PL) + lane / PL; };
@@ -191,7 +182,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
     }
   };
 
-  // ---- operands of 64 k
+  // ---- operands, of 64 k each
   const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
   const uint32_t at0 = col * BK + (((2 * half) ^ turn(col)) << 4);
   auto operand = [&](const lds_u8* rows, int kk) {
@@ -216,8 +207,8 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
   // power of two of an fp32 scale of w; its rest, 1 <= |unit| < 2, is the unit that the accumulators are kept
   // in, changed by one product for each of them and block, half of what adding scaled sums takes.
   uint32_t xsoff[TM], xs[TM], xs_next[TM];
-  const uint8_t* const xs_base = p.xs + s_begin * BK / 128;
-  const int xs_last = p.xsrow - 4 - s_begin * BK / 128;
+  const uint8_t* const xs_base = p.xs + s_begin;
+  const int xs_last = p.xsrow - 4 - s_begin;
 #pragma unroll
   for (int t = 0; t < TM; ++t) {
     xsoff[t] = row_of(wm + 32 * t + col) * (uint32_t)p.xsrow;
@@ -225,7 +216,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
   }
   const int nb = __builtin_amdgcn_readfirstlane(min(n0 + wn, p.N - 1) >> 7);
   auto scale_at = [&](int s) {  // of local step s, at most the last
-    const int b = (s_begin + min(s, steps - 1)) * BK / 128;
+    const int b = s_begin + min(s, steps - 1);
     return expert * p.wsexpert + (TR ? (int64_t)b * p.wsrow + nb : (int64_t)nb * p.wsrow + b);
   };
   float unit_of = 1.f, ratio = 1.f, ws_next = 0.f;
@@ -257,26 +248,25 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
     for (int t = 0; t < TM; ++t) acc[n][t] = f32x16{};
 
   auto step = [&](int s0, auto I, auto TAIL) {
-    constexpr int i = decltype(I)::value, block = i * BK / 128;
-    constexpr bool tail = decltype(TAIL)::value, first_of_block = i * BK % 128 == 0;
+    constexpr int i = decltype(I)::value;
+    constexpr bool tail = decltype(TAIL)::value;
     lds_u8 *const cx = stage_at(I), *const cw = cx + XP * 1024;
     const int s = s0 + i;
-    // this wave's pieces of the step have landed when at most the loads issued after them are under way: NS - 2
-    // later stages, and x's scales where they were issued behind the step's own stage
+    // this wave's pieces of the step have landed when at most x's scales, issued behind them, are under way
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(wait_vm((NS - 2) * LOADS + (i > 0 && i < NS ? TM : 0)));
+    __builtin_amdgcn_s_waitcnt(wait_vm(i == 1 ? TM : 0));
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    stage(s + NS - 1, std::integral_constant<int, i + NS - 1>{});
-    if constexpr (first_of_block) next_scale(s);
-    if constexpr (!E8M0 && (i + 1) * BK % 128 == 0) ws_next = *(const_float*)(static_cast<const float*>(p.ws) + scale_at(s + 1));
+    stage(s + 1, std::integral_constant<int, i + 1>{});
+    next_scale(s);
+    if constexpr (!E8M0) ws_next = *(const_float*)(static_cast<const float*>(p.ws) + scale_at(s + 1));
     if constexpr (i == 0) {
 #pragma unroll
       for (int t = 0; t < TM; ++t) {
         xs[t] = xs_next[t];
         uint32_t off = xsoff[t];
         asm("" : "+v"(off));
-        xs_next[t] = *reinterpret_cast<const uint32_t*>(xs_base + min((s + GROUP) * BK / 128, xs_last) + off);
+        xs_next[t] = *reinterpret_cast<const uint32_t*>(xs_base + min(s + 4, xs_last) + off);
       }
     }
     if (tail && s >= steps) return;
@@ -284,32 +274,32 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
     if (sa < 0) return;
     int sb[TM];
 #pragma unroll
-    for (int t = 0; t < TM; ++t) sb[t] = (int)(xs[t] >> (8 * block));
-    i32x8 a[TN][KK], b[TM][KK];
+    for (int t = 0; t < TM; ++t) sb[t] = (int)(xs[t] >> (8 * i));
+    i32x8 a[TN][2], b[TM][2];
 #pragma unroll
     for (int n = 0; n < TN; ++n)
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) a[n][kk] = TR ? operand_t(cw, n, kk) : operand(cw + (wn + 32 * n) * BK, kk);
+      for (int kk = 0; kk < 2; ++kk) a[n][kk] = TR ? operand_t(cw, n, kk) : operand(cw + (wn + 32 * n) * BK, kk);
 #pragma unroll
     for (int t = 0; t < TM; ++t)
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) b[t][kk] = operand(cx + (wm + 32 * t) * BK, kk);
+      for (int kk = 0; kk < 2; ++kk) b[t][kk] = operand(cx + (wm + 32 * t) * BK, kk);
     static_for<0, TM * TN>([&](auto J) {
       constexpr int t = decltype(J)::value / TN, n = decltype(J)::value % TN;
       f32x16& c = acc[n][t];
-      if constexpr (!E8M0 && first_of_block) {
+      if constexpr (!E8M0) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) c[e] *= ratio;
       }
 #pragma unroll
-      for (int kk = 0; kk < KK; ++kk) c = mfma_fp8(a[n][kk], b[t][kk], c, sa, sb[t]);
+      for (int kk = 0; kk < 2; ++kk) c = mfma_fp8(a[n][kk], b[t][kk], c, sa, sb[t]);
       __builtin_amdgcn_sched_barrier(0);  // (one tile's products beside the next one's change of unit)
     });
   };
-  static_for<0, NS - 1>([&](auto I) { stage(decltype(I)::value, I); });
-  int s0 = 0;
-  for (; s0 + GROUP <= steps; s0 += GROUP) static_for<0, GROUP>([&](auto I) { step(s0, I, std::false_type{}); });
-  if (s0 < steps) static_for<0, GROUP>([&](auto I) { step(s0, I, std::true_type{}); });
+  stage(0, std::integral_constant<int, 0>{});
+  int s0 = 0;  // four steps to a word of x's scales
+  for (; s0 + 4 <= steps; s0 += 4) static_for<0, 4>([&](auto I) { step(s0, I, std::false_type{}); });
+  if (s0 < steps) static_for<0, 4>([&](auto I) { step(s0, I, std::true_type{}); });
   __builtin_amdgcn_s_waitcnt(0);  // (no load may land in LDS after the workgroup's end)
 
   auto store = [&](auto type) {
@@ -387,20 +377,19 @@ __global__ __launch_bounds__(256) void fp8_sum_kernel(const float* __restrict__ 
   }
 }
 
-template <bool E8M0, bool TR, int BM, int BN, int WM, int WN, int BK, int NS, int WPS>
+template <bool E8M0, bool TR, int BM, int BN, int WM, int WN, int WPS>
 void launch_tile(const Fp8Params& p, int64_t units, hipStream_t s) {
-  hipLaunchKernelGGL((fp8_tile_kernel<E8M0, TR, BM, BN, WM, WN, BK, NS, WPS>), dim3((unsigned)units),
+  hipLaunchKernelGGL((fp8_tile_kernel<E8M0, TR, BM, BN, WM, WN, WPS>), dim3((unsigned)units),
                      dim3(64 * (BM / WM) * (BN / WN)), 0, s, p);
 }
 
 template <bool E8M0, bool TR>
 void launch_kind(const Fp8Params& p, int bm, int64_t units, hipStream_t s) {
   switch (bm) {
-    case 256: return launch_tile<E8M0, TR, 256, 256, 128, 64, 64, 4, 2>(p, units, s);
-    case 128: return launch_tile<E8M0, TR, 128, 128, 64, 64, 128, 2, 2>(p, units, s);
-    case 96: return launch_tile<E8M0, TR, 96, 128, 96, 32, 128, 2, 2>(p, units, s);
-    case 64: return launch_tile<E8M0, TR, 64, 128, 64, 32, 128, 2, 3>(p, units, s);
-    default: return launch_tile<E8M0, TR, 32, 128, 32, 32, 128, 2, 3>(p, units, s);
+    case 128: return launch_tile<E8M0, TR, 128, 128, 64, 64, 2>(p, units, s);
+    case 96: return launch_tile<E8M0, TR, 96, 128, 96, 32, 2>(p, units, s);
+    case 64: return launch_tile<E8M0, TR, 64, 128, 64, 32, 3>(p, units, s);
+    default: return launch_tile<E8M0, TR, 32, 128, 32, 32, 3>(p, units, s);
   }
 }
 
@@ -415,20 +404,15 @@ Fp8Tiles plan_fp8_tiles(int64_t M, int64_t N, int64_t K, int E, bool experts, in
   else if (tokens <= 64) t.bm = 64;
   else if (tokens <= 96 && !experts) t.bm = 96;
   else t.bm = 128;
-  // 256 x 256 where that still gives every CU a tile in full rounds
-  if (t.bm == 128) {
-    const int64_t wide = ceil_div(tokens, 256) * ceil_div(N, 256) * (experts ? E : 1);
-    if (tokens > 128 && wide >= 2 * cus) t.bm = 256;
-  }
-  t.bn = t.bm == 256 ? 256 : 128;
+  t.bn = 128;
   t.tiles_n = (int)ceil_div(N, t.bn);
   // every bucket of the order may end with a part of a tile
   t.tiles_m = (int)(experts ? M / t.bm + std::min<int64_t>(M, E + 1) : ceil_div(M, t.bm));
-  const int bk = t.bm == 256 ? 64 : 128, steps = (int)ceil_div(K, bk);
+  const int steps = (int)ceil_div(K, kFp8Block);
   t.splits = 1;
   t.steps = steps;
   const int64_t tiles = (int64_t)t.tiles_m * t.tiles_n;
-  if (!experts && t.bm < 256) {
+  if (!experts) {
     // fewer tiles than two a CU: ranges of K, of four blocks or more
     const int64_t want = std::min<int64_t>(2 * cus / std::max<int64_t>(tiles, 1), steps / 4);
     if (want > 1) {

@@ -257,7 +257,7 @@ MOE = [
     (5, 2, 3, 144, 128, "one", False), (16, 4, 64, 64, 512, "skewed", True), (40, 2, 8, 200, 256, "some", False),
     (33, 6, 60, 32, 144, "all", True), (150, 1, 2, 130, 272, "skewed", False), (70, 8, 9, 64, 128, "skewed", False),
     (9, 3, 5, 80, 256, "none", True), (300, 2, 3, 144, 160, "some", True), (64, 8, 4, 32, 128, "all", False), (3, 5, 2, 48, 128, "all", True),
-    (130, 3, 1000, 16, 64, "all", False),
+    (130, 3, 1000, 16, 64, "all", False), (100, 8, 256, 32, 128, "skewed", False), (120, 8, 240, 40, 272, "some", True),
 ]
 
 
