@@ -71,20 +71,21 @@ struct Fp8Args {
   int E = 1, topk = 1;             // x row of slot s: s / topk, or s (topk 1)
   float* part = nullptr;           // fp8_partial_bytes
 };
-// tiles of bm tokens (experts: slots) x bn features, and K ranges of `steps` steps
+// tiles of bm tokens (experts: slots) x 128 features, and K ranges of `steps` blocks
 struct Fp8Tiles {
-  int bm, bn, tiles_m, tiles_n, splits, steps;
+  int bm, tiles_m, tiles_n, splits, steps;
 };
 constexpr int64_t kMaxFp8Tiles = int64_t(1) << 22;  // of a launch: its threads stay below 2^32
 Fp8Tiles plan_fp8_tiles(int64_t M, int64_t N, int64_t K, int E, bool experts, int cus);
 size_t fp8_partial_bytes(const Fp8Tiles& t, int64_t M, int64_t N);
 hipError_t launch_fp8_gemm(const Fp8Args& a, const Fp8Tiles& t, hipStream_t s);
 
-// Few tokens (experts: few slots for each): whether they are decoded, one
-// launch that takes x as it is where its rows are 16-byte aligned (x_dtype
-// DT_F16 or DT_BF16; a.x is not read), or codes (any other), and the slots' ids
-// without an order.
+// Few tokens (experts: few slots for each): whether they are decoded, by one
+// launch that takes the slots' ids without an order and either x as it is
+// (x_dtype DT_F16 or DT_BF16, 16-byte aligned, where fp8_decode_quantizes says
+// so: two workgroups' tokens fit a CU's LDS) or codes (any other).
 bool fp8_decodes(int64_t M, int64_t N, int64_t K, int E, bool experts, bool transpose);
+bool fp8_decode_quantizes(int64_t M, int64_t K);
 hipError_t launch_fp8_decode(const Fp8Args& a, const void* x, int x_dtype, const int32_t* ids, hipStream_t s);
 
 }  // namespace w4a16

@@ -168,7 +168,7 @@ w4a16_status fp8_product(const char* what, const void* x, const uint8_t* x_scale
   a.x = static_cast<const uint8_t*>(x);
   a.xs = x_scales;
   // (rows of K % 16 == 0 values: aligned where the first one is)
-  const bool in_place = p.decode && !codes && aligned(x, 16);
+  const bool in_place = p.decode && !codes && aligned(x, 16) && w4a16::fp8_decode_quantizes(slots, K);
   if (!codes && !in_place) {
     uint8_t* const q = reinterpret_cast<uint8_t*>(base + p.codes);
     uint8_t* const qs = reinterpret_cast<uint8_t*>(base + p.scales);

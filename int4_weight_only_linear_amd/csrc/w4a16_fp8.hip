@@ -29,21 +29,10 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint16_t* __restric
     for (int i = 0; i < 8; ++i)
       if (k + i < K) v[i / 2] |= (uint32_t)x[m * K + k + i] << (16 * (i & 1));
   }
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) top = max(top, max(finite_bits<DT>(v[i]), finite_bits<DT>(v[i] >> 16)));
-#pragma unroll
-  for (int o = 8; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
-  const int e = block_exponent<DT>(top);
-  const float scale = exp2_int(e);
-  short2_t lo = {0, 0}, hi = {0, 0};
-  lo = codes_of<DT, false>(lo, v[0], scale);
-  lo = codes_of<DT, true>(lo, v[1], scale);
-  hi = codes_of<DT, false>(hi, v[2], scale);
-  hi = codes_of<DT, true>(hi, v[3], scale);
+  int e;
+  const u32x2 c = quantize_run<DT>(v, e);
   if (k < columns)
-    *reinterpret_cast<u32x2*>(codes + m * columns + k) =
-        u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+    *reinterpret_cast<u32x2*>(codes + m * columns + k) = c;
   const int e1 = __shfl(e, 16), e2 = __shfl(e, 32), e3 = __shfl(e, 48);
   if (lane == 0)
     scales[run] = (uint32_t)(e + 127) | (uint32_t)(e1 + 127) << 8 | (uint32_t)(e2 + 127) << 16 | (uint32_t)(e3 + 127) << 24;

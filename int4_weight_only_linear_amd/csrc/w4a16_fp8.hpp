@@ -39,4 +39,23 @@ __device__ __forceinline__ short2_t codes_of(short2_t old, uint32_t pair, float 
     return __builtin_amdgcn_cvt_scalef32_pk_fp8_bf16(old, __builtin_bit_cast(bf16x2_t, pair), scale, HIGH);
 }
 
+// Codes of a lane's eight values, sixteen lanes holding a block of 128, and the
+// exponent of their scale.
+template <int DT>
+__device__ __forceinline__ u32x2 quantize_run(u32x4 v, int& e) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) top = max(top, max(finite_bits<DT>(v[i]), finite_bits<DT>(v[i] >> 16)));
+#pragma unroll
+  for (int o = 8; o; o >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, o));
+  e = block_exponent<DT>(top);
+  const float scale = exp2_int(e);
+  short2_t lo = {0, 0}, hi = {0, 0};
+  lo = codes_of<DT, false>(lo, v[0], scale);
+  lo = codes_of<DT, true>(lo, v[1], scale);
+  hi = codes_of<DT, false>(hi, v[2], scale);
+  hi = codes_of<DT, true>(hi, v[3], scale);
+  return u32x2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
+}
+
 }  // namespace w4a16

@@ -24,6 +24,7 @@ struct DecodeParams {
   const float* slot_weights;
   int M, N, K, E, topk;
   int blocks, xsrow, wsrow;
+  int tokens;          // whose codes LDS holds: min(16, M)
   int64_t wexpert, wsexpert;
   bool f16;
 };
@@ -34,30 +35,33 @@ __device__ __forceinline__ f32x4 mfma16(i32x8 a, i32x8 b, f32x4 c, int sa, int s
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 0, 0, 0, sa, 0, sb);
 }
 
-// A workgroup owns sixteen features and up to sixteen tokens; its waves take the
-// blocks of 128 k in turn, load weights and tokens straight into the operands
-// (lane l: row l % 16, k 16 (l / 16) .. of either half of the block), quantise
-// the tokens there, and are added through LDS in wave order.
+// A workgroup owns 16 TN features and up to sixteen tokens.  Its waves take the
+// blocks of 128 k in turn, weights straight into the operands (lane l: row
+// l % 16, k 16 (l / 16) .. of either half of the block), DEPTH blocks ahead.
+// Meanwhile, before the first product, they quantise the tokens into LDS (rows
+// 16 bytes longer than their codes, so that sixteen rows' pieces of one k meet
+// all banks); given codes are read where they are.  The waves' sums are added
+// through LDS in wave order.
 // Experts: workgroup (slot, features) does the products of its slot's expert for
 // that slot and the next ones of the same expert, sixteen together, where an
 // even sixteen of them come before it, and nothing otherwise; so an expert's
 // weights are read once for sixteen of its slots, without a list made before.
-template <int DT, bool E8M0>
+template <int DT, bool E8M0, int TN>
 __global__ __launch_bounds__(1024) void fp8_decode_kernel(DecodeParams p) {
-  extern __shared__ __attribute__((aligned(16))) float red[];
-  constexpr int DEPTH = DT == DT_CODES ? 4 : 2;  // blocks loaded before they are multiplied
+  extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+  constexpr int DEPTH = 4, BN = 16 * TN;
   const int lane = threadIdx.x & 63, waves = blockDim.x >> 6;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
-  const int tiles = (p.N + 15) >> 4;
-  const int n0 = (p.ids ? (int)(blockIdx.x % tiles) : (int)blockIdx.x) * 16;
+  const int tiles = (p.N + BN - 1) / BN;
+  const int n0 = (p.ids ? (int)(blockIdx.x % tiles) : (int)blockIdx.x) * BN;
 
   int expert = 0, slot = col, count = p.M;
   if (p.ids) {
     const int s = blockIdx.x / tiles;
     expert = p.ids[s];
     if (expert < 0 || expert >= p.E) {  // no expert: zeros
-      if (threadIdx.x < 16 && n0 + threadIdx.x < p.N) p.y[(size_t)s * p.N + n0 + threadIdx.x] = 0;
+      if (threadIdx.x < BN && n0 + threadIdx.x < p.N) p.y[(size_t)s * p.N + n0 + threadIdx.x] = 0;
       return;
     }
     // lane j < 16: the j-th slot of this expert from s on
@@ -80,91 +84,97 @@ __global__ __launch_bounds__(1024) void fp8_decode_kernel(DecodeParams p) {
     }
     if (before & 15) return;
   }
-  const bool live = col < count;
-  const int64_t row = live ? (p.ids ? slot / p.topk : slot) : 0;
-  const uint8_t* const wrow = p.w + expert * p.wexpert + (int64_t)min(n0 + col, p.N - 1) * p.K;
+  const uint8_t* const we = p.w + expert * p.wexpert;
   const int64_t ws0 = expert * p.wsexpert + (int64_t)(n0 >> 7) * p.wsrow;
-
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-  for (int b0 = wave; b0 < p.blocks; b0 += waves * DEPTH) {
-    u32x4 wv[DEPTH][2], xv[DEPTH][DT == DT_CODES ? 2 : 4];
-    int xsb[DEPTH];
-    float wsf[DEPTH];
-    int wsb[DEPTH];
+  uint32_t wrow[TN];
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-      const int b = min(b0 + waves * d, p.blocks - 1);
+  for (int t = 0; t < TN; ++t) wrow[t] = (uint32_t)min(n0 + 16 * t + col, p.N - 1) * (uint32_t)p.K;
+  u32x4 wv[DEPTH][TN][2];
+  auto load = [&](int b, u32x4 (&v)[TN][2]) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // past the last k: bytes of the same row, which meet zero codes
-        const int k = 128 * b + 64 * h + 16 * quad;
-        wv[d][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(wrow + min(k, p.K - 16)));
-        if constexpr (DT == DT_CODES) {
-          xv[d][h] = u32x4{0u, 0u, 0u, 0u};
-          if (live) xv[d][h] = *reinterpret_cast<const u32x4*>(static_cast<const uint8_t*>(p.x) + row * (128 * p.blocks) + k);
-        } else {
+    for (int h = 0; h < 2; ++h) {
+      // past the last k: bytes of the same row, which meet zero codes
+      const uint32_t at = min(128 * b + 64 * h + 16 * quad, p.K - 16);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            xv[d][2 * h + q] = u32x4{0u, 0u, 0u, 0u};
-            if (live && k < p.K)
-              xv[d][2 * h + q] = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.x) + row * p.K + k + 8 * q);
-          }
-        }
-      }
-      if constexpr (DT == DT_CODES) xsb[d] = p.xs[row * p.xsrow + b];
-      if constexpr (E8M0) wsb[d] = static_cast<const uint8_t*>(p.ws)[ws0 + b];
-      else wsf[d] = static_cast<const float*>(p.ws)[ws0 + b];
+      for (int t = 0; t < TN; ++t) v[t][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(we + wrow[t] + at));
     }
+  };
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d)
+    if (wave + waves * d < p.blocks) load(wave + waves * d, wv[d]);
+
+  const bool live = col < count;
+  const int stride = 128 * p.blocks + 16;
+  unsigned char* const lds_scales = lds + p.tokens * stride;  // [tokens][blocks]
+  if constexpr (DT != DT_CODES) {
+    // runs of 512 values, eight a lane, as the quantisation kernel takes them
+    const int per_row = (p.blocks + 3) >> 2;
+    for (int run = wave; run < count * per_row; run += waves) {
+      const int t = run / per_row, k = 512 * (run - t * per_row) + 8 * lane;
+      const int64_t row = p.ids ? __builtin_amdgcn_readlane(slot, t) / p.topk : t;
+      u32x4 v = {0u, 0u, 0u, 0u};
+      if (k < p.K) v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(p.x) + row * p.K + k);
+      int e;
+      const u32x2 c = quantize_run<DT>(v, e);
+      if (k < 128 * p.blocks) {
+        *reinterpret_cast<u32x2*>(lds + t * stride + k) = c;
+        if (col == 0) lds_scales[t * p.blocks + (k >> 7)] = (unsigned char)(e + 127);
+      }
+    }
+    __syncthreads();
+  }
+  const int64_t row = DT == DT_CODES && live ? (p.ids ? slot / p.topk : slot) : 0;
+  f32x4 acc[TN];
+#pragma unroll
+  for (int t = 0; t < TN; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int b0 = wave; b0 < p.blocks; b0 += waves * DEPTH) {
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
-      if (b0 + waves * d >= p.blocks) break;
-      i32x8 xo;
-      if constexpr (DT == DT_CODES) {
+      const int b = b0 + waves * d;
+      if (b >= p.blocks) break;
+      u32x4 x0 = {0u, 0u, 0u, 0u}, x1 = x0;
+      int xsb = 127;
+      if (live) {
+        const unsigned char* const src = (DT == DT_CODES ? static_cast<const unsigned char*>(p.x) + row * (128 * p.blocks)
+                                                         : lds + col * stride) + 128 * b + 16 * quad;
+        x0 = *reinterpret_cast<const u32x4*>(src), x1 = *reinterpret_cast<const u32x4*>(src + 64);
+        xsb = DT == DT_CODES ? p.xs[row * p.xsrow + b] : lds_scales[col * p.blocks + b];
+      }
+      const i32x8 xo = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
+      float wsf = 1.f;
+      int wsb = 127;
+      if constexpr (E8M0) wsb = static_cast<const uint8_t*>(p.ws)[ws0 + b];
+      else wsf = static_cast<const float*>(p.ws)[ws0 + b];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) xo[i] = (int)xv[d][i / 4][i % 4];
-      } else {
-        uint32_t top = 0;
+      for (int t = 0; t < TN; ++t) {
+        i32x8 wo;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const uint32_t v = xv[d][i / 4][i % 4];
-          top = max(top, max(finite_bits<DT>(v), finite_bits<DT>(v >> 16)));
-        }
-        top = max(top, (uint32_t)__shfl_xor((int)top, 16));
-        top = max(top, (uint32_t)__shfl_xor((int)top, 32));
-        const int e = block_exponent<DT>(top);
-        const float scale = exp2_int(e);
-        xsb[d] = e + 127;
+        for (int i = 0; i < 8; ++i) wo[i] = (int)wv[d][t][i / 4][i % 4];
+        if constexpr (E8M0) {
+          acc[t] = mfma16(wo, xo, acc[t], wsb, xsb);
+        } else {
+          const f32x4 v = mfma16(wo, xo, f32x4{0.f, 0.f, 0.f, 0.f}, 127, xsb);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          short2_t c = {0, 0};
-          c = codes_of<DT, false>(c, xv[d][i / 2][2 * (i % 2)], scale);
-          c = codes_of<DT, true>(c, xv[d][i / 2][2 * (i % 2) + 1], scale);
-          xo[i] = __builtin_bit_cast(int, c);
+          for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(v[i], wsf, acc[t][i]);
         }
       }
-      i32x8 wo;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) wo[i] = (int)wv[d][i / 4][i % 4];
-      if constexpr (E8M0) {
-        acc = mfma16(wo, xo, acc, wsb[d], xsb[d]);
-      } else {
-        const f32x4 v = mfma16(wo, xo, f32x4{0.f, 0.f, 0.f, 0.f}, 127, xsb[d]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(v[i], wsf[d], acc[i]);
-      }
+      if (b + waves * DEPTH < p.blocks) load(b + waves * DEPTH, wv[d]);
     }
   }
+  float* const red = reinterpret_cast<float*>(lds);
+  if constexpr (DT != DT_CODES) __syncthreads();  // (the codes have been read)
   // red[wave][token][feature]
 #pragma unroll
-  for (int i = 0; i < 4; ++i) red[wave * 256 + col * 16 + 4 * quad + i] = acc[i];
+  for (int t = 0; t < TN; ++t)
+    *reinterpret_cast<f32x4*>(red + wave * 16 * BN + col * BN + 16 * t + 4 * quad) = acc[t];
   __syncthreads();
-  for (int i = threadIdx.x; i < 256; i += blockDim.x) {
-    const int t = i >> 4, n = n0 + (i & 15);
-    // (whole waves: 256 values are four of them)
+  for (int i = threadIdx.x; i < 16 * BN; i += blockDim.x) {
+    const int t = i / BN, n = n0 + i % BN;
+    // (whole waves: 16 BN values are a number of them)
     const int s = p.ids ? __shfl(slot, t) : t;
     if (t >= count || n >= p.N) continue;
     float v = 0.f;
-    for (int u = 0; u < waves; ++u) v += red[u * 256 + i];
+    for (int u = 0; u < waves; ++u) v += red[u * 16 * BN + i];
     if (p.bias) {
       const uint16_t bits = p.bias[(size_t)expert * p.N + n];
       v += p.f16 ? act_to_f32<DT_F16>(bits) : act_to_f32<DT_BF16>(bits);
@@ -174,19 +184,27 @@ __global__ __launch_bounds__(1024) void fp8_decode_kernel(DecodeParams p) {
   }
 }
 
-template <int DT>
-void launch_decode(const DecodeParams& p, bool e8m0, dim3 grid, int waves, hipStream_t s) {
-  const size_t lds = (size_t)waves * 256 * sizeof(float);
-  if (e8m0) hipLaunchKernelGGL((fp8_decode_kernel<DT, true>), grid, dim3(64 * waves), lds, s, p);
-  else hipLaunchKernelGGL((fp8_decode_kernel<DT, false>), grid, dim3(64 * waves), lds, s, p);
+// codes of the tokens and their scales
+size_t decode_lds(int64_t tokens, int64_t blocks) { return (size_t)(tokens * (129 * blocks + 16)); }
+
+template <int DT, int TN>
+void launch_decode(const DecodeParams& p, bool e8m0, int64_t slots, int waves, hipStream_t s) {
+  const dim3 grid((unsigned)((p.N + 16 * TN - 1) / (16 * TN) * slots)), block(64 * waves);
+  const size_t lds = std::max((size_t)waves * 256 * TN * sizeof(float), DT == DT_CODES ? 0 : decode_lds(p.tokens, p.blocks));
+  if (e8m0) hipLaunchKernelGGL((fp8_decode_kernel<DT, true, TN>), grid, block, lds, s, p);
+  else hipLaunchKernelGGL((fp8_decode_kernel<DT, false, TN>), grid, block, lds, s, p);
 }
 
 }  // namespace
 
 bool fp8_decodes(int64_t M, int64_t N, int64_t K, int E, bool experts, bool transpose) {
   if (transpose) return false;
-  if (!experts) return M <= 16;
-  return M <= 1024 && M <= 4 * (int64_t)E && M * ((N + 15) / 16) <= kMaxFp8Tiles;
+  if (!experts) return M <= 2 || (M <= 8 && N * K <= int64_t(1) << 26);
+  return M <= 1024 && M <= 2 * (int64_t)E && M * ((N + 15) / 16) <= kMaxFp8Tiles;
+}
+
+bool fp8_decode_quantizes(int64_t M, int64_t K) {
+  return decode_lds(std::min<int64_t>(16, M), fp8_columns(K) / kFp8Block) <= 80 * 1024;
 }
 
 hipError_t launch_fp8_decode(const Fp8Args& a, const void* x, int x_dtype, const int32_t* ids, hipStream_t s) {
@@ -206,15 +224,24 @@ hipError_t launch_fp8_decode(const Fp8Args& a, const void* x, int x_dtype, const
   p.topk = a.topk;
   p.blocks = (int)(fp8_columns(a.K) / kFp8Block);
   p.xsrow = (int)fp8_scales(a.K);
+  p.tokens = (int)std::min<int64_t>(16, a.M);
   p.wsrow = p.blocks;
   p.wexpert = a.N * a.K;
   p.wsexpert = (a.N + kFp8Block - 1) / kFp8Block * p.blocks;
   p.f16 = a.dtype == DT_F16;
-  const int waves = std::clamp((p.blocks + 1) / 2, 1, 16);
-  const dim3 grid((unsigned)((a.N + 15) / 16 * (ids ? a.M : 1)));
-  if (x_dtype == DT_F16) launch_decode<DT_F16>(p, a.e8m0, grid, waves, s);
-  else if (x_dtype == DT_BF16) launch_decode<DT_BF16>(p, a.e8m0, grid, waves, s);
-  else launch_decode<DT_CODES>(p, a.e8m0, grid, waves, s);
+  const int64_t slots = ids ? a.M : 1;
+  // four blocks to a wave, all of them on their way at once; 32 features a workgroup where 16 would give
+  // more than eight for each CU
+  const int waves = std::clamp((p.blocks + 3) / 4, 1, 16);
+  const bool two = (a.N + 31) / 32 * slots >= 1024;
+  auto go = [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    if (two && ids) launch_decode<DT, 2>(p, a.e8m0, slots, waves, s);
+    else launch_decode<DT, 1>(p, a.e8m0, slots, waves, s);
+  };
+  if (x_dtype == DT_F16) go(std::integral_constant<int, DT_F16>{});
+  else if (x_dtype == DT_BF16) go(std::integral_constant<int, DT_BF16>{});
+  else go(std::integral_constant<int, DT_CODES>{});
   return hipGetLastError();
 }
 

@@ -252,9 +252,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
     constexpr bool tail = decltype(TAIL)::value;
     lds_u8 *const cx = stage_at(I), *const cw = cx + XP * 1024;
     const int s = s0 + i;
-    // this wave's pieces of the step have landed when at most x's scales, issued behind them, are under way
+    // this wave's pieces of the step, and x's scales, have landed
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(wait_vm(i == 1 ? TM : 0));
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     stage(s + 1, std::integral_constant<int, i + 1>{});
@@ -320,6 +320,10 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
           for (int e = 0; e < 4; ++e) v[e] = E8M0 ? acc[n][t][4 * g + e] : acc[n][t][4 * g + e] * unit_of;
           if (p.part) {
             float* const out = p.part + ((size_t)split * p.M + slot) * p.N + f;
+            if (p.N % 4 == 0 && f < p.N) {
+              *reinterpret_cast<f32x4*>(out) = f32x4{v[0], v[1], v[2], v[3]};
+              continue;
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if (f + e < p.N) out[e] = v[e];
@@ -352,12 +356,13 @@ __global__ __launch_bounds__(256) void fp8_sum_kernel(const float* __restrict__ 
   for (int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4; i < values; i += (int64_t)gridDim.x * 1024) {
     if (N % 4 == 0) {
       f32x4 v = {0.f, 0.f, 0.f, 0.f};
-      for (int s0 = 0; s0 < splits; s0 += 4) {  // four at a time, so that their loads overlap
-        f32x4 q[4];
+      for (int s0 = 0; s0 < splits; s0 += 8) {  // eight at a time, so that their loads overlap
+        f32x4 q[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) q[k] = *reinterpret_cast<const f32x4*>(part + (int64_t)min(s0 + k, splits - 1) * values + i);
+        for (int k = 0; k < 8; ++k)
+          if (s0 + k < splits) q[k] = *reinterpret_cast<const f32x4*>(part + (int64_t)(s0 + k) * values + i);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < 8; ++k)
           if (s0 + k < splits) v += q[k];
       }
       const int n = (int)(i % N);
@@ -397,30 +402,43 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
+// The tile height and K ranges of the smallest estimate.  A CU holds `resident`
+// workgroups of a height; alone, one takes `alone` us for a step, and never less
+// than the 1.1 us after which weights come from memory; a full CU ends a step
+// every `full` us.  Weights come at 4.2 TB/s at most, and the sums of K ranges
+// cost a launch and their way to memory and back.  (Fitted to measured times:
+// 512 tokens x 4096 x 4096 27.3 us with tiles of 64, 33.7 with 128, which win
+// from 1024 x 6144 on; 128 x 4096 x 4096 18.3 with 32 in two ranges.)
 Fp8Tiles plan_fp8_tiles(int64_t M, int64_t N, int64_t K, int E, bool experts, int cus) {
-  Fp8Tiles t{};
-  const int64_t tokens = experts ? ceil_div(M, E) : M;  // of a product, about
-  if (tokens <= 32) t.bm = 32;
-  else if (tokens <= 64) t.bm = 64;
-  else if (tokens <= 96 && !experts) t.bm = 96;
-  else t.bm = 128;
-  t.bn = 128;
-  t.tiles_n = (int)ceil_div(N, t.bn);
-  // every bucket of the order may end with a part of a tile
-  t.tiles_m = (int)(experts ? M / t.bm + std::min<int64_t>(M, E + 1) : ceil_div(M, t.bm));
+  static const struct { int bm, resident; double alone, full; } kHeights[] = {
+      {32, 3, 0.42, 0.36}, {64, 3, 0.60, 0.50}, {96, 2, 0.75, 0.60}, {128, 2, 0.85, 0.69}};
   const int steps = (int)ceil_div(K, kFp8Block);
-  t.splits = 1;
-  t.steps = steps;
-  const int64_t tiles = (int64_t)t.tiles_m * t.tiles_n;
-  if (!experts) {
-    // fewer tiles than two a CU: ranges of K, of four blocks or more
-    const int64_t want = std::min<int64_t>(2 * cus / std::max<int64_t>(tiles, 1), steps / 4);
-    if (want > 1) {
-      t.steps = (int)ceil_div(ceil_div(steps, want), 4) * 4;  // (whole words of x's scales)
-      t.splits = (int)ceil_div(steps, t.steps);
+  const int64_t tiles_n = ceil_div(N, 128);
+  Fp8Tiles best{};
+  double least = 0;
+  for (const auto& h : kHeights) {
+    // experts: half of a tile more for each
+    const int64_t tiles = (experts ? ceil_div(2 * M + h.bm * std::min<int64_t>(E, M), 2 * h.bm) : ceil_div(M, h.bm)) * tiles_n;
+    for (int want = 1; want <= (experts ? 1 : std::min(32, std::max(1, steps / 4))); ++want) {
+      // (whole words of x's scales)
+      const int per = want == 1 ? steps : (int)ceil_div(ceil_div(steps, want), 4) * 4, splits = (int)ceil_div(steps, per);
+      if (splits != want) continue;
+      const int64_t each = ceil_div(tiles * splits, cus);
+      double us = per * std::max(std::max(h.alone, 1.1) * (double)ceil_div(each, h.resident), h.full * (double)each);
+      us = std::max(us, (double)N * (double)K * (experts ? std::min<int64_t>(E, M) : 1) / 4.2e6);
+      if (splits > 1) us += 3 + (double)splits * M * N * 8 / 4e6;
+      if (best.bm == 0 || us < least) {
+        least = us;
+        best.bm = h.bm;
+        best.splits = splits;
+        best.steps = per;
+      }
     }
   }
-  return t;
+  best.tiles_n = (int)tiles_n;
+  // every bucket of the order may end with a part of a tile
+  best.tiles_m = (int)(experts ? M / best.bm + std::min<int64_t>(M, E + 1) : ceil_div(M, best.bm));
+  return best;
 }
 
 size_t fp8_partial_bytes(const Fp8Tiles& t, int64_t M, int64_t N) {
