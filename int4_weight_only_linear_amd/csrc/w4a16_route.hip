@@ -39,14 +39,11 @@ __device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOM
 
 constexpr int kRouteWaves = 4;
 
-// One wave a row, V experts a lane (expert 64 v + lane).
+// A row by one wave, keys in 64 bits, V experts a lane (expert 64 v + lane);
+// keys [64 V] and group_key [kMaxGroups] are the wave's own LDS.
 template <int DT, int V>
-__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
-  __shared__ double keys[kRouteWaves][64 * V];
-  __shared__ double group_key[kRouteWaves][kMaxGroups];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t m = (int64_t)blockIdx.x * kRouteWaves + wave;
-  if (m >= a.M) return;  // (waves share nothing)
+__device__ void route_row(const RouteArgs& a, int64_t m, double* keys, double* group_key) {
+  const int lane = threadIdx.x & 63;
   const double none = -__builtin_inf();
   float l[V];
   bool nan = false;
@@ -89,24 +86,24 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
   if (a.groups > 1) {
     const int per = a.E / a.groups;
 #pragma unroll
-    for (int v = 0; v < V; ++v) keys[wave][64 * v + lane] = key[v];
+    for (int v = 0; v < V; ++v) keys[64 * v + lane] = key[v];
     wave_lds_fence();
     double mine = none;
     if (lane < a.groups) {
       double first = none, second = none;
       for (int i = 0; i < per; ++i) {
-        const double k = keys[wave][lane * per + i];
+        const double k = keys[lane * per + i];
         second = fmax(second, fmin(first, k));
         first = fmax(first, k);
       }
       mine = a.group_top == 2 && second > none ? first + second : first;
-      group_key[wave][lane] = mine;
+      group_key[lane] = mine;
     }
     wave_lds_fence();
     int rank = 0;
     if (lane < a.groups)
       for (int g = 0; g < a.groups; ++g) {
-        const double k = group_key[wave][g];
+        const double k = group_key[g];
         rank += k > mine || (k == mine && g < lane);
       }
     const uint64_t kept = __ballot(lane < a.groups && rank < a.topk_groups);
@@ -147,132 +144,372 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
   }
 }
 
-// One wave a row, V experts a lane (expert 64 v + lane).
+// Any number of experts: one wave a row.
 template <int DT, int V>
-__global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteBackwardArgs a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+__global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
+  __shared__ double keys[kRouteWaves][64 * V];
+  __shared__ double group_key[kRouteWaves][kMaxGroups];
+  const int wave = threadIdx.x >> 6;
   const int64_t m = (int64_t)blockIdx.x * kRouteWaves + wave;
-  if (m >= a.M) return;
-  float s[V], rest[V], ds[V];  // score, 1 - score, its gradient
-  if (a.sigmoid) {
-    bool nan = false;
+  if (m < a.M) route_row<DT, V>(a, m, keys[wave], group_key[wave]);  // (waves share nothing)
+}
+
+// ---- sixteen lanes a row, four rows a wave ----------------------------------------
+// Lane c of a row holds its experts V c .. V c + V - 1.
+
+// WHOLE: rows are whole 16-byte pieces, and so is each lane's part
+template <int DT, int V, bool WHOLE>
+__device__ __forceinline__ void load_part(const void* logits, int64_t row, int c, int E, float (&l)[V]) {
+  constexpr int PER = DT == DT_F32 ? 4 : 8;  // logits of a piece
+  if constexpr (WHOLE && V % PER == 0) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = 64 * v + lane;
-      const float l = e < a.E ? load_logit<DT>(a.logits, m * a.E + e) : -__builtin_inff();
-      // (of the two, the small one is formed without a difference)
-      const float t = expf(-fabsf(l)), q = 1.f / (1.f + t);
-      s[v] = l >= 0 ? q : t * q;
-      rest[v] = l >= 0 ? t * q : q;
-      nan |= l != l;
-    }
-    // a NaN makes its row NaN, as in the forward pass
-    if (__ballot(nan)) {
+    for (int q = 0; q < V / PER; ++q) {
+      const int e = V * c + PER * q;
+      u32x4 w = {0u, 0u, 0u, 0u};
+      if (e < E) w = *reinterpret_cast<const u32x4*>(static_cast<const char*>(logits) + (row * E + e) * (16 / PER));
 #pragma unroll
-      for (int v = 0; v < V; ++v) s[v] = __builtin_nanf("");
+      for (int i = 0; i < PER; ++i) {
+        float v;
+        const uint32_t word = w[PER == 4 ? i : i / 2];  // (a bit cast of w[i] itself takes element 0)
+        if constexpr (DT == DT_F32) v = __builtin_bit_cast(float, word);
+        else v = act_to_f32<DT>((uint16_t)(word >> (16 * (i & 1))));
+        l[PER * q + i] = e < E ? v : -__builtin_inff();
+      }
     }
   } else {
-    float top = -__builtin_inff(), sum = 0;
-    bool nan = false;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int e = 64 * v + lane;
-      s[v] = e < a.E ? load_logit<DT>(a.logits, m * a.E + e) : -__builtin_inff();
-      nan |= s[v] != s[v];
-      top = fmaxf(top, s[v]);
-    }
-    top = wave_max(top);
-    nan = __ballot(nan) != 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      s[v] = s[v] == -__builtin_inff() ? 0.f : (s[v] == top ? 1.f : expf(s[v] - top));
-      sum += s[v];
-    }
-    sum = wave_sum(sum);
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = nan ? __builtin_nanf("") : (sum > 0 ? s[v] / sum : 0.f);
+    for (int v = 0; v < V; ++v) l[v] = V * c + v < E ? load_logit<DT>(logits, row * E + V * c + v) : -__builtin_inff();
   }
-  // lane j: slot j's expert and gradient
-  const int id = lane < a.topk ? a.ids[m * a.topk + lane] : -1;
-  const bool named = id >= 0 && id < a.E;
-  float g = named ? a.dweights[m * a.topk + lane] * a.scale : 0.f;
-  if (a.renormalize) {
-    float p = 0;
-    for (int j = 0; j < a.topk; ++j) {
-      const int e = __shfl(id, j);
-      if (e < 0 || e >= a.E) continue;
-      float at = 0;
+}
+
+// over the sixteen lanes of a row
+__device__ __forceinline__ float row_max(float v) {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (e >> 6 == v) at = s[v];
-      at = __shfl(at, e & 63);
-      if (lane == j) p = at;
-    }
-    const float sum = wave_sum(p);
-    const float inv = sum > 0 ? 1.f / sum : (sum == 0 ? 0.f : sum);
-    const float c = wave_sum(p * inv * g);
-    g = named ? (g - c) * inv : 0.f;
+  for (int o = 8; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+  return v;
+}
+__device__ __forceinline__ float row_min(float v) { return -row_max(-v); }
+template <typename T>
+__device__ __forceinline__ T row_sum(T v) {
+#pragma unroll
+  for (int o = 8; o; o >>= 1) v += __shfl_xor(v, o);
+  return v;
+}
+// a tree of V terms
+template <int V, typename T>
+__device__ __forceinline__ T part_sum(const T (&x)[V]) {
+  T t[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) t[v] = x[v];
+#pragma unroll
+  for (int n = V / 2; n; n /= 2)
+#pragma unroll
+    for (int v = 0; v < n; ++v) t[v] += t[v + n];
+  return t[0];
+}
+// whether any lane of this lane's row says so
+__device__ __forceinline__ bool row_any(bool b) { return (__ballot(b) >> (threadIdx.x & 48)) & 0xFFFF; }
+
+// Keys are formed in 32 bits, within 2^-21 (1 + |key|) of those in 64; a row whose
+// choice or order hangs on less than twice that is done again by route_row, so
+// every row's choice is that of the 64-bit keys.  The weights are formed in 64
+// bits, of the chosen logits (softmax: all) alone.
+// Bound by its instructions: a round of the choice is about 4 V of them for four
+// rows.
+template <int DT, int V, bool WHOLE>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs a) {
+  constexpr int V64 = V > 4 ? V / 4 : 1;
+  __shared__ double keys[kRouteWaves][64 * V64];
+  __shared__ double group_key[kRouteWaves][kMaxGroups];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15;
+  const int64_t m0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * 4;
+  if (m0 >= a.M) return;  // (waves share nothing)
+  const int64_t m = min(m0 + (lane >> 4), a.M - 1);
+  constexpr float none = -__builtin_inff();
+  float l[V], key[V];
+  load_part<DT, V, WHOLE>(a.logits, m, c, a.E, l);
+  bool nan = false;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    nan |= l[v] != l[v];
+    l[v] = l[v] == l[v] ? l[v] : none;
   }
-#pragma unroll
-  for (int v = 0; v < V; ++v) ds[v] = 0;
-  for (int j = 0; j < a.topk; ++j) {
-    const int e = __shfl(id, j);
-    const float gj = __shfl(g, j);
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (e == 64 * v + lane) ds[v] += gj;
-  }
-  float dot = 0;
+  nan = row_any(nan);
+  const bool by_logit = !a.bias && a.group_top == 1;
+  float top = none;
+  double sum = 1;
   if (!a.sigmoid) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) dot += s[v] * ds[v];
-    dot = wave_sum(dot);
+    for (int v = 0; v < V; ++v) top = fmaxf(top, l[v]);
+    top = row_max(top);
+    double e[V];
+    // (equal to the largest: 1, also where that is infinite)
+#pragma unroll
+    for (int v = 0; v < V; ++v) e[v] = l[v] == none ? 0.0 : (l[v] == top ? 1.0 : exp((double)l[v] - (double)top));
+    sum = row_sum(part_sum<V>(e));
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = sum > 0 ? (float)e[v] / (float)sum : 0.f;
+  } else if (!by_logit) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = 1.f / (1.f + expf(-l[v]));
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = 64 * v + lane;
-    if (e >= a.E) continue;
-    store_logit<DT>(a.dlogits, m * a.E + e, a.sigmoid ? ds[v] * s[v] * rest[v] : s[v] * (ds[v] - dot));
+    const int e = V * c + v;
+    if (by_logit) key[v] = l[v];
+    else if (a.bias && e < a.E) key[v] += a.bias[e];
+    if (!(l[v] > none) || !(key[v] > none)) key[v] = none;
+  }
+  // (an infinite key has no distance to the others)
+  bool unsure = false;
+  constexpr float kNear = 0x1p-20f;
+  if (a.groups > 1) {
+    const int lanes = a.E / a.groups / V;  // of a group: 1, 2, 4, 8 or 16
+    float first = none, second = none;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      second = fmaxf(second, fminf(first, key[v]));
+      first = fmaxf(first, key[v]);
+    }
+    for (int o = 1; o < lanes; o <<= 1) {
+      const float f = __shfl_xor(first, o), s = __shfl_xor(second, o);
+      second = fmaxf(fmaxf(second, s), fminf(first, f));
+      first = fmaxf(first, f);
+    }
+    const float mine = a.group_top == 2 && second > none ? first + second : first;
+    int rank = 0;
+    for (int o = 0; o < 16; o += lanes) {
+      const float other = __shfl(mine, (lane & 48) + o);
+      rank += V * o < a.E && (other > mine || (other == mine && o < c / lanes * lanes));
+    }
+    const bool kept = rank < a.topk_groups;
+    if (!by_logit) {
+      const float low = row_min(kept ? mine : __builtin_inff()), high = row_max(kept ? none : mine);
+      // (the sum of two keys may be far smaller than they are)
+      const float size = row_max(first > none ? fabsf(first) + (second > none ? fabsf(second) : 0.f) : 0.f);
+      unsure = high > none && !(low - high > 2 * kNear * (2 + size));
+    }
+    if (!kept) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) key[v] = none;
+    }
+  }
+  // the largest key, then the next: lane j of a row keeps the j-th
+  int id = -1;
+  float before = __builtin_inff();
+  for (int j = 0; j <= a.topk; ++j) {
+    float best = key[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) best = fmaxf(best, key[v]);
+    const float most = row_max(best);
+    if (!by_logit) unsure |= most > none && !(before - most > kNear * (2 + 2 * fabsf(most))) && j > 0;
+    unsure |= !by_logit && most == __builtin_inff();
+    before = most;
+    if (j == a.topk) break;
+    const uint64_t hits = (__ballot(best == most && most > none) >> (lane & 48)) & 0xFFFF;
+    const int owner = hits ? __builtin_ctzll(hits) : -1;  // the lowest lane: the lowest experts
+    int at = 0;
+#pragma unroll
+    for (int v = V - 1; v >= 0; --v) at = key[v] == most ? v : at;
+#pragma unroll
+    for (int v = 0; v < V; ++v) key[v] = c == owner && v == at ? none : key[v];
+    const int e = __shfl(V * c + at, (lane & 48) + max(owner, 0));
+    if (c == j && owner >= 0) id = e;
+  }
+  double weight = 0;
+  if (id >= 0) {
+    const float x = load_logit<DT>(a.logits, m * a.E + id);
+    weight = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : (x == top ? 1.0 : exp((double)x - (double)top)) / sum;
+  }
+  if (a.renormalize) {
+    const double total = row_sum(weight);
+    weight = total > 0 ? weight / total : 0.0;
+  }
+  if (c < a.topk && m0 + (lane >> 4) < a.M) {
+    a.weights[m * a.topk + c] = nan ? __builtin_nanf("") : (float)(weight * (double)a.scale);
+    a.ids[m * a.topk + c] = id;
+  }
+  uint64_t again = __ballot(unsure && c == 0 && m0 + (lane >> 4) < a.M);
+  while (again) {
+    const int r = __builtin_ctzll(again) >> 4;
+    again &= again - 1;
+    route_row<DT, V64>(a, m0 + r, keys[wave], group_key[wave]);
   }
 }
 
-template <template <int, int> class Launch, typename Args>
-hipError_t by_type_and_size(const Args& a, hipStream_t s) {
-  auto size = [&](auto dt) {
-    constexpr int DT = decltype(dt)::value;
-    if (a.E <= 64) return Launch<DT, 1>::run(a, s);
-    if (a.E <= 128) return Launch<DT, 2>::run(a, s);
-    if (a.E <= 256) return Launch<DT, 4>::run(a, s);
-    if (a.E <= 512) return Launch<DT, 8>::run(a, s);
-    return Launch<DT, 16>::run(a, s);
+// The gradient, sixteen lanes a row: lane j has slot j's gradient (and those of
+// slots j + 16, ..), and every lane adds what meets its own experts.
+template <int DT, int V, bool WHOLE>
+__global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteBackwardArgs a) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, base = lane & 48;
+  const int64_t row = ((int64_t)blockIdx.x * kRouteWaves + wave) * 4 + (lane >> 4);
+  if (row - (lane >> 4) >= a.M) return;
+  const int64_t m = min(row, a.M - 1);
+  float s[V], ds[V];
+  load_part<DT, V, WHOLE>(a.logits, m, c, a.E, s);
+  bool nan = false;
+#pragma unroll
+  for (int v = 0; v < V; ++v) nan |= s[v] != s[v], ds[v] = 0.f;
+  nan = row_any(nan);
+  float top = -__builtin_inff(), total = 1.f;
+  if (!a.sigmoid) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) top = fmaxf(top, s[v]);
+    top = row_max(top);
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] = s[v] == -__builtin_inff() ? 0.f : (s[v] == top ? 1.f : expf(s[v] - top));
+    total = row_sum(part_sum<V>(s));
+    const float inv = total > 0.f ? 1.f / total : 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) s[v] *= inv;
+  }
+  // a slot's score and 1 - score (of the two, the small one is formed without a difference)
+  auto score_of = [&](int id, float& rest) {
+    const float l = load_logit<DT>(a.logits, m * a.E + id);
+    rest = 1.f;
+    if (!a.sigmoid) return l == -__builtin_inff() ? 0.f : (l == top ? 1.f : expf(l - top)) / total;
+    const float t = expf(-fabsf(l)), q = 1.f / (1.f + t);
+    rest = l >= 0 ? t * q : q;
+    return l >= 0 ? q : t * q;
   };
-  if (a.dtype == DT_F16) return size(std::integral_constant<int, DT_F16>{});
-  if (a.dtype == DT_BF16) return size(std::integral_constant<int, DT_BF16>{});
-  return size(std::integral_constant<int, DT_F32>{});
+  float sum = 1.f, mean = 0.f;
+  if (a.renormalize) {
+    float p = 0.f, pg = 0.f;
+    for (int j = c; j < a.topk; j += 16) {
+      const int id = a.ids[m * a.topk + j];
+      if (id < 0 || id >= a.E) continue;
+      float rest;
+      const float q = score_of(id, rest);
+      p += q;
+      pg += q * (a.dweights[m * a.topk + j] * a.scale);
+    }
+    sum = row_sum(p);
+    mean = sum > 0.f ? row_sum(pg) / sum : 0.f;
+  }
+  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+  for (int j0 = 0; j0 < a.topk; j0 += 16) {
+    const int j = j0 + c;
+    int id = j < a.topk ? a.ids[m * a.topk + j] : -1;
+    float g = 0.f;
+    if (id >= 0 && id < a.E) {
+      g = (a.dweights[m * a.topk + j] * a.scale - mean) * (a.renormalize ? inv : 1.f);
+      if (a.sigmoid) {  // the logit's gradient at once: other experts have none
+        float rest;
+        const float q = score_of(id, rest);
+        g = g * q * rest;
+      }
+    }
+    const int n = min(16, a.topk - j0);
+    for (int k = 0; k < n; ++k) {
+      const int e = __shfl(id, base + k) - V * c;
+      const float gk = __shfl(g, base + k);
+#pragma unroll
+      for (int v = 0; v < V; ++v) ds[v] += e == v ? gk : 0.f;
+    }
+  }
+  float dot = 0.f;
+  if (!a.sigmoid) {
+    float t[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) t[v] = s[v] * ds[v];
+    dot = row_sum(part_sum<V>(t));
+  }
+  float dl[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) dl[v] = nan ? __builtin_nanf("") : (a.sigmoid ? ds[v] : s[v] * (ds[v] - dot));
+  if (row >= a.M) return;
+  constexpr int PER = DT == DT_F32 ? 4 : 8;
+  if constexpr (WHOLE && V % PER == 0) {
+#pragma unroll
+    for (int q = 0; q < V / PER; ++q) {
+      const int e = V * c + PER * q;
+      if (e >= a.E) continue;
+      u32x4 w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (DT == DT_F32) w[i] = __builtin_bit_cast(uint32_t, dl[PER * q + i]);
+        else w[i] = f32x2_to_act_pair<DT>(dl[PER * q + 2 * i], dl[PER * q + 2 * i + 1]);
+      }
+      *reinterpret_cast<u32x4*>(static_cast<char*>(a.dlogits) + (m * a.E + e) * (16 / PER)) = w;
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (V * c + v < a.E) store_logit<DT>(a.dlogits, m * a.E + V * c + v, dl[v]);
+  }
 }
 
-dim3 route_grid(int64_t M) { return dim3((unsigned)((M + kRouteWaves - 1) / kRouteWaves)); }
+dim3 rows_grid(int64_t M, int rows) { return dim3((unsigned)((M + rows - 1) / rows)); }
 
-template <int DT, int V>
-struct RouteLaunch {
-  static hipError_t run(const RouteArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((route_kernel<DT, V>), route_grid(a.M), dim3(64 * kRouteWaves), 0, s, a);
-    return hipGetLastError();
-  }
-};
-template <int DT, int V>
-struct RouteBackwardLaunch {
-  static hipError_t run(const RouteBackwardArgs& a, hipStream_t s) {
-    hipLaunchKernelGGL((route_backward_kernel<DT, V>), route_grid(a.M), dim3(64 * kRouteWaves), 0, s, a);
-    return hipGetLastError();
-  }
-};
+// f(type, experts a lane) for a type and at least E / lanes experts a lane
+template <typename F>
+void by_type(int dtype, F&& f) {
+  if (dtype == DT_F16) f(std::integral_constant<int, DT_F16>{});
+  else if (dtype == DT_BF16) f(std::integral_constant<int, DT_BF16>{});
+  else f(std::integral_constant<int, DT_F32>{});
+}
+template <typename F>
+void by_size(int E, int lanes, F&& f) {
+  const int v = (E + lanes - 1) / lanes;
+  if (v <= 1) f(std::integral_constant<int, 1>{});
+  else if (v <= 2) f(std::integral_constant<int, 2>{});
+  else if (v <= 4) f(std::integral_constant<int, 4>{});
+  else if (v <= 8) f(std::integral_constant<int, 8>{});
+  else if (v <= 16) f(std::integral_constant<int, 16>{});
+  else if (v <= 32) f(std::integral_constant<int, 32>{});
+  else f(std::integral_constant<int, 64>{});
+}
+int part_of(int E) {  // experts a lane of sixteen
+  int v = 1;
+  while (16 * v < E) v *= 2;
+  return v;
+}
+// rows of whole 16-byte pieces
+bool whole_rows(const void* p, const void* q, int E, int dtype) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p) | reinterpret_cast<uintptr_t>(q);
+  return at % 16 == 0 && (size_t)E * (dtype == DT_F32 ? 4 : 2) % 16 == 0;
+}
 
 }  // namespace
 
-hipError_t launch_route(const RouteArgs& a, hipStream_t s) { return by_type_and_size<RouteLaunch>(a, s); }
+hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
+  // sixteen lanes a row for up to 512 experts and 16 of them chosen, where a group is a power of two of lanes
+  const int v = part_of(a.E), per = a.E / a.groups;
+  const bool quick = a.E <= 512 && a.topk <= 16 && (a.groups == 1 || (per % v == 0 && (per / v & (per / v - 1)) == 0 && per / v <= 16));
+  const bool whole = whole_rows(a.logits, nullptr, a.E, a.dtype);
+  by_type(a.dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    if (quick)
+      by_size(a.E, 16, [&](auto n) {
+        constexpr int V = decltype(n)::value;
+        if constexpr (V <= 32) {
+          const dim3 grid = rows_grid(a.M, 4 * kRouteWaves);
+          if (whole) hipLaunchKernelGGL((route_quick_kernel<DT, V, true>), grid, dim3(64 * kRouteWaves), 0, s, a);
+          else hipLaunchKernelGGL((route_quick_kernel<DT, V, false>), grid, dim3(64 * kRouteWaves), 0, s, a);
+        }
+      });
+    else
+      by_size(a.E, 64, [&](auto n) {
+        constexpr int V = decltype(n)::value;
+        if constexpr (V <= 16)
+          hipLaunchKernelGGL((route_kernel<DT, V>), rows_grid(a.M, kRouteWaves), dim3(64 * kRouteWaves), 0, s, a);
+      });
+  });
+  return hipGetLastError();
+}
+
 hipError_t launch_route_backward(const RouteBackwardArgs& a, hipStream_t s) {
-  return by_type_and_size<RouteBackwardLaunch>(a, s);
+  const bool whole = whole_rows(a.logits, a.dlogits, a.E, a.dtype);
+  by_type(a.dtype, [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    by_size(a.E, 16, [&](auto n) {
+      constexpr int V = decltype(n)::value;
+      const dim3 grid = rows_grid(a.M, 4 * kRouteWaves);
+      if (whole) hipLaunchKernelGGL((route_backward_kernel<DT, V, true>), grid, dim3(64 * kRouteWaves), 0, s, a);
+      else hipLaunchKernelGGL((route_backward_kernel<DT, V, false>), grid, dim3(64 * kRouteWaves), 0, s, a);
+    });
+  });
+  return hipGetLastError();
 }
 
 }  // namespace w4a16
