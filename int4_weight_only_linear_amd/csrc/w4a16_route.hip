@@ -182,19 +182,39 @@ __device__ __forceinline__ void load_part(const void* logits, int64_t row, int c
   }
 }
 
-// over the sixteen lanes of a row
-__device__ __forceinline__ float row_max(float v) {
-#pragma unroll
-  for (int o = 8; o; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
+// Moves between the sixteen lanes of a row, in the vector unit.
+constexpr int dpp_rotate(int n) { return 0x120 + n; }
+constexpr int kDppNext = 0xB1, kDppNextPair = 0x4E, kDppMirror8 = 0x141, kDppMirror16 = 0x140;
+template <int CTRL, typename T>
+__device__ __forceinline__ T dpp(T v) {
+  if constexpr (sizeof(T) == 8) {
+    uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)u, CTRL, 15, 15, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(uint32_t)(u >> 32), CTRL, 15, 15, true);
+    return __builtin_bit_cast(T, (uint64_t)hi << 32 | lo);
+  } else {
+    return __builtin_bit_cast(T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 15, 15, true));
+  }
 }
-__device__ __forceinline__ float row_min(float v) { return -row_max(-v); }
+// over the sixteen lanes of a row; every lane gets the same
+template <typename T, typename F>
+__device__ __forceinline__ T row_all(T v, F&& f) {
+  v = f(v, dpp<dpp_rotate(8)>(v));
+  v = f(v, dpp<dpp_rotate(4)>(v));
+  v = f(v, dpp<dpp_rotate(2)>(v));
+  return f(v, dpp<dpp_rotate(1)>(v));
+}
+__device__ __forceinline__ float row_max(float v) { return row_all(v, [](float a, float b) { return fmaxf(a, b); }); }
+__device__ __forceinline__ float row_min(float v) { return row_all(v, [](float a, float b) { return fminf(a, b); }); }
+__device__ __forceinline__ int row_max(int v) { return row_all(v, [](int a, int b) { return max(a, b); }); }
 template <typename T>
-__device__ __forceinline__ T row_sum(T v) {
-#pragma unroll
-  for (int o = 8; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+__device__ __forceinline__ T row_sum(T v) { return row_all(v, [](T a, T b) { return a + b; }); }
+// order kept, compared as an integer (no zero of either sign apart, no NaN), and back
+__device__ __forceinline__ int ordered(float v) {
+  const int b = __builtin_bit_cast(int, v + 0.f);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
 }
+__device__ __forceinline__ float of_ordered(int b) { return __builtin_bit_cast(float, b ^ ((b >> 31) & 0x7FFFFFFF)); }
 // a tree of V terms
 template <int V, typename T>
 __device__ __forceinline__ T part_sum(const T (&x)[V]) {
@@ -210,12 +230,56 @@ __device__ __forceinline__ T part_sum(const T (&x)[V]) {
 // whether any lane of this lane's row says so
 __device__ __forceinline__ bool row_any(bool b) { return (__ballot(b) >> (threadIdx.x & 48)) & 0xFFFF; }
 
-// Keys are formed in 32 bits, within 2^-21 (1 + |key|) of those in 64; a row whose
-// choice or order hangs on less than twice that is done again by route_row, so
-// every row's choice is that of the 64-bit keys.  The weights are formed in 64
-// bits, of the chosen logits (softmax: all) alone.
-// Bound by its instructions: a round of the choice is about 4 V of them for four
-// rows.
+// A group's key, from its lanes' keys.
+template <int V, typename T>
+__device__ __forceinline__ T group_key_of(const T (&key)[V], int lanes, int top, T& size) {
+  const T none = -__builtin_inf();
+  T first = none, second = none;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    second = max(second, min(first, key[v]));
+    first = max(first, key[v]);
+  }
+  auto join = [&](auto ctrl) {
+    const T f = dpp<decltype(ctrl)::value>(first), s = dpp<decltype(ctrl)::value>(second);
+    second = max(max(second, s), min(first, f));
+    first = max(first, f);
+  };
+  if (lanes > 1) join(std::integral_constant<int, kDppNext>{});
+  if (lanes > 2) join(std::integral_constant<int, kDppNextPair>{});
+  if (lanes > 4) join(std::integral_constant<int, kDppMirror8>{});
+  if (lanes > 8) join(std::integral_constant<int, kDppMirror16>{});
+  // (the sum of two keys may be far smaller than they are)
+  size = first > none ? fabs(first) + (second > none ? fabs(second) : 0) : 0;
+  return top == 2 && second > none ? first + second : first;
+}
+// Lanes of a row whose key is before this lane's: larger, or equal and `at` lower.
+// step 2, 4, ..: one lane of that many alone, the others hold the same.
+template <typename T>
+__device__ __forceinline__ int rank_of(T key, int at, int step) {
+  int ahead = 0;
+  static_for<1, 16>([&](auto R) {
+    constexpr int r = decltype(R)::value;
+    if (r & (step - 1)) return;
+    const T other = dpp<dpp_rotate(r)>(key);
+    const int oat = dpp<dpp_rotate(r)>(at);
+    ahead += other > key || (other == key && oat < at);
+  });
+  return ahead;
+}
+
+// Keys are formed in 32 bits; what hangs on less than their error is decided by
+// the 64-bit keys of the experts concerned, so that every choice is that of the
+// 64-bit keys:
+//  - groups: all keys of the wave's rows again in 64 bits;
+//  - experts: the choice goes on until the next key is clearly below (lane j holds
+//    the j-th expert), and those found are ranked by their 64-bit keys, of which
+//    the weights need the scores anyway;
+//  - a row with more than sixteen in question (a row of equal scores): route_row.
+// The error is below 2^-22 (1 + |key|): an exponential of one unit, t, in
+// 1 / (1 + t) is t / (1 + t)^2 <= 1/4 unit of 2^-23, the sum and the quotient half
+// a unit each of at most 1, and adding the bias 2^-24 |key|; softmax's rounding to
+// 32 bits of both sides and the quotient is no more.
 template <int DT, int V, bool WHOLE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs a) {
   constexpr int V64 = V > 4 ? V / 4 : 1;
@@ -224,8 +288,10 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15;
   const int64_t m0 = ((int64_t)blockIdx.x * kRouteWaves + wave) * 4;
   if (m0 >= a.M) return;  // (waves share nothing)
-  const int64_t m = min(m0 + (lane >> 4), a.M - 1);
+  const bool there = m0 + (lane >> 4) < a.M;
+  const int64_t m = there ? m0 + (lane >> 4) : a.M - 1;
   constexpr float none = -__builtin_inff();
+  constexpr float kNear = 0x1.1p-21f;  // two keys' errors, and that of their difference
   float l[V], key[V];
   load_part<DT, V, WHOLE>(a.logits, m, c, a.E, l);
   bool nan = false;
@@ -238,17 +304,21 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs
   const bool by_logit = !a.bias && a.group_top == 1;
   float top = none;
   double sum = 1;
+  auto exp_of = [&](float x) {  // (equal to the largest: 1, also where that is infinite)
+    return x == none ? 0.0 : (x == top ? 1.0 : exp((double)x - (double)top));
+  };
+  auto score_of = [&](float x) { return a.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : (sum > 0 ? exp_of(x) / sum : 0.0); };
   if (!a.sigmoid) {
 #pragma unroll
     for (int v = 0; v < V; ++v) top = fmaxf(top, l[v]);
     top = row_max(top);
     double e[V];
-    // (equal to the largest: 1, also where that is infinite)
 #pragma unroll
-    for (int v = 0; v < V; ++v) e[v] = l[v] == none ? 0.0 : (l[v] == top ? 1.0 : exp((double)l[v] - (double)top));
+    for (int v = 0; v < V; ++v) e[v] = exp_of(l[v]);
     sum = row_sum(part_sum<V>(e));
+    const float whole = (float)sum;
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = sum > 0 ? (float)e[v] / (float)sum : 0.f;
+    for (int v = 0; v < V; ++v) key[v] = whole > 0 ? (float)e[v] / whole : 0.f;
   } else if (!by_logit) {
 #pragma unroll
     for (int v = 0; v < V; ++v) key[v] = 1.f / (1.f + expf(-l[v]));
@@ -260,76 +330,79 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs
     else if (a.bias && e < a.E) key[v] += a.bias[e];
     if (!(l[v] > none) || !(key[v] > none)) key[v] = none;
   }
-  // (an infinite key has no distance to the others)
-  bool unsure = false;
-  constexpr float kNear = 0x1p-20f;
   if (a.groups > 1) {
     const int lanes = a.E / a.groups / V;  // of a group: 1, 2, 4, 8 or 16
-    float first = none, second = none;
+    float size;
+    const float mine = group_key_of<V>(key, lanes, a.group_top, size);
+    // (lanes past the last expert have no key and the highest places: behind)
+    bool kept = rank_of(mine, c, lanes) < a.topk_groups;
+    const float low = row_min(kept ? mine : __builtin_inff()), high = row_max(kept ? none : mine);
+    size = row_max(size);
+    const bool close = !by_logit && high > none && !(low - high > 1.25f * kNear * (2 + size));
+    if (__ballot(close)) {
+      double k[V], unused;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      second = fmaxf(second, fminf(first, key[v]));
-      first = fmaxf(first, key[v]);
-    }
-    for (int o = 1; o < lanes; o <<= 1) {
-      const float f = __shfl_xor(first, o), s = __shfl_xor(second, o);
-      second = fmaxf(fmaxf(second, s), fminf(first, f));
-      first = fmaxf(first, f);
-    }
-    const float mine = a.group_top == 2 && second > none ? first + second : first;
-    int rank = 0;
-    for (int o = 0; o < 16; o += lanes) {
-      const float other = __shfl(mine, (lane & 48) + o);
-      rank += V * o < a.E && (other > mine || (other == mine && o < c / lanes * lanes));
-    }
-    const bool kept = rank < a.topk_groups;
-    if (!by_logit) {
-      const float low = row_min(kept ? mine : __builtin_inff()), high = row_max(kept ? none : mine);
-      // (the sum of two keys may be far smaller than they are)
-      const float size = row_max(first > none ? fabsf(first) + (second > none ? fabsf(second) : 0.f) : 0.f);
-      unsure = high > none && !(low - high > 2 * kNear * (2 + size));
+      for (int v = 0; v < V; ++v) {
+        const int e = V * c + v;
+        k[v] = key[v] > none ? score_of(l[v]) + (a.bias ? (double)a.bias[e] : 0.0) : (double)none;
+      }
+      const double exact = group_key_of<V>(k, lanes, a.group_top, unused);
+      kept = rank_of(exact, c, lanes) < a.topk_groups;
     }
     if (!kept) {
 #pragma unroll
       for (int v = 0; v < V; ++v) key[v] = none;
     }
   }
-  // the largest key, then the next: lane j of a row keeps the j-th
+  // the largest key, then the next
+  int left[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) left[v] = ordered(key[v]);
+  const int empty = ordered(none);
   int id = -1;
   float before = __builtin_inff();
-  for (int j = 0; j <= a.topk; ++j) {
-    float best = key[0];
+  bool doubt = false, open = true;  // open: the j-th may be as large as the last one chosen
+  for (int j = 0;; ++j) {
+    int best = left[0];
 #pragma unroll
-    for (int v = 1; v < V; ++v) best = fmaxf(best, key[v]);
-    const float most = row_max(best);
-    if (!by_logit) unsure |= most > none && !(before - most > kNear * (2 + 2 * fabsf(most))) && j > 0;
-    unsure |= !by_logit && most == __builtin_inff();
-    before = most;
-    if (j == a.topk) break;
-    const uint64_t hits = (__ballot(best == most && most > none) >> (lane & 48)) & 0xFFFF;
-    const int owner = hits ? __builtin_ctzll(hits) : -1;  // the lowest lane: the lowest experts
-    int at = 0;
+    for (int v = 1; v < V; ++v) best = max(best, left[v]);
+    const int most = row_max(best);
+    const float k = of_ordered(most);
+    const bool close = !by_logit && j > 0 && most > empty && !(before - k > kNear * (1 + fabsf(k)));
+    if (j >= a.topk) {
+      open &= close;
+      if (j == 16 || !__ballot(open)) break;
+    }
+    doubt |= open && close;
+    before = k;
+    const uint32_t hits = (uint32_t)(__ballot(best == most && most > empty) >> (lane & 48)) & 0xFFFF;
+    const int owner = hits ? __builtin_ctz(hits) : -1;  // the lowest lane: the lowest experts
+    int at = -1;
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v) at = key[v] == most ? v : at;
+    for (int v = V - 1; v >= 0; --v) at = left[v] == most ? v : at;
+    at = c == owner ? at : -1;
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = c == owner && v == at ? none : key[v];
-    const int e = __shfl(V * c + at, (lane & 48) + max(owner, 0));
-    if (c == j && owner >= 0) id = e;
+    for (int v = 0; v < V; ++v) left[v] = v == at ? empty : left[v];
+    const int e = row_max(at < 0 ? -1 : V * c + at);
+    id = c == j && open ? e : id;
   }
   double weight = 0;
-  if (id >= 0) {
-    const float x = load_logit<DT>(a.logits, m * a.E + id);
-    weight = a.sigmoid ? 1.0 / (1.0 + exp(-(double)x)) : (x == top ? 1.0 : exp((double)x - (double)top)) / sum;
+  int slot = c;
+  if (id >= 0) weight = score_of(load_logit<DT>(a.logits, m * a.E + id));
+  if (__ballot(doubt)) {
+    const double k = id >= 0 ? weight + (a.bias ? (double)a.bias[id] : 0.0) : (double)none;
+    slot = rank_of(k, id >= 0 ? id : kMaxExperts + c, 1);
   }
+  if (slot >= a.topk) weight = 0;
   if (a.renormalize) {
     const double total = row_sum(weight);
     weight = total > 0 ? weight / total : 0.0;
   }
-  if (c < a.topk && m0 + (lane >> 4) < a.M) {
-    a.weights[m * a.topk + c] = nan ? __builtin_nanf("") : (float)(weight * (double)a.scale);
-    a.ids[m * a.topk + c] = id;
+  if (slot < a.topk && there) {
+    a.weights[m * a.topk + slot] = nan ? __builtin_nanf("") : (float)(weight * (double)a.scale);
+    a.ids[m * a.topk + slot] = id;
   }
-  uint64_t again = __ballot(unsure && c == 0 && m0 + (lane >> 4) < a.M);
+  uint64_t again = __ballot(open && c == 0 && there);
   while (again) {
     const int r = __builtin_ctzll(again) >> 4;
     again &= again - 1;
