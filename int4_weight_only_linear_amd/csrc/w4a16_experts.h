@@ -52,6 +52,9 @@ hipError_t launch_fp8_quantize(const void* x, uint8_t* codes, uint8_t* scales, i
 // (the others follow), start[E + 1] all; order: the slots, expert by expert, in
 // slot order.
 hipError_t launch_expert_order(const int32_t* ids, int32_t* start, int32_t* order, int slots, int E, hipStream_t s);
+// both of them
+hipError_t launch_fp8_quantize_and_order(const void* x, uint8_t* codes, uint8_t* scales, int64_t M, int64_t K, int dtype,
+                                         const int32_t* ids, int32_t* start, int32_t* order, int slots, int E, hipStream_t s);
 
 // ---- products -----------------------------------------------------------------
 struct Fp8Args {

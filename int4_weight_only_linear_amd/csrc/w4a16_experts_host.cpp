@@ -169,13 +169,20 @@ w4a16_status fp8_product(const char* what, const void* x, const uint8_t* x_scale
   a.xs = x_scales;
   // (rows of K % 16 == 0 values: aligned where the first one is)
   const bool in_place = p.decode && !codes && aligned(x, 16) && w4a16::fp8_decode_quantizes(slots, K);
+  const bool sorts = experts && !p.decode;
+  int32_t* const start = reinterpret_cast<int32_t*>(base + p.start);
+  int32_t* const order = reinterpret_cast<int32_t*>(base + p.order);
   if (!codes && !in_place) {
     uint8_t* const q = reinterpret_cast<uint8_t*>(base + p.codes);
     uint8_t* const qs = reinterpret_cast<uint8_t*>(base + p.scales);
-    const hipError_t e = w4a16::launch_fp8_quantize(x, q, qs, rows, K, dtype, s);
+    const hipError_t e = sorts ? w4a16::launch_fp8_quantize_and_order(x, q, qs, rows, K, dtype, ids, start, order, (int)slots, (int)E, s)
+                               : w4a16::launch_fp8_quantize(x, q, qs, rows, K, dtype, s);
     if (e != hipSuccess) return launched(e);
     a.x = q;
     a.xs = qs;
+  } else if (sorts) {
+    const hipError_t e = w4a16::launch_expert_order(ids, start, order, (int)slots, (int)E, s);
+    if (e != hipSuccess) return launched(e);
   }
   a.w = static_cast<const uint8_t*>(w);
   a.ws = w_scales;
@@ -192,11 +199,7 @@ w4a16_status fp8_product(const char* what, const void* x, const uint8_t* x_scale
   a.topk = per_slot ? 1 : (int)topk;
   if (p.decode)
     return launched(w4a16::launch_fp8_decode(a, in_place ? x : a.x, in_place ? dtype : (int)W4A16_E4M3, ids, s));
-  if (experts) {
-    int32_t* const start = reinterpret_cast<int32_t*>(base + p.start);
-    int32_t* const order = reinterpret_cast<int32_t*>(base + p.order);
-    const hipError_t e = w4a16::launch_expert_order(ids, start, order, (int)slots, (int)E, s);
-    if (e != hipSuccess) return launched(e);
+  if (sorts) {
     a.start = start;
     a.order = order;
   }

@@ -184,6 +184,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
 
   // ---- operands, of 64 k each
   const int wm = wave % (BM / WM) * WM, wn = wave / (BM / WM) * WN;
+  const bool idle = wm >= count;  // this wave's places are all past the last: it stages, and leaves the matrix units to others
   const uint32_t at0 = col * BK + (((2 * half) ^ turn(col)) << 4);
   auto operand = [&](const lds_u8* rows, int kk) {
     const uint32_t at = at0 ^ (64 * kk);
@@ -270,6 +271,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
       }
     }
     if (tail && s >= steps) return;
+    if (idle) sa = -1;
     if constexpr (E8M0) asm("" : "+s"(sa));  // (a branch that may be taken keeps the steps apart: gathered, they spill)
     if (sa < 0) return;
     int sb[TM];
