@@ -157,30 +157,36 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_kernel(RouteArgs a) {
 // ---- sixteen lanes a row, four rows a wave ----------------------------------------
 // Lane c of a row holds its experts V c .. V c + V - 1.
 
-// WHOLE: rows are whole 16-byte pieces, and so is each lane's part
+// The lane's part of a row, minus infinity past the last expert.  All of its loads
+// are issued at once (past the end: of the last one's place; behind a condition
+// each would be waited for alone).  WHOLE: rows are whole 16-byte pieces.
 template <int DT, int V, bool WHOLE>
-__device__ __forceinline__ void load_part(const void* logits, int64_t row, int c, int E, float (&l)[V]) {
-  constexpr int PER = DT == DT_F32 ? 4 : 8;  // logits of a piece
+__device__ __forceinline__ void load_part(const void* values, int64_t row, int c, int E, float (&l)[V]) {
+  constexpr int PER = DT == DT_F32 ? 4 : 8;  // values of a piece
+  constexpr float none = -__builtin_inff();
   if constexpr (WHOLE && V % PER == 0) {
+    u32x4 w[V / PER];
 #pragma unroll
-    for (int q = 0; q < V / PER; ++q) {
-      const int e = V * c + PER * q;
-      u32x4 w = {0u, 0u, 0u, 0u};
-      if (e < E) w = *reinterpret_cast<const u32x4*>(static_cast<const char*>(logits) + (row * E + e) * (16 / PER));
+    for (int q = 0; q < V / PER; ++q)
+      w[q] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(values) + (row * E + min(V * c + PER * q, E - PER)) * (16 / PER));
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        float v;
-        const uint32_t word = w[PER == 4 ? i : i / 2];  // (a bit cast of w[i] itself takes element 0)
-        if constexpr (DT == DT_F32) v = __builtin_bit_cast(float, word);
-        else v = act_to_f32<DT>((uint16_t)(word >> (16 * (i & 1))));
-        l[PER * q + i] = e < E ? v : -__builtin_inff();
-      }
+    for (int v = 0; v < V; ++v) {
+      const uint32_t word = w[v / PER][v % PER * 4 / PER];  // (a bit cast of the element itself takes element 0)
+      float x;
+      if constexpr (DT == DT_F32) x = __builtin_bit_cast(float, word);
+      else x = act_to_f32<DT>((uint16_t)(word >> (16 * (v & 1))));
+      l[v] = V * c + v < E ? x : none;
     }
   } else {
 #pragma unroll
-    for (int v = 0; v < V; ++v) l[v] = V * c + v < E ? load_logit<DT>(logits, row * E + V * c + v) : -__builtin_inff();
+    for (int v = 0; v < V; ++v) l[v] = load_logit<DT>(values, row * E + min(V * c + v, E - 1));
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = V * c + v < E ? l[v] : none;
   }
 }
+
+// whether any lane of this lane's row says so
+__device__ __forceinline__ bool row_any(bool b) { return (__ballot(b) >> (threadIdx.x & 48)) & 0xFFFF; }
 
 // Moves between the sixteen lanes of a row, in the vector unit.
 constexpr int dpp_rotate(int n) { return 0x120 + n; }
@@ -227,32 +233,32 @@ __device__ __forceinline__ T part_sum(const T (&x)[V]) {
     for (int v = 0; v < n; ++v) t[v] += t[v + n];
   return t[0];
 }
-// whether any lane of this lane's row says so
-__device__ __forceinline__ bool row_any(bool b) { return (__ballot(b) >> (threadIdx.x & 48)) & 0xFFFF; }
+// a or b, both by value (a choice of elements would become an index into the array)
+template <typename T>
+__device__ __forceinline__ T pick(bool which, T a, T b) { return which ? a : b; }
 
-// A group's key, from its lanes' keys.
-template <int V, typename T>
-__device__ __forceinline__ T group_key_of(const T (&key)[V], int lanes, int top, T& size) {
-  const T none = -__builtin_inf();
-  T first = none, second = none;
-#pragma unroll
-  for (int v = 0; v < V; ++v) {
-    second = max(second, min(first, key[v]));
-    first = max(first, key[v]);
+// The two largest so far
+template <typename T>
+struct TwoLargest {
+  T first = -__builtin_inf(), second = -__builtin_inf();
+  __device__ __forceinline__ void add(T k) {
+    second = max(second, min(first, k));
+    first = max(first, k);
   }
-  auto join = [&](auto ctrl) {
-    const T f = dpp<decltype(ctrl)::value>(first), s = dpp<decltype(ctrl)::value>(second);
-    second = max(max(second, s), min(first, f));
-    first = max(first, f);
-  };
-  if (lanes > 1) join(std::integral_constant<int, kDppNext>{});
-  if (lanes > 2) join(std::integral_constant<int, kDppNextPair>{});
-  if (lanes > 4) join(std::integral_constant<int, kDppMirror8>{});
-  if (lanes > 8) join(std::integral_constant<int, kDppMirror16>{});
-  // (the sum of two keys may be far smaller than they are)
-  size = first > none ? fabs(first) + (second > none ? fabs(second) : 0) : 0;
-  return top == 2 && second > none ? first + second : first;
-}
+  // over `lanes` neighbouring lanes
+  __device__ __forceinline__ void join(int lanes) {
+    auto with = [&](auto ctrl) {
+      const T f = dpp<decltype(ctrl)::value>(first), s = dpp<decltype(ctrl)::value>(second);
+      second = max(max(second, s), min(first, f));
+      first = max(first, f);
+    };
+    if (lanes > 1) with(std::integral_constant<int, kDppNext>{});
+    if (lanes > 2) with(std::integral_constant<int, kDppNextPair>{});
+    if (lanes > 4) with(std::integral_constant<int, kDppMirror8>{});
+    if (lanes > 8) with(std::integral_constant<int, kDppMirror16>{});
+  }
+  __device__ __forceinline__ T key(int top) const { return top == 2 && second > -__builtin_inf() ? first + second : first; }
+};
 // Lanes of a row whose key is before this lane's: larger, or equal and `at` lower.
 // step 2, 4, ..: one lane of that many alone, the others hold the same.
 template <typename T>
@@ -268,18 +274,47 @@ __device__ __forceinline__ int rank_of(T key, int at, int step) {
   return ahead;
 }
 
+// Batcher's network of odd and even merges for V values.
+template <int V>
+struct SortNetwork {
+  int n = 0, low[200] = {}, high[200] = {};
+  constexpr SortNetwork() {
+    for (int p = 1; p < V; p *= 2)
+      for (int k = p; k >= 1; k /= 2)
+        for (int j = k % p; j + k < V; j += 2 * k)
+          for (int i = j; i < j + k && i + k < V; ++i)
+            if (i / (2 * p) == (i + k) / (2 * p)) low[n] = i, high[n] = i + k, ++n;
+  }
+};
+// the largest first
+template <int V>
+__device__ __forceinline__ void sort_part(int (&x)[V]) {
+  constexpr SortNetwork<V> net;
+  static_for<0, net.n>([&](auto I) {
+    constexpr SortNetwork<V> with;
+    constexpr int lo = with.low[decltype(I)::value], hi = with.high[decltype(I)::value];
+    const int a = x[lo], b = x[hi];
+    x[lo] = max(a, b);
+    x[hi] = min(a, b);
+  });
+}
+
 // Keys are formed in 32 bits; what hangs on less than their error is decided by
 // the 64-bit keys of the experts concerned, so that every choice is that of the
 // 64-bit keys:
-//  - groups: all keys of the wave's rows again in 64 bits;
+//  - groups: those of the experts that may be among a group's largest;
 //  - experts: the choice goes on until the next key is clearly below (lane j holds
 //    the j-th expert), and those found are ranked by their 64-bit keys, of which
 //    the weights need the scores anyway;
 //  - a row with more than sixteen in question (a row of equal scores): route_row.
-// The error is below 2^-22 (1 + |key|): an exponential of one unit, t, in
-// 1 / (1 + t) is t / (1 + t)^2 <= 1/4 unit of 2^-23, the sum and the quotient half
-// a unit each of at most 1, and adding the bias 2^-24 |key|; softmax's rounding to
-// 32 bits of both sides and the quotient is no more.
+// The error is below 2^-22 (1 + |key|).  Sigmoid, in units of 2^-23: with t the
+// exponential, 1 / (1 + t) changes by t / (1 + t)^2 <= 1/4 of t's relative error, of
+// one unit by the instruction, and by at most 0.23 of that of the exponent x (x t /
+// (1 + t)^2 <= 0.23), of one unit by log2(e)'s rounding and the product's; half a
+// unit by the sum's rounding and one by the reciprocal's: 1.98.  Softmax rounds both
+// sides and the quotient, half a unit each.  The bias is added with 2^-24 |key|.
+// A lane sorts its keys once, as integers whose lowest bits name the place (V units
+// of 2^-23 |key| more), so that a round of the choice looks at sixteen first places.
 template <int DT, int V, bool WHOLE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs a) {
   constexpr int V64 = V > 4 ? V / 4 : 1;
@@ -292,8 +327,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs
   const int64_t m = there ? m0 + (lane >> 4) : a.M - 1;
   constexpr float none = -__builtin_inff();
   constexpr float kNear = 0x1.1p-21f;  // two keys' errors, and that of their difference
-  float l[V], key[V];
+  float l[V], key[V], b[V];
   load_part<DT, V, WHOLE>(a.logits, m, c, a.E, l);
+  if (a.bias) load_part<DT_F32, V, WHOLE>(a.bias, 0, c, a.E, b);
   bool nan = false;
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -321,33 +357,43 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs
     for (int v = 0; v < V; ++v) key[v] = whole > 0 ? (float)e[v] / whole : 0.f;
   } else if (!by_logit) {
 #pragma unroll
-    for (int v = 0; v < V; ++v) key[v] = 1.f / (1.f + expf(-l[v]));
+    for (int v = 0; v < V; ++v) key[v] = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(l[v] * -1.44269504f));
   }
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int e = V * c + v;
     if (by_logit) key[v] = l[v];
-    else if (a.bias && e < a.E) key[v] += a.bias[e];
+    else if (a.bias) key[v] += b[v];
     if (!(l[v] > none) || !(key[v] > none)) key[v] = none;
   }
   if (a.groups > 1) {
     const int lanes = a.E / a.groups / V;  // of a group: 1, 2, 4, 8 or 16
-    float size;
-    const float mine = group_key_of<V>(key, lanes, a.group_top, size);
+    TwoLargest<float> two;
+#pragma unroll
+    for (int v = 0; v < V; ++v) two.add(key[v]);
+    two.join(lanes);
+    const float mine = two.key(a.group_top);
     // (lanes past the last expert have no key and the highest places: behind)
     bool kept = rank_of(mine, c, lanes) < a.topk_groups;
     const float low = row_min(kept ? mine : __builtin_inff()), high = row_max(kept ? none : mine);
-    size = row_max(size);
+    // (the sum of two keys may be far smaller than they are)
+    const float size = row_max(two.first > none ? fabsf(two.first) + (two.second > none ? fabsf(two.second) : 0.f) : 0.f);
     const bool close = !by_logit && high > none && !(low - high > 1.25f * kNear * (2 + size));
     if (__ballot(close)) {
-      double k[V], unused;
+      const float least = a.group_top == 2 ? two.second : two.first, from = least - kNear * (1 + fabsf(least));
+      uint32_t concerned = 0;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int e = V * c + v;
-        k[v] = key[v] > none ? score_of(l[v]) + (a.bias ? (double)a.bias[e] : 0.0) : (double)none;
+      for (int v = 0; v < V; ++v) concerned |= key[v] > none && !(key[v] < from) ? 1u << v : 0u;
+      TwoLargest<double> exact;
+      while (__ballot(concerned)) {
+        const int at = concerned ? __builtin_ctz(concerned) : -1;
+        concerned &= concerned - 1;
+        float x = none;
+#pragma unroll
+        for (int v = 0; v < V; ++v) x = pick(v == at, l[v], x);
+        if (at >= 0) exact.add(score_of(x) + (a.bias ? (double)a.bias[V * c + at] : 0.0));
       }
-      const double exact = group_key_of<V>(k, lanes, a.group_top, unused);
-      kept = rank_of(exact, c, lanes) < a.topk_groups;
+      exact.join(lanes);
+      kept = rank_of(exact.key(a.group_top), c, lanes) < a.topk_groups;
     }
     if (!kept) {
 #pragma unroll
@@ -355,42 +401,41 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs
     }
   }
   // the largest key, then the next
+  constexpr int empty = INT32_MIN;
   int left[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) left[v] = ordered(key[v]);
-  const int empty = ordered(none);
+  for (int v = 0; v < V; ++v) left[v] = pick(key[v] > none, (ordered(key[v]) & -V) | (V - 1 - v), empty);
+  sort_part<V>(left);
+  // logits of 16 bits are whole in what is left of 32
+  const bool whole_keys = by_logit && DT != DT_F32;
   int id = -1;
   float before = __builtin_inff();
   bool doubt = false, open = true;  // open: the j-th may be as large as the last one chosen
   for (int j = 0;; ++j) {
-    int best = left[0];
-#pragma unroll
-    for (int v = 1; v < V; ++v) best = max(best, left[v]);
-    const int most = row_max(best);
+    const int head = left[0] & -V, most = row_max(head);  // (INT32_MIN stays itself)
     const float k = of_ordered(most);
-    const bool close = !by_logit && j > 0 && most > empty && !(before - k > kNear * (1 + fabsf(k)));
+    const float near = V * 0x1p-23f * fabsf(k) + 0x1p-120f + (by_logit ? 0.f : kNear * (1 + fabsf(k)));
+    const bool close = !whole_keys && j > 0 && most != empty && !(before - k > near);
     if (j >= a.topk) {
       open &= close;
       if (j == 16 || !__ballot(open)) break;
     }
     doubt |= open && close;
     before = k;
-    const uint32_t hits = (uint32_t)(__ballot(best == most && most > empty) >> (lane & 48)) & 0xFFFF;
-    const int owner = hits ? __builtin_ctz(hits) : -1;  // the lowest lane: the lowest experts
-    int at = -1;
+    const uint32_t hits = (uint32_t)(__ballot(head == most) >> (lane & 48)) & 0xFFFF;
+    const bool taken = c == __builtin_ctz(hits);  // the lowest lane: the lowest experts
+    const int e = row_max(taken ? V * c + V - 1 - (left[0] & (V - 1)) : -1);
+    if (c == j && open && most != empty) id = e;
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v) at = left[v] == most ? v : at;
-    at = c == owner ? at : -1;
-#pragma unroll
-    for (int v = 0; v < V; ++v) left[v] = v == at ? empty : left[v];
-    const int e = row_max(at < 0 ? -1 : V * c + at);
-    id = c == j && open ? e : id;
+    for (int v = 0; v + 1 < V; ++v) left[v] = pick(taken, left[v + 1], left[v]);
+    left[V - 1] = pick(taken, empty, left[V - 1]);
   }
   double weight = 0;
   int slot = c;
   if (id >= 0) weight = score_of(load_logit<DT>(a.logits, m * a.E + id));
   if (__ballot(doubt)) {
-    const double k = id >= 0 ? weight + (a.bias ? (double)a.bias[id] : 0.0) : (double)none;
+    double k = none;
+    if (id >= 0) k = by_logit ? (double)load_logit<DT>(a.logits, m * a.E + id) : weight + (a.bias ? (double)a.bias[id] : 0.0);
     slot = rank_of(k, id >= 0 ? id : kMaxExperts + c, 1);
   }
   if (slot >= a.topk) weight = 0;
@@ -549,7 +594,7 @@ hipError_t launch_route(const RouteArgs& a, hipStream_t s) {
   // sixteen lanes a row for up to 512 experts and 16 of them chosen, where a group is a power of two of lanes
   const int v = part_of(a.E), per = a.E / a.groups;
   const bool quick = a.E <= 512 && a.topk <= 16 && (a.groups == 1 || (per % v == 0 && (per / v & (per / v - 1)) == 0 && per / v <= 16));
-  const bool whole = whole_rows(a.logits, nullptr, a.E, a.dtype);
+  const bool whole = whole_rows(a.logits, a.bias, a.E, a.dtype);
   by_type(a.dtype, [&](auto dt) {
     constexpr int DT = decltype(dt)::value;
     if (quick)
