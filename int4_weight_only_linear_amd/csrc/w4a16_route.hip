@@ -456,15 +456,33 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs
 }
 
 // The gradient, sixteen lanes a row: lane j has slot j's gradient (and those of
-// slots j + 16, ..), and every lane adds what meets its own experts.
+// slots j + 16, ..), and every lane adds what meets its own experts.  Lanes take
+// turns over a row's pieces, so that a row's loads and stores are whole lines.
 template <int DT, int V, bool WHOLE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteBackwardArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, base = lane & 48;
   const int64_t row = ((int64_t)blockIdx.x * kRouteWaves + wave) * 4 + (lane >> 4);
   if (row - (lane >> 4) >= a.M) return;
   const int64_t m = min(row, a.M - 1);
+  constexpr int PER = DT == DT_F32 ? 4 : 8, P = WHOLE && V % PER == 0 ? PER : 1;  // experts of a piece
+  auto place = [](int v) { return v / P * 16 * P + v % P; };  // the lane's v-th expert is place(v) + P c
   float s[V], ds[V];
-  load_part<DT, V, WHOLE>(a.logits, m, c, a.E, s);
+  u32x4 w[V / P];
+#pragma unroll
+  for (int i = 0; i < V / P; ++i) {
+    const int64_t at = m * a.E + min(place(P * i) + P * c, a.E - P);
+    if constexpr (P > 1) w[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.logits) + at * (16 / PER));
+    else s[i] = load_logit<DT>(a.logits, at);
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if constexpr (P > 1) {
+      const uint32_t word = w[v / PER][v % PER * 4 / PER];
+      if constexpr (DT == DT_F32) s[v] = __builtin_bit_cast(float, word);
+      else s[v] = act_to_f32<DT>((uint16_t)(word >> (16 * (v & 1))));
+    }
+    if (place(v) + P * c >= a.E) s[v] = -__builtin_inff();
+  }
   bool nan = false;
 #pragma unroll
   for (int v = 0; v < V; ++v) nan |= s[v] != s[v], ds[v] = 0.f;
@@ -519,10 +537,10 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
     }
     const int n = min(16, a.topk - j0);
     for (int k = 0; k < n; ++k) {
-      const int e = __shfl(id, base + k) - V * c;
+      const int e = __shfl(id, base + k) - P * c;
       const float gk = __shfl(g, base + k);
 #pragma unroll
-      for (int v = 0; v < V; ++v) ds[v] += e == v ? gk : 0.f;
+      for (int v = 0; v < V; ++v) ds[v] += e == place(v) ? gk : 0.f;
     }
   }
   float dot = 0.f;
@@ -536,24 +554,20 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
 #pragma unroll
   for (int v = 0; v < V; ++v) dl[v] = nan ? __builtin_nanf("") : (a.sigmoid ? ds[v] : s[v] * (ds[v] - dot));
   if (row >= a.M) return;
-  constexpr int PER = DT == DT_F32 ? 4 : 8;
-  if constexpr (WHOLE && V % PER == 0) {
 #pragma unroll
-    for (int q = 0; q < V / PER; ++q) {
-      const int e = V * c + PER * q;
-      if (e >= a.E) continue;
-      u32x4 w;
+  for (int i = 0; i < V / P; ++i) {
+    const int e = place(P * i) + P * c;
+    if (e >= a.E) continue;
+    if constexpr (P > 1) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (DT == DT_F32) w[i] = __builtin_bit_cast(uint32_t, dl[PER * q + i]);
-        else w[i] = f32x2_to_act_pair<DT>(dl[PER * q + 2 * i], dl[PER * q + 2 * i + 1]);
+      for (int h = 0; h < 4; ++h) {
+        if constexpr (DT == DT_F32) w[i][h] = __builtin_bit_cast(uint32_t, dl[P * i + h]);
+        else w[i][h] = f32x2_to_act_pair<DT>(dl[P * i + 2 * h], dl[P * i + 2 * h + 1]);
       }
-      *reinterpret_cast<u32x4*>(static_cast<char*>(a.dlogits) + (m * a.E + e) * (16 / PER)) = w;
+      *reinterpret_cast<u32x4*>(static_cast<char*>(a.dlogits) + (m * a.E + e) * (16 / PER)) = w[i];
+    } else {
+      store_logit<DT>(a.dlogits, m * a.E + e, dl[i]);
     }
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (V * c + v < a.E) store_logit<DT>(a.dlogits, m * a.E + V * c + v, dl[v]);
   }
 }
 
