@@ -11,7 +11,10 @@ namespace {
 
 // A wave takes a run of 512 values of a row: eight a lane, so that sixteen lanes
 // hold a block of 128 and the wave the four scales of a word.  ALIGNED: rows
-// are whole 16-byte pieces; otherwise values are loaded one by one.
+// are whole 16-byte pieces; otherwise values are loaded one by one.  A block's
+// largest value goes over sixteen lanes, and a value's code is the matrix unit's own
+// conversion with the scale's power of two, rounded once.  Bound by memory: 8192 x
+// 14336 65 us, 5.4 TB/s; 67 x 2560 2.7 us, a launch.
 struct QuantizeParams {
   const uint16_t* x;
   uint8_t* codes;
@@ -52,7 +55,8 @@ __global__ __launch_bounds__(256) void quantize_kernel(QuantizeParams p) {
 // their own and those below e, and after one barrier write theirs behind the
 // waves before them.  No atomics, so the order is always the same.  Bound by the
 // latency of its loads, sixteen of which are under way at a time: 16384 slots of
-// 64 experts .. us (one at a time 11.6).
+// 64 experts 10 us together with 2048 rows' quantisation, 11.6 and 7.4 one after
+// the other with one load at a time.
 constexpr int kOrderWaves = 16, kOrderLoads = 16;
 struct OrderParams {
   const int32_t* ids;

@@ -46,6 +46,10 @@ __device__ __forceinline__ f32x4 mfma16(i32x8 a, i32x8 b, f32x4 c, int sa, int s
 // that slot and the next ones of the same expert, sixteen together, where an
 // even sixteen of them come before it, and nothing otherwise; so an expert's
 // weights are read once for sixteen of its slots, without a list made before.
+// Bound by memory where the weights are many (8 tokens, 8 of 128 experts, 2048 x 1536, 35
+// us, 4.7 TB/s), by the latency of a launch and two trips to memory where they are
+// few (4096 x 4096, one token: 6.2 us in the kernel, 3.4 of them its bytes).  One
+// launch: quantising first took 14.9 us for that token, 8.3 now.
 template <int DT, bool E8M0, int TN>
 __global__ __launch_bounds__(1024) void fp8_decode_kernel(DecodeParams p) {
   extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
@@ -197,12 +201,19 @@ void launch_decode(const DecodeParams& p, bool e8m0, int64_t slots, int waves, h
 
 }  // namespace
 
+// Where this kernel beats the tiles, us of both: 4096 x 4096 7.2 and 11.0 with one
+// token, 10.7 and 11.5 with 8, 11.0 and 11.4 with 9 (left to the tiles); 4096 x
+// 28672 27.6 and 29.4 with 2, 32.6 and 29.6 with 4; 14336 x 4096 21.9 and 23.6 with
+// 8.  64 experts of 4096 x 2048, 8 a token: 106 and 116 with 16 tokens (2 slots an
+// expert), 133 and 124 with 24.
 bool fp8_decodes(int64_t M, int64_t N, int64_t K, int E, bool experts, bool transpose) {
   if (transpose) return false;
   if (!experts) return M <= 2 || (M <= 8 && N * K <= int64_t(1) << 26);
   return M <= 1024 && M <= 2 * (int64_t)E && M * ((N + 15) / 16) <= kMaxFp8Tiles;
 }
 
+// The codes of a workgroup's tokens leave room for a second workgroup on a CU;
+// longer rows are quantised by a launch of their own.
 bool fp8_decode_quantizes(int64_t M, int64_t K) {
   return decode_lds(std::min<int64_t>(16, M), fp8_columns(K) / kFp8Block) <= 80 * 1024;
 }
@@ -231,7 +242,8 @@ hipError_t launch_fp8_decode(const Fp8Args& a, const void* x, int x_dtype, const
   p.f16 = a.dtype == DT_F16;
   const int64_t slots = ids ? a.M : 1;
   // four blocks to a wave, all of them on their way at once; 32 features a workgroup where 16 would give
-  // more than eight for each CU
+  // more than eight for each CU (64 experts of 4096 x 2048: 54.2 us with 32, 58.8 with 16 for 32 slots, 78.7 and
+  // 92.9 for 64)
   const int waves = std::clamp((p.blocks + 3) / 4, 1, 16);
   const bool two = (a.N + 31) / 32 * slots >= 1024;
   auto go = [&](auto dt) {

@@ -86,6 +86,13 @@ __device__ __forceinline__ bool find_tile(const int32_t* start, int E, int t, in
   return false;
 }
 
+// What bounds it at 1920 x 28672 x 4096 (305 us, 1.48 PFLOP/s with fp32 scales): the
+// card's power.  The clock falls to 1.97 GHz with the matrix units 36 % busy, and
+// neither more stages (steps of 64 k, four deep), nor three workgroups a CU, nor
+// tiles of 256 x 256, nor other orders of loads, reads and products change it by
+// more than 5 %; without the change of unit (E8M0 scales) it is 1.47 to 1.66 at the
+// same clock.  Of experts' slots (294 us, 16384 of 64 experts x 4096 x 2048) a
+// quarter of the tiles' rows are past a tile's last slot.
 // A workgroup owns BM tokens (or slots of one expert) x BN features and one K
 // range, in steps of a block of 128 k; its waves own WM x WN of it each.  A
 // step's rows of x and w go straight from memory to LDS, one step ahead; the
@@ -351,7 +358,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
   else store(std::integral_constant<int, DT_BF16>{});
 }
 
-// y = the K ranges' sums in range order, and the bias
+// y = the K ranges' sums in range order, and the bias.  (67 x 4096 in ten ranges: 4.2 us.)
 template <int DT>
 __global__ __launch_bounds__(256) void fp8_sum_kernel(const float* __restrict__ part, const uint16_t* __restrict__ bias,
                                                       uint16_t* __restrict__ y, int64_t values, int N, int splits) {

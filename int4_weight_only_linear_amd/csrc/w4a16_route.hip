@@ -1,4 +1,7 @@
-// Routing of tokens to experts and its gradient.
+// Routing of tokens to experts and its gradient (include/w4a16.h, w4a16_route):
+//   s = softmax(l) or sigmoid(l), key = s + bias, the largest keys of the groups kept,
+//   w = s of those, over their sum where asked, times a scale.
+// Every choice is that of keys in 64 bits; equal keys go to the lower expert.
 #include <algorithm>
 
 #include "w4a16_device.hpp"
@@ -39,7 +42,10 @@ __device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOM
 
 constexpr int kRouteWaves = 4;
 
-// A row by one wave, keys in 64 bits, V experts a lane (expert 64 v + lane);
+// A row by one wave, keys in 64 bits, V experts a lane (expert 64 v + lane): what
+// the rows of more than 512 experts or 16 choices take (16384 rows of 256 take 57.6
+// us here, of which 64-bit exponentials and wave-wide reductions of pairs are most,
+// and 14.8 with sixteen lanes a row), and single rows of equal keys;
 // keys [64 V] and group_key [kMaxGroups] are the wave's own LDS.
 template <int DT, int V>
 __device__ void route_row(const RouteArgs& a, int64_t m, double* keys, double* group_key) {
@@ -314,7 +320,10 @@ __device__ __forceinline__ void sort_part(int (&x)[V]) {
 // unit by the sum's rounding and one by the reciprocal's: 1.98.  Softmax rounds both
 // sides and the quotient, half a unit each.  The bias is added with 2^-24 |key|.
 // A lane sorts its keys once, as integers whose lowest bits name the place (V units
-// of 2^-23 |key| more), so that a round of the choice looks at sixteen first places.
+// of 2^-23 |key| more), so that a round of the choice looks at sixteen first places
+// (rounds that search all V and take one out: 2 us more at 16384 x 256).
+// Bound by the chain of a wave's instructions, of which four rows share one: 16384 x
+// 256 in fp32 with 8 groups 14.8 us, 1.2 TB/s; 4 rows 4.7 us in the kernel.
 template <int DT, int V, bool WHOLE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs a) {
   constexpr int V64 = V > 4 ? V / 4 : 1;
@@ -457,7 +466,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs
 
 // The gradient, sixteen lanes a row: lane j has slot j's gradient (and those of
 // slots j + 16, ..), and every lane adds what meets its own experts.  Lanes take
-// turns over a row's pieces, so that a row's loads and stores are whole lines.
+// turns over a row's pieces, so that a row's loads and stores are whole lines (parts
+// of 64 bytes a lane: 13.4 us at 16384 x 256).  In fp32.  Memory and the slots' chain
+// bound it: 16384 x 256 in fp32 10.3 us, 3.4 TB/s.
 template <int DT, int V, bool WHOLE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteBackwardArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, base = lane & 48;

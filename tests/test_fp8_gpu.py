@@ -451,3 +451,39 @@ def test_the_routers_choice_feeds_the_4_bit_experts():
     got = y.cpu().double().numpy()
     assert np.abs(got - ref.reshape(got.shape)).max() <= TOL[1] * np.abs(ref).max()
     assert not got[2 * topk + 1].any()
+
+
+@pytest.mark.parametrize("M,N,K", [(8, 192, 9216), (8, 96, 9856), (8, 96, 10240), (2, 64, 38400), (2, 64, 40960)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_few_tokens_of_many_features(M, N, K, dtype):
+    # the tokens' codes fill more than half of a CU's memory, or are made by a launch of their own
+    rng = np.random.default_rng([M, N, K])
+    layer = Layer(rng, N, K, False, dtype == "f16", bias=dtype)
+    x = values(rng, M, K, dtype)
+    codes, scales = X.fp8_quantize_ref(x.double().numpy())
+    t = X.e4m3_values()
+    ref = (t[codes[:, :K]] * np.repeat(2.0 ** (scales - 127.0), 128, 1)[:, :K]) @ (t[layer.w] * X.spread(layer.ws, N, K)).T
+    ref += layer.bias.cpu().double().numpy()
+    y = L.w4a16_minifloat_linear(x.cuda(), layer.tw, layer.ts, layer.bias)
+    assert np.abs(y.cpu().double().numpy() - ref).max() <= TOL[0 if dtype == "f16" else 1] * np.abs(ref).max()
+    c, s = L.w4a16_minifloat_quantize(x.cuda())
+    y2 = L.w4a16_minifloat_linear(c, layer.tw, layer.ts, layer.bias, x_scales=s, dtype=TYPES[dtype])
+    assert torch.equal(y.view(torch.int16), y2.view(torch.int16))
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_experts_with_a_few_slots_more_than_a_tile(transpose):
+    # tiles whose last half, quarter or all but one place is empty, beside full ones
+    rng = np.random.default_rng(12)
+    N, K = 144, 272
+    ids = np.repeat(np.arange(8), [129, 160, 192, 193, 224, 255, 256, 1])
+    layer = Layer(rng, N, K, transpose, False, E=8)
+    x = values(rng, len(ids), K, "bf16")
+    order = rng.permutation(len(ids))
+    ids = ids[order].astype(np.int32).reshape(-1, 1)
+    y = L.w4a16_minifloat_moe_linear(x.cuda(), layer.tw, layer.ts, torch.from_numpy(ids).cuda(), transpose=transpose)
+    codes, scales = X.fp8_quantize_ref(x.double().numpy())
+    for e in range(8):
+        rows = np.nonzero(ids[:, 0] == e)[0]
+        ref, slack = X.fp8_linear_ref(codes[rows], scales[rows], layer.w[e], layer.ws[e], K, transpose)
+        check(y.reshape(len(ids), -1)[torch.from_numpy(rows).cuda()], ref, slack, "bf16")

@@ -222,3 +222,55 @@ def test_out_streams_and_graphs():
     with pytest.raises(L.W4A16Error):
         L.w4a16_route(t, 300, **kw)
     assert L.w4a16_route(t[:0], 8, **kw)[0].shape == (0, 8)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,kept,top", [(256, 8, 4, 2), (256, 8, 3, 1), (64, 4, 2, 2), (512, 2, 1, 2), (16, 16, 5, 1), (32, 16, 7, 2)])
+def test_groups_next_to_each_other(score, E, groups, kept, top):
+    # every group holds the same logits in an order of its own, some of them moved by a unit, and biases
+    # far larger than what the groups differ by: sums that 32 bits cannot tell apart
+    rng = np.random.default_rng([E, groups, top])
+    per = E // groups
+    l = np.empty((40, E), dtype=np.float32)
+    for m in range(40):
+        part = rng.normal(0, 1.5, per).astype(np.float32)
+        for g in range(groups):
+            l[m, g * per:(g + 1) * per] = rng.permutation(part)
+        for e in rng.integers(0, E, 3) if m % 2 else ():
+            l[m, e] = np.nextafter(l[m, e], np.float32(np.inf if m % 4 == 1 else -np.inf))
+    kw = dict(score=score, groups=groups, topk_groups=kept, group_top=top, renormalize=True)
+    topk = min(8, kept * per)
+    for bias in (None, np.zeros(E, np.float32), np.tile(np.where(np.arange(per) % 2, 3.0, -3.0).astype(np.float32), groups)):
+        tb = None if bias is None else torch.from_numpy(bias).cuda()
+        check(l.astype(np.float64), L.w4a16_route(torch.from_numpy(l).cuda(), topk, tb, **kw), topk, bias, **kw)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("E", [32, 100, 256, 512, 513])
+@pytest.mark.parametrize("topk", [1, 15, 16, 17])
+def test_many_equal_keys(dtype, E, topk):
+    # more equal keys than sixteen, at the front, across the last choice, and behind it
+    rng = np.random.default_rng([E, topk])
+    for equal in (3, 16, 17, 24, E):
+        l = rng.normal(0, 1, (9, E))
+        for m in range(9):
+            l[m, rng.permutation(E)[:equal]] = 2.5 if m % 3 == 0 else (0.5 if m % 3 == 1 else -1.0)
+        t = torch.from_numpy(l).to(TYPES[dtype])
+        l = t.double().numpy()
+        for score in ("softmax", "sigmoid"):
+            for bias in (None, np.full(E, 0.25, np.float32)):
+                tb = None if bias is None else torch.from_numpy(bias).cuda()
+                check(l, L.w4a16_route(t.cuda(), topk, tb, score=score), topk, bias, score=score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_logits_far_out_and_unaligned(score):
+    # scores that saturate, biases of every size, and a bias that starts 4 bytes behind a 16-byte piece
+    rng = np.random.default_rng(8)
+    l = (rng.normal(0, 60, (64, 128)) * rng.choice([1e-3, 1, 10], (64, 1))).astype(np.float32)
+    b = (rng.normal(0, 1, 129) * 10.0 ** rng.integers(-8, 9, 129)).astype(np.float32)
+    tb = torch.from_numpy(b).cuda()[1:]
+    assert tb.data_ptr() % 16 == 4
+    for g, kept, top in ((1, 1, 1), (8, 3, 1), (8, 3, 2)):
+        kw = dict(score=score, groups=g, topk_groups=kept, group_top=top)
+        check(l.astype(np.float64), L.w4a16_route(torch.from_numpy(l).cuda(), 8, tb, **kw), 8, b[1:], **kw)
