@@ -234,6 +234,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
   float unit_of = 1.f, ratio = 1.f, ws_next = 0.f;
   if constexpr (!E8M0) ws_next = *(const_float*)(static_cast<const float*>(p.ws) + scale_at(0));
   int sa = 127;
+  bool zero = false;
   auto next_scale = [&](int s) {
     if constexpr (E8M0) {
       // (a word at a time: it holds the byte, so it lies in the same allocation)
@@ -245,11 +246,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
       sa = (int)field;
       if (field == 255) u = ws_next, sa = 127;      // infinite or NaN
       if (field == 0) u = ws_next * 0x1p126f, sa = 1;  // below the normal numbers
-      if (u == 0.f) {
-        ratio = 1.f, sa = -1;  // (the block adds nothing)
-      } else {
-        ratio = unit_of / u, unit_of = u;
-      }
+      zero = u == 0.f;
+      if (zero) ratio = 1.f, sa = 127;
+      else ratio = unit_of / u, unit_of = u;
     }
   };
 
@@ -297,6 +296,15 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
     for (int t = 0; t < TM; ++t)
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) b[t][kk] = operand(cx + (wm + 32 * t) * BK, kk);
+    if (!E8M0 && zero) {
+      // a scale of zero: the block's weights are zeros, but for the NaN codes among them
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) a[n][kk][e] = ((((a[n][kk][e] & 0x7F7F7F7F) + 0x01010101) >> 7) & 0x01010101) * 0x7F;
+    }
     static_for<0, TM * TN>([&](auto J) {
       constexpr int t = decltype(J)::value / TN, n = decltype(J)::value % TN;
       f32x16& c = acc[n][t];

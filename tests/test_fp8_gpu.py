@@ -487,3 +487,45 @@ def test_experts_with_a_few_slots_more_than_a_tile(transpose):
         rows = np.nonzero(ids[:, 0] == e)[0]
         ref, slack = X.fp8_linear_ref(codes[rows], scales[rows], layer.w[e], layer.ws[e], K, transpose)
         check(y.reshape(len(ids), -1)[torch.from_numpy(rows).cuda()], ref, slack, "bf16")
+
+
+@pytest.mark.parametrize("M", [1, 5, 40, 100, 150])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("experts", [False, True])
+def test_a_zero_scale_keeps_what_is_not_a_number(M, transpose, experts):
+    # blocks of scale zero between others: their weights count as zeros, and a NaN of x or w in one stays one
+    rng = np.random.default_rng(M)
+    N, K = 272, 528
+    layer = Layer(rng, N, K, transpose, False, E=2 if experts else None)
+    zero = rng.random(layer.ws.shape) < 0.5
+    zero[..., 0, 0] = True
+    zero[..., -1, -1] = False
+    layer.ts[torch.from_numpy(zero).cuda()] = 0
+    w = layer.w.copy()
+    k, n = 5, 7                           # in the first block, whose scale is zero
+    w[..., k if transpose else n, n if transpose else k] = 255
+    x = values(rng, M, K, "bf16")
+    x[M // 2, 9] = float("nan")
+    ws = np.where(zero, 0.0, layer.ws)
+    tw = torch.from_numpy(w).view(torch.float8_e4m3fn).cuda()
+    codes, scales = X.fp8_quantize_ref(x.double().numpy())
+    if experts:
+        ids = torch.from_numpy(rng.integers(0, 2, (M, 1)).astype(np.int32))
+        y = L.w4a16_minifloat_moe_linear(x.cuda(), tw, layer.ts, ids.cuda(), transpose=transpose).cpu()
+    else:
+        ids = torch.zeros((M, 1), dtype=torch.int32)
+        y = L.w4a16_minifloat_linear(x.cuda(), tw, layer.ts, transpose=transpose).cpu()
+    for e in range(2):
+        rows = np.nonzero(ids[:, 0].numpy() == e)[0]
+        if not len(rows):
+            continue
+        we, se = (w[e], ws[e]) if experts else (w, ws)
+        got = y[rows].double().numpy()
+        nan = np.zeros((len(rows), N), dtype=bool)
+        nan[:, n] = True
+        nan[rows == M // 2] = True
+        assert np.array_equal(np.isnan(got), nan)
+        ok, c = np.where(we == 255, 0, we).astype(np.uint8), np.where(np.isin(codes[rows], (127, 255)), 0, codes[rows]).astype(np.uint8)
+        ref, slack = X.fp8_linear_ref(c, scales[rows], ok, se, K, transpose)
+        allowed = torch.finfo(torch.bfloat16).eps / 2 * (np.abs(ref) + slack) + slack
+        assert (np.abs(got - ref) <= allowed)[~nan].all()
