@@ -758,11 +758,12 @@ def w4a16_route(logits, topk: int, bias=None, *, score: str = "softmax", groups:
     _require_device(logits, "logits", device)
     if out is None:
         weights, ids = logits.new_empty((M, topk), dtype=torch.float32), logits.new_empty((M, topk), dtype=torch.int32)
+        _require_all(device, (bias, "bias"))
     else:
         weights, ids = out
         if weights.dtype != torch.float32 or ids.dtype != torch.int32 or weights.shape != (M, topk) or ids.shape != (M, topk):
             raise ValueError(f"out must be float32 and int32 {(M, topk)}")
-    _require_all(device, (bias, "bias"), (weights, "weights"), (ids, "ids"))
+        _require_all(device, (bias, "bias"), (weights, "weights"), (ids, "ids"))
     _invoke(device, lib.w4a16_route, logits.data_ptr(), _ptr(bias), weights.data_ptr(), ids.data_ptr(), M, E, topk, groups,
             topk_groups, group_top, code, _score_code(score), int(bool(renormalize)), scale, _raw_stream(device))
     return weights, ids
@@ -823,40 +824,55 @@ def w4a16_minifloat_quantize(x, *, out=None):
 
 
 def _fp8_args(x, w, scales, bias, transpose, x_scales, dtype, rows, lead):
-    """Checks of both products; lead: () or (E,).  Returns (output dtype, its code, x's code,
-    the scales' code, N, K)."""
+    """Checks of both products; lead: () or (E,).  Returns (device, output dtype, its code, x's
+    code, the scales' code, x's rows, N, K)."""
     torch = _torch()
-    if w.dim() != 2 + len(lead) or w.dtype != torch.float8_e4m3fn:
-        raise TypeError(f"w must be float8_e4m3fn with {2 + len(lead)} dimensions, got {w.dtype} {tuple(w.shape)}")
-    if scales.dtype not in (torch.float32, torch.float8_e8m0fnu):
-        raise TypeError(f"scales must be float32 or float8_e8m0fnu, got {scales.dtype}")
-    K, N = w.shape[-2:] if transpose else w.shape[:-3:-1]
-    if scales.shape != lead + (_blocks(w.shape[-2]), _blocks(w.shape[-1])):
-        raise ValueError(f"scales are {tuple(scales.shape)}, expected {lead + (_blocks(w.shape[-2]), _blocks(w.shape[-1]))}")
-    if x.dim() != 2 or (rows is not None and x.shape[0] != rows):
-        raise ValueError(f"x must be 2-D [{'M' if rows is None else rows}, K], got {tuple(x.shape)}")
-    if x.dtype == torch.float8_e4m3fn:
+    shape, s_dtype, x_dtype, x_shape = w.shape, scales.dtype, x.dtype, x.shape
+    if len(shape) != 2 + len(lead) or w.dtype != torch.float8_e4m3fn:
+        raise TypeError(f"w must be float8_e4m3fn with {2 + len(lead)} dimensions, got {w.dtype} {tuple(shape)}")
+    if s_dtype == torch.float32:
+        s_code = W4A16_F32
+    elif s_dtype == torch.float8_e8m0fnu:
+        s_code = W4A16_E8M0
+    else:
+        raise TypeError(f"scales must be float32 or float8_e8m0fnu, got {s_dtype}")
+    R, C = shape[-2:]
+    K, N = (R, C) if transpose else (C, R)
+    expected = (*lead, (R + 127) // 128, (C + 127) // 128)
+    if scales.shape != expected:
+        raise ValueError(f"scales are {tuple(scales.shape)}, expected {expected}")
+    if len(x_shape) != 2 or (rows is not None and x_shape[0] != rows):
+        raise ValueError(f"x must be 2-D [{'M' if rows is None else rows}, K], got {tuple(x_shape)}")
+    if x_dtype == torch.float8_e4m3fn:
         x_code, dtype = W4A16_E4M3, torch.bfloat16 if dtype is None else dtype
         if dtype not in (torch.float16, torch.bfloat16):
             raise TypeError(f"dtype must be float16 or bfloat16, got {dtype}")
-        if x.shape[1] != _blocks(K) * 128:
-            raise ValueError(f"codes are {tuple(x.shape)}, expected {_blocks(K) * 128} columns for K={K}")
-        if x_scales is None or x_scales.dtype != torch.float8_e8m0fnu or x_scales.shape != (x.shape[0], (K + 511) // 512 * 4):
-            raise ValueError(f"codes need x_scales, float8_e8m0fnu {(x.shape[0], (K + 511) // 512 * 4)}")
+        if x_shape[1] != _blocks(K) * 128:
+            raise ValueError(f"codes are {tuple(x_shape)}, expected {_blocks(K) * 128} columns for K={K}")
+        if x_scales is None or x_scales.dtype != torch.float8_e8m0fnu or x_scales.shape != (x_shape[0], (K + 511) // 512 * 4):
+            raise ValueError(f"codes need x_scales, float8_e8m0fnu {(x_shape[0], (K + 511) // 512 * 4)}")
+        dt = W4A16_F16 if dtype == torch.float16 else W4A16_BF16
     else:
-        x_code = _act_code(x)
-        if x_scales is not None or dtype not in (None, x.dtype):
+        dt = x_code = _act_code(x)
+        if x_scales is not None or (dtype is not None and dtype != x_dtype):
             raise ValueError("x_scales and another dtype go with float8_e4m3fn codes")
-        dtype = x.dtype
-        if x.shape[1] != K:
-            raise ValueError(f"x is {tuple(x.shape)}, expected {K} columns")
-    if bias is not None and (bias.dtype != dtype or bias.shape != lead + (N,)):
-        raise ValueError(f"bias must be {dtype} {lead + (N,)}")
+        dtype = x_dtype
+        if x_shape[1] != K:
+            raise ValueError(f"x is {tuple(x_shape)}, expected {K} columns")
+    if bias is not None and (bias.dtype != dtype or bias.shape != (*lead, N)):
+        raise ValueError(f"bias must be {dtype} {(*lead, N)}")
     device = x.device
     _require_device(x, "x", device)
     _require_all(device, (w, "w"), (scales, "scales"), (bias, "bias"), (x_scales, "x_scales"))
-    return (dtype, W4A16_F16 if dtype == torch.float16 else W4A16_BF16, x_code,
-            W4A16_F32 if scales.dtype == torch.float32 else W4A16_E8M0, N, K)
+    return device, dtype, dt, x_code, s_code, x_shape[0], N, K
+
+
+def _fp8_workspace(device, stream, workspace, fn, *sizes):
+    """(its pointer, its bytes): the caller's, or the one of the device and stream."""
+    if workspace is not None:
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    workspace = _workspace(device, stream, _size_of(device, fn, *sizes))
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
 
 
 def _fp8_out(x, out, dtype, shape):
@@ -880,14 +896,10 @@ def w4a16_minifloat_linear(x, w, scales, bias=None, *, transpose: bool = False, 
     transpose w is [K, N], y = x . (w * scales): w4a16_minifloat_linear(dy, w, scales, transpose=True) is
     the gradient of a layer's input.  Not recorded by autograd.  workspace: as for
     w4a16_lora_linear, of w4a16_minifloat_linear_workspace_size."""
-    dtype, dt, x_code, s_code, N, K = _fp8_args(x, w, scales, bias, transpose, x_scales, dtype, None, ())
-    M, device = x.shape[0], x.device
+    device, dtype, dt, x_code, s_code, M, N, K = _fp8_args(x, w, scales, bias, transpose, x_scales, dtype, None, ())
     out = _fp8_out(x, out, dtype, (M, N))
     stream, transpose = _raw_stream(device), int(bool(transpose))
-    if workspace is None:
-        workspace = _workspace(device, stream, _size_of(device, lib.w4a16_minifloat_linear_workspace_size, M, N, K, x_code, transpose))
-    ws_ptr = None if workspace is None else workspace.data_ptr()
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_ptr, ws_bytes = _fp8_workspace(device, stream, workspace, lib.w4a16_minifloat_linear_workspace_size, M, N, K, x_code, transpose)
     _invoke(device, lib.w4a16_minifloat_linear, x.data_ptr(), _ptr(x_scales), w.data_ptr(), scales.data_ptr(), _ptr(bias),
             out.data_ptr(), M, N, K, x_code, s_code, dt, transpose, ws_ptr, ws_bytes, stream)
     return out
@@ -909,18 +921,15 @@ def w4a16_minifloat_moe_linear(x, w, scales, topk_ids, topk_weights=None, bias=N
         raise TypeError("topk_ids must be int32 [M, topk]")
     M, topk = topk_ids.shape
     E = w.shape[0]
-    dtype, dt, x_code, s_code, N, K = _fp8_args(x, w, scales, bias, transpose, x_scales, dtype, M * topk if x_per_slot else M, (E,))
+    device, dtype, dt, x_code, s_code, _, N, K = _fp8_args(x, w, scales, bias, transpose, x_scales, dtype,
+                                                           M * topk if x_per_slot else M, (E,))
     if topk_weights is not None and (topk_weights.dtype != torch.float32 or topk_weights.shape != (M, topk)):
         raise ValueError(f"topk_weights must be float32 {(M, topk)}")
-    device = x.device
     _require_all(device, (topk_ids, "topk_ids"), (topk_weights, "topk_weights"))
     out = _fp8_out(x, out, dtype, (M * topk, N))
     stream, transpose, x_per_slot = _raw_stream(device), int(bool(transpose)), int(bool(x_per_slot))
-    if workspace is None:
-        workspace = _workspace(device, stream, _size_of(device, lib.w4a16_minifloat_moe_workspace_size, M, topk, E, N, K, x_code,
-                                                        transpose, x_per_slot))
-    ws_ptr = None if workspace is None else workspace.data_ptr()
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_ptr, ws_bytes = _fp8_workspace(device, stream, workspace, lib.w4a16_minifloat_moe_workspace_size, M, topk, E, N, K, x_code,
+                                      transpose, x_per_slot)
     _invoke(device, lib.w4a16_minifloat_moe_linear, x.data_ptr(), _ptr(x_scales), w.data_ptr(), scales.data_ptr(), _ptr(bias),
             topk_ids.data_ptr(), _ptr(topk_weights), out.data_ptr(), M, topk, E, N, K, x_code, s_code, dt, transpose, x_per_slot,
             ws_ptr, ws_bytes, stream)
