@@ -86,7 +86,7 @@ __device__ __forceinline__ bool find_tile(const int32_t* start, int E, int t, in
   return false;
 }
 
-// What bounds it at 1920 x 28672 x 4096 (305 us, 1.48 PFLOP/s with fp32 scales): no
+// What bounds it at 1920 x 28672 x 4096 (313 us, 1.44 PFLOP/s with fp32 scales): no
 // unit alone.  At the 1.97 GHz that the card keeps under this load a step of one of
 // a CU's two workgroups takes 1400 cycles, of which LDS serves 790 (operands 533,
 // the next pieces 256), the vector units 530 and the matrix units 512.  In the same
