@@ -158,10 +158,13 @@ w4a16_status fp8_product(const char* what, const void* x, const uint8_t* x_scale
   const Buffer ws[] = {{workspace, p.bytes}};
   if (any_overlap(ws, in) || any_overlap(ws, out))
     return fail(W4A16_ERR_INVALID_ARG, "%s: the workspace must not overlap an input or an output", what);
-  if (w4a16::tuning().log)
-    std::fprintf(stderr, "[w4a16] %s slots=%lld E=%lld N=%lld K=%lld %s%s%s\n", what, (long long)slots, (long long)E,
+  if (w4a16::tuning().log) {
+    char plan[64] = "decode";
+    if (!p.decode) std::snprintf(plan, sizeof(plan), "tile=%dx128 splits=%d steps=%d", p.tiles.bm, p.tiles.splits, p.tiles.steps);
+    std::fprintf(stderr, "[w4a16] %s slots=%lld E=%lld N=%lld K=%lld %s%s%s %s\n", what, (long long)slots, (long long)E,
                  (long long)N, (long long)K, dtype == W4A16_F16 ? "f16" : "bf16", scale_dtype == W4A16_E8M0 ? " e8m0" : "",
-                 transpose ? " transposed" : "");
+                 transpose ? " transposed" : "", plan);
+  }
   char* const base = static_cast<char*>(workspace);
   hipStream_t s = static_cast<hipStream_t>(stream);
   w4a16::Fp8Args a{};
