@@ -94,7 +94,10 @@ __global__ __launch_bounds__(1024) void fp8_decode_kernel(DecodeParams p) {
 #pragma unroll
   for (int t = 0; t < TN; ++t) wrow[t] = (uint32_t)min(n0 + 16 * t + col, p.N - 1) * (uint32_t)p.K;
   u32x4 wv[DEPTH][TN][2];
-  auto load = [&](int b, u32x4 (&v)[TN][2]) {
+  uint32_t wsv[DEPTH];  // the blocks' scales, as they are
+  auto load = [&](int b, u32x4 (&v)[TN][2], uint32_t& scale) {
+    if constexpr (E8M0) scale = static_cast<const uint8_t*>(p.ws)[ws0 + b];
+    else scale = static_cast<const uint32_t*>(p.ws)[ws0 + b];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       // past the last k: bytes of the same row, which meet zero codes
@@ -105,7 +108,7 @@ __global__ __launch_bounds__(1024) void fp8_decode_kernel(DecodeParams p) {
   };
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d)
-    if (wave + waves * d < p.blocks) load(wave + waves * d, wv[d]);
+    if (wave + waves * d < p.blocks) load(wave + waves * d, wv[d], wsv[d]);
 
   const bool live = col < count;
   const int stride = 128 * p.blocks + 16;
@@ -147,8 +150,16 @@ __global__ __launch_bounds__(1024) void fp8_decode_kernel(DecodeParams p) {
       const i32x8 xo = {(int)x0[0], (int)x0[1], (int)x0[2], (int)x0[3], (int)x1[0], (int)x1[1], (int)x1[2], (int)x1[3]};
       float wsf = 1.f;
       int wsb = 127;
-      if constexpr (E8M0) wsb = static_cast<const uint8_t*>(p.ws)[ws0 + b];
-      else wsf = static_cast<const float*>(p.ws)[ws0 + b];
+      if constexpr (E8M0) {
+        wsb = (int)wsv[d];
+      } else {
+        // the scale's power of two goes to the matrix unit, so that a block's sum stays in range wherever its
+        // product with the scale does (zero, infinite, NaN: 1/2; subnormal: 2^-126)
+        const float whole = __builtin_bit_cast(float, wsv[d]);
+        const int e = max(__builtin_amdgcn_frexp_expf(whole), -125);
+        wsb = e + 126;
+        wsf = __builtin_amdgcn_ldexpf(whole, 1 - e);
+      }
 #pragma unroll
       for (int t = 0; t < TN; ++t) {
         i32x8 wo;
@@ -157,12 +168,12 @@ __global__ __launch_bounds__(1024) void fp8_decode_kernel(DecodeParams p) {
         if constexpr (E8M0) {
           acc[t] = mfma16(wo, xo, acc[t], wsb, xsb);
         } else {
-          const f32x4 v = mfma16(wo, xo, f32x4{0.f, 0.f, 0.f, 0.f}, 127, xsb);
+          const f32x4 v = mfma16(wo, xo, f32x4{0.f, 0.f, 0.f, 0.f}, wsb, xsb);
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[t][i] = __builtin_fmaf(v[i], wsf, acc[t][i]);
         }
       }
-      if (b + waves * DEPTH < p.blocks) load(b + waves * DEPTH, wv[d]);
+      if (b + waves * DEPTH < p.blocks) load(b + waves * DEPTH, wv[d], wsv[d]);
     }
   }
   float* const red = reinterpret_cast<float*>(lds);

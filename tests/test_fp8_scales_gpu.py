@@ -191,3 +191,24 @@ def test_powers_of_two_at_their_ends(M, N, height, transpose, planned):  # noqa:
         # (below the normal numbers the matrix unit may give zero, for each of the 80 sums of eight products)
         allowed = 2.0 ** -8 * (np.abs(total) + slack) + slack + 81 * 2.0 ** -126
         assert (np.abs(have - total) <= allowed)[fine].all()
+
+
+@pytest.mark.parametrize("M,N,height", ROWS)
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("size,scale", [(2.0 ** 121, 2e-4), (2.0 ** -110, 2e30), (2.0 ** -129, 2e37), (1e6, 1e-36)])
+def test_tokens_and_scales_far_from_one(M, N, height, transpose, size, scale, planned):  # noqa: F811
+    # the sum of a block's codes with one of the scales alone may pass fp32's range, the product does not
+    rng = np.random.default_rng([M, N, 2])
+    K = 640
+    if transpose:
+        N, K = (N + 15) // 16 * 16, 637
+        height = height or 32
+    blocks = ((K + 127) // 128, (N + 127) // 128) if transpose else ((N + 127) // 128, (K + 127) // 128)
+    layer = Weights(rng, N, K, transpose, False, scales=(rng.uniform(0.5, 1.5, blocks) * scale).astype(np.float32))
+    x = torch.from_numpy(rng.uniform(0.5, 8, (M, K)) * rng.choice([-1, 1], (M, K)) * size).to(torch.bfloat16)
+    y, plan = planned(lambda: L.w4a16_minifloat_linear(x.cuda(), layer.tw, layer.ts, transpose=transpose))
+    assert plan == (None if height is None else (height, 1))
+    rows = edges(rng, M, height or 16, 6)
+    cols = np.arange(N) if N < 2000 else edges(rng, N, 128, 160)
+    codes, scales = X.fp8_quantize_ref(x[rows].double().numpy())
+    compare(y[torch.from_numpy(rows).cuda()][:, torch.from_numpy(cols).cuda()], codes, scales, layer, cols, None, "bf16")
