@@ -467,8 +467,13 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs
 // The gradient, sixteen lanes a row: lane j has slot j's gradient (and those of
 // slots j + 16, ..), and every lane adds what meets its own experts.  Lanes take
 // turns over a row's pieces, so that a row's loads and stores are whole lines (parts
-// of 64 bytes a lane: 13.4 us at 16384 x 256).  In fp32.  Memory and the slots' chain
-// bound it: 16384 x 256 in fp32 10.3 us, 3.4 TB/s.
+// of 64 bytes a lane: 13.4 us at 16384 x 256).  In fp32, but for renormalised
+// weights: with the shares r_j = p_j / S and c the sum of r_j g_j, d l of a chosen
+// expert is r_j (g_j - c), times 1 - s_j for sigmoid, and that of the others 0
+// (softmax's sum of s_k d s_k is c - c).  The scores p_j are taken in 64 bits, as
+// the forward pass takes them: all of a row's may lie below fp32's range and their
+// shares be ordinary numbers.  Memory and the slots' chain bound it: 16384 x 256
+// in fp32 10.5 us, 3.3 TB/s.
 template <int DT, int V, bool WHOLE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteBackwardArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, base = lane & 48;
@@ -498,11 +503,14 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
 #pragma unroll
   for (int v = 0; v < V; ++v) nan |= s[v] != s[v], ds[v] = 0.f;
   nan = row_any(nan);
+  const bool whole_row = !a.sigmoid && !a.renormalize;  // every expert has a gradient
   float top = -__builtin_inff(), total = 1.f;
   if (!a.sigmoid) {
 #pragma unroll
     for (int v = 0; v < V; ++v) top = fmaxf(top, s[v]);
     top = row_max(top);
+  }
+  if (whole_row) {
 #pragma unroll
     for (int v = 0; v < V; ++v) s[v] = s[v] == -__builtin_inff() ? 0.f : (s[v] == top ? 1.f : expf(s[v] - top));
     total = row_sum(part_sum<V>(s));
@@ -510,42 +518,53 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
 #pragma unroll
     for (int v = 0; v < V; ++v) s[v] *= inv;
   }
-  // a slot's score and 1 - score (of the two, the small one is formed without a difference)
-  auto score_of = [&](int id, float& rest) {
-    const float l = load_logit<DT>(a.logits, m * a.E + id);
-    rest = 1.f;
-    if (!a.sigmoid) return l == -__builtin_inff() ? 0.f : (l == top ? 1.f : expf(l - top)) / total;
-    const float t = expf(-fabsf(l)), q = 1.f / (1.f + t);
-    rest = l >= 0 ? t * q : q;
-    return l >= 0 ? q : t * q;
-  };
-  float sum = 1.f, mean = 0.f;
-  if (a.renormalize) {
-    float p = 0.f, pg = 0.f;
-    for (int j = c; j < a.topk; j += 16) {
-      const int id = a.ids[m * a.topk + j];
-      if (id < 0 || id >= a.E) continue;
-      float rest;
-      const float q = score_of(id, rest);
-      p += q;
-      pg += q * (a.dweights[m * a.topk + j] * a.scale);
-    }
-    sum = row_sum(p);
-    mean = sum > 0.f ? row_sum(pg) / sum : 0.f;
-  }
-  const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-  for (int j0 = 0; j0 < a.topk; j0 += 16) {
-    const int j = j0 + c;
-    int id = j < a.topk ? a.ids[m * a.topk + j] : -1;
-    float g = 0.f;
-    if (id >= 0 && id < a.E) {
-      g = (a.dweights[m * a.topk + j] * a.scale - mean) * (a.renormalize ? inv : 1.f);
-      if (a.sigmoid) {  // the logit's gradient at once: other experts have none
-        float rest;
-        const float q = score_of(id, rest);
-        g = g * q * rest;
+  // Sixteen slots at a time, lane c the c-th of them: with shares once for the scores' sum and the mean of the
+  // gradients, then for the gradients (the first sixteen are kept for that where there are no others).
+  const int rounds = (a.topk + 15) / 16;
+  int id = -1;
+  float g = 0.f;
+  double p = 0, rest = 1, sum = 0, mean = 0;
+  for (int r = a.renormalize ? 0 : rounds; r < 2 * rounds; ++r) {
+    const int j0 = 16 * (r < rounds ? r : r - rounds), j = j0 + c;
+    if (r < rounds || rounds > 1 || !a.renormalize) {
+      id = j < a.topk ? a.ids[m * a.topk + j] : -1;
+      if (id < 0 || id >= a.E) id = -1;
+      g = p = 0;
+      if (id >= 0) {
+        g = a.dweights[m * a.topk + j] * a.scale;
+        const float l = load_logit<DT>(a.logits, m * a.E + id);
+        if (a.renormalize) {
+          const double t = exp(a.sigmoid ? -(double)l : (double)l - (double)top);
+          if (a.sigmoid) {
+            p = 1.0 / (1.0 + t);
+            rest = t == __builtin_inf() ? 1.0 : t * p;
+          } else {
+            p = l == -__builtin_inff() ? 0.0 : (l == top ? 1.0 : t);
+          }
+          p *= 0x1p60;  // (1 / sum is finite, also of subnormal scores)
+        } else if (a.sigmoid) {
+          // score and 1 - score (of the two, the small one is formed without a difference)
+          const float t = expf(-fabsf(l)), q = 1.f / (1.f + t);
+          g = g * (l >= 0 ? q : t * q) * (l >= 0 ? t * q : q);
+        }
       }
     }
+    if (r < rounds) {
+      sum += p;
+      mean += id >= 0 ? p * (double)g : 0.0;
+      if (r + 1 < rounds) continue;
+      sum = row_sum(sum);
+      mean = row_sum(mean);
+      const double inv = 1.0 / sum;
+      mean = sum > 0 ? mean * inv : 0.0;
+      sum = sum > 0 ? inv : 0.0;  // (from here on its reciprocal)
+      // (0, or NaN where a gradient is not finite: softmax hands it to the whole row)
+      const float others = a.sigmoid ? 0.f : (float)(mean - mean);
+#pragma unroll
+      for (int v = 0; v < V; ++v) ds[v] = others;
+      continue;
+    }
+    if (a.renormalize) g = sum > 0 ? (float)(p * sum * ((double)g - mean) * rest) : 0.f;
     const int n = min(16, a.topk - j0);
     for (int k = 0; k < n; ++k) {
       const int e = __shfl(id, base + k) - P * c;
@@ -555,7 +574,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
     }
   }
   float dot = 0.f;
-  if (!a.sigmoid) {
+  if (whole_row) {
     float t[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) t[v] = s[v] * ds[v];
@@ -563,7 +582,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
   }
   float dl[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) dl[v] = nan ? __builtin_nanf("") : (a.sigmoid ? ds[v] : s[v] * (ds[v] - dot));
+  for (int v = 0; v < V; ++v) dl[v] = nan ? __builtin_nanf("") : (whole_row ? s[v] * (ds[v] - dot) : ds[v]);
   if (row >= a.M) return;
 #pragma unroll
   for (int i = 0; i < V / P; ++i) {
