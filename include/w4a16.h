@@ -476,7 +476,7 @@ w4a16_status w4a16_adamw_moments(const void* table, const w4a16_adamw_plan* plan
  *   ids[m, j]     = i_j
  * Keys are formed and compared in 64 bits (without a bias, and with group_top 1,
  * the logits themselves are compared: scores grow with them); weights are
- * rounded once, to fp32.
+ * rounded once, to fp32 (scale is taken in 64 bits).
  *   logits fp16, bf16 or fp32 [M, E]   bias fp32 [E] or NULL
  *   weights fp32 [M, topk]             ids int32 [M, topk]
  * An expert whose logit is -infinity or NaN, or whose key is, is never chosen:

@@ -23,7 +23,7 @@ struct RouteArgs {
   int64_t M;
   int E, topk, groups, topk_groups, group_top;
   int dtype, sigmoid, renormalize;
-  float scale;
+  double scale;
 };
 hipError_t launch_route(const RouteArgs& a, hipStream_t s);
 
@@ -35,7 +35,7 @@ struct RouteBackwardArgs {
   int64_t M;
   int E, topk;
   int dtype, sigmoid, renormalize;
-  float scale;
+  double scale;
 };
 hipError_t launch_route_backward(const RouteBackwardArgs& a, hipStream_t s);
 

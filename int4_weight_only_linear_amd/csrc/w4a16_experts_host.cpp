@@ -239,7 +239,7 @@ w4a16_status w4a16_route(const void* logits, const float* bias, float* weights, 
   st = device_info(&dev);
   if (st != W4A16_OK) return st;
   const w4a16::RouteArgs a{logits, bias, weights, ids, M, (int)E, (int)topk, (int)groups, (int)topk_groups,
-                           groups > 1 ? (int)group_top : 1, dtype, score == W4A16_SCORE_SIGMOID, renormalize != 0, (float)scale};
+                           groups > 1 ? (int)group_top : 1, dtype, score == W4A16_SCORE_SIGMOID, renormalize != 0, scale};
   return launched(w4a16::launch_route(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -261,7 +261,7 @@ w4a16_status w4a16_route_backward(const float* dweights, const void* logits, con
   st = device_info(&dev);
   if (st != W4A16_OK) return st;
   const w4a16::RouteBackwardArgs a{dweights, logits, ids, dlogits, M, (int)E, (int)topk, dtype, score == W4A16_SCORE_SIGMOID,
-                                   renormalize != 0, (float)scale};
+                                   renormalize != 0, scale};
   return launched(w4a16::launch_route_backward(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -145,7 +145,7 @@ __device__ void route_row(const RouteArgs& a, int64_t m, double* keys, double* g
     weight = sum > 0 ? weight / sum : 0.0;
   }
   if (lane < a.topk) {
-    a.weights[m * a.topk + lane] = nan ? __builtin_nanf("") : (float)(weight * (double)a.scale);
+    a.weights[m * a.topk + lane] = nan ? __builtin_nanf("") : (float)(weight * a.scale);
     a.ids[m * a.topk + lane] = id;
   }
 }
@@ -453,7 +453,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs
     weight = total > 0 ? weight / total : 0.0;
   }
   if (slot < a.topk && there) {
-    a.weights[m * a.topk + slot] = nan ? __builtin_nanf("") : (float)(weight * (double)a.scale);
+    a.weights[m * a.topk + slot] = nan ? __builtin_nanf("") : (float)(weight * a.scale);
     a.ids[m * a.topk + slot] = id;
   }
   uint64_t again = __ballot(open && c == 0 && there);
@@ -531,7 +531,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
       if (id < 0 || id >= a.E) id = -1;
       g = p = 0;
       if (id >= 0) {
-        g = a.dweights[m * a.topk + j] * a.scale;
+        g = (float)((double)a.dweights[m * a.topk + j] * a.scale);
         const float l = load_logit<DT>(a.logits, m * a.E + id);
         if (a.renormalize) {
           const double t = exp(a.sigmoid ? -(double)l : (double)l - (double)top);
