@@ -452,7 +452,9 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs
     const double total = row_sum(weight);
     weight = total > 0 ? weight / total : 0.0;
   }
-  if (slot < a.topk && there) {
+  // (rows that are done again below are stored there alone: by other lanes of this wave, whose stores nothing would
+  // order behind these)
+  if (slot < a.topk && there && !open) {
     a.weights[m * a.topk + slot] = nan ? __builtin_nanf("") : (float)(weight * a.scale);
     a.ids[m * a.topk + slot] = id;
   }
