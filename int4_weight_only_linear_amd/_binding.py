@@ -346,6 +346,19 @@ def _workspace(device, stream_ptr: int, nbytes: int):
         return buf
 
 
+def _given_workspace(device, workspace):
+    """(the pointer, the bytes) of a caller's workspace, which must lie on `device`: its pointer
+    goes to kernels; contiguous, since an expanded tensor has fewer bytes than elements."""
+    _require_device(workspace, "workspace", device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _own_workspace(device, stream_ptr: int, nbytes: int):
+    """(the pointer, the bytes) of the workspace kept for the device and stream."""
+    workspace = _workspace(device, stream_ptr, nbytes)
+    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+
+
 def _linear_args(x, wq, scales, zp, bias, group_size, out):
     torch = _torch()
     dtype = x.dtype
@@ -394,10 +407,8 @@ def w4a16_linear_path(x, wq, scales, zp=None, bias=None, *, group_size: int, pat
     stream = torch.cuda.current_stream(x.device).cuda_stream
     with torch.cuda.device(x.device):
         need = w4a16_workspace_size(M, N, K, group_size, dt, zp is not None, path)
-        if workspace is None:
-            workspace = _workspace(x.device, stream, need)
-        ws_ptr = None if workspace is None else workspace.data_ptr()
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws_ptr, ws_bytes = (_own_workspace(x.device, stream, need) if workspace is None
+                            else _given_workspace(x.device, workspace))
         _check(lib.w4a16_linear_path(x.data_ptr(), wq.data_ptr(), scales.data_ptr(), _ptr(zp),
                                      _ptr(bias), out.data_ptr(), M, N, K, group_size, dt, ws_ptr,
                                      ws_bytes, stream, path))
@@ -481,10 +492,8 @@ def w4a16_linear_dense(x, w, bias=None, *, out=None, workspace=None):
     stream = torch.cuda.current_stream(x.device).cuda_stream
     with torch.cuda.device(x.device):
         need = w4a16_dense_workspace_size(M, N, K, dt, bias is not None)
-        if workspace is None:
-            workspace = _workspace(x.device, stream, need)
-        ws_ptr = None if workspace is None else workspace.data_ptr()
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        ws_ptr, ws_bytes = (_own_workspace(x.device, stream, need) if workspace is None
+                            else _given_workspace(x.device, workspace))
         _check(lib.w4a16_linear_dense(x.data_ptr(), w.data_ptr(), _ptr(bias), out.data_ptr(), M, N, K,
                                       dt, ws_ptr, ws_bytes, stream))
     return out
@@ -569,11 +578,9 @@ def w4a16_lora_linear(x, wq, scales, la, lb, ids, zp=None, bias=None, alpha=None
     device = x.device
     u = torch.empty((M, R), dtype=torch.float32, device=device) if save_u else None
     stream = _raw_stream(device)
-    if workspace is None:
-        workspace = _workspace(device, stream, _size_of(device, lib.w4a16_lora_workspace_size, M, N, K, group_size, dt,
-                                                        int(zp is not None), R, int(save_u)))
-    ws_ptr = None if workspace is None else workspace.data_ptr()
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_ptr, ws_bytes = (_own_workspace(device, stream, _size_of(device, lib.w4a16_lora_workspace_size, M, N, K, group_size, dt,
+                                                                int(zp is not None), R, int(save_u)))
+                        if workspace is None else _given_workspace(device, workspace))
     _invoke(device, lib.w4a16_lora_linear, x.data_ptr(), wq.data_ptr(), scales.data_ptr(), _ptr(zp), _ptr(bias),
             la.data_ptr(), lb.data_ptr(), ids.data_ptr(), _ptr(alpha), out.data_ptr(), _ptr(u), M, N, K, group_size, S, R,
             dt, ws_ptr, ws_bytes, stream)
@@ -613,11 +620,9 @@ def w4a16_lora_backward(dy, x, u, wq, scales, la, lb, ids, zp=None, alpha=None, 
                 raise ValueError(f"{name} must be {x.dtype} {tuple(like.shape)}")
             _require_device(t, name, device)
     stream = _raw_stream(device)
-    if workspace is None:
-        workspace = _workspace(device, stream, _size_of(device, lib.w4a16_lora_backward_workspace_size, M, N, K, group_size,
-                                                        S, R, dt))
-    ws_ptr = None if workspace is None else workspace.data_ptr()
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws_ptr, ws_bytes = (_own_workspace(device, stream, _size_of(device, lib.w4a16_lora_backward_workspace_size, M, N, K, group_size,
+                                                                S, R, dt))
+                        if workspace is None else _given_workspace(device, workspace))
     _invoke(device, lib.w4a16_lora_backward, dy.data_ptr(), x.data_ptr(), u.data_ptr(), wq.data_ptr(), scales.data_ptr(),
             _ptr(zp), la.data_ptr(), lb.data_ptr(), ids.data_ptr(), _ptr(alpha), _ptr(dx), dla.data_ptr(), dlb.data_ptr(),
             M, N, K, group_size, S, R, dt, ws_ptr, ws_bytes, stream)
@@ -870,9 +875,8 @@ def _fp8_args(x, w, scales, bias, transpose, x_scales, dtype, rows, lead):
 def _fp8_workspace(device, stream, workspace, fn, *sizes):
     """(its pointer, its bytes): the caller's, or the one of the device and stream."""
     if workspace is not None:
-        return workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    workspace = _workspace(device, stream, _size_of(device, fn, *sizes))
-    return (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+        return _given_workspace(device, workspace)
+    return _own_workspace(device, stream, _size_of(device, fn, *sizes))
 
 
 def _fp8_out(x, out, dtype, shape):
