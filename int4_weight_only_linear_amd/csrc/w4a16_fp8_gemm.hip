@@ -217,10 +217,12 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
 
   // ---- scales.  x's, a word of four blocks for each token, go to the matrix unit as they are.  So does the
   // power of two of an fp32 scale of w; its rest, 1 <= |unit| < 2, is the unit that the accumulators are kept
-  // in, changed by one product for each of them and block, half of what adding scaled sums takes.  Blocks whose
-  // scale is no normal number (zero, subnormal, infinite or NaN) are left out of the loop, so that a change of
-  // unit is always between 1/2 and 2, and added behind it; in the loop, as a second form of a step, they made
-  // the compiler keep the accumulators twice (1920 x 28672 x 4096 311 -> 326 us).
+  // in, changed by one product for each of them and block, half of what adding scaled sums takes.  What a
+  // subnormal scale's power of two lies below the smallest one of a normal number is taken from x's; a zero
+  // scale brings both down to where nothing is left of finite products; NaN goes to the matrix unit.  Blocks of
+  // an infinite scale are left out of the loop and added behind it: in the loop, as a second form of a step, they
+  // made the compiler keep the accumulators twice (1920 x 28672 x 4096 311 -> 326 us), and behind it they take
+  // their loads' whole latency, which zero scales must not (all of them zero there: 524 us).
   uint32_t xsoff[TM], xs[TM], xs_next[TM];
   const uint8_t* const xs_base = p.xs + s_begin;
   const int xs_last = p.xsrow - 4 - s_begin;
@@ -237,20 +239,32 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
   float unit_of = 1.f, ratio = 1.f, ws_next = 0.f;
   if constexpr (!E8M0) ws_next = *(const_float*)(static_cast<const float*>(p.ws) + scale_at(0));
   int sa = 127;
-  bool apart = false, any_apart = false;  // the block is (a block was) left out
+  int lower = 0;           // what x's powers of two are lowered by
+  bool infinite = false;   // a block was left out
   auto next_scale = [&](int s) {
     if constexpr (E8M0) {
       // (a word at a time: it holds the byte, so it lies in the same allocation)
       const uintptr_t at = reinterpret_cast<uintptr_t>(static_cast<const uint8_t*>(p.ws) + scale_at(s));
       sa = (int)(*(const_u32*)(at & ~(uintptr_t)3) >> (8 * (at & 3))) & 255;
     } else {
-      const uint32_t bits = __builtin_bit_cast(uint32_t, ws_next), field = (bits >> 23) & 255;
-      const float u = __builtin_bit_cast(float, (bits & 0x807FFFFFu) | 0x3F800000u);
-      apart = field == 0 || field == 255;
-      any_apart |= apart;
+      const uint32_t bits = __builtin_bit_cast(uint32_t, ws_next), field = (bits >> 23) & 255, rest = bits & 0x007FFFFFu;
+      float u = __builtin_bit_cast(float, (bits & 0x807FFFFFu) | 0x3F800000u);
       sa = (int)field;
+      lower = 0;
+      if (field == 0 && rest) {
+        lower = __builtin_clz(rest) - 8;
+        u = __builtin_bit_cast(float, (bits & 0x80000000u) | 0x3F800000u | ((rest << lower) & 0x007FFFFFu));
+        sa = 1;
+      } else if (field == 0) {
+        u = unit_of;
+        lower = 255;
+      } else if (field == 255) {
+        u = unit_of;
+        infinite |= !rest;
+        sa = rest ? 255 : -1;
+      }
       ratio = unit_of / u;
-      if (!apart) unit_of = u;
+      unit_of = u;
     }
   };
 
@@ -283,12 +297,16 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
       }
     }
     if (tail && s >= steps) return;
-    if (idle || apart) sa = -1;
+    if (idle) sa = -1;
     if constexpr (E8M0) asm("" : "+s"(sa));  // (a branch that may be taken keeps the steps apart: gathered, they spill)
     if (sa < 0) return;
     int sb[TM];
 #pragma unroll
     for (int t = 0; t < TM; ++t) sb[t] = (int)(xs[t] >> (8 * i));
+    if (!E8M0 && lower) {
+#pragma unroll
+      for (int t = 0; t < TM; ++t) sb[t] = (sb[t] & 255) == 255 ? 255 : max((sb[t] & 255) - lower, 0);
+    }
     i32x8 a[TN][2], b[TM][2];
 #pragma unroll
     for (int n = 0; n < TN; ++n)
@@ -318,10 +336,9 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
   if constexpr (!E8M0) {
     // the blocks that were left out (the same ones for all waves: BN features share a scale)
     static_assert(BN == 128);
-    for (int s = 0; any_apart && s < steps; ++s) {
+    for (int s = 0; infinite && s < steps; ++s) {
       const float w = *(const_float*)(static_cast<const float*>(p.ws) + scale_at(s));
-      const uint32_t field = (__builtin_bit_cast(uint32_t, w) >> 23) & 255;
-      if (field != 0 && field != 255) continue;
+      if (fabsf(w) != __builtin_inff()) continue;
       auto meet = [&] {  // every wave's loads have landed, and its reads are done
         __builtin_amdgcn_sched_barrier(0);
         __builtin_amdgcn_s_waitcnt(wait_vm(0));
@@ -332,10 +349,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
       stage(s, std::integral_constant<int, 0>{});
       meet();
       if (idle) continue;
-      // (of the power of two that makes a subnormal scale normal, half goes to the matrix unit, where sums of codes
-      // then stay below 2^90, whatever x's scale)
-      const int half_power = field ? 127 : 64;
-      const float rest = (field ? w : w * 0x1p63f) / unit_of;
+      const float rest = w / unit_of;
       static_for<0, TM * TN>([&](auto J) {
         constexpr int t = decltype(J)::value / TN, n = decltype(J)::value % TN;
         const int sb = xs_base[xsoff[t] + s];
@@ -343,7 +357,7 @@ __global__ __launch_bounds__(64 * (BM / WM) * (BN / WN), WAVES_PER_SIMD) void fp
 #pragma unroll
         for (int kk = 0; kk < 2; ++kk)
           v = mfma_fp8(TR ? operand_t((lds_u8*)st0 + XP * 1024, n, kk) : operand((lds_u8*)st0 + XP * 1024 + (wn + 32 * n) * BK, kk),
-                       operand((lds_u8*)st0 + (wm + 32 * t) * BK, kk), v, half_power, sb);
+                       operand((lds_u8*)st0 + (wm + 32 * t) * BK, kk), v, 127, sb);
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[n][t][e] = __builtin_fmaf(v[e], rest, acc[n][t][e]);
       });
