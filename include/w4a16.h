@@ -499,10 +499,10 @@ w4a16_status w4a16_route(const void* logits, const float* bias, float* weights, 
  *   d s_{i_j} = g_j                   (renormalize == 0), (g_j - c) / S (renormalize != 0)
  *   d l_e = s_e (d s_e - sum over k of s_k d s_k)   softmax
  *         = d s_e s_e (1 - s_e)                     sigmoid
- * in fp32 (with renormalize the scores and their shares in 64 bits, as in
- * w4a16_route: the scores may all lie below fp32's range; a sum that is zero gives
- * no gradient), rounded once to the logits' type.  ids as w4a16_route wrote them
- * (any choice is taken: an id outside [0, E) adds nothing, one that is there twice
+ * in fp32 for softmax without renormalize, otherwise from scores in 64 bits, as in
+ * w4a16_route (renormalised ones may all lie below fp32's range; a sum that is
+ * zero gives no gradient), rounded once to the logits' type.  ids as w4a16_route
+ * wrote them (any choice is taken: an id outside [0, E) adds nothing, one that is there twice
  * counts twice).  Every element of dlogits [M, E] is written; -infinite logits
  * get zero, a row with a NaN logit NaN (softmax: one with an infinite or NaN
  * gradient as well). */

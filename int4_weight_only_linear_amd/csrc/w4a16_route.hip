@@ -469,13 +469,13 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs
 // The gradient, sixteen lanes a row: lane j has slot j's gradient (and those of
 // slots j + 16, ..), and every lane adds what meets its own experts.  Lanes take
 // turns over a row's pieces, so that a row's loads and stores are whole lines (parts
-// of 64 bytes a lane: 13.4 us at 16384 x 256).  In fp32, but for renormalised
-// weights: with the shares r_j = p_j / S and c the sum of r_j g_j, d l of a chosen
-// expert is r_j (g_j - c), times 1 - s_j for sigmoid, and that of the others 0
-// (softmax's sum of s_k d s_k is c - c).  The scores p_j are taken in 64 bits, as
-// the forward pass takes them: all of a row's may lie below fp32's range and their
-// shares be ordinary numbers.  Memory and the slots' chain bound it: 16384 x 256
-// in fp32 10.5 us, 3.3 TB/s.
+// of 64 bytes a lane: 13.4 us at 16384 x 256).  Softmax without renormalisation is
+// formed over the whole row, in fp32; otherwise only chosen experts have gradients,
+// from scores in 64 bits.  Renormalised, with the shares r_j = p_j / S and c the sum
+// of r_j g_j, d l is r_j (g_j - c), times 1 - s_j for sigmoid (softmax's sum of
+// s_k d s_k is c - c); all p_j of a row may lie below fp32's range and their shares
+// be ordinary numbers.  Memory and the slots' chain bound it: 16384 x 256 in fp32
+// 10.5 us, 3.3 TB/s (in fp32 throughout 10.4).
 template <int DT, int V, bool WHOLE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteBackwardArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, base = lane & 48;
@@ -516,9 +516,10 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
 #pragma unroll
     for (int v = 0; v < V; ++v) s[v] = s[v] == -__builtin_inff() ? 0.f : (s[v] == top ? 1.f : expf(s[v] - top));
     total = row_sum(part_sum<V>(s));
-    const float inv = total > 0.f ? 1.f / total : 0.f;
+    // (the reciprocal and what it lacks: a score is rounded once)
+    const float inv = total > 0.f ? 1.f / total : 0.f, lack = __builtin_fmaf(-total, inv, 1.f) * inv;
 #pragma unroll
-    for (int v = 0; v < V; ++v) s[v] *= inv;
+    for (int v = 0; v < V; ++v) s[v] = __builtin_fmaf(s[v], inv, s[v] * lack);
   }
   // Sixteen slots at a time, lane c the c-th of them: with shares once for the scores' sum and the mean of the
   // gradients, then for the gradients (the first sixteen are kept for that where there are no others).
@@ -535,19 +536,16 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
       if (id >= 0) {
         g = (float)((double)a.dweights[m * a.topk + j] * a.scale);
         const float l = load_logit<DT>(a.logits, m * a.E + id);
-        if (a.renormalize) {
+        if (!whole_row) {
           const double t = exp(a.sigmoid ? -(double)l : (double)l - (double)top);
           if (a.sigmoid) {
             p = 1.0 / (1.0 + t);
-            rest = t == __builtin_inf() ? 1.0 : t * p;
+            rest = t == __builtin_inf() ? 1.0 : t * p;  // 1 - p, without a difference
           } else {
             p = l == -__builtin_inff() ? 0.0 : (l == top ? 1.0 : t);
           }
+          if (!a.renormalize) g = (float)((double)g * p * rest);
           p *= 0x1p60;  // (1 / sum is finite, also of subnormal scores)
-        } else if (a.sigmoid) {
-          // score and 1 - score (of the two, the small one is formed without a difference)
-          const float t = expf(-fabsf(l)), q = 1.f / (1.f + t);
-          g = g * (l >= 0 ? q : t * q) * (l >= 0 ? t * q : q);
         }
       }
     }
