@@ -86,17 +86,18 @@ __device__ __forceinline__ bool find_tile(const int32_t* start, int E, int t, in
   return false;
 }
 
-// What bounds it at 1920 x 28672 x 4096 (313 us, 1.44 PFLOP/s with fp32 scales): no
+// What bounds it at 1920 x 28672 x 4096 (311 us, 1.45 PFLOP/s with fp32 scales): no
 // unit alone.  At the 1.97 GHz that the card keeps under this load a step of one of
 // a CU's two workgroups takes 1400 cycles, of which LDS serves 790 (operands 533,
-// the next pieces 256), the vector units 530 and the matrix units 512.  In the same
-// harness (358 us there): steps of 64 k four deep 398, three workgroups a CU 395,
-// 256 x 256 in steps of 64 k 346, all reads of a step before its loads 343 (E8M0
-// scales 315 against 308), 128 x 256 with waves of 64 x 128 in steps of 64 k 339
-// (transposed 318 against 352, where there are tiles for two on each CU).  Without
-// the change of unit (E8M0) the product takes 308.  Of experts' slots (16384 of 64
-// experts x 4096 x 2048, 294 us) a quarter of the tiles' places are empty; skipping
-// products of empty 32s inside a wave as well gains nothing.
+// the next pieces 256), the vector units 510 and the matrix units 512.  Without the
+// change of unit (E8M0) the product takes 283.  In a harness whose base of 358 us
+// was slower than this kernel, so that its order need not carry over: steps of 64 k
+// four deep 398, three workgroups a CU 395, 256 x 256 in steps of 64 k 346, all reads
+// of a step before its loads 343, 128 x 256 with waves of 64 x 128 in steps of 64 k
+// 339 (transposed 318 against 352, where there are tiles for two on each CU).  Of
+// experts' slots (16384 of 64 experts x 4096 x 2048, 297 us; transposed 2048 x 4096
+// 382) a quarter of the tiles' places are empty; skipping products of empty 32s
+// inside a wave as well gains nothing.
 // A workgroup owns BM tokens (or slots of one expert) x BN features and one K
 // range, in steps of a block of 128 k; its waves own WM x WN of it each.  A
 // step's rows of x and w go straight from memory to LDS, one step ahead; the

@@ -43,9 +43,11 @@ __device__ __forceinline__ void wave_lds_fence() { __builtin_amdgcn_fence(__ATOM
 constexpr int kRouteWaves = 4;
 
 // A row by one wave, keys in 64 bits, V experts a lane (expert 64 v + lane): what
-// the rows of more than 512 experts or 16 choices take (16384 rows of 256 take 57.6
-// us here, of which 64-bit exponentials and wave-wide reductions of pairs are most,
-// and 14.8 with sixteen lanes a row), and single rows of equal keys;
+// rows of more than 512 experts or 16 choices take, those whose groups are not a
+// power of two of whole lanes in the sixteen-lane form, and single rows of equal
+// keys.  Bound by the vector unit (160 experts: 1225 instructions a row): 16384 rows
+// of 160 experts in 8 groups 41 us, of 60 in 4 27, of 1024 88; 32 choices of 256
+// 171; with sixteen lanes a row 128 experts in 8 groups take 8.8, 256 14.5;
 // keys [64 V] and group_key [kMaxGroups] are the wave's own LDS.
 template <int DT, int V>
 __device__ void route_row(const RouteArgs& a, int64_t m, double* keys, double* group_key) {
@@ -322,8 +324,10 @@ __device__ __forceinline__ void sort_part(int (&x)[V]) {
 // A lane sorts its keys once, as integers whose lowest bits name the place (V units
 // of 2^-23 |key| more), so that a round of the choice looks at sixteen first places
 // (rounds that search all V and take one out: 2 us more at 16384 x 256).
-// Bound by the chain of a wave's instructions, of which four rows share one: 16384 x
-// 256 in fp32 with 8 groups 14.8 us, 1.2 TB/s; 4 rows 4.7 us in the kernel.
+// Bound by the vector unit: 16384 x 256 in fp32 with 8 groups 14.5 us, 1.2 TB/s, of
+// which a launch is 2.4; a wave of four rows issues 1400 vector instructions, and
+// those of a SIMD's four waves take 23000 of the 24200 cycles that they live.  4 rows
+// take 3.7 us in the kernel.
 template <int DT, int V, bool WHOLE>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs a) {
   constexpr int V64 = V > 4 ? V / 4 : 1;
