@@ -503,9 +503,9 @@ w4a16_status w4a16_route(const void* logits, const float* bias, float* weights, 
  * w4a16_route (renormalised ones may all lie below fp32's range; a sum that is
  * zero gives no gradient), rounded to fp32 and then to the logits' type.  ids as
  * w4a16_route wrote them (any choice is taken: an id outside [0, E) adds nothing,
- * one that is there twice counts twice).  Every element of dlogits [M, E] is written; -infinite logits
- * get zero, a row with a NaN logit NaN (softmax: one with an infinite or NaN
- * gradient as well). */
+ * one that is there twice counts twice).  Every element of dlogits [M, E] is
+ * written; -infinite logits get zero, a row with a NaN logit NaN (softmax: one
+ * with an infinite or NaN gradient as well). */
 w4a16_status w4a16_route_backward(const float* dweights, const void* logits, const int32_t* ids, void* dlogits,
                                   int64_t M, int64_t E, int64_t topk, int32_t dtype, int32_t score,
                                   int32_t renormalize, double scale, void* stream);
@@ -546,8 +546,9 @@ w4a16_status w4a16_minifloat_quantize(const void* x, void* codes, uint8_t* scale
  * 128 tokens and 128 features in all K ranges (W4A16_ERR_UNSUPPORTED above).
  * Workspace: w4a16_minifloat_linear_workspace_size bytes (0: none; enough for x of
  * any alignment, though 16-byte aligned rows of few tokens are quantised without
- * it), 256-byte aligned, under w4a16_linear's rules.  w and codes 16-byte, scales 4-byte (e8m0 w_scales
- * any), the others 2-byte aligned; y and the workspace overlap nothing. */
+ * it), 256-byte aligned, under w4a16_linear's rules.  w and codes 16-byte, scales
+ * 4-byte (e8m0 w_scales any), the others 2-byte aligned; y and the workspace
+ * overlap nothing. */
 size_t w4a16_minifloat_linear_workspace_size(int64_t M, int64_t N, int64_t K, int32_t x_dtype, int32_t transpose);
 w4a16_status w4a16_minifloat_linear(const void* x, const uint8_t* x_scales, const void* w, const void* w_scales,
                               const void* bias, void* y, int64_t M, int64_t N, int64_t K, int32_t x_dtype,
