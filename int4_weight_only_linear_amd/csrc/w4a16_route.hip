@@ -473,14 +473,14 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_quick_kernel(RouteArgs
 // The gradient, sixteen lanes a row: lane j has slot j's gradient (and those of
 // slots j + 16, ..), and every lane adds what meets its own experts.  Lanes take
 // turns over a row's pieces, so that a row's loads and stores are whole lines (parts
-// of 64 bytes a lane: 13.4 us at 16384 x 256).  Softmax without renormalisation is
-// formed over the whole row, in fp32; otherwise only chosen experts have gradients,
-// from scores in 64 bits.  Renormalised, with the shares r_j = p_j / S and c the sum
+// of 64 bytes a lane: 13.4 us at 16384 x 256).  Softmax without renormalisation (ROW)
+// is formed over the whole row, in fp32; otherwise only chosen experts have
+// gradients, from scores in 64 bits.  Renormalised, with the shares r_j = p_j / S and c the sum
 // of r_j g_j, d l is r_j (g_j - c), times 1 - s_j for sigmoid (softmax's sum of
 // s_k d s_k is c - c); all p_j of a row may lie below fp32's range and their shares
-// be ordinary numbers.  Memory and the slots' chain bound it: 16384 x 256 in fp32
-// 10.5 us, 3.3 TB/s (in fp32 throughout 10.4).
-template <int DT, int V, bool WHOLE>
+// be ordinary numbers.  A kernel for each of the two, since one with both held the
+// registers of both (16384 rows of 1024 experts, sigmoid: 38.5 us, 34.0 apart).  Memory and the slots' chain bound it: 16384 x 256 in fp32 10.2 us, 3.4 TB/s.
+template <int DT, int V, bool WHOLE, bool ROW>
 __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteBackwardArgs a) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = lane & 15, base = lane & 48;
   const int64_t row = ((int64_t)blockIdx.x * kRouteWaves + wave) * 4 + (lane >> 4);
@@ -509,14 +509,13 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
 #pragma unroll
   for (int v = 0; v < V; ++v) nan |= s[v] != s[v], ds[v] = 0.f;
   nan = row_any(nan);
-  const bool whole_row = !a.sigmoid && !a.renormalize;  // every expert has a gradient
   float top = -__builtin_inff(), total = 1.f;
-  if (!a.sigmoid) {
+  if (ROW || !a.sigmoid) {
 #pragma unroll
     for (int v = 0; v < V; ++v) top = fmaxf(top, s[v]);
     top = row_max(top);
   }
-  if (whole_row) {
+  if constexpr (ROW) {
 #pragma unroll
     for (int v = 0; v < V; ++v) s[v] = s[v] == -__builtin_inff() ? 0.f : (s[v] == top ? 1.f : expf(s[v] - top));
     total = row_sum(part_sum<V>(s));
@@ -531,16 +530,17 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
   int id = -1;
   float g = 0.f;
   double p = 0, rest = 1, sum = 0, mean = 0;
-  for (int r = a.renormalize ? 0 : rounds; r < 2 * rounds; ++r) {
+  const bool shares = !ROW && a.renormalize;
+  for (int r = shares ? 0 : rounds; r < 2 * rounds; ++r) {
     const int j0 = 16 * (r < rounds ? r : r - rounds), j = j0 + c;
-    if (r < rounds || rounds > 1 || !a.renormalize) {
+    if (r < rounds || rounds > 1 || !shares) {
       id = j < a.topk ? a.ids[m * a.topk + j] : -1;
       if (id < 0 || id >= a.E) id = -1;
       g = p = 0;
       if (id >= 0) {
         g = (float)((double)a.dweights[m * a.topk + j] * a.scale);
-        const float l = load_logit<DT>(a.logits, m * a.E + id);
-        if (!whole_row) {
+        if constexpr (!ROW) {
+          const float l = load_logit<DT>(a.logits, m * a.E + id);
           const double t = exp(a.sigmoid ? -(double)l : (double)l - (double)top);
           if (a.sigmoid) {
             p = 1.0 / (1.0 + t);
@@ -548,7 +548,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
           } else {
             p = l == -__builtin_inff() ? 0.0 : (l == top ? 1.0 : t);
           }
-          if (!a.renormalize) g = (float)((double)g * p * rest);
+          if (!shares) g = (float)((double)g * p * rest);
           p *= 0x1p60;  // (1 / sum is finite, also of subnormal scores)
         }
       }
@@ -568,7 +568,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
       for (int v = 0; v < V; ++v) ds[v] = others;
       continue;
     }
-    if (a.renormalize) g = sum > 0 ? (float)(p * sum * ((double)g - mean) * rest) : 0.f;
+    if (shares) g = sum > 0 ? (float)(p * sum * ((double)g - mean) * rest) : 0.f;
     const int n = min(16, a.topk - j0);
     for (int k = 0; k < n; ++k) {
       const int e = __shfl(id, base + k) - P * c;
@@ -578,7 +578,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
     }
   }
   float dot = 0.f;
-  if (whole_row) {
+  if constexpr (ROW) {
     float t[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) t[v] = s[v] * ds[v];
@@ -586,7 +586,7 @@ __global__ __launch_bounds__(64 * kRouteWaves) void route_backward_kernel(RouteB
   }
   float dl[V];
 #pragma unroll
-  for (int v = 0; v < V; ++v) dl[v] = nan ? __builtin_nanf("") : (whole_row ? s[v] * (ds[v] - dot) : ds[v]);
+  for (int v = 0; v < V; ++v) dl[v] = nan ? __builtin_nanf("") : (ROW ? s[v] * (ds[v] - dot) : ds[v]);
   if (row >= a.M) return;
 #pragma unroll
   for (int i = 0; i < V / P; ++i) {
@@ -671,8 +671,13 @@ hipError_t launch_route_backward(const RouteBackwardArgs& a, hipStream_t s) {
     by_size(a.E, 16, [&](auto n) {
       constexpr int V = decltype(n)::value;
       const dim3 grid = rows_grid(a.M, 4 * kRouteWaves);
-      if (whole) hipLaunchKernelGGL((route_backward_kernel<DT, V, true>), grid, dim3(64 * kRouteWaves), 0, s, a);
-      else hipLaunchKernelGGL((route_backward_kernel<DT, V, false>), grid, dim3(64 * kRouteWaves), 0, s, a);
+      auto go = [&](auto row) {
+        constexpr bool ROW = decltype(row)::value;
+        if (whole) hipLaunchKernelGGL((route_backward_kernel<DT, V, true, ROW>), grid, dim3(64 * kRouteWaves), 0, s, a);
+        else hipLaunchKernelGGL((route_backward_kernel<DT, V, false, ROW>), grid, dim3(64 * kRouteWaves), 0, s, a);
+      };
+      if (!a.sigmoid && !a.renormalize) go(std::true_type{});
+      else go(std::false_type{});
     });
   });
   return hipGetLastError();
